@@ -389,6 +389,138 @@ kda_status kda_prefill(const kda_bf16* q, const kda_bf16* k, const kda_bf16* v, 
                        const int64_t* checkpoint_cu_starts_host, int64_t checkpoint_every_n_tokens,
                        int32_t* device_status, struct CUstream_st* stream);
 
+/* Linear attention with a decay for each head, and the norm and position
+ * rotation of its queries and keys.
+ *
+ * The method (next to the delta rule above: no normalisation inside, no delta
+ * correction): per (sequence, value head h) a value-first FP32 state S[128, 128],
+ *   S_t = exp(g_t) S_{t-1} + v_t k_t^T,     o_t = scale S_t q_t
+ * with value head h reading query/key head h / (Hv / Hqk).
+ * Shared by the entry points kda_decay_attn_*:
+ *   q, k        BF16 [B, T, Hqk, 128], v BF16 [B, T, Hv, 128]. `strides` may give
+ *               their token and head strides in elements (q token, q head, k token,
+ *               k head, v token, v head; multiples of 8, batch rows T token strides
+ *               apart), so that they can be views of one fused projection; NULL
+ *               for contiguous tensors. 16-byte aligned.
+ *   log_decay   g <= 0 (meant; larger values let the state grow): FP32 [Hv], fixed
+ *               for each head (decay_per_token 0), or BF16 [B, T, Hv]
+ *               (decay_per_token 1). -inf resets the state.
+ *   cu_seqlens  packed layout as above (B = 1, device tensor and host mirror);
+ *               sequences may be empty here: their state passes through. The
+ *               kernels hold device offsets that disagree with the mirror inside
+ *               the tensors (the result is then unspecified).
+ *   scale       any finite number; NaN selects 1/sqrt(128). head_dim must be 128.
+ *   T may be 0 (token pointers are then not read).
+ *   device_status  optional device int32, bits only ever set: 1 a bounded device
+ *               wait gave up (outputs incomplete), 4 a device slot index outside the
+ *               pool. NULL uses a word inside the library.
+ * Outputs are caller-owned, overwritten, and must not overlap an input, each other
+ * or the workspace. Arithmetic: products of BF16 operands with FP32 accumulation;
+ * states, decays and sums are FP32, and states that reach an FP32 output keep its
+ * accuracy. Results do not depend on the order of execution.
+ * Errors: as above (KDA_ERR_INVALID_ARGUMENT, _UNSUPPORTED, _ALIASING,
+ * _WORKSPACE_TOO_SMALL, _CUDA), all before any launch; nothing is allocated; calls
+ * only launch kernels on `stream` and may be captured into a CUDA graph. */
+
+/* Bytes of device workspace (256-byte aligned) for this problem: `training` 1
+ * for kda_decay_attn_fwd and _bwd, 0 for kda_decay_attn_prefill (which may need
+ * none). The packed layout's mirror is read for the sequences' lengths. */
+kda_status kda_decay_attn_workspace_bytes(int64_t B, int64_t T, int64_t Hqk, int64_t Hv,
+                                          const int64_t* cu_seqlens_host, int64_t num_seqs,
+                                          int32_t training, size_t* bytes);
+
+/* Training forward: o BF16 [B, T, Hv, 128] and h_T FP32 [N, Hv, 128, 128] from
+ * h0 FP32 (NULL for zeros). Leaves in the workspace what kda_decay_attn_bwd reads:
+ * pass it there untouched, with the same inputs. */
+kda_status kda_decay_attn_fwd(const kda_bf16* q, const kda_bf16* k, const kda_bf16* v,
+                              const void* log_decay, int32_t decay_per_token, const float* h0,
+                              const int64_t* cu_seqlens_dev, const int64_t* cu_seqlens_host,
+                              int64_t num_seqs, int64_t B, int64_t T, int64_t Hqk, int64_t Hv,
+                              int64_t head_dim, float scale, const int64_t* strides, kda_bf16* o,
+                              float* h_T, void* workspace, size_t workspace_bytes,
+                              int32_t* device_status, struct CUstream_st* stream);
+
+/* Training backward of the kda_decay_attn_fwd call that filled the workspace.
+ * d_o BF16 [B, T, Hv, 128], d_hT FP32 [N, Hv, 128, 128] or NULL (zeros); dq, dk BF16
+ * [B, T, Hqk, 128] (sums over the value heads of the group, rounded once), dv BF16
+ * [B, T, Hv, 128], dlog_decay BF16 [B, T, Hv] (NULL with a fixed decay, which
+ * has no gradient here), dh0 FP32 or NULL. All gradients contiguous. */
+kda_status kda_decay_attn_bwd(const kda_bf16* q, const kda_bf16* k, const kda_bf16* v,
+                              const void* log_decay, int32_t decay_per_token, const float* h0,
+                              const int64_t* cu_seqlens_dev, const int64_t* cu_seqlens_host,
+                              int64_t num_seqs, int64_t B, int64_t T, int64_t Hqk, int64_t Hv,
+                              int64_t head_dim, float scale, const int64_t* strides,
+                              const kda_bf16* d_o, const float* d_hT, kda_bf16* dq, kda_bf16* dk,
+                              kda_bf16* dv, kda_bf16* dlog_decay, float* dh0, void* workspace,
+                              size_t workspace_bytes, int32_t* device_status,
+                              struct CUstream_st* stream);
+
+/* Inference prefill from a state pool, as kda_prefill: the final state of every
+ * sequence goes back to its slot. state, state_dtype, state_indices (device and
+ * host mirror) and num_slots as for kda_decode. */
+kda_status kda_decay_attn_prefill(const kda_bf16* q, const kda_bf16* k, const kda_bf16* v,
+                                  const void* log_decay, int32_t decay_per_token,
+                                  const int64_t* cu_seqlens_dev, const int64_t* cu_seqlens_host,
+                                  int64_t num_seqs, int64_t B, int64_t T, int64_t Hqk, int64_t Hv,
+                                  int64_t head_dim, float scale, const int64_t* strides, void* state,
+                                  int32_t state_dtype, const int32_t* state_indices,
+                                  const int32_t* state_indices_host, int64_t num_slots, kda_bf16* o,
+                                  void* workspace, size_t workspace_bytes, int32_t* device_status,
+                                  struct CUstream_st* stream);
+
+/* One decode step, T = 1, on the pool in place: q, k [N, 1, Hqk, 128],
+ * v, o [N, 1, Hv, 128], log_decay BF16 [N, 1, Hv] or FP32 [Hv]. Slots as for
+ * kda_decode: a device index outside the pool leaves it alone and sets that
+ * sequence's o to NaN. N may be 0. */
+kda_status kda_decay_attn_decode(const kda_bf16* q, const kda_bf16* k, const kda_bf16* v,
+                                 const void* log_decay, int32_t decay_per_token, void* state,
+                                 int32_t state_dtype, const int32_t* state_indices,
+                                 const int32_t* state_indices_host, int64_t num_slots, int64_t N,
+                                 int64_t Hqk, int64_t Hv, int64_t head_dim, float scale,
+                                 const int64_t* strides, kda_bf16* o, struct CUstream_st* stream);
+
+/* Element types of kda_qk_norm_rope_*. */
+enum { KDA_DTYPE_BF16 = 0, KDA_DTYPE_FP32 = 1, KDA_DTYPE_FP16 = 2 };
+
+/* RMS norm of every query and key head and the rotation by position, in one pass.
+ * For a head x[D] of the token at position p, weight w and pair d of the first
+ * rotary_dim dimensions ((d, d + rotary_dim / 2); interleaved: (2d, 2d + 1)):
+ *   n = x w / sqrt(mean(x^2) + eps),
+ *   y_a = n_a cos(p f_d) - n_b sin(p f_d),  y_b = n_b cos(p f_d) + n_a sin(p f_d)
+ *   q, q_out [num_tokens, Hq, head_dim], k, k_out [num_tokens, Hk, head_dim] of type
+ *               dtype; `strides`: token and head strides in elements of q, k,
+ *               q_out, k_out (8 numbers, each a multiple of 16 bytes), NULL for
+ *               contiguous tensors. An output may be its own input (same pointer and
+ *               strides); other overlaps are refused.
+ *   q_weight, k_weight  FP32 [head_dim], or NULL for 1
+ *   positions   int64 [num_tokens]; inv_freq FP64 [rotary_dim / 2], radians per
+ *               position (angles are reduced exactly, so far positions keep
+ *               their accuracy). Both unused when rotary_dim is 0 (norm alone).
+ *   head_dim: a multiple of 16 up to 256; rotary_dim: a multiple of 16 up to it.
+ * Arithmetic is FP32, rounded once to dtype. */
+kda_status kda_qk_norm_rope_fwd(const void* q, const void* k, int32_t dtype, const float* q_weight,
+                                const float* k_weight, const int64_t* positions,
+                                const double* inv_freq, int64_t num_tokens, int64_t Hq, int64_t Hk,
+                                int64_t head_dim, int64_t rotary_dim, float eps, int32_t interleaved,
+                                const int64_t* strides, void* q_out, void* k_out,
+                                struct CUstream_st* stream);
+
+/* Device bytes (16-byte aligned) that kda_qk_norm_rope_bwd needs for the weights' gradients. */
+kda_status kda_qk_norm_rope_workspace_bytes(int64_t head_dim, size_t* bytes);
+
+/* Its gradients: from the outputs' (dq, dk) and the forward's inputs to dq_out, dk_out
+ * (of dtype) and dq_weight, dk_weight (FP32 [head_dim], summed over tokens and heads in
+ * a fixed order; NULL exactly where the weight is). `strides`: token and head strides of q, k,
+ * dq_out, dk_out, dq, dk (12 numbers). dq_out may be q or dq, dk_out may be k or dk.
+ * workspace may be NULL when there is no weight. */
+kda_status kda_qk_norm_rope_bwd(const void* dq, const void* dk, const void* q, const void* k,
+                                int32_t dtype, const float* q_weight, const float* k_weight,
+                                const int64_t* positions, const double* inv_freq, int64_t num_tokens,
+                                int64_t Hq, int64_t Hk, int64_t head_dim, int64_t rotary_dim,
+                                float eps, int32_t interleaved, const int64_t* strides,
+                                void* dq_out, void* dk_out, float* dq_weight, float* dk_weight,
+                                void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
+
 /* Self-test of the device-side timeout path (no counterpart on the pages: the
  * kernels' own failure handling). Launches one CTA of 32 threads on `stream`
  * whose mbarrier wait can never complete, because nothing arrives on the

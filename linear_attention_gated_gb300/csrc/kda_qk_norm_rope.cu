@@ -1,0 +1,574 @@
+// kda_qk_norm_rope.cu -- RMS norm of every query and key head and the rotation
+// by position, in one pass, and their gradients.
+//
+// For a head row x[D] at position p, with weight w and pair (a, b) of the first
+// R dimensions ((d, d + R/2), or (2d, 2d + 1) when interleaved):
+//   r = 1 / sqrt(mean(x^2) + eps),   n = x r w,
+//   y_a = n_a cos(p f_d) - n_b sin(p f_d),   y_b = n_b cos(p f_d) + n_a sin(p f_d)
+// and the dimensions from R on pass through as n. Backward, dn = R(p)^T dy:
+//   dw = sum over rows of dn x r,   dx = r (dn w - x r mean(dn w x r)).
+//
+// Memory bound: 10 to 20 flops per value moved. A row belongs to a group of
+// G = 4, 8 or 16 lanes (the power of two at or above D / 16); each lane holds
+// the two 8-value vectors whose elements rotate into each other, so the rotation
+// needs no exchange and the norm log2(G) shuffles. A CTA takes a tile of whole
+// tokens of one tensor (queries or keys), keeps that tensor's weight in
+// registers and computes each token's cosines and sines once for all its heads.
+//
+// Angles: p f is reduced modulo one turn in 64-bit fixed point, f / 2 pi scaled
+// by 2^64 and multiplied by p with wrap-around, so a far position loses nothing
+// (error p 2^-53 f turns); sincospif then sees half-turns in [-1, 1).
+#include "../../include/kda.h"
+#include "kda_common.cuh"
+#include "kda_host.h"
+
+#include <cuda_fp16.h>
+
+#include <cmath>
+#include <cstdio>
+
+namespace kda {
+namespace {
+
+constexpr int kNrThreads = 256;
+constexpr int kNrTokens = 64;  // most tokens of one tile
+
+struct NrTensor {
+  const void* x;
+  const void* dy;   // backward
+  void* y;          // forward: y; backward: dx
+  const float* w;   // [D] or null
+  int64_t xt, xh, dt, dh, yt, yh;  // token and head strides of x, dy and y (elements)
+  int H;
+  int tokens;       // tokens of one tile
+  int64_t tiles;
+};
+
+struct NrArgs {
+  NrTensor t[2];         // queries, keys
+  const int64_t* pos;    // [n]
+  const double* freq;    // [R / 2]
+  float* dw_part;        // backward: [CTAs, D], the queries' CTAs first
+  int64_t n;
+  int D, R;
+  float eps;
+  int ctas0;             // CTAs of the queries
+};
+
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<__nv_bfloat16> {
+  uint4 r;
+  __device__ __forceinline__ void load(const void* p) { r = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float* x) const { unpack_bf16x8(r, x); }
+  static __device__ __forceinline__ void store(void* p, const float* x) {
+    store_bf16x8(reinterpret_cast<__nv_bfloat16*>(p), x);
+  }
+};
+template <>
+struct Vec8<__half> {
+  uint4 r;
+  __device__ __forceinline__ void load(const void* p) { r = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float* x) const {
+    const __half2* h = reinterpret_cast<const __half2*>(&r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(h[i]);
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+  static __device__ __forceinline__ void store(void* p, const float* x) {
+    uint4 v;
+    __half2* h = reinterpret_cast<__half2*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+    *reinterpret_cast<uint4*>(p) = v;
+  }
+};
+template <>
+struct Vec8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void get(float* x) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+  static __device__ __forceinline__ void store(void* p, const float* x) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+};
+
+template <int G>
+__device__ __forceinline__ float group_sum(float x) {
+#pragma unroll
+  for (int o = G / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// cos and sin of pos * f, f the fixed-point frequency (2^64 to the turn)
+__device__ __forceinline__ float2 cos_sin(int64_t pos, uint64_t f) {
+  const uint64_t a = (uint64_t)pos * f;
+  const float half_turns = (float)(int32_t)(a >> 32) * 4.656612873077393e-10f;  // 2^-31
+  float2 cs;
+  sincospif(half_turns, &cs.y, &cs.x);
+  return cs;
+}
+
+__device__ __forceinline__ uint64_t fixed_turns(double f) {
+  double t = f * 0.15915494309189533577;  // 1 / (2 pi)
+  t -= floor(t);
+  return t >= 1.0 ? 0ull : (uint64_t)(t * 18446744073709551616.0);
+}
+
+// Rotates the lane's 8 pairs by (cos, sin) (sgn = -1: back). Half pairs: (a[e], b[e]).
+// Interleaved: neighbours inside a (pairs 0..3) and b (pairs 4..7).
+template <bool kInter>
+__device__ __forceinline__ void rotate8(float* a, float* b, const float2* cs, float sgn) {
+  if constexpr (kInter) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float s0 = sgn * cs[e].y, s1 = sgn * cs[4 + e].y;
+      const float x0 = a[2 * e], y0 = a[2 * e + 1], x1 = b[2 * e], y1 = b[2 * e + 1];
+      a[2 * e] = x0 * cs[e].x - y0 * s0;
+      a[2 * e + 1] = y0 * cs[e].x + x0 * s0;
+      b[2 * e] = x1 * cs[4 + e].x - y1 * s1;
+      b[2 * e + 1] = y1 * cs[4 + e].x + x1 * s1;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float s = sgn * cs[e].y, x = a[e], y = b[e];
+      a[e] = x * cs[e].x - y * s;
+      b[e] = y * cs[e].x + x * s;
+    }
+  }
+}
+
+template <typename T, int G, bool kInter, bool kBwd>
+__global__ void __launch_bounds__(kNrThreads, kBwd ? 3 : 4) kda_qk_norm_rope_kernel(const NrArgs a) {
+  extern __shared__ __align__(16) unsigned char nr_smem[];
+  float2* cs = reinterpret_cast<float2*>(nr_smem);  // [tokens of the tile][R / 2]
+  constexpr int kGroups = kNrThreads / G;
+  const int which = (int)blockIdx.x >= a.ctas0;
+  const NrTensor& t = a.t[which];
+  const int64_t first = which ? (int64_t)blockIdx.x - a.ctas0 : blockIdx.x;
+  const int64_t step = which ? (int64_t)gridDim.x - a.ctas0 : a.ctas0;
+  const int tid = threadIdx.x, lane = tid % G, group = tid / G;
+  const int R = a.R, half = R / 2;
+  const bool active = lane < a.D / 16;
+  const bool turns = active && 16 * lane < R;
+  // the lane's two vectors: the halves of its pairs, or 16 neighbouring values
+  int c0 = 16 * lane, c1 = 16 * lane + 8;
+  if (!kInter && turns) {
+    c0 = 8 * lane;
+    c1 = 8 * lane + half;
+  }
+  float w0[8], w1[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w0[e] = w1[e] = 1.f;
+  if (active && t.w) {
+    Vec8<float> v;
+    v.load(t.w + c0); v.get(w0);
+    v.load(t.w + c1); v.get(w1);
+  }
+  float g0[8], g1[8];  // backward: this lane's share of dw
+#pragma unroll
+  for (int e = 0; e < 8; ++e) g0[e] = g1[e] = 0.f;
+  const float inv_d = 1.f / (float)a.D;
+  const T* x = reinterpret_cast<const T*>(t.x);
+  const T* dy = reinterpret_cast<const T*>(t.dy);
+  T* y = reinterpret_cast<T*>(t.y);
+
+  for (int64_t tile = first; tile < t.tiles; tile += step) {
+    const int64_t tok0 = tile * t.tokens;
+    const int ntok = (int)(a.n - tok0 < t.tokens ? a.n - tok0 : t.tokens);
+    if (R) {
+      __syncthreads();  // the last tile's rows are done with cs
+      for (int i = tid; i < ntok * half; i += kNrThreads) {
+        const int tt = i / half, d = i - tt * half;
+        cs[i] = cos_sin(a.pos[tok0 + tt], fixed_turns(a.freq[d]));
+      }
+      __syncthreads();
+    }
+    const int rows = ntok * t.H;
+    // all lanes of a warp make the same number of rounds: the shuffles are warp wide
+    for (int row0 = 0; row0 < rows; row0 += kGroups) {
+      const int row = row0 + group;
+      const bool live = active && row < rows;
+      int tt = 0, h = row;
+      if (t.tokens > 1) {
+        tt = row / t.H;
+        h = row - tt * t.H;
+      }
+      const int64_t tok = tok0 + tt;
+      float p[8], q[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = q[e] = 0.f;
+      Vec8<T> va, vb, da, db;
+      if (live) {
+        const T* src = x + tok * t.xt + h * t.xh;
+        va.load(src + c0);
+        vb.load(src + c1);
+        if constexpr (kBwd) {
+          const T* sd = dy + tok * t.dt + h * t.dh;
+          da.load(sd + c0);
+          db.load(sd + c1);
+        }
+        va.get(p);
+        vb.get(q);
+      }
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss += p[e] * p[e] + q[e] * q[e];
+      const float r = rsqrtf(group_sum<G>(ss) * inv_d + a.eps);
+      float2 c[8];
+      if (turns) {
+        const float4* src = reinterpret_cast<const float4*>(cs + (live ? tt : 0) * half + 8 * lane);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 v = src[e];
+          c[2 * e] = make_float2(v.x, v.y);
+          c[2 * e + 1] = make_float2(v.z, v.w);
+        }
+      }
+      if constexpr (!kBwd) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          p[e] = p[e] * r * w0[e];
+          q[e] = q[e] * r * w1[e];
+        }
+        if (turns) rotate8<kInter>(p, q, c, 1.f);
+      } else {
+        float u[8], v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = v[e] = 0.f;
+        if (live) {
+          da.get(u);
+          db.get(v);
+        }
+        if (turns) rotate8<kInter>(u, v, c, -1.f);
+        float dot = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          p[e] *= r;
+          q[e] *= r;
+          g0[e] = fmaf(u[e], p[e], g0[e]);
+          g1[e] = fmaf(v[e], q[e], g1[e]);
+          u[e] *= w0[e];
+          v[e] *= w1[e];
+          dot += u[e] * p[e] + v[e] * q[e];
+        }
+        dot = group_sum<G>(dot) * inv_d;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          p[e] = r * (u[e] - p[e] * dot);
+          q[e] = r * (v[e] - q[e] * dot);
+        }
+      }
+      if (live) {
+        T* dst = y + tok * t.yt + h * t.yh;
+        Vec8<T>::store(dst + c0, p);
+        Vec8<T>::store(dst + c1, q);
+      }
+    }
+  }
+  if (kBwd && a.dw_part) {  // (no weights, no workspace: nothing to sum)
+    // the CTA's share of dw: the groups' sums in a fixed order
+    float* acc = reinterpret_cast<float*>(nr_smem);  // [groups of a warp summed: warps][16 G]
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+#pragma unroll
+      for (int o = G; o < 32; o <<= 1) {
+        g0[e] += __shfl_xor_sync(0xffffffffu, g0[e], o);
+        g1[e] += __shfl_xor_sync(0xffffffffu, g1[e], o);
+      }
+    }
+    const int warp = tid >> 5;
+    if ((tid & 31) < G && active) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        acc[warp * a.D + c0 + e] = g0[e];
+        acc[warp * a.D + c1 + e] = g1[e];
+      }
+    }
+    __syncthreads();
+    for (int d = tid; d < a.D; d += kNrThreads) {
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < kNrThreads / 32; ++k) s += acc[k * a.D + d];
+      a.dw_part[(int64_t)blockIdx.x * a.D + d] = s;
+    }
+  }
+}
+
+// dw of queries (block y 0) and keys (1): 32 columns a CTA, eight partial sums each.
+__global__ void __launch_bounds__(256) kda_norm_weight_grad_kernel(const float* part, int ctas0, int ctas, int D,
+                                                                   float* dqw, float* dkw) {
+  __shared__ float s[8][32];
+  const int col = threadIdx.x & 31, lane = threadIdx.x >> 5, d = blockIdx.x * 32 + col;
+  const int lo = blockIdx.y ? ctas0 : 0, hi = blockIdx.y ? ctas : ctas0;
+  float* out = blockIdx.y ? dkw : dqw;
+  float x = 0.f;
+  if (d < D && out)
+    for (int i = lo + lane; i < hi; i += 8) x += part[(int64_t)i * D + d];
+  s[lane][col] = x;
+  __syncthreads();
+  if (lane == 0 && d < D && out) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) x += s[k][col];
+    out[d] = x;
+  }
+}
+
+kda_status nfail(kda_status st, const char* msg) {
+  set_last_error(msg);
+  return st;
+}
+
+constexpr int64_t kNrMaxCtas = 152 * 4;  // CTAs of one tensor in the backward: rows of dw_part
+
+// A strided [tokens, heads, D] view in bytes.
+struct View {
+  uintptr_t p;
+  int64_t token, extent;  // token stride; bytes from the first to past the last value of one token
+  int64_t n;
+};
+
+View view_of(const void* p, int64_t ts, int64_t hs, int64_t H, int64_t D, int64_t n, int64_t size) {
+  return View{(uintptr_t)p, ts * size, ((H - 1) * hs + D) * size, n};
+}
+
+// False only where no value of one view is a value of the other: apart in memory, or rows of
+// the same stride whose ranges within it are apart (queries and keys of one projection).
+bool may_overlap(const View& a, const View& b) {
+  if (!a.n || !b.n) return false;
+  const uintptr_t a1 = a.p + (a.n - 1) * a.token + a.extent, b1 = b.p + (b.n - 1) * b.token + b.extent;
+  if (a1 <= b.p || b1 <= a.p) return false;
+  if (a.token != b.token || a.token <= 0) return true;
+  const int64_t s = a.token;
+  int64_t d = ((int64_t)(b.p - a.p)) % s;
+  if (d < 0) d += s;
+  return !(d >= a.extent && d + b.extent <= s);
+}
+
+// The two tensors of one call, checked: strides[4 i ..] = token and head strides of input i, etc.
+struct NrCall {
+  const void *q, *k, *dq, *dk;
+  void *q_out, *k_out;
+  int32_t dtype;
+  const float *qw, *kw;
+  float *dqw, *dkw;
+  const int64_t* pos;
+  const double* freq;
+  int64_t n, Hq, Hk, D, R;
+  float eps;
+  int32_t inter;
+  const int64_t* strides;
+  float* part;
+  bool bwd;
+  cudaStream_t stream;
+};
+
+template <typename T, int G, bool kInter, bool kBwd>
+cudaError_t nr_launch(const NrArgs& a, int64_t ctas, size_t smem, cudaStream_t s) {
+  auto kern = kda_qk_norm_rope_kernel<T, G, kInter, kBwd>;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<(unsigned)ctas, kNrThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int G>
+cudaError_t nr_by_mode(const NrArgs& a, int64_t ctas, size_t smem, bool inter, bool bwd, cudaStream_t s) {
+  if (inter) return bwd ? nr_launch<T, G, true, true>(a, ctas, smem, s) : nr_launch<T, G, true, false>(a, ctas, smem, s);
+  return bwd ? nr_launch<T, G, false, true>(a, ctas, smem, s) : nr_launch<T, G, false, false>(a, ctas, smem, s);
+}
+
+template <typename T>
+cudaError_t nr_by_group(const NrArgs& a, int64_t ctas, size_t smem, bool inter, bool bwd, cudaStream_t s) {
+  if (a.D <= 64) return nr_by_mode<T, 4>(a, ctas, smem, inter, bwd, s);
+  if (a.D <= 128) return nr_by_mode<T, 8>(a, ctas, smem, inter, bwd, s);
+  return nr_by_mode<T, 16>(a, ctas, smem, inter, bwd, s);
+}
+
+kda_status nr_run(const NrCall& c) {
+  if (c.dtype != KDA_DTYPE_BF16 && c.dtype != KDA_DTYPE_FP32 && c.dtype != KDA_DTYPE_FP16)
+    return nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: dtype must be KDA_DTYPE_BF16, KDA_DTYPE_FP32 or KDA_DTYPE_FP16");
+  if (c.n < 0 || c.Hq < 1 || c.Hk < 1)
+    return nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: num_tokens must be >= 0, Hq and Hk >= 1");
+  if (size_limit_violation(1, c.n ? c.n : 1, c.Hq, 0) || size_limit_violation(1, c.n ? c.n : 1, c.Hk, 0))
+    return nfail(KDA_ERR_UNSUPPORTED, "qk_norm_rope: problem too large");
+  if (c.Hq > 65536 || c.Hk > 65536) return nfail(KDA_ERR_UNSUPPORTED, "qk_norm_rope: more than 65536 heads");
+  if (c.D < 16 || c.D > 256 || c.D % 16)
+    return nfail(KDA_ERR_UNSUPPORTED, "qk_norm_rope: head_dim must be a multiple of 16 from 16 to 256");
+  if (c.R < 0 || c.R > c.D || c.R % 16)
+    return nfail(KDA_ERR_UNSUPPORTED, "qk_norm_rope: rotary_dim must be a multiple of 16 from 0 to head_dim");
+  if (!(c.eps >= 0.f) || std::isinf(c.eps)) return nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: eps must be finite and >= 0");
+  if (c.inter != 0 && c.inter != 1) return nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: interleaved must be 0 or 1");
+  if (c.bwd && (c.dqw == nullptr) != (c.qw == nullptr))
+    return nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: dq_weight goes with q_weight");
+  if (c.bwd && (c.dkw == nullptr) != (c.kw == nullptr))
+    return nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: dk_weight goes with k_weight");
+  const int64_t size = c.dtype == KDA_DTYPE_FP32 ? 4 : 2;
+  // (token stride, head stride) of q, k, q_out, k_out and, backward, dq, dk
+  int64_t st[12];
+  const int nst = c.bwd ? 12 : 8;
+  const int64_t heads[6] = {c.Hq, c.Hk, c.Hq, c.Hk, c.Hq, c.Hk};
+  for (int i = 0; i < nst; ++i)
+    st[i] = c.strides ? c.strides[i] : (i & 1 ? c.D : heads[i / 2] * c.D);
+  for (int i = 0; i < nst; i += 2) {
+    if (st[i + 1] < c.D || st[i] < (heads[i / 2] - 1) * st[i + 1] + c.D)
+      return nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: heads or tokens of a tensor overlap (strides too small)");
+    if ((st[i] * size) % 16 || (st[i + 1] * size) % 16)
+      return nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: token and head strides must be multiples of 16 bytes");
+    if (st[i] > (int64_t(1) << 40)) return nfail(KDA_ERR_UNSUPPORTED, "qk_norm_rope: token stride too large");
+  }
+  if (c.n) {
+    const void* ptrs[] = {c.q, c.k, c.q_out, c.k_out, c.bwd ? c.dq : c.q, c.bwd ? c.dk : c.k};
+    for (const void* p : ptrs) {
+      if (!p) return nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: null tensor pointer");
+      if ((uintptr_t)p & 15u) return nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: tensors must be 16-byte aligned");
+    }
+    if (c.R && (!c.pos || !c.freq))
+      return nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: a rotation needs positions and inv_freq");
+    if (((uintptr_t)c.qw | (uintptr_t)c.kw) & 15u)
+      return nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: weights must be 16-byte aligned");
+  }
+  if (c.bwd && (c.dqw || c.dkw) && !c.part)
+    return nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: the weights' gradients need the workspace");
+  // an output may be the input of the same tensor (each row is read before it is written), else
+  // nothing that is read or written may be written by another
+  const View in[4] = {view_of(c.q, st[0], st[1], c.Hq, c.D, c.n, size), view_of(c.k, st[2], st[3], c.Hk, c.D, c.n, size),
+                      c.bwd ? view_of(c.dq, st[8], st[9], c.Hq, c.D, c.n, size) : View{0, 0, 0, 0},
+                      c.bwd ? view_of(c.dk, st[10], st[11], c.Hk, c.D, c.n, size) : View{0, 0, 0, 0}};
+  const int64_t in_hs[4] = {st[1], st[3], c.bwd ? st[9] : 0, c.bwd ? st[11] : 0};
+  const View out[2] = {view_of(c.q_out, st[4], st[5], c.Hq, c.D, c.n, size), view_of(c.k_out, st[6], st[7], c.Hk, c.D, c.n, size)};
+  const int64_t out_hs[2] = {st[5], st[7]};
+  for (int i = 0; i < 2; ++i) {
+    for (int j = 0; j < 4; ++j) {
+      const bool same = (j & 1) == i && in[j].p == out[i].p && in[j].token == out[i].token && in_hs[j] == out_hs[i];
+      if (!same && may_overlap(in[j], out[i]))
+        return nfail(KDA_ERR_ALIASING, "qk_norm_rope: an output overlaps an input that is not its own");
+    }
+    const View flat[] = {View{(uintptr_t)c.qw, 0, 4 * c.D, c.qw ? 1 : 0}, View{(uintptr_t)c.kw, 0, 4 * c.D, c.kw ? 1 : 0},
+                         View{(uintptr_t)c.pos, 0, 8 * c.n, c.R ? 1 : 0}, View{(uintptr_t)c.freq, 0, 4 * c.R, c.R ? 1 : 0}};
+    for (const View& f : flat)
+      if (may_overlap(f, out[i])) return nfail(KDA_ERR_ALIASING, "qk_norm_rope: an output overlaps an input");
+  }
+  if (may_overlap(out[0], out[1])) return nfail(KDA_ERR_ALIASING, "qk_norm_rope: the outputs overlap");
+
+  int dev = -1, major = 0, minor = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  if (e != cudaSuccess) return nfail(KDA_ERR_CUDA, cudaGetErrorString(e));
+  if (major != 10 || minor != 3) return nfail(KDA_ERR_UNSUPPORTED, "qk_norm_rope: kernels are built for sm_103a");
+
+  NrArgs a{};
+  a.pos = c.pos;
+  a.freq = c.freq;
+  a.dw_part = c.part;
+  a.n = c.n;
+  a.D = (int)c.D;
+  a.R = (int)c.R;
+  a.eps = c.eps;
+  int64_t ctas[2];
+  int most = 1;
+  for (int i = 0; i < 2; ++i) {
+    NrTensor& t = a.t[i];
+    t.x = i ? c.k : c.q;
+    t.dy = i ? c.dk : c.dq;
+    t.y = i ? c.k_out : c.q_out;
+    t.w = i ? c.kw : c.qw;
+    t.xt = st[2 * i]; t.xh = st[2 * i + 1];
+    t.yt = st[4 + 2 * i]; t.yh = st[5 + 2 * i];
+    t.dt = c.bwd ? st[8 + 2 * i] : 0; t.dh = c.bwd ? st[9 + 2 * i] : 0;
+    t.H = (int)heads[i];
+    // whole tokens, at least 64 rows a tile where there are as many
+    int64_t tt = (63 + t.H) / t.H;
+    if (tt > kNrTokens) tt = kNrTokens;
+    t.tokens = (int)tt;
+    t.tiles = (c.n + tt - 1) / tt;
+    ctas[i] = c.bwd && t.tiles > kNrMaxCtas ? kNrMaxCtas : t.tiles;
+    if (ctas[i] > INT32_MAX / 4) return nfail(KDA_ERR_UNSUPPORTED, "qk_norm_rope: too many tokens");
+    if (t.tokens > most) most = t.tokens;
+  }
+  a.ctas0 = (int)ctas[0];
+  size_t smem = (size_t)most * (c.R / 2) * sizeof(float2);
+  if (c.bwd && smem < sizeof(float) * 8 * c.D) smem = sizeof(float) * 8 * c.D;
+  const int64_t grid = ctas[0] + ctas[1];
+  if (grid > 0) {
+    if (c.dtype == KDA_DTYPE_BF16) e = nr_by_group<__nv_bfloat16>(a, grid, smem, c.inter, c.bwd, c.stream);
+    else if (c.dtype == KDA_DTYPE_FP16) e = nr_by_group<__half>(a, grid, smem, c.inter, c.bwd, c.stream);
+    else e = nr_by_group<float>(a, grid, smem, c.inter, c.bwd, c.stream);
+    if (e != cudaSuccess) return nfail(KDA_ERR_CUDA, cudaGetErrorString(e));
+  }
+  if (c.bwd && (c.dqw || c.dkw)) {
+    kda_norm_weight_grad_kernel<<<dim3((unsigned)((c.D + 31) / 32), 2), 256, 0, c.stream>>>(
+        c.part, (int)ctas[0], (int)grid, (int)c.D, c.dqw, c.dkw);
+    if ((e = cudaGetLastError()) != cudaSuccess) return nfail(KDA_ERR_CUDA, cudaGetErrorString(e));
+  }
+  return KDA_OK;
+}
+
+}  // namespace
+}  // namespace kda
+
+extern "C" kda_status kda_qk_norm_rope_fwd(const void* q, const void* k, int32_t dtype, const float* q_weight,
+                                           const float* k_weight, const int64_t* positions, const double* inv_freq,
+                                           int64_t num_tokens, int64_t Hq, int64_t Hk, int64_t head_dim,
+                                           int64_t rotary_dim, float eps, int32_t interleaved, const int64_t* strides,
+                                           void* q_out, void* k_out, struct CUstream_st* stream) {
+  return kda::guarded([&]() -> kda_status {
+    kda::NrCall c{};
+    c.q = q; c.k = k; c.q_out = q_out; c.k_out = k_out;
+    c.dtype = dtype;
+    c.qw = q_weight; c.kw = k_weight;
+    c.pos = positions; c.freq = inv_freq;
+    c.n = num_tokens; c.Hq = Hq; c.Hk = Hk; c.D = head_dim; c.R = rotary_dim;
+    c.eps = eps; c.inter = interleaved; c.strides = strides;
+    c.stream = stream;
+    return kda::nr_run(c);
+  });
+}
+
+extern "C" kda_status kda_qk_norm_rope_workspace_bytes(int64_t head_dim, size_t* bytes) {
+  if (!bytes || head_dim < 16 || head_dim > 256 || head_dim % 16)
+    return kda::nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: bytes is NULL or head_dim unsupported");
+  *bytes = 2 * kda::kNrMaxCtas * (size_t)head_dim * sizeof(float);
+  return KDA_OK;
+}
+
+extern "C" kda_status kda_qk_norm_rope_bwd(const void* dq, const void* dk, const void* q, const void* k, int32_t dtype,
+                                           const float* q_weight, const float* k_weight, const int64_t* positions,
+                                           const double* inv_freq, int64_t num_tokens, int64_t Hq, int64_t Hk,
+                                           int64_t head_dim, int64_t rotary_dim, float eps, int32_t interleaved,
+                                           const int64_t* strides, void* dq_out, void* dk_out, float* dq_weight,
+                                           float* dk_weight, void* workspace, size_t workspace_bytes,
+                                           struct CUstream_st* stream) {
+  return kda::guarded([&]() -> kda_status {
+    kda::NrCall c{};
+    c.q = q; c.k = k; c.dq = dq; c.dk = dk; c.q_out = dq_out; c.k_out = dk_out;
+    c.dtype = dtype;
+    c.qw = q_weight; c.kw = k_weight; c.dqw = dq_weight; c.dkw = dk_weight;
+    c.pos = positions; c.freq = inv_freq;
+    c.n = num_tokens; c.Hq = Hq; c.Hk = Hk; c.D = head_dim; c.R = rotary_dim;
+    c.eps = eps; c.inter = interleaved; c.strides = strides;
+    c.part = reinterpret_cast<float*>(workspace);
+    c.bwd = true;
+    c.stream = stream;
+    if (workspace && workspace_bytes < 2 * kda::kNrMaxCtas * (size_t)(head_dim > 0 ? head_dim : 0) * sizeof(float))
+      return kda::nfail(KDA_ERR_WORKSPACE_TOO_SMALL, "qk_norm_rope: workspace below kda_qk_norm_rope_workspace_bytes()");
+    if ((uintptr_t)workspace & 15u) return kda::nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: workspace must be 16-byte aligned");
+    return kda::nr_run(c);
+  });
+}

@@ -1,0 +1,405 @@
+"""Linear attention with a decay for each head, and the norm and position rotation of its queries
+and keys (Python binding of the ``kda_decay_attn_*`` and ``kda_qk_norm_rope_*`` entry points of
+include/kda.h).
+
+Argument marshalling only: torch provides device memory and the current CUDA stream; all arithmetic
+runs in libkda.so's kernels, and there is no CPU fallback. Every call enqueues on the current stream
+of its tensors' device.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from .kda import KdaError, _check, load_library
+
+DIM = 128
+_NAN = float("nan")
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_STATE = {torch.bfloat16: 0, torch.float32: 1}
+_ROPE_TYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
+
+
+class _on:
+    """The device of the call's tensors made current, where it is not already, and its stream."""
+
+    __slots__ = ("device", "index", "before")
+
+    def __init__(self, device):
+        if device.type != "cuda":
+            raise ValueError("tensors must be CUDA tensors")
+        self.index = device.index
+        self.before = None
+
+    def __enter__(self):
+        now = torch.cuda.current_device()
+        if now != self.index:
+            self.before = now
+            torch.cuda.set_device(self.index)
+        return torch.cuda.current_stream(self.index).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.before is not None:
+            torch.cuda.set_device(self.before)
+
+
+def _typed(t, name, dtype, shape, device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+
+
+def _want(t, name, dtype, shape, device):
+    _typed(t, name, dtype, shape, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _strides(t, name):
+    """Token and head strides of a [B, T, H, D] tensor whose heads are contiguous rows."""
+    B, T, H, D = t.shape
+    sb, st, sh, sd = t.stride()
+    if D > 1 and sd != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    if H == 1:
+        sh = D
+    if T == 1:
+        st = sb if B > 1 else H * sh
+    elif B > 1 and sb != T * st:
+        raise ValueError(f"{name}: batch rows must be T token strides apart")
+    return st, sh
+
+
+def _all_strides(named):
+    """None when every tensor is contiguous, else the token and head strides of all as a C array."""
+    for _, t in named:
+        if not t.is_contiguous():
+            break
+    else:
+        return None
+    flat = [s for name, t in named for s in (_strides(t, name) if t.numel() else (t.shape[2] * t.shape[3], t.shape[3]))]
+    return (ctypes.c_int64 * len(flat))(*flat)
+
+
+def _decay_inputs(q, k, v, log_decay):
+    """Checks of the token tensors; (B, T, Hqk, Hv, per_token, strides)."""
+    for name, t in (("q", q), ("v", v)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{name} must be a [B, T, H, 128] tensor")
+    B, T, Hqk, D = q.shape
+    Hv = v.shape[2]
+    dev = q.device
+    _typed(q, "q", _BF16, q.shape, dev)
+    _typed(k, "k", _BF16, q.shape, dev)
+    _typed(v, "v", _BF16, (B, T, Hv, D), dev)
+    per_token = not (isinstance(log_decay, torch.Tensor) and log_decay.dim() == 1)
+    if per_token:
+        _want(log_decay, "log_decay", _BF16, (B, T, Hv), dev)
+    else:
+        _want(log_decay, "log_decay", _F32, (Hv,), dev)
+    return B, T, Hqk, Hv, D, int(per_token), _all_strides((("q", q), ("k", k), ("v", v)))
+
+
+def _offsets(cu_seqlens, cu_seqlens_cpu, dev, need_mirror):
+    if cu_seqlens is None:
+        if cu_seqlens_cpu is not None:
+            raise ValueError("cu_seqlens_cpu given without cu_seqlens")
+        return None
+    if cu_seqlens_cpu is None:
+        if need_mirror:
+            raise ValueError("packed input requires cu_seqlens_cpu, a trusted CPU mirror of cu_seqlens")
+        cu_seqlens_cpu = cu_seqlens.cpu()
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be a 1-D tensor of N + 1 offsets")
+    _want(cu_seqlens, "cu_seqlens", _I64, cu_seqlens.shape, dev)
+    _want(cu_seqlens_cpu, "cu_seqlens_cpu", _I64, cu_seqlens.shape, torch.device("cpu"))
+    return cu_seqlens_cpu
+
+
+def _slots(state_indices, state_indices_cpu, N, dev):
+    if state_indices is None:
+        if state_indices_cpu is not None:
+            raise ValueError("state_indices_cpu given without state_indices")
+        return None
+    _want(state_indices, "state_indices", _I32, (N,), dev)
+    if state_indices_cpu is None:
+        return state_indices.cpu()
+    _want(state_indices_cpu, "state_indices_cpu", _I32, (N,), torch.device("cpu"))
+    return state_indices_cpu
+
+
+def _pool(state, Hv, D, dev):
+    if not isinstance(state, torch.Tensor) or state.dtype not in _STATE:
+        raise TypeError("state must be a bfloat16 or float32 tensor")
+    if state.dim() != 4 or state.shape[1:] != (Hv, D, D) or not state.is_contiguous():
+        raise ValueError(f"state must be contiguous [num_slots, {Hv}, {D}, {D}]")
+    if state.device != dev:
+        raise ValueError(f"state must be on {dev}")
+    return _STATE[state.dtype]
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def decay_workspace_bytes(B, T, Hqk, Hv, cu_seqlens_cpu=None, training=True) -> int:
+    """Device bytes that kda_decay_attn_fwd and _bwd (or, training False, kda_decay_attn_prefill)
+    need for this problem."""
+    lib = load_library()
+    out = ctypes.c_size_t(0)
+    n = 0 if cu_seqlens_cpu is None else cu_seqlens_cpu.numel() - 1
+    _check(lib.kda_decay_attn_workspace_bytes(B, T, Hqk, Hv, _p(cu_seqlens_cpu), n, int(training), ctypes.byref(out)))
+    return out.value
+
+
+class DecayContext:
+    """What the backward of one forward call needs: the borrowed inputs with their tensor versions
+    (they must not change before the backward) and the workspace the forward filled. Passing it back
+    as ``context_out`` reuses the workspace for another call of the same shapes."""
+
+    def __init__(self, key, nbytes, device):
+        self.key = key
+        self.device = device
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.device_status = torch.zeros(1, dtype=_I32, device=device)
+        self.inputs = ()
+        self.versions = ()
+
+    def _snapshot(self, inputs, call, cu, shapes):
+        self.inputs = inputs
+        self.versions = tuple(t._version for t in inputs if t is not None)
+        self.call, self.cu, self.shapes = call, cu, shapes
+
+    def check_unchanged(self):
+        if not self.inputs:
+            raise KdaError(4, "the context holds no forward")
+        if self.versions != tuple(t._version for t in self.inputs if t is not None):
+            raise KdaError(4, "an input of the forward was modified before the backward")
+
+    def status(self):
+        """Waits for the device and raises if a bounded device wait of these calls gave up."""
+        if int(self.device_status.item()) & 1:
+            raise KdaError(6, "a device-side wait gave up; the outputs are incomplete")
+
+
+def kda_decay_attn_fwd(q, k, v, log_decay, initial_state=None, cu_seqlens=None, scale=None, out=None,
+                       final_state_out=None, context_out=None, *, cu_seqlens_cpu=None):
+    """Training forward of linear attention with a decay for each head:
+    S_t = exp(g_t) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t, per sequence and value head (head h reads
+    query/key head h // (Hv / Hqk)). Returns (o, final_state, ctx).
+
+    q, k [B, T, Hqk, 128] and v [B, T, Hv, 128] BF16, contiguous or views with whole heads contiguous
+    (slices of one projection); log_decay FP32 [Hv], fixed for each head, or BF16 [B, T, Hv];
+    initial_state FP32 [N, Hv, 128, 128] value-first, None for zeros. Packed sequences (B = 1) have
+    cu_seqlens int64 [N + 1] on the device and its CPU mirror; sequences may be empty. scale defaults to
+    1 / sqrt(128). ctx goes to kda_decay_attn_bwd; as ``context_out`` of a later call of the same shapes
+    its workspace is used again."""
+    lib = load_library()
+    B, T, Hqk, Hv, D, per_token, strides = _decay_inputs(q, k, v, log_decay)
+    dev = q.device
+    cu_host = _offsets(cu_seqlens, cu_seqlens_cpu, dev, True)
+    N = B if cu_host is None else cu_host.numel() - 1
+    if initial_state is not None:
+        _want(initial_state, "initial_state", _F32, (N, Hv, D, D), dev)
+    ctx = context_out
+    key = (B, T, Hqk, Hv, N)
+    if ctx is None:
+        ctx = DecayContext(key, decay_workspace_bytes(B, T, Hqk, Hv, cu_host), dev)
+    elif ctx.key != key or ctx.device != dev:
+        raise KdaError(4, "context reuse needs the same shapes and device")
+    o = torch.empty((B, T, Hv, D), dtype=_BF16, device=dev) if out is None else out
+    hT = torch.empty((N, Hv, D, D), dtype=_F32, device=dev) if final_state_out is None else final_state_out
+    if out is not None:
+        _want(out, "out", _BF16, (B, T, Hv, D), dev)
+    if final_state_out is not None:
+        _want(final_state_out, "final_state_out", _F32, (N, Hv, D, D), dev)
+    s = _NAN if scale is None else float(scale)
+    call = (q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), per_token, _p(initial_state), _p(cu_seqlens),
+            _p(cu_host), N, B, T, Hqk, Hv, D, s, strides)
+    ws = ctx.workspace
+    with _on(dev) as stream:
+        _check(lib.kda_decay_attn_fwd(*call, o.data_ptr(), hT.data_ptr(), ws.data_ptr(), ws.numel(),
+                                      ctx.device_status.data_ptr(), stream))
+    ctx._snapshot((q, k, v, log_decay, initial_state, cu_seqlens), call, cu_host,
+                  (q.shape, v.shape, (N, Hv, D, D), per_token))
+    return o, hT, ctx
+
+
+def kda_decay_attn_bwd(ctx: DecayContext, do, dfinal_state=None, out=None):
+    """Training backward from the context of kda_decay_attn_fwd. Returns
+    (dq, dk, dv, dlog_decay, dinitial_state): BF16 but for dinitial_state FP32; dlog_decay is None
+    for decays fixed for each head and dinitial_state None where there was no initial state.
+    ``out``: five tensors (or None in those two places) in that order."""
+    lib = load_library()
+    if not isinstance(ctx, DecayContext):
+        raise KdaError(4, "not a forward context")
+    ctx.check_unchanged()
+    qs, vs, ss, per_token = ctx.shapes
+    dev = ctx.device
+    _want(do, "do", _BF16, vs, dev)
+    if dfinal_state is not None:
+        _want(dfinal_state, "dfinal_state", _F32, ss, dev)
+    shapes = (qs, qs, vs, vs[:3] if per_token else None, ss if ctx.inputs[4] is not None else None)
+    if out is None:
+        out = tuple(None if s is None else torch.empty(s, dtype=_F32 if i == 4 else _BF16, device=dev)
+                    for i, s in enumerate(shapes))
+    else:
+        if len(out) != 5:
+            raise ValueError("out must hold five gradient tensors in return order")
+        for i, (t, s) in enumerate(zip(out, shapes)):
+            if s is None:
+                if t is not None:
+                    raise ValueError("out holds a tensor for a gradient that this call does not have")
+            else:
+                _want(t, ("dq", "dk", "dv", "dlog_decay", "dinitial_state")[i], _F32 if i == 4 else _BF16, s, dev)
+    ws = ctx.workspace
+    with _on(dev) as stream:
+        _check(lib.kda_decay_attn_bwd(*ctx.call, do.data_ptr(), _p(dfinal_state), *[_p(t) for t in out], ws.data_ptr(),
+                                      ws.numel(), ctx.device_status.data_ptr(), stream))
+    return tuple(out)
+
+
+def kda_decay_attn_prefill(q, k, v, log_decay, state, cu_seqlens=None, state_indices=None, scale=None, out=None,
+                           device_status=None, workspace=None, *, cu_seqlens_cpu=None, state_indices_cpu=None):
+    """Inference prefill of linear attention with a decay for each head, from a state pool: returns o;
+    every sequence starts from its slot of ``state`` (BF16 or FP32 [num_slots, Hv, 128, 128], slot n
+    without state_indices) and leaves its final state there. Token tensors as for kda_decay_attn_fwd.
+    The ``*_cpu`` keywords pass trusted CPU mirrors of the device index tensors; without them the mirrors
+    are copied from the device, which waits for it. ``workspace``: a uint8 tensor of
+    decay_workspace_bytes(..., training=False); None takes one for the call."""
+    lib = load_library()
+    B, T, Hqk, Hv, D, per_token, strides = _decay_inputs(q, k, v, log_decay)
+    dev = q.device
+    cu_host = _offsets(cu_seqlens, cu_seqlens_cpu, dev, False)
+    N = B if cu_host is None else cu_host.numel() - 1
+    idx_host = _slots(state_indices, state_indices_cpu, N, dev)
+    sdt = _pool(state, Hv, D, dev)
+    if out is None:
+        out = torch.empty((B, T, Hv, D), dtype=_BF16, device=dev)
+    else:
+        _want(out, "out", _BF16, (B, T, Hv, D), dev)
+    if device_status is not None:
+        _want(device_status, "device_status", _I32, device_status.shape, dev)
+    if workspace is None:
+        nbytes = decay_workspace_bytes(B, T, Hqk, Hv, cu_host, False)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    else:
+        _want(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    with _on(dev) as stream:
+        _check(lib.kda_decay_attn_prefill(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), per_token, _p(cu_seqlens), _p(cu_host), N, B, T,
+            Hqk, Hv, D, _NAN if scale is None else float(scale), strides, state.data_ptr(), sdt, _p(state_indices),
+            _p(idx_host), state.shape[0], out.data_ptr(), _p(workspace), 0 if workspace is None else workspace.numel(),
+            _p(device_status), stream))
+    return out
+
+
+def kda_decay_attn_decode(q, k, v, log_decay, state, state_indices=None, scale=None, out=None, *, state_indices_cpu=None):
+    """One decode step (T = 1) of linear attention with a decay for each head: updates ``state`` (BF16 or
+    FP32 [num_slots, Hv, 128, 128]) in place at slot state_indices[n] (int32 [N], slot n when None) and
+    returns o. q, k [N, 1, Hqk, 128], v [N, 1, Hv, 128] BF16; log_decay BF16 [N, 1, Hv] or FP32 [Hv].
+    ``state_indices_cpu``, a trusted CPU copy of state_indices, is what the library validates; without it
+    the indices are copied to the host, which waits for the device. One launch."""
+    lib = load_library()
+    N, T, Hqk, Hv, D, per_token, strides = _decay_inputs(q, k, v, log_decay)
+    if T != 1:
+        raise ValueError("decode takes one token per sequence (T = 1)")
+    dev = q.device
+    sdt = _pool(state, Hv, D, dev)
+    idx_host = _slots(state_indices, state_indices_cpu, N, dev)
+    if out is None:
+        out = torch.empty((N, 1, Hv, D), dtype=_BF16, device=dev)
+    else:
+        _want(out, "out", _BF16, (N, 1, Hv, D), dev)
+    with _on(dev) as stream:
+        _check(lib.kda_decay_attn_decode(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), per_token, state.data_ptr(), sdt,
+            _p(state_indices), _p(idx_host), state.shape[0], N, Hqk, Hv, D, _NAN if scale is None else float(scale), strides,
+            out.data_ptr(), stream))
+    return out
+
+
+def _rope_inputs(q, k, q_weight, k_weight, positions, inv_freq):
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("q and k must be [B, T, H, D] tensors")
+    if q.dtype not in _ROPE_TYPES:
+        raise TypeError("q must be bfloat16, float16 or float32")
+    B, T, Hq, D = q.shape
+    Hk = k.shape[2]
+    dev = q.device
+    _typed(k, "k", q.dtype, (B, T, Hk, D), dev)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _want(w, name, _F32, (D,), dev)
+    R = 0
+    if inv_freq is not None:
+        R = 2 * inv_freq.numel()
+        _want(inv_freq, "inv_freq", torch.float64, (R // 2,), dev)
+        _want(positions, "positions", _I64, (B, T), dev)
+    return B, T, Hq, Hk, D, R, dev
+
+
+def kda_qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interleaved=False, q_out=None, k_out=None):
+    """RMS norm of every query and key head and the rotation by position, in one pass: returns
+    (q_out, k_out). q [B, T, Hq, D] and k [B, T, Hk, D] of one type (BF16, FP16 or FP32), contiguous or views
+    with whole heads contiguous; q_weight, k_weight FP32 [D] or None; positions int64 [B, T]; inv_freq
+    FP64 [R / 2], the angle of a pair per position: pairs are (d, d + R / 2) of the first R dimensions, or
+    (2d, 2d + 1) when interleaved; None for the norm alone. D and R are multiples of 16, D up to 256.
+    q_out and k_out may be q and k."""
+    lib = load_library()
+    B, T, Hq, Hk, D, R, dev = _rope_inputs(q, k, q_weight, k_weight, positions, inv_freq)
+    if q_out is None:
+        q_out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=dev)
+    else:
+        _typed(q_out, "q_out", q.dtype, q.shape, dev)
+    if k_out is None:
+        k_out = torch.empty((B, T, Hk, D), dtype=q.dtype, device=dev)
+    else:
+        _typed(k_out, "k_out", q.dtype, k.shape, dev)
+    strides = _all_strides((("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out)))
+    with _on(dev) as stream:
+        _check(lib.kda_qk_norm_rope_fwd(q.data_ptr(), k.data_ptr(), _ROPE_TYPES[q.dtype], _p(q_weight), _p(k_weight),
+                                        _p(positions) if R else None, _p(inv_freq) if R else None, B * T, Hq, Hk, D, R,
+                                        eps, int(bool(interleaved)), strides, q_out.data_ptr(), k_out.data_ptr(), stream))
+    return q_out, k_out
+
+
+def kda_qk_norm_rope_bwd(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interleaved=False, out=None,
+                         workspace=None):
+    """Gradients of kda_qk_norm_rope_fwd from those of its outputs (dq, dk) and its inputs: returns
+    (dq_in, dk_in, dq_weight, dk_weight), the last two FP32 [D], summed over all tokens and heads, or None
+    where there is no weight. ``out``: (dq_in, dk_in) buffers, which may be dq and dk. ``workspace``: a uint8
+    tensor for the weights' partial sums (kda_qk_norm_rope_workspace_bytes); None takes one for the call."""
+    lib = load_library()
+    B, T, Hq, Hk, D, R, dev = _rope_inputs(q, k, q_weight, k_weight, positions, inv_freq)
+    _typed(dq, "dq", q.dtype, q.shape, dev)
+    _typed(dk, "dk", q.dtype, k.shape, dev)
+    if out is None:
+        gq, gk = (torch.empty(t.shape, dtype=q.dtype, device=dev) for t in (q, k))
+    else:
+        gq, gk = out
+        _typed(gq, "out[0]", q.dtype, q.shape, dev)
+        _typed(gk, "out[1]", q.dtype, k.shape, dev)
+    gqw = None if q_weight is None else torch.empty(D, dtype=_F32, device=dev)
+    gkw = None if k_weight is None else torch.empty(D, dtype=_F32, device=dev)
+    if workspace is None and (gqw is not None or gkw is not None):
+        n = ctypes.c_size_t(0)
+        _check(lib.kda_qk_norm_rope_workspace_bytes(D, ctypes.byref(n)))
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+    elif workspace is not None:
+        _want(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    strides = _all_strides((("q", q), ("k", k), ("out[0]", gq), ("out[1]", gk), ("dq", dq), ("dk", dk)))
+    with _on(dev) as stream:
+        _check(lib.kda_qk_norm_rope_bwd(dq.data_ptr(), dk.data_ptr(), q.data_ptr(), k.data_ptr(), _ROPE_TYPES[q.dtype],
+                                        _p(q_weight), _p(k_weight), _p(positions) if R else None, _p(inv_freq) if R else None,
+                                        B * T, Hq, Hk, D, R, eps, int(bool(interleaved)), strides, gq.data_ptr(),
+                                        gk.data_ptr(), _p(gqw), _p(gkw), _p(workspace),
+                                        0 if workspace is None else workspace.numel(), stream))
+    return gq, gk, gqw, gkw

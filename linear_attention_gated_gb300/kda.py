@@ -32,7 +32,9 @@ EXPORTED = ("kda_ctx_workspace_bytes", "kda_fwd", "kda_bwd", "kda_ctx_status", "
             "kda_status_string", "kda_last_error_message", "kda_chunk_tokens",
             "kda_checkpoint_tokens", "kda_bwd_noalloc", "kda_decode", "kda_prefill",
             "kda_selftest_device_timeout", "kda_step_arena_bytes", "kda_step_host",
-            "kda_bwd_standalone_workspace_bytes", "kda_bwd_standalone", "kda_noalloc_status")
+            "kda_bwd_standalone_workspace_bytes", "kda_bwd_standalone", "kda_noalloc_status",
+            "kda_decay_attn_workspace_bytes", "kda_decay_attn_fwd", "kda_decay_attn_bwd", "kda_decay_attn_prefill",
+            "kda_decay_attn_decode", "kda_qk_norm_rope_fwd", "kda_qk_norm_rope_bwd", "kda_qk_norm_rope_workspace_bytes")
 
 
 class KdaError(RuntimeError):
@@ -90,6 +92,21 @@ def load_library(path: str = LIB_PATH):
     lib.kda_prefill.restype = ctypes.c_int
     lib.kda_selftest_device_timeout.argtypes = [P]
     lib.kda_selftest_device_timeout.restype = ctypes.c_int
+    i32 = ctypes.c_int32
+    decay = [P] * 4 + [i32]  # q, k, v, log_decay, decay_per_token
+    shape = [P, P, I, I, I, I, I, I, F, P]  # cu_seqlens, its mirror, N, B, T, Hqk, Hv, head_dim, scale, strides
+    lib.kda_decay_attn_workspace_bytes.argtypes = [I, I, I, I, P, I, i32, ctypes.POINTER(S)]
+    lib.kda_decay_attn_fwd.argtypes = decay + [P] + shape + [P, P, P, S, P, P]
+    lib.kda_decay_attn_bwd.argtypes = decay + [P] + shape + [P] * 7 + [P, S, P, P]
+    lib.kda_decay_attn_prefill.argtypes = decay + shape + [P, i32, P, P, I, P, P, S, P, P]
+    lib.kda_decay_attn_decode.argtypes = decay + [P, i32, P, P, I, I, I, I, I, F, P, P, P]
+    rope = [i32, P, P, P, P, I, I, I, I, I, F, i32, P, P, P]  # dtype to the two outputs
+    lib.kda_qk_norm_rope_fwd.argtypes = [P, P] + rope + [P]
+    lib.kda_qk_norm_rope_bwd.argtypes = [P] * 4 + rope + [P, P, P, S, P]
+    lib.kda_qk_norm_rope_workspace_bytes.argtypes = [I, ctypes.POINTER(S)]
+    for name in EXPORTED:
+        if name.startswith(("kda_decay", "kda_qk")):
+            getattr(lib, name).restype = ctypes.c_int
     lib.kda_chunk_tokens.argtypes = []
     lib.kda_chunk_tokens.restype = ctypes.c_int32
     lib.kda_checkpoint_tokens.argtypes = []
