@@ -6,6 +6,15 @@
 
 namespace kda {
 
+constexpr int kDecayChunk = 64;  // tokens of a chunk
+
+// 2^x, 0 below 2^-126 (the hardware's approximation, 2 ulp)
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The token tensors of one call. Strides in elements; heads of q, k: Hqk, of v: Hv.
 struct DecayProblem {
   const __nv_bfloat16* q;
@@ -18,6 +27,8 @@ struct DecayProblem {
   int Hqk, Hv, r;          // r = Hv / Hqk
   int per_token;
   float scale;
+  int64_t seg;             // tokens of a segment, 0 for whole sequences (decay_segment_tokens)
+  int64_t longest;         // tokens of the longest sequence
   int32_t* status;         // bit 0: a bounded device wait gave up; bit 2: a device slot index out of the pool
 };
 
@@ -64,7 +75,11 @@ __device__ __forceinline__ float decay_g(const DecayProblem& P, int64_t tok, int
                      : reinterpret_cast<const float*>(P.g)[h];
 }
 
-size_t decay_workspace_bytes(int64_t N, int64_t Ttot, int64_t Hqk, int64_t Hv, bool training);
+// Tokens of the segments the forward cuts sequences into, 0 for none. cu: host offsets or null.
+int64_t decay_segment_tokens(const int64_t* cu, int64_t N, int64_t T, int64_t Hv);
+// Workspace: the forward's segments, then (training) what the backward needs.
+size_t decay_forward_workspace(int64_t N, int64_t Ttot, int64_t Hv, int64_t seg);
+size_t decay_workspace_bytes(int64_t N, int64_t Ttot, int64_t Hqk, int64_t Hv, int64_t seg, bool training);
 cudaError_t launch_decay_forward(const DecayProblem& P, const DecayStates& st, __nv_bfloat16* o, void* ws,
                                  bool training, cudaStream_t s);
 cudaError_t launch_decay_backward(const DecayProblem& P, const float* h0, const DecayGrads& g, void* ws,

@@ -42,7 +42,7 @@ bool aliasing(const Span (&outs)[NO], const Span (&ins)[NI]) {
 }
 
 struct Shape {
-  int64_t N, Ttot;
+  int64_t N, Ttot, seg, longest;
 };
 
 kda_status check_shape(int64_t B, int64_t T, int64_t Hqk, int64_t Hv, const int64_t* cu, int64_t num_seqs, Shape* s) {
@@ -61,6 +61,11 @@ kda_status check_shape(int64_t B, int64_t T, int64_t Hqk, int64_t Hv, const int6
     s->N = num_seqs;
   }
   if (s->N > INT32_MAX / Hv) return fail(KDA_ERR_UNSUPPORTED, "too many (sequence, head) units");
+  if (s->Ttot >= INT32_MAX) return fail(KDA_ERR_UNSUPPORTED, "problem too large (2^31 tokens)");
+  s->longest = cu ? 0 : T;
+  for (int64_t i = 0; cu && i < s->N; ++i)
+    if (cu[i + 1] - cu[i] > s->longest) s->longest = cu[i + 1] - cu[i];
+  s->seg = kda::decay_segment_tokens(cu, s->N, T, Hv);
   return KDA_OK;
 }
 
@@ -72,7 +77,7 @@ kda_status check_tokens(const void* q, const void* k, const void* v, const void*
                         kda::DecayProblem* P, Span (&spans)[5]) {
   if ((cu_dev == nullptr) != (cu_host == nullptr))
     return fail(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens needs its host mirror (and the reverse)");
-  Shape s;
+  Shape s{};
   const kda_status st = check_shape(B, T, Hqk, Hv, cu_host, num_seqs, &s);
   if (st != KDA_OK) return st;
   if (head_dim != kda::kDim) return fail(KDA_ERR_UNSUPPORTED, "head_dim must be 128");
@@ -109,12 +114,14 @@ kda_status check_tokens(const void* q, const void* k, const void* v, const void*
   P->Hv = (int)Hv;
   P->r = (int)(Hv / Hqk);
   P->per_token = per_token;
+  P->seg = s.seg;
+  P->longest = s.longest;
   P->scale = std::isnan(scale) ? 1.0f / std::sqrt(128.0f) : scale;
   return KDA_OK;
 }
 
 kda_status check_workspace(const kda::DecayProblem& P, void* ws, size_t bytes, bool training) {
-  const size_t need = kda::decay_workspace_bytes(P.N, P.Ttot, P.Hqk, P.Hv, training);
+  const size_t need = kda::decay_workspace_bytes(P.N, P.Ttot, P.Hqk, P.Hv, P.seg, training);
   if (need && (!ws || bytes < need))
     return fail(KDA_ERR_WORKSPACE_TOO_SMALL, "workspace below kda_decay_attn_workspace_bytes()");
   if ((uintptr_t)ws & 255u) return fail(KDA_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
@@ -141,10 +148,10 @@ extern "C" kda_status kda_decay_attn_workspace_bytes(int64_t B, int64_t T, int64
                                                      int32_t training, size_t* bytes) {
   return kda::guarded([&]() -> kda_status {
     if (!bytes) return fail(KDA_ERR_INVALID_ARGUMENT, "bytes is NULL");
-    Shape s;
+    Shape s{};
     const kda_status st = check_shape(B, T, Hqk, Hv, cu_seqlens_host, num_seqs, &s);
     if (st != KDA_OK) return st;
-    *bytes = kda::decay_workspace_bytes(s.N, s.Ttot, Hqk, Hv, training != 0);
+    *bytes = kda::decay_workspace_bytes(s.N, s.Ttot, Hqk, Hv, s.seg, training != 0);
     return KDA_OK;
   });
 }

@@ -154,32 +154,14 @@ cudaError_t scan(const DecayProblem& P, const ScanArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t decay_workspace_bytes(int64_t N, int64_t Ttot, int64_t, int64_t Hv, bool training) {
-  return training ? carve(N, Ttot, Hv).total : 0;
-}
-
-cudaError_t launch_decay_forward(const DecayProblem& P, const DecayStates& st, __nv_bfloat16* o, void* ws,
-                                 bool training, cudaStream_t s) {
-  ScanArgs a{};
-  a.a = Src{P.k, P.kt, P.kh, P.r};
-  a.b = Src{P.v, P.vt, P.vh, 1};
-  a.x = Src{P.q, P.qt, P.qh, P.r};
-  a.b_scale = 1.f;
-  a.y_scale = P.scale;
-  a.m0 = st.in;
-  a.m1 = st.out;
-  a.m1_copy = training ? reinterpret_cast<float*>(ws) : nullptr;
-  a.bf16 = st.bf16;
-  a.slots = st.slots;
-  a.num_slots = st.num_slots;
-  a.y = o;
-  return scan<false>(P, a, s);
+size_t decay_workspace_bytes(int64_t N, int64_t Ttot, int64_t, int64_t Hv, int64_t seg, bool training) {
+  return decay_forward_workspace(N, Ttot, Hv, seg) + (training ? carve(N, Ttot, Hv).total : 0);
 }
 
 cudaError_t launch_decay_backward(const DecayProblem& P, const float* h0, const DecayGrads& g, void* ws,
                                   cudaStream_t s) {
   const Ws w = carve(P.N, P.Ttot, P.Hv);
-  char* base = reinterpret_cast<char*>(ws);
+  char* base = reinterpret_cast<char*>(ws) + decay_forward_workspace(P.N, P.Ttot, P.Hv, P.seg);
   float* hT = reinterpret_cast<float*>(base + w.hT);
   float* dq = reinterpret_cast<float*>(base + w.dq);
   float* dk = reinterpret_cast<float*>(base + w.dk);

@@ -68,6 +68,48 @@ __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, 
       ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc));
 }
 
+// ---- kind::f16 with BF16 operands and FP32 accumulation. Operands lie in shared memory in the
+// 128-byte swizzle a tiled copy writes: panels of 64 elements (128-byte rows, 16-byte chunk c of
+// row r at chunk c ^ (r & 7)), panels 1024-byte aligned. Read K-major (K along the row): 8-row groups
+// 1024 bytes apart, a K-step of 16 elements 32 bytes further along. Read MN-major (M or N along the
+// row, K down the rows): panels `panel` bytes apart along M or N, a K-step of 16 rows 2048 bytes.
+__device__ __forceinline__ uint64_t swdesc(uint32_t saddr, uint32_t lbo) {
+  return sdesc(saddr, lbo, 1024u) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ uint64_t kmajor(uint32_t saddr) { return swdesc(saddr, 16u); }
+__device__ __forceinline__ uint64_t mnmajor(uint32_t saddr, uint32_t panel) { return swdesc(saddr, panel); }
+
+// Instruction descriptor: BF16 A and B, FP32 accumulator; mn: that operand is MN-major.
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool mnA, bool mnB) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((mnA ? 1u : 0u) << 15) | ((mnB ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, int acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+      ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+// A operand in tensor memory: 128 lanes, two K elements to a 32-bit column.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, int acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
+}
+
+// Tiled copy global -> shared of a 3-D box at element (x, y, z); x on a 16-byte boundary.
+__device__ __forceinline__ void tma_load3(uint32_t dst_smem, const void* map, int x, int y, int z, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+      ::"r"(dst_smem), "l"(map), "r"(mbar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_map(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // A operand read from tensor memory (128 lanes x K columns at a_tmem).
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, int acc) {
   asm volatile(
@@ -223,6 +265,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
         "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
         "r"(__float_as_uint(v[15])));
 }
+// Store 8 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]));
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Shape .16x128b, four repeats along the columns (16 columns of 16 lanes): register
@@ -262,6 +309,35 @@ __device__ __forceinline__ void tmem_st16x128(uint32_t taddr, const float* v) {
                  "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
                  "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])));
 }
+
+// Shape .16x256b, four repeats (32 columns of 16 lanes): registers 4 i + 2 j and 4 i + 2 j + 1 of lane l
+// hold lane (taddr lane) + 8 j + l / 4, columns (taddr column) + 8 i + 2 (l % 4) and the next.
+__device__ __forceinline__ void tmem_ld16x256(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// Two FP32 operations in one instruction, on register pairs.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
+        "l"(reinterpret_cast<const unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.f, -1.f), a); }
 
 // 4x4 transpose among the four lanes of an aligned lane quad: on entry lane (quad base + j) holds
 // row j of the block, on exit it holds column j (four shuffles; the whole warp takes part).
