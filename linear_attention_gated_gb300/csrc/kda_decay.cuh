@@ -29,6 +29,7 @@ struct DecayProblem {
   float scale;
   int64_t seg;             // tokens of a segment, 0 for whole sequences (decay_segment_tokens)
   int64_t longest;         // tokens of the longest sequence
+  const int64_t* cu_host;  // host offsets (packed layout), for the call only
   int32_t* status;         // bit 0: a bounded device wait gave up; bit 2: a device slot index out of the pool
 };
 
@@ -75,10 +76,9 @@ __device__ __forceinline__ float decay_g(const DecayProblem& P, int64_t tok, int
                      : reinterpret_cast<const float*>(P.g)[h];
 }
 
-// Tokens of the segments the forward cuts sequences into, 0 for none. cu: host offsets or null.
+// Tokens of the segments sequences are cut into, 0 for none. cu: host offsets or null.
 int64_t decay_segment_tokens(const int64_t* cu, int64_t N, int64_t T, int64_t Hv);
-// Workspace: the forward's segments, then (training) what the backward needs.
-size_t decay_forward_workspace(int64_t N, int64_t Ttot, int64_t Hv, int64_t seg);
+// Workspace: the segments' states, then (training) what the backward needs.
 size_t decay_workspace_bytes(int64_t N, int64_t Ttot, int64_t Hqk, int64_t Hv, int64_t seg, bool training);
 cudaError_t launch_decay_forward(const DecayProblem& P, const DecayStates& st, __nv_bfloat16* o, void* ws,
                                  bool training, cudaStream_t s);

@@ -116,6 +116,7 @@ kda_status check_tokens(const void* q, const void* k, const void* v, const void*
   P->per_token = per_token;
   P->seg = s.seg;
   P->longest = s.longest;
+  P->cu_host = cu_host;
   P->scale = std::isnan(scale) ? 1.0f / std::sqrt(128.0f) : scale;
   return KDA_OK;
 }

@@ -1,0 +1,945 @@
+// kda_decay_pass.cu -- the chunked pass of the linear attention with a decay for
+// each head, on sm_103a tensor cores: one kernel for the forward and for the three
+// passes of the backward.
+//
+// With roles Q, K, V (token tensors) and a state S [V dims, K dims] per (sequence, head), it computes
+// for chunks of C = 64 tokens, b_i the sum of the chunk's log decays up to token i,
+//   Y^T = S Q^T diag(e^{b_i}) + V^T P^T,   P_ij = e^{b_i - b_j} q_i . k_j  (j <= i)
+//   S  <- e^{b_C} S + V^T K~,              K~_j = e^{b_C - b_j} k_j
+// and backwards in time (last chunk first), where S is the adjoint of the state after the first token of the
+// chunk done before, c_i the sum of the log decays from token i + 1 up to and with that token, and b_i the sum
+// from the chunk's second token up to i,
+//   Y^T = S Q^T diag(e^{c_i}) + V^T P^T,   P_ij = e^{b_j - b_i} q_i . k_j  (j >= i)
+//   S  <- e^{c_1} S + V^T K~,              K~_j = e^{b_j} k_j
+// All exponents are <= 0 and the largest factor in K~ is 1, so nothing overflows, and nothing that counts
+// underflows, for any decay.
+//   o :  Q = q,  K = k,  V = v     forward,   S = the state                      (value first)
+//   dq:  Q = do, K = v,  V = k     forward,   S = the state, transposed
+//   dk:  Q = v,  K = do, V = q     backwards, S = the state's adjoint, transposed
+//   dv:  Q = k,  K = q,  V = do    backwards, S = the state's adjoint            (its end is dh0)
+// Nothing is saved by the forward: what the backward needs of the states it carries again, which moves
+// fewer bytes than a state stored and read for every chunk would (32 KiB against the 16 KiB of a tile).
+//
+// One CTA an SM, 20 warps with roles, so that the copies, the products and the element-wise work of
+// neighbouring chunks (and units) run side by side; only the state's update is a chain.
+//   warp 0   copies: Q, K, V tiles by tiled copies (128-byte swizzle), three stages; the next unit's
+//            number (cluster launch control: the grid has a CTA for each unit and a running CTA takes
+//            over the next one that has not started)
+//   warp 1   products (tcgen05.mma kind::f16, BF16 operands, FP32 accumulators in tensor memory)
+//   warp 2   decays of each chunk: sums from both ends, so that the exponents that matter most in
+//            each, the small ones, are sums of few terms
+//   warps 4-11   K~ (over K and beside) and P
+//   warps 12-19  the state, 64 of a row's 128 values a thread in registers, S = e^{b_C} S + U with U = V^T K~
+//            from tensor memory, and as A operand back there; Y
+// K~, P and S are operands in two BF16 parts, hi + lo: 16 mantissa bits. The carried state then keeps FP32-level
+// accuracy, and Y is off by little more than its own rounding also where heads or long sums cancel.
+// A unit is one (sequence, head), longest sequences first, or one segment of it.
+//
+// Long axis, few units: each sequence is cut into segments. A first pass runs the state part alone
+// over every segment but the last in time, a small kernel chains the segments' states, and
+// the main pass starts every segment from its state.
+#include <algorithm>
+
+#include "kda_decay.cuh"
+#include "kda_layout.h"
+#include "kda_tma.h"
+#include "tc.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kC = kDecayChunk;
+constexpr int kStages = 3, kDecs = 4, kRing = 4;
+constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpDecay = 2, kWarpA = 4, kWarpB = 12;
+constexpr int kGroup = 8;                  // warps of A and of B
+constexpr int kThreads = 32 * 20;
+// Registers a thread of the control, A and B warps (setmaxnreg): 128 x 40 + 256 x 72 + 256 x 144 = 60,416 of the
+// 640 x 96 = 61,440 the block is launched with (a split above that would wait for ever).
+constexpr uint32_t kTile = kC * kDim * 2;  // bytes of a Q, K or V tile
+constexpr uint32_t kPanel = kC * 128;      // bytes of its 64-element half
+constexpr uint32_t kColU = 0;              // U: 128 columns
+constexpr uint32_t kColS = 128;            // the state as A operand, 64 + 64: its high and low BF16 parts, or (one part)
+                                           // that of two chunks
+constexpr uint32_t kColO = 256;            // S Q^T, then V^T P^T: 64 + 64
+constexpr uint32_t kColP = 384;            // scores (M = 64) of two chunks: 64 + 64
+
+struct Smem {
+  unsigned char tile[kStages][3][kTile];  // Q, K, V
+  unsigned char lo[2][kTile];             // low parts of K~
+  unsigned char P[2][2][kC * kC * 2];     // high and low parts of P
+  float b[kDecs][kC];    // cumulative log2 decay of the chunk
+  float eb[kDecs][kC];   // factor of S q_i
+  float w[kDecs][kC];    // factor of k_j in K~
+  float lam[kDecs];      // e^{b_C}
+  uint4 clc;             // response: the next unit
+  int ring[kRing];       // units to come, -1: none
+  // full, empty: a stage's tiles are there / read by all products; dec: a chunk's decays; g0, gu, gy: products done
+  // (scores, U, Y); aready: K~ and P are there; ufree, yfree: U, Y are read; sready: the state is there
+  unsigned long long full[kStages], empty[kStages], dec[kDecs], g0[2], gu, gy, aready[2], ufree, sready, yfree;
+  unsigned long long clcbar, rfull[kRing], rempty[kRing];
+  uint32_t tmem;
+};
+constexpr int kSmemBytes = (int)sizeof(Smem) + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+
+struct Segments {
+  int64_t len;       // tokens of a segment (a multiple of kC), 0: sequences are not cut
+  int most;          // most segments of a sequence
+  float* state;      // [slots, H, 128, 128]: the segments' own states, then their initial states
+  float* decay;      // [slots, H]: log2 of a segment's decay
+};
+// Slot of a sequence's first segment: floor(t0 / len) + n leaves each sequence ceil(len_n / len) slots.
+__device__ __forceinline__ int64_t seg_slot(const Segments& g, int64_t t0, int64_t n) { return t0 / g.len + n; }
+
+constexpr int kOrder = 512;  // sequences whose order is passed (more run in index order)
+
+struct PassArgs {
+  DecayProblem P;
+  int qdiv, kdiv, vdiv;               // head of a role's tensor: h / div
+  float s_inter, s_intra, s_w;        // scales of S q, of P and of K~
+  DecayStates st;
+  int transposed;                     // S is the stored state transposed
+  Segments sg;
+  __nv_bfloat16* y;                   // [Ttot, Hv, 128], or
+  float* y32;
+  int ordered;
+  uint16_t order[kOrder];             // longest sequence first
+};
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+__device__ __forceinline__ uint32_t pack2(float2 x) { return pack2(x.x, x.y); }
+__device__ __forceinline__ float2 unpack2(uint32_t x) {
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+// x as BF16 pairs hi + lo: 16 mantissa bits together
+__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
+  hi = pack2(x);
+  lo = pack2(tc::sub2(x, unpack2(hi)));
+}
+
+// One unit of work.
+struct Unit {
+  int h;
+  int64_t n, seg, t0, len, nchunks, end;  // end: the sequence's
+  int64_t slot, sslot;
+  bool run;   // there is something to do
+  bool last;  // the last segment in time order of the pass
+};
+template <bool kRev, bool kState>
+__device__ __forceinline__ Unit unit_of(const PassArgs& a, int u) {
+  const DecayProblem& P = a.P;
+  Unit x;
+  const int64_t p = u / P.Hv;
+  x.h = u - (int)(p * P.Hv);
+  x.seg = p / P.N;
+  x.n = p - x.seg * P.N;
+  if (a.ordered) x.n = a.order[x.n];
+  const DecaySpan sp = decay_span(P, x.n);
+  x.t0 = sp.t0;
+  x.len = sp.len;
+  x.end = sp.t0 + sp.len;
+  x.slot = a.st.slots ? a.st.slots[x.n] : x.n;
+  x.sslot = 0;
+  x.last = true;
+  x.run = x.slot >= 0 && x.slot < a.st.num_slots;
+  if (a.sg.len) {
+    const int64_t from = x.seg * a.sg.len;
+    x.sslot = seg_slot(a.sg, sp.t0, x.n) + x.seg;
+    const bool tail = from + a.sg.len >= sp.len;
+    x.last = kRev ? x.seg == 0 : tail;
+    if ((x.seg > 0 && from >= sp.len) || (kState && x.last)) x.run = false;
+    x.t0 += from;
+    x.len = tail ? sp.len - from : a.sg.len;
+  }
+  x.nchunks = x.run ? (x.len + kC - 1) / kC : 0;
+  return x;
+}
+
+// kRev: backwards in time. kState: the first pass over segments (states alone). kSplit: S Q^T with the state in
+// two BF16 parts.
+template <bool kRev, bool kState, bool kSplit>
+__global__ void __launch_bounds__(kThreads, 1)
+kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PassArgs a) {
+  extern __shared__ unsigned char raw_smem[];
+  Smem& sm = *reinterpret_cast<Smem*>(raw_smem + ((1024 - (tc::smem_u32(raw_smem) & 1023)) & 1023));
+  const DecayProblem& P = a.P;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto bar = [](unsigned long long& b) { return tc::smem_u32(&b); };
+
+  if (warp == kWarpMma) tc::tmem_alloc(tc::smem_u32(&sm.tmem), 512);
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) { tc::mbar_init(bar(sm.full[i]), 1); tc::mbar_init(bar(sm.empty[i]), 1); }
+    for (int i = 0; i < kDecs; ++i) tc::mbar_init(bar(sm.dec[i]), 1);
+    for (int i = 0; i < 2; ++i) { tc::mbar_init(bar(sm.g0[i]), 1); tc::mbar_init(bar(sm.aready[i]), kGroup); }
+    tc::mbar_init(bar(sm.gu), 1);
+    tc::mbar_init(bar(sm.gy), 1);
+    tc::mbar_init(bar(sm.ufree), kGroup);
+    tc::mbar_init(bar(sm.sready), kGroup);
+    tc::mbar_init(bar(sm.yfree), kGroup);
+    tc::mbar_init(bar(sm.clcbar), 1);
+    for (int i = 0; i < kRing; ++i) { tc::mbar_init(bar(sm.rfull[i]), 1); tc::mbar_init(bar(sm.rempty[i]), 2 + 2 * kGroup); }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tbase = sm.tmem;
+  bool ok = true;  // false: a wait gave up; the warp touches only its own CTA's memory and leaves
+
+  // The ring of units, as a consumer (a warp): its place, and the next unit or -1.
+  uint32_t ur = 0;
+  auto next_unit = [&]() -> int {
+    if (ok) ok = tc::mbar_wait_warp(bar(sm.rfull[ur % kRing]), (ur / kRing) & 1);
+    const int u = ok ? sm.ring[ur % kRing] : -1;
+    __syncwarp();
+    if (ok && lane == 0) tc::mbar_arrive(bar(sm.rempty[ur % kRing]));
+    ++ur;
+    return u;
+  };
+  auto arrive = [&](unsigned long long& b) {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bar(b));
+  };
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == kWarpLoad) {
+      // ================= units and copies
+      uint32_t g = 0;  // chunks so far
+      uint32_t asked = 0;
+      bool pending = false;
+      for (int u = blockIdx.x;;) {
+        // the next unit is asked for before this one's copies
+        if (ok && u >= 0) {
+          if (lane == 0) {
+            tc::mbar_arrive_expect_tx(bar(sm.clcbar), 16);
+            asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                         ::"r"(tc::smem_u32(&sm.clc)), "r"(bar(sm.clcbar)) : "memory");
+          }
+          __syncwarp();
+          pending = true;
+        }
+        if (ur >= kRing && ok) ok = tc::mbar_wait_warp(bar(sm.rempty[ur % kRing]), (ur / kRing - 1) & 1);
+        if (lane == 0) {
+          sm.ring[ur % kRing] = ok ? u : -1;
+          tc::mbar_arrive(bar(sm.rfull[ur % kRing]));
+        }
+        __syncwarp();
+        ++ur;
+        if (!ok || u < 0) break;
+        const Unit x = unit_of<kRev, kState>(a, u);
+        for (int64_t c = 0; c < x.nchunks && ok; ++c, ++g) {
+          const int s = g % kStages;
+          if (g >= kStages) ok = tc::mbar_wait_warp(bar(sm.empty[s]), (g / kStages - 1) & 1);
+          if (ok && lane == 0) {
+            const int t = (int)(x.t0 + (kRev ? x.nchunks - 1 - c : c) * kC);
+            tc::mbar_arrive_expect_tx(bar(sm.full[s]), (kState ? 2 : 3) * kTile);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              tc::tma_load3(tc::smem_u32(sm.tile[s][1]) + p * kPanel, &maps.k, 64 * p, x.h / a.kdiv, t, bar(sm.full[s]));
+              if (!kState)
+                tc::tma_load3(tc::smem_u32(sm.tile[s][0]) + p * kPanel, &maps.q, 64 * p, x.h / a.qdiv, t, bar(sm.full[s]));
+              tc::tma_load3(tc::smem_u32(sm.tile[s][2]) + p * kPanel, &maps.v, 64 * p, x.h / a.vdiv, t, bar(sm.full[s]));
+            }
+          }
+          __syncwarp();
+          if (!ok) break;
+        }
+        const bool came = tc::mbar_wait_warp(bar(sm.clcbar), asked & 1);
+        ++asked;
+        pending = false;
+        ok = ok && came;
+        uint32_t more = 0, nx = 0;
+        if (came) {
+          asm volatile(
+              "{\n .reg .b128 r;\n .reg .pred p;\n ld.shared.b128 r, [%2];\n"
+              " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+              " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}\n"
+              : "=r"(more), "=r"(nx) : "r"(tc::smem_u32(&sm.clc)) : "memory");
+          tc::fence_async_smem();  // read before the next response is written
+        }
+        __syncwarp();
+        u = more ? (int)nx : -1;
+      }
+      if (!ok) {
+        // flag it, and let this CTA's copies (and the response) land before its memory is given back
+        if (lane == 0) atomicOr(P.status, 1);
+        if (pending) tc::mbar_wait_warp(bar(sm.clcbar), asked & 1);
+        for (uint32_t k = g > kStages ? g - kStages : 0; k < g; ++k)
+          tc::mbar_wait_warp(bar(sm.full[k % kStages]), (k / kStages) & 1);
+      }
+    } else if (warp == kWarpMma) {
+      // ================= products
+      uint32_t g = 0;
+      // scores of the chunk numbered k, if its tiles are there (wait: wait for them)
+      auto scores = [&](uint32_t k) {
+        if (ok && tc::elect_one()) {
+          const uint64_t dq = tc::kmajor(tc::smem_u32(sm.tile[k % kStages][0]));
+          const uint64_t dk = tc::kmajor(tc::smem_u32(sm.tile[k % kStages][1]));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t off = (i >> 2) * (kPanel >> 4) + (i & 3) * 2;
+            tc::mma_bf16_ss(tbase + kColP + 64 * (k & 1), dq + off, dk + off, tc::idesc_bf16(64, 64, false, false), i > 0);
+          }
+          tc::mma_commit(bar(sm.g0[k & 1]));
+        }
+        __syncwarp();
+      };
+      auto tiles = [&](uint32_t k) {
+        if (ok) ok = tc::mbar_wait_warp(bar(sm.full[k % kStages]), (k / kStages) & 1);
+        tc::fence_after();
+      };
+      for (int u; (u = next_unit()) >= 0;) {
+        const Unit x = unit_of<kRev, kState>(a, u);
+        if (!kState && x.nchunks) {
+          tiles(g);
+          scores(g);
+        }
+        for (int64_t c = 0; c < x.nchunks; ++c, ++g) {
+          const int s = g % kStages;
+          const uint64_t dv = tc::mnmajor(tc::smem_u32(sm.tile[s][2]), kPanel);
+          if (kState) {
+            tiles(g);
+          } else if (c + 1 < x.nchunks) {  // the next chunk's scores (its buffer was read before the last aready)
+            tiles(g + 1);
+            scores(g + 1);
+          }
+          // U, once K~ is there and the last U is read
+          if (ok) ok = tc::mbar_wait_warp(bar(sm.aready[g & 1]), (g >> 1) & 1);
+          if (ok && g > 0) ok = tc::mbar_wait_warp(bar(sm.ufree), (g - 1) & 1);
+          tc::fence_after();
+          if (ok && tc::elect_one()) {
+            const uint64_t dh = tc::mnmajor(tc::smem_u32(sm.tile[s][1]), kPanel);
+            const uint64_t dl = tc::mnmajor(tc::smem_u32(sm.lo[g & 1]), kPanel);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc::mma_bf16_ss(tbase + kColU, dv + 128 * k, dh + 128 * k, tc::idesc_bf16(128, 128, true, true), k > 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc::mma_bf16_ss(tbase + kColU, dv + 128 * k, dl + 128 * k, tc::idesc_bf16(128, 128, true, true), 1);
+            tc::mma_commit(bar(sm.gu));
+            if (kState) tc::mma_commit(bar(sm.empty[s]));
+          }
+          __syncwarp();
+          if (kState) continue;
+          // Y, once the state is there and the last Y is read
+          if (ok) ok = tc::mbar_wait_warp(bar(sm.sready), g & 1);
+          if (ok && g > 0) ok = tc::mbar_wait_warp(bar(sm.yfree), (g - 1) & 1);
+          tc::fence_after();
+          if (ok && tc::elect_one()) {
+            const uint64_t dq = tc::kmajor(tc::smem_u32(sm.tile[s][0]));
+            const uint64_t dp = tc::kmajor(tc::smem_u32(sm.P[g & 1][0])), dr = tc::kmajor(tc::smem_u32(sm.P[g & 1][1]));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t off = (i >> 2) * (kPanel >> 4) + (i & 3) * 2;
+              tc::mma_bf16_ts(tbase + kColO, tbase + kColS + (kSplit ? 0 : 64 * (g & 1)) + 8 * i, dq + off,
+                              tc::idesc_bf16(128, 64, false, false), i > 0);
+              if (kSplit)
+                tc::mma_bf16_ts(tbase + kColO, tbase + kColS + 64 + 8 * i, dq + off, tc::idesc_bf16(128, 64, false, false), 1);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              tc::mma_bf16_ss(tbase + kColO + 64, dv + 128 * k, dp + 2 * k, tc::idesc_bf16(128, 64, true, false), k > 0);
+              tc::mma_bf16_ss(tbase + kColO + 64, dv + 128 * k, dr + 2 * k, tc::idesc_bf16(128, 64, true, false), 1);
+            }
+            tc::mma_commit(bar(sm.gy));
+            tc::mma_commit(bar(sm.empty[s]));
+          }
+          __syncwarp();
+        }
+      }
+    } else if (warp == kWarpDecay) {
+      // ================= decays, two tokens a lane
+      uint32_t g = 0;
+      for (int u; (u = next_unit()) >= 0;) {
+        const Unit x = unit_of<kRev, kState>(a, u);
+        float total = 0.f, n0 = 0.f, n1 = 0.f;
+        auto fetch = [&](int64_t c) {
+          const int64_t j = (kRev ? x.nchunks - 1 - c : c) * kC + 2 * lane;
+          n0 = c < x.nchunks && j < x.len ? decay_g(P, x.t0 + j, x.h) : 0.f;
+          n1 = c < x.nchunks && j + 1 < x.len ? decay_g(P, x.t0 + j + 1, x.h) : 0.f;
+        };
+        fetch(0);
+        // backwards: the decay of the token that follows the chunk
+        float follow = kRev && x.nchunks && x.t0 + x.len < x.end ? decay_log2(decay_g(P, x.t0 + x.len, x.h)) : 0.f;
+        for (int64_t c = 0; c < x.nchunks; ++c, ++g) {
+          float g0 = decay_log2(n0);
+          const float g1 = decay_log2(n1);
+          const float lead = __shfl_sync(0xffffffffu, g0, 0);
+          if (kRev && lane == 0) g0 = 0.f;
+          fetch(c + 1);
+          float pre = g0 + g1, suf = pre;
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const float p = __shfl_up_sync(0xffffffffu, pre, d), q = __shfl_down_sync(0xffffffffu, suf, d);
+            if (lane >= d) pre += p;
+            if (lane + d < 32) suf += q;
+          }
+          const float before = __shfl_up_sync(0xffffffffu, pre, 1), after = __shfl_down_sync(0xffffffffu, suf, 1);
+          const float p0 = (lane ? before : 0.f) + g0, s1 = (lane < 31 ? after : 0.f) + follow;
+          const float2 up = make_float2(exp2f(p0), exp2f(pre)), down = make_float2(exp2f(s1 + g1), exp2f(s1));
+          const float2 e = kRev ? down : up, w = kRev ? up : down;
+          // the slot was last read for chunk g - 4: its Y was read before chunk g - 3's products began
+          if (ok && g >= kStages) ok = tc::mbar_wait_warp(bar(sm.empty[g % kStages]), (g / kStages - 1) & 1);
+          const int d = g % kDecs;
+          *reinterpret_cast<float2*>(&sm.b[d][2 * lane]) = make_float2(p0, pre);
+          *reinterpret_cast<float2*>(&sm.eb[d][2 * lane]) = make_float2(a.s_inter * e.x, a.s_inter * e.y);
+          *reinterpret_cast<float2*>(&sm.w[d][2 * lane]) = make_float2(a.s_w * w.x, a.s_w * w.y);
+          if (lane == 31) sm.lam[d] = exp2f(pre + follow);
+          total += pre + follow;  // lane 31's is the chunk's
+          if (kRev) follow = lead;
+          arrive(sm.dec[d]);
+        }
+        if (kState && x.run && lane == 31) a.sg.decay[x.sslot * P.Hv + x.h] = total;
+      }
+    }
+  } else if (warp < kWarpB) {
+    // ================= K~ and P
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    const int at = tid - 32 * kWarpA, wq = (warp - kWarpA) & 3, half = (warp - kWarpA) >> 2;
+    const uint32_t tl = tbase + ((uint32_t)(32 * wq) << 16);
+    const float2 scale = make_float2(a.s_intra, a.s_intra);
+    uint32_t g = 0;
+    for (int u; (u = next_unit()) >= 0;) {
+      const Unit x = unit_of<kRev, kState>(a, u);
+      for (int64_t c = 0; c < x.nchunks; ++c, ++g) {
+        const int s = g % kStages, d = g % kDecs;
+        const int64_t left = x.len - (kRev ? x.nchunks - 1 - c : c) * kC;
+        const int nt = (int)(left < kC ? left : kC);
+        unsigned char* Ks = sm.tile[s][1];
+        unsigned char* Ls = sm.lo[g & 1];
+        if (ok) ok = tc::mbar_wait_warp(bar(sm.dec[d]), (g / kDecs) & 1);
+        if (ok) ok = tc::mbar_wait_warp(bar(sm.full[s]), (g / kStages) & 1);
+        // K is free once the scores are done; they follow chunk g - 2's products, which read lo and P of this parity
+        if (!kState) {
+          if (ok) ok = tc::mbar_wait_warp(bar(sm.g0[g & 1]), (g >> 1) & 1);
+        } else if (g >= 2) {
+          if (ok) ok = tc::mbar_wait_warp(bar(sm.empty[(g - 2) % kStages]), ((g - 2) / kStages) & 1);
+        }
+        tc::fence_after();
+        float p[16];
+        if (!kState) tc::tmem_ld16x256(tl + kColP + 64 * (g & 1) + 32 * half, p);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {  // 16-byte chunks i
+          const int i = at + 32 * kGroup * m, row = (i >> 3) & (kC - 1);
+          const uint4 r = *reinterpret_cast<const uint4*>(Ks + 16 * i);
+          const float w1 = sm.w[d][row];
+          const float2 w = make_float2(w1, w1);
+          uint4 hi, lo;
+          split2(tc::mul2(unpack2(r.x), w), hi.x, lo.x);
+          split2(tc::mul2(unpack2(r.y), w), hi.y, lo.y);
+          split2(tc::mul2(unpack2(r.z), w), hi.z, lo.z);
+          split2(tc::mul2(unpack2(r.w), w), hi.w, lo.w);
+          if (row >= nt) hi = lo = make_uint4(0u, 0u, 0u, 0u);  // rows past the end hold other tokens
+          *reinterpret_cast<uint4*>(Ks + 16 * i) = hi;
+          *reinterpret_cast<uint4*>(Ls + 16 * i) = lo;
+        }
+        if (nt < kC)
+          for (int i = at; i < (kC - nt) * 16; i += 32 * kGroup)
+            *reinterpret_cast<uint4*>(sm.tile[s][2] + ((i >> 3) & 1) * kPanel + (nt + (i >> 4)) * 128 + (i & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        if (!kState) {
+          // rows i = 16 wq + lane / 4 (+ 8), columns 32 half + 8 m + 2 (lane % 4) (+ 1)
+          const int i0 = 16 * wq + (lane >> 2), j0 = 32 * half + 2 * (lane & 3);
+          const float b0 = sm.b[d][i0], b1 = sm.b[d][i0 + 8];
+          unsigned char* Pt = sm.P[g & 1][0];
+          tc::tmem_wait_ld(p);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const int j = j0 + 8 * m;
+            const float2 bj = *reinterpret_cast<const float2*>(&sm.b[d][j]);
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              const int i = i0 + 8 * v;
+              const float bi = v ? b1 : b0;
+              const float2 e = kRev ? make_float2(fast_exp2(bj.x - bi), fast_exp2(bj.y - bi))
+                                    : make_float2(fast_exp2(bi - bj.x), fast_exp2(bi - bj.y));
+              float2 y = tc::mul2(tc::mul2(make_float2(p[4 * m + 2 * v], p[4 * m + 2 * v + 1]), scale), e);
+              // (selected, not multiplied: rows past the end may hold anything)
+              y.x = (kRev ? j >= i && j < nt : j <= i && i < nt) ? y.x : 0.f;
+              y.y = (kRev ? j + 1 >= i && j + 1 < nt : j < i && i < nt) ? y.y : 0.f;
+              uint32_t hi, lo;
+              split2(y, hi, lo);
+              uint32_t* dst = reinterpret_cast<uint32_t*>(Pt + i * 128 + (((4 * half + m) ^ (i & 7)) << 4) + 4 * (lane & 3));
+              dst[0] = hi;
+              dst[kC * kC / 2] = lo;
+            }
+          }
+        }
+        tc::fence_async_smem();
+        tc::fence_before();
+        arrive(sm.aready[g & 1]);
+      }
+    }
+  } else {
+    // ================= the state and Y
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    const int wq = (warp - kWarpB) & 3, half = (warp - kWarpB) >> 2;
+    const int v = 32 * wq + lane;  // state row of this thread, its columns 64 half .. + 63; value of Y, tokens 32 half .. + 31
+    const uint32_t tl = tbase + ((uint32_t)(32 * wq) << 16);
+    uint32_t g = 0;
+    for (int u; (u = next_unit()) >= 0;) {
+      const Unit x = unit_of<kRev, kState>(a, u);
+      if (!x.run) {
+        // a device slot index outside the pool (it no longer matches the host mirror the call was checked
+        // against, as in a replayed graph): flagged, and the pool is not touched
+        if ((x.slot < 0 || x.slot >= a.st.num_slots) && warp == kWarpB && lane == 0) atomicOr(P.status, 4);
+        continue;
+      }
+      float2 S[32];
+      const int64_t at = (x.slot * P.Hv + x.h) * kDim * kDim;
+      if (kState || (!a.sg.len && !a.st.in)) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) S[j] = make_float2(0.f, 0.f);
+      } else if (a.sg.len) {  // (the segments' states are kept as S is)
+        const float4* src = reinterpret_cast<const float4*>(a.sg.state + ((x.sslot * P.Hv + x.h) * kDim + v) * kDim + 64 * half);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float4 r = src[j];
+          S[2 * j] = make_float2(r.x, r.y);
+          S[2 * j + 1] = make_float2(r.z, r.w);
+        }
+      } else if (a.transposed) {
+        const float* src = reinterpret_cast<const float*>(a.st.in) + at + (int64_t)64 * half * kDim + v;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) S[j] = make_float2(src[2 * j * kDim], src[(2 * j + 1) * kDim]);
+      } else if (a.st.bf16) {
+        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.st.in) + at + v * kDim + 64 * half);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 r = src[j];
+          S[4 * j] = unpack2(r.x); S[4 * j + 1] = unpack2(r.y); S[4 * j + 2] = unpack2(r.z); S[4 * j + 3] = unpack2(r.w);
+        }
+      } else {
+        const float4* src = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.st.in) + at + v * kDim + 64 * half);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float4 r = src[j];
+          S[2 * j] = make_float2(r.x, r.y);
+          S[2 * j + 1] = make_float2(r.z, r.w);
+        }
+      }
+      auto put_state = [&](uint32_t k) {  // as chunk k's A operand
+        const uint32_t col = tl + kColS + (kSplit ? 0 : 64 * (k & 1)) + 32 * half;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (kSplit) split2(S[8 * m + e], hi[e], lo[e]);
+            else hi[e] = pack2(S[8 * m + e]);
+          }
+          tc::tmem_st8(col + 8 * m, hi);
+          if (kSplit) tc::tmem_st8(col + 64 + 8 * m, lo);
+        }
+        tc::tmem_wait_st();
+        tc::fence_before();
+        arrive(sm.sready);
+      };
+      if (!kState && x.nchunks) put_state(g);
+      for (int64_t c = 0; c < x.nchunks; ++c, ++g) {
+        const int d = g % kDecs;
+        const int64_t ci = kRev ? x.nchunks - 1 - c : c;
+        const int nt = (int)(x.len - ci * kC < kC ? x.len - ci * kC : kC);
+        if (ok) ok = tc::mbar_wait_warp(bar(sm.dec[d]), (g / kDecs) & 1);
+        const float2 lam = make_float2(sm.lam[d], sm.lam[d]);
+        if (ok) ok = tc::mbar_wait_warp(bar(sm.gu), g & 1);
+        tc::fence_after();
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          float r[16];
+          tc::tmem_ld16(tl + kColU + 64 * half + 16 * m, r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) S[8 * m + j] = tc::fma2(lam, S[8 * m + j], make_float2(r[2 * j], r[2 * j + 1]));
+        }
+        tc::fence_before();
+        arrive(sm.ufree);
+        if (kState) continue;
+        // (in one part, the last chunk's S Q^T has left the other columns: its Y was waited for)
+        if (!kSplit && c + 1 < x.nchunks) put_state(g + 1);
+        if (ok) ok = tc::mbar_wait_warp(bar(sm.gy), g & 1);
+        tc::fence_after();
+        if (kSplit && c + 1 < x.nchunks) put_state(g + 1);
+        const int64_t row = (x.t0 + ci * kC + 32 * half) * P.Hv + x.h;
+        uint32_t packed[16];  // pairs of tokens
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          float r[16], y[16];
+          tc::tmem_ld16_nowait(tl + kColO + 32 * half + 16 * m, r);
+          tc::tmem_ld16_nowait(tl + kColO + 64 + 32 * half + 16 * m, y);
+          tc::tmem_wait_ld2(r, y);
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 e = *reinterpret_cast<const float4*>(&sm.eb[d][32 * half + 16 * m + j]);
+            const float2 p = tc::fma2(make_float2(e.x, e.y), make_float2(r[j], r[j + 1]), make_float2(y[j], y[j + 1]));
+            const float2 q = tc::fma2(make_float2(e.z, e.w), make_float2(r[j + 2], r[j + 3]), make_float2(y[j + 2], y[j + 3]));
+            packed[8 * m + j / 2] = pack2(p);
+            packed[8 * m + j / 2 + 1] = pack2(q);
+            y[j] = p.x; y[j + 1] = p.y; y[j + 2] = q.x; y[j + 3] = q.y;
+          }
+          if (a.y32) {
+            float* dst = a.y32 + (row + 16 * m * (int64_t)P.Hv) * kDim + v;
+            const int left = nt - 32 * half - 16 * m;
+#pragma unroll
+            for (int j = 0; j < 16; ++j, dst += (int64_t)P.Hv * kDim)
+              if (j < left) *dst = y[j];
+          }
+        }
+        tc::fence_before();
+        arrive(sm.yfree);
+        if (a.y) {
+          // neighbours exchange, so that each stores two values of a token
+          const int odd = lane & 1;
+          const uint32_t pick = odd ? 0x3276u : 0x5410u;  // (own low, neighbour's low) or (neighbour's high, own high)
+          __nv_bfloat16* dst = a.y + (row + odd * P.Hv) * kDim + (v & ~1);
+          const int64_t step = 2 * (int64_t)P.Hv * kDim;
+          const int left = nt - 32 * half - odd;
+#pragma unroll
+          for (int j = 0; j < 16; ++j, dst += step) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, packed[j], 1);
+            if (2 * j < left) *reinterpret_cast<uint32_t*>(dst) = __byte_perm(packed[j], got, pick);
+          }
+        }
+      }
+      if (!ok) break;
+      if (kState) {
+        float4* dst = reinterpret_cast<float4*>(a.sg.state + ((x.sslot * P.Hv + x.h) * kDim + v) * kDim + 64 * half);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) dst[j] = make_float4(S[2 * j].x, S[2 * j].y, S[2 * j + 1].x, S[2 * j + 1].y);
+      } else if (x.last && a.st.out) {  // (never transposed)
+        if (kRev && x.nchunks) {  // the initial state's adjoint: through the first token's decay
+          const float e = exp2f(decay_log2(decay_g(P, x.t0, x.h)));
+#pragma unroll
+          for (int j = 0; j < 32; ++j) S[j] = tc::mul2(S[j], make_float2(e, e));
+        }
+        if (a.st.bf16) {
+          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.st.out) + at + v * kDim + 64 * half);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dst[j] = make_uint4(pack2(S[4 * j]), pack2(S[4 * j + 1]), pack2(S[4 * j + 2]), pack2(S[4 * j + 3]));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.st.out) + at + v * kDim + 64 * half);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) dst[j] = make_float4(S[2 * j].x, S[2 * j].y, S[2 * j + 1].x, S[2 * j + 1].y);
+        }
+      }
+    }
+    if (!ok && lane == 0) atomicOr(P.status, 1);
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc::fence_after();
+    tc::tmem_dealloc(tbase, 512);
+  }
+}
+
+// Chains the segments of one (sequence, head): in, each segment's own state (from zero) but the last's;
+// out, the state each segment starts from. A CTA takes 1024 of the state's values.
+template <bool kRev>
+__global__ void __launch_bounds__(256) kda_decay_chain_kernel(const __grid_constant__ PassArgs a) {
+  const DecayProblem& P = a.P;
+  const Segments& sg = a.sg;
+  const int64_t n = blockIdx.x / P.Hv;
+  const int h = (int)(blockIdx.x % P.Hv);
+  const DecaySpan sp = decay_span(P, n);
+  const int64_t slot = a.st.slots ? a.st.slots[n] : n;
+  if (slot < 0 || slot >= a.st.num_slots) return;  // the main pass flags it
+  const int at = 1024 * blockIdx.y + 4 * threadIdx.x, row = at / kDim, col = at % kDim;
+  const int64_t from = (slot * P.Hv + h) * kDim * kDim;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.st.in && a.transposed) {
+    const float* src = reinterpret_cast<const float*>(a.st.in) + from + (int64_t)col * kDim + row;
+    x = make_float4(src[0], src[kDim], src[2 * kDim], src[3 * kDim]);
+  } else if (a.st.in && a.st.bf16) {
+    const uint2 r = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(a.st.in) + from + at);
+    const float2 p = unpack2(r.x), q = unpack2(r.y);
+    x = make_float4(p.x, p.y, q.x, q.y);
+  } else if (a.st.in) {
+    x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.st.in) + from + at);
+  }
+  const int64_t base = seg_slot(sg, sp.t0, n);
+  const int64_t m = sp.len > sg.len ? (sp.len + sg.len - 1) / sg.len : 1;
+  auto slot_of = [&](int64_t i) { return (base + (kRev ? m - 1 - i : i)) * P.Hv + h; };
+  constexpr int kAhead = 8;  // loads in flight: none waits for the chain
+  for (int64_t i = 0; i < m; i += kAhead) {
+    float4 u[kAhead];
+    float d[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (i + j + 1 < m) {
+        u[j] = *reinterpret_cast<const float4*>(sg.state + slot_of(i + j) * kDim * kDim + at);
+        d[j] = sg.decay[slot_of(i + j)];
+      }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (i + j >= m) break;
+      *reinterpret_cast<float4*>(sg.state + slot_of(i + j) * kDim * kDim + at) = x;
+      if (i + j + 1 < m) {
+        const float e = exp2f(d[j]);
+        x.x = fmaf(e, x.x, u[j].x); x.y = fmaf(e, x.y, u[j].y);
+        x.z = fmaf(e, x.z, u[j].z); x.w = fmaf(e, x.w, u[j].w);
+      }
+    }
+  }
+}
+
+// Sums of a query/key head's value heads, rounded once.
+__global__ void __launch_bounds__(256) kda_decay_group_sum_kernel(const float* x, __nv_bfloat16* y, int64_t rows, int r) {
+  const int64_t at = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) * 4;
+  if (at >= rows * kDim) return;
+  const int64_t row = at / kDim, d = at % kDim;
+  const float* src = x + row * r * kDim + d;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j = 0; j < r; ++j) {
+    const float4 v = *reinterpret_cast<const float4*>(src + (int64_t)j * kDim);
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  *reinterpret_cast<uint2*>(y + at) = make_uint2(pack2(s.x, s.y), pack2(s.z, s.w));
+}
+
+// What crosses each token, q . dq - k . dk of one value head: a warp a row.
+__global__ void __launch_bounds__(256) kda_decay_cross_kernel(const DecayProblem P, const float* dq, const float* dk, float* z) {
+  const int64_t row = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= P.Ttot * P.Hv) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t tok = row / P.Hv;
+  const int hq = (int)(row - tok * P.Hv) / P.r;
+  const uint2 q = *reinterpret_cast<const uint2*>(P.q + tok * P.qt + hq * P.qh + 4 * lane);
+  const uint2 k = *reinterpret_cast<const uint2*>(P.k + tok * P.kt + hq * P.kh + 4 * lane);
+  const float4 a = *reinterpret_cast<const float4*>(dq + row * kDim + 4 * lane);
+  const float4 b = *reinterpret_cast<const float4*>(dk + row * kDim + 4 * lane);
+  const float2 q0 = unpack2(q.x), q1 = unpack2(q.y), k0 = unpack2(k.x), k1 = unpack2(k.y);
+  float x = q0.x * a.x + q0.y * a.y + q1.x * a.z + q1.y * a.w - (k0.x * b.x + k0.y * b.y + k1.x * b.z + k1.y * b.w);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if (lane == 0) z[row] = x;
+}
+
+// dg of one (sequence, head): a decay scales all that crosses its token, so
+//   dg_t = sum_{i >= t} (q_i . dq_i - k_i . dk_i) + <S_T, dS_T>.
+// The sums cancel over long sequences: FP64. 256 threads, from the end in runs of 1024 tokens.
+__global__ void __launch_bounds__(256) kda_decay_gate_grad_kernel(const DecayProblem P, const float* z, const float* hT,
+                                                                 const float* dhT, __nv_bfloat16* dg) {
+  __shared__ double part[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t n = blockIdx.x / P.Hv;
+  const int h = (int)(blockIdx.x % P.Hv);
+  const DecaySpan sp = decay_span(P, n);
+  auto block_sum = [&](double x) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    __syncthreads();
+    if (lane == 0) part[warp] = x;
+    __syncthreads();
+    double s = 0.0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += part[k];
+    return s;
+  };
+  double acc = 0.0;
+  if (dhT) {
+    const int64_t base = (n * P.Hv + h) * kDim * kDim;
+    float x = 0.f;  // (64 products a thread)
+    for (int j = tid; j < kDim * kDim; j += 256) x = fmaf(hT[base + j], dhT[base + j], x);
+    acc = block_sum((double)x);
+  }
+  for (int64_t end = sp.len; end > 0; end -= 1024) {
+    // this thread's four tokens, the last first
+    const int64_t t = end - 1 - 4 * tid;
+    double s[4], run = 0.0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      run += t - j >= 0 ? (double)z[(sp.t0 + t - j) * P.Hv + h] : 0.0;
+      s[j] = run;
+    }
+    double pre = run;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const double p = __shfl_up_sync(0xffffffffu, pre, d);
+      if (lane >= d) pre += p;
+    }
+    __syncthreads();
+    if (lane == 31) part[warp] = pre;
+    __syncthreads();
+    double before = acc + pre - run, all = 0.0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (k < warp) before += part[k];
+      all += part[k];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (t - j >= 0) dg[(sp.t0 + t - j) * P.Hv + h] = __float2bfloat16_rn((float)(before + s[j]));
+    acc += all;
+  }
+}
+
+// Aimed at when sequences are cut: units, twice the SMs (the grid hands them out as CTAs get free).
+constexpr int64_t kUnits = 2 * 152;
+
+struct SegWs {
+  size_t state, decay, total;
+};
+SegWs carve_segments(int64_t N, int64_t Ttot, int64_t Hv, int64_t seg) {
+  SegWs w{0, 0, 0};
+  if (!seg) return w;
+  const size_t slots = (size_t)(Ttot / seg + N);
+  w.decay = ctx_align_up(sizeof(float) * slots * Hv * kDim * kDim);
+  w.total = ctx_align_up(w.decay + sizeof(float) * slots * Hv);
+  return w;
+}
+
+// After the segments: the final state (for the decays' gradient), FP32 dq and dk of each value head, and
+// what crosses each token and head.
+struct GradWs {
+  size_t hT, dq, dk, z, total;
+};
+GradWs carve_grads(int64_t N, int64_t Ttot, int64_t Hqk, int64_t Hv, bool per_token) {
+  GradWs w{0, 0, 0, 0, 0};
+  size_t at = 0;
+  const size_t rows = (size_t)Ttot * Hv;
+  if (per_token) at = ctx_align_up(sizeof(float) * (size_t)N * Hv * kDim * kDim);
+  w.dq = w.dk = w.z = at;
+  if (per_token || Hqk != Hv) {
+    w.dk = ctx_align_up(w.dq + sizeof(float) * rows * kDim);
+    w.z = ctx_align_up(w.dk + sizeof(float) * rows * kDim);
+    at = w.z;
+  }
+  if (per_token) at = ctx_align_up(w.z + sizeof(float) * rows);
+  w.total = at;
+  return w;
+}
+
+template <bool kRev, bool kState, bool kSplit>
+cudaError_t launch(const Maps& maps, const PassArgs& a, cudaStream_t s) {
+  auto kern = kda_decay_pass_kernel<kRev, kState, kSplit>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)(a.P.N * a.P.Hv * a.sg.most), kThreads, kSmemBytes, s>>>(maps, a);
+  return cudaGetLastError();
+}
+
+struct Role {
+  const __nv_bfloat16* p;
+  int64_t t, h;
+  int heads;
+};
+
+// One pass with the given roles; ws: the segments' workspace.
+template <bool kRev>
+cudaError_t pass(const DecayProblem& P, const Role& q, const Role& k, const Role& v, float s_inter, float s_intra, float s_w,
+                 const DecayStates& st, bool transposed, __nv_bfloat16* y, float* y32, void* ws, cudaStream_t s) {
+  Maps maps{};
+  PassArgs a{};
+  cudaError_t e;
+  if (P.N * P.Hv == 0) return cudaSuccess;
+  if (P.Ttot) {
+    if ((e = token_map(&maps.q, q.p, q.heads, P.Ttot, q.h, q.t, kC)) != cudaSuccess) return e;
+    if ((e = token_map(&maps.k, k.p, k.heads, P.Ttot, k.h, k.t, kC)) != cudaSuccess) return e;
+    if ((e = token_map(&maps.v, v.p, v.heads, P.Ttot, v.h, v.t, kC)) != cudaSuccess) return e;
+  }
+  a.P = P;
+  a.qdiv = P.Hv / q.heads;
+  a.kdiv = P.Hv / k.heads;
+  a.vdiv = P.Hv / v.heads;
+  a.s_inter = s_inter;
+  a.s_intra = s_intra;
+  a.s_w = s_w;
+  a.st = st;
+  a.transposed = transposed;
+  a.y = y;
+  a.y32 = y32;
+  if (P.cu_host && P.N > 1 && P.N <= kOrder) {
+    a.ordered = 1;
+    for (int64_t i = 0; i < P.N; ++i) a.order[i] = (uint16_t)i;
+    std::stable_sort(a.order, a.order + P.N, [&](uint16_t i, uint16_t j) {
+      return P.cu_host[i + 1] - P.cu_host[i] > P.cu_host[j + 1] - P.cu_host[j];
+    });
+  }
+  a.sg.most = 1;
+  if (P.seg) {
+    const SegWs w = carve_segments(P.N, P.Ttot, P.Hv, P.seg);
+    a.sg.len = P.seg;
+    a.sg.most = (int)((P.longest + P.seg - 1) / P.seg);
+    a.sg.state = reinterpret_cast<float*>(ws);
+    a.sg.decay = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + w.decay);
+    if ((e = launch<kRev, true, false>(maps, a, s)) != cudaSuccess) return e;
+    kda_decay_chain_kernel<kRev><<<dim3((unsigned)(P.N * P.Hv), 16), 256, 0, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  return y32 ? launch<kRev, false, true>(maps, a, s) : launch<kRev, false, false>(maps, a, s);
+}
+
+}  // namespace
+
+int64_t decay_segment_tokens(const int64_t* cu, int64_t N, int64_t T, int64_t Hv) {
+  auto chunks_of = [&](int64_t n) { return ((cu ? cu[n + 1] - cu[n] : T) + kC - 1) / kC; };
+  int64_t longest = 0, chunks = 0;
+  for (int64_t n = 0; n < (cu ? N : 1); ++n) {
+    chunks += chunks_of(n);
+    longest = std::max(longest, chunks_of(n));
+  }
+  if (!cu) chunks *= N;
+  // an even share of the chunks for each of kUnits units, 8 chunks at least
+  const int64_t seg = std::max<int64_t>((chunks * Hv + kUnits - 1) / kUnits, 8);
+  // cutting adds a pass over keys and values: only where the longest sequence alone takes well over an SM's share
+  return longest <= 3 * seg ? 0 : seg * kC;
+}
+
+size_t decay_workspace_bytes(int64_t N, int64_t Ttot, int64_t Hqk, int64_t Hv, int64_t seg, bool training) {
+  // (the larger of the two kinds of decay: the size does not depend on which a call uses)
+  return carve_segments(N, Ttot, Hv, seg).total + (training ? carve_grads(N, Ttot, Hqk, Hv, true).total : 0);
+}
+
+cudaError_t launch_decay_forward(const DecayProblem& P, const DecayStates& st, __nv_bfloat16* o, void* ws,
+                                 bool training, cudaStream_t s) {
+  const Role q{P.q, P.qt, P.qh, P.Hqk}, k{P.k, P.kt, P.kh, P.Hqk}, v{P.v, P.vt, P.vh, P.Hv};
+  cudaError_t e = pass<false>(P, q, k, v, P.scale, P.scale, 1.f, st, false, o, nullptr, ws, s);
+  if (e == cudaSuccess && training && P.per_token)
+    e = cudaMemcpyAsync(reinterpret_cast<char*>(ws) + carve_segments(P.N, P.Ttot, P.Hv, P.seg).total, st.out,
+                        sizeof(float) * P.N * P.Hv * kDim * kDim, cudaMemcpyDeviceToDevice, s);
+  return e;
+}
+
+cudaError_t launch_decay_backward(const DecayProblem& P, const float* h0, const DecayGrads& g, void* ws,
+                                  cudaStream_t s) {
+  char* base = reinterpret_cast<char*>(ws) + carve_segments(P.N, P.Ttot, P.Hv, P.seg).total;
+  const GradWs w = carve_grads(P.N, P.Ttot, P.Hqk, P.Hv, P.per_token);
+  // summed over a group's heads, and in the decays' gradient over the whole sequence (differences of large numbers):
+  // dq and dk stay FP32 until then
+  const bool f32 = g.dg || P.r > 1;
+  float* dq = f32 ? reinterpret_cast<float*>(base + w.dq) : nullptr;
+  float* dk = f32 ? reinterpret_cast<float*>(base + w.dk) : nullptr;
+  const Role q{P.q, P.qt, P.qh, P.Hqk}, k{P.k, P.kt, P.kh, P.Hqk}, v{P.v, P.vt, P.vh, P.Hv};
+  const Role d{g.d_o, (int64_t)P.Hv * kDim, kDim, P.Hv};
+  const float c = P.scale;
+  cudaError_t e;
+  const DecayStates none{g.d_hT, nullptr, 0, nullptr, P.N};
+  if ((e = pass<false>(P, d, v, k, c, c, 1.f, DecayStates{h0, nullptr, 0, nullptr, P.N}, true, f32 ? nullptr : g.dq, dq,
+                       ws, s)) != cudaSuccess) return e;
+  if ((e = pass<true>(P, v, d, q, 1.f, c, c, none, true, f32 ? nullptr : g.dk, dk, ws, s)) != cudaSuccess)
+    return e;
+  if ((e = pass<true>(P, k, q, d, 1.f, c, c, DecayStates{g.d_hT, g.dh0, 0, nullptr, P.N}, false, g.dv, nullptr, ws,
+                      s)) != cudaSuccess) return e;
+  if (P.Ttot == 0 || !f32) return cudaSuccess;
+  if (g.dg) {
+    float* z = reinterpret_cast<float*>(base + w.z);
+    kda_decay_cross_kernel<<<(unsigned)((P.Ttot * P.Hv + 7) / 8), 256, 0, s>>>(P, dq, dk, z);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    kda_decay_gate_grad_kernel<<<(unsigned)(P.N * P.Hv), 256, 0, s>>>(P, z, reinterpret_cast<const float*>(base), g.d_hT, g.dg);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  const int64_t rows = P.Ttot * P.Hqk;
+  const unsigned grid = (unsigned)((rows * kDim / 4 + 255) / 256);
+  kda_decay_group_sum_kernel<<<grid, 256, 0, s>>>(dq, g.dq, rows, P.r);
+  kda_decay_group_sum_kernel<<<grid, 256, 0, s>>>(dk, g.dk, rows, P.r);
+  return cudaGetLastError();
+}
+
+}  // namespace kda
