@@ -75,7 +75,7 @@ struct Smem {
   int ring[kRing];       // units to come, -1: none
   // full, empty: a stage's tiles are there / read by all products; dec: a chunk's decays; g0, gu, gy: products done
   // (scores, U, Y); aready: K~ and P are there; ufree, yfree: U, Y are read; sready: the state is there
-  unsigned long long full[kStages], empty[kStages], dec[kDecs], g0[2], gu, gy, aready[2], ufree, sready, yfree;
+  unsigned long long full[kStages], empty[kStages], dec[kDecs], g0[2], gu, gy, aready[2], ufree, sready[2], yfree;
   unsigned long long clcbar, rfull[kRing], rempty[kRing];
   uint32_t tmem;
 };
@@ -177,11 +177,14 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) { tc::mbar_init(bar(sm.full[i]), 1); tc::mbar_init(bar(sm.empty[i]), 1); }
     for (int i = 0; i < kDecs; ++i) tc::mbar_init(bar(sm.dec[i]), 1);
-    for (int i = 0; i < 2; ++i) { tc::mbar_init(bar(sm.g0[i]), 1); tc::mbar_init(bar(sm.aready[i]), kGroup); }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bar(sm.g0[i]), 1);
+      tc::mbar_init(bar(sm.aready[i]), kGroup);
+      tc::mbar_init(bar(sm.sready[i]), kGroup);
+    }
     tc::mbar_init(bar(sm.gu), 1);
     tc::mbar_init(bar(sm.gy), 1);
     tc::mbar_init(bar(sm.ufree), kGroup);
-    tc::mbar_init(bar(sm.sready), kGroup);
     tc::mbar_init(bar(sm.yfree), kGroup);
     tc::mbar_init(bar(sm.clcbar), 1);
     for (int i = 0; i < kRing; ++i) { tc::mbar_init(bar(sm.rfull[i]), 1); tc::mbar_init(bar(sm.rempty[i]), 2 + 2 * kGroup); }
@@ -195,7 +198,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
   // The ring of units, as a consumer (a warp): its place, and the next unit or -1.
   uint32_t ur = 0;
   auto next_unit = [&]() -> int {
-    if (ok) ok = tc::mbar_wait_warp(bar(sm.rfull[ur % kRing]), (ur / kRing) & 1);
+    if (ok) ok = tc::mbar_wait_lanes(bar(sm.rfull[ur % kRing]), (ur / kRing) & 1);
     const int u = ok ? sm.ring[ur % kRing] : -1;
     __syncwarp();
     if (ok && lane == 0) tc::mbar_arrive(bar(sm.rempty[ur % kRing]));
@@ -225,7 +228,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           __syncwarp();
           pending = true;
         }
-        if (ur >= kRing && ok) ok = tc::mbar_wait_warp(bar(sm.rempty[ur % kRing]), (ur / kRing - 1) & 1);
+        if (ur >= kRing && ok) ok = tc::mbar_wait_lanes(bar(sm.rempty[ur % kRing]), (ur / kRing - 1) & 1);
         if (lane == 0) {
           sm.ring[ur % kRing] = ok ? u : -1;
           tc::mbar_arrive(bar(sm.rfull[ur % kRing]));
@@ -236,7 +239,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         const Unit x = unit_of<kRev, kState>(a, u);
         for (int64_t c = 0; c < x.nchunks && ok; ++c, ++g) {
           const int s = g % kStages;
-          if (g >= kStages) ok = tc::mbar_wait_warp(bar(sm.empty[s]), (g / kStages - 1) & 1);
+          if (g >= kStages) ok = tc::mbar_wait_lanes(bar(sm.empty[s]), (g / kStages - 1) & 1);
           if (ok && lane == 0) {
             const int t = (int)(x.t0 + (kRev ? x.nchunks - 1 - c : c) * kC);
             tc::mbar_arrive_expect_tx(bar(sm.full[s]), (kState ? 2 : 3) * kTile);
@@ -251,7 +254,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           __syncwarp();
           if (!ok) break;
         }
-        const bool came = tc::mbar_wait_warp(bar(sm.clcbar), asked & 1);
+        const bool came = tc::mbar_wait_lanes(bar(sm.clcbar), asked & 1);
         ++asked;
         pending = false;
         ok = ok && came;
@@ -270,9 +273,9 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
       if (!ok) {
         // flag it, and let this CTA's copies (and the response) land before its memory is given back
         if (lane == 0) atomicOr(P.status, 1);
-        if (pending) tc::mbar_wait_warp(bar(sm.clcbar), asked & 1);
+        if (pending) tc::mbar_wait_lanes(bar(sm.clcbar), asked & 1);
         for (uint32_t k = g > kStages ? g - kStages : 0; k < g; ++k)
-          tc::mbar_wait_warp(bar(sm.full[k % kStages]), (k / kStages) & 1);
+          tc::mbar_wait_lanes(bar(sm.full[k % kStages]), (k / kStages) & 1);
       }
     } else if (warp == kWarpMma) {
       // ================= products
@@ -292,7 +295,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         __syncwarp();
       };
       auto tiles = [&](uint32_t k) {
-        if (ok) ok = tc::mbar_wait_warp(bar(sm.full[k % kStages]), (k / kStages) & 1);
+        if (ok) ok = tc::mbar_wait_lanes(bar(sm.full[k % kStages]), (k / kStages) & 1);
         tc::fence_after();
       };
       for (int u; (u = next_unit()) >= 0;) {
@@ -311,8 +314,8 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
             scores(g + 1);
           }
           // U, once K~ is there and the last U is read
-          if (ok) ok = tc::mbar_wait_warp(bar(sm.aready[g & 1]), (g >> 1) & 1);
-          if (ok && g > 0) ok = tc::mbar_wait_warp(bar(sm.ufree), (g - 1) & 1);
+          if (ok) ok = tc::mbar_wait_lanes(bar(sm.aready[g & 1]), (g >> 1) & 1);
+          if (ok && g > 0) ok = tc::mbar_wait_lanes(bar(sm.ufree), (g - 1) & 1);
           tc::fence_after();
           if (ok && tc::elect_one()) {
             const uint64_t dh = tc::mnmajor(tc::smem_u32(sm.tile[s][1]), kPanel);
@@ -329,8 +332,8 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           __syncwarp();
           if (kState) continue;
           // Y, once the state is there and the last Y is read
-          if (ok) ok = tc::mbar_wait_warp(bar(sm.sready), g & 1);
-          if (ok && g > 0) ok = tc::mbar_wait_warp(bar(sm.yfree), (g - 1) & 1);
+          if (ok) ok = tc::mbar_wait_lanes(bar(sm.sready[g & 1]), (g >> 1) & 1);
+          if (ok && g > 0) ok = tc::mbar_wait_lanes(bar(sm.yfree), (g - 1) & 1);
           tc::fence_after();
           if (ok && tc::elect_one()) {
             const uint64_t dq = tc::kmajor(tc::smem_u32(sm.tile[s][0]));
@@ -386,7 +389,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           const float2 up = make_float2(exp2f(p0), exp2f(pre)), down = make_float2(exp2f(s1 + g1), exp2f(s1));
           const float2 e = kRev ? down : up, w = kRev ? up : down;
           // the slot was last read for chunk g - 4: its Y was read before chunk g - 3's products began
-          if (ok && g >= kStages) ok = tc::mbar_wait_warp(bar(sm.empty[g % kStages]), (g / kStages - 1) & 1);
+          if (ok && g >= kStages) ok = tc::mbar_wait_lanes(bar(sm.empty[g % kStages]), (g / kStages - 1) & 1);
           const int d = g % kDecs;
           *reinterpret_cast<float2*>(&sm.b[d][2 * lane]) = make_float2(p0, pre);
           *reinterpret_cast<float2*>(&sm.eb[d][2 * lane]) = make_float2(a.s_inter * e.x, a.s_inter * e.y);
@@ -414,17 +417,15 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         const int nt = (int)(left < kC ? left : kC);
         unsigned char* Ks = sm.tile[s][1];
         unsigned char* Ls = sm.lo[g & 1];
-        if (ok) ok = tc::mbar_wait_warp(bar(sm.dec[d]), (g / kDecs) & 1);
-        if (ok) ok = tc::mbar_wait_warp(bar(sm.full[s]), (g / kStages) & 1);
+        if (ok) ok = tc::mbar_wait_lanes(bar(sm.dec[d]), (g / kDecs) & 1);
+        if (ok) ok = tc::mbar_wait_lanes(bar(sm.full[s]), (g / kStages) & 1);
         // K is free once the scores are done; they follow chunk g - 2's products, which read lo and P of this parity
         if (!kState) {
-          if (ok) ok = tc::mbar_wait_warp(bar(sm.g0[g & 1]), (g >> 1) & 1);
+          if (ok) ok = tc::mbar_wait_lanes(bar(sm.g0[g & 1]), (g >> 1) & 1);
         } else if (g >= 2) {
-          if (ok) ok = tc::mbar_wait_warp(bar(sm.empty[(g - 2) % kStages]), ((g - 2) / kStages) & 1);
+          if (ok) ok = tc::mbar_wait_lanes(bar(sm.empty[(g - 2) % kStages]), ((g - 2) / kStages) & 1);
         }
         tc::fence_after();
-        float p[16];
-        if (!kState) tc::tmem_ld16x256(tl + kColP + 64 * (g & 1) + 32 * half, p);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {  // 16-byte chunks i
           const int i = at + 32 * kGroup * m, row = (i >> 3) & (kC - 1);
@@ -449,6 +450,8 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           const int i0 = 16 * wq + (lane >> 2), j0 = 32 * half + 2 * (lane & 3);
           const float b0 = sm.b[d][i0], b1 = sm.b[d][i0 + 8];
           unsigned char* Pt = sm.P[g & 1][0];
+          float p[16];  // (nothing between the load and its wait, where a register could be moved too early)
+          tc::tmem_ld16x256(tl + kColP + 64 * (g & 1) + 32 * half, p);
           tc::tmem_wait_ld(p);
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
@@ -540,16 +543,16 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         }
         tc::tmem_wait_st();
         tc::fence_before();
-        arrive(sm.sready);
+        arrive(sm.sready[k & 1]);
       };
       if (!kState && x.nchunks) put_state(g);
       for (int64_t c = 0; c < x.nchunks; ++c, ++g) {
         const int d = g % kDecs;
         const int64_t ci = kRev ? x.nchunks - 1 - c : c;
         const int nt = (int)(x.len - ci * kC < kC ? x.len - ci * kC : kC);
-        if (ok) ok = tc::mbar_wait_warp(bar(sm.dec[d]), (g / kDecs) & 1);
+        if (ok) ok = tc::mbar_wait_lanes(bar(sm.dec[d]), (g / kDecs) & 1);
         const float2 lam = make_float2(sm.lam[d], sm.lam[d]);
-        if (ok) ok = tc::mbar_wait_warp(bar(sm.gu), g & 1);
+        if (ok) ok = tc::mbar_wait_lanes(bar(sm.gu), g & 1);
         tc::fence_after();
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
@@ -563,7 +566,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         if (kState) continue;
         // (in one part, the last chunk's S Q^T has left the other columns: its Y was waited for)
         if (!kSplit && c + 1 < x.nchunks) put_state(g + 1);
-        if (ok) ok = tc::mbar_wait_warp(bar(sm.gy), g & 1);
+        if (ok) ok = tc::mbar_wait_lanes(bar(sm.gy), g & 1);
         tc::fence_after();
         if (kSplit && c + 1 < x.nchunks) put_state(g + 1);
         const int64_t row = (x.t0 + ci * kC + 32 * half) * P.Hv + x.h;
