@@ -28,6 +28,7 @@
 //   warp 1   products (tcgen05.mma kind::f16, BF16 operands, FP32 accumulators in tensor memory)
 //   warp 2   decays of each chunk: sums from both ends, so that the exponents that matter most in
 //            each, the small ones, are sums of few terms
+//   warp 3   the next unit's initial state, on its way to L2
 //   warps 4-11   K~ (over K and beside) and P
 //   warps 12-19  the state, 64 of a row's 128 values a thread in registers, S = e^{b_C} S + U with U = V^T K~
 //            from tensor memory, and as A operand back there; Y
@@ -63,6 +64,16 @@ constexpr uint32_t kColS = 128;            // the state as A operand, 64 + 64: i
 constexpr uint32_t kColO = 256;            // S Q^T, then V^T P^T: 64 + 64
 constexpr uint32_t kColP = 384;            // scores (M = 64) of two chunks: 64 + 64
 
+// One unit of work.
+struct Unit {
+  int64_t n, t0, len, nchunks, end;  // sequence, first token, tokens and chunks of the unit; the sequence's end
+  int64_t slot, sslot;               // of its state, and of its segment's
+  int h;
+  bool run;   // there is something to do
+  bool last;  // the last segment in time order of the pass
+  bool none;  // no unit: the end
+};
+
 struct Smem {
   unsigned char tile[kStages][3][kTile];  // Q, K, V
   unsigned char lo[2][kTile];             // low parts of K~
@@ -72,7 +83,7 @@ struct Smem {
   float w[kDecs][kC];    // factor of k_j in K~
   float lam[kDecs];      // e^{b_C}
   uint4 clc;             // response: the next unit
-  int ring[kRing];       // units to come, -1: none
+  Unit ring[kRing];      // units to come
   // full, empty: a stage's tiles are there / read by all products; dec: a chunk's decays; g0, gu, gy: products done
   // (scores, U, Y); aready: K~ and P are there; ufree, yfree: U, Y are read; sready: the state is there
   unsigned long long full[kStages], empty[kStages], dec[kDecs], g0[2], gu, gy, aready[2], ufree, sready[2], yfree;
@@ -124,22 +135,14 @@ __device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
   lo = pack2(tc::sub2(x, unpack2(hi)));
 }
 
-// One unit of work.
-struct Unit {
-  int h;
-  int64_t n, seg, t0, len, nchunks, end;  // end: the sequence's
-  int64_t slot, sslot;
-  bool run;   // there is something to do
-  bool last;  // the last segment in time order of the pass
-};
 template <bool kRev, bool kState>
 __device__ __forceinline__ Unit unit_of(const PassArgs& a, int u) {
   const DecayProblem& P = a.P;
   Unit x;
   const int64_t p = u / P.Hv;
   x.h = u - (int)(p * P.Hv);
-  x.seg = p / P.N;
-  x.n = p - x.seg * P.N;
+  const int64_t seg = p / P.N;
+  x.n = p - seg * P.N;
   if (a.ordered) x.n = a.order[x.n];
   const DecaySpan sp = decay_span(P, x.n);
   x.t0 = sp.t0;
@@ -150,15 +153,16 @@ __device__ __forceinline__ Unit unit_of(const PassArgs& a, int u) {
   x.last = true;
   x.run = x.slot >= 0 && x.slot < a.st.num_slots;
   if (a.sg.len) {
-    const int64_t from = x.seg * a.sg.len;
-    x.sslot = seg_slot(a.sg, sp.t0, x.n) + x.seg;
+    const int64_t from = seg * a.sg.len;
+    x.sslot = seg_slot(a.sg, sp.t0, x.n) + seg;
     const bool tail = from + a.sg.len >= sp.len;
-    x.last = kRev ? x.seg == 0 : tail;
-    if ((x.seg > 0 && from >= sp.len) || (kState && x.last)) x.run = false;
+    x.last = kRev ? seg == 0 : tail;
+    if ((seg > 0 && from >= sp.len) || (kState && x.last)) x.run = false;
     x.t0 += from;
     x.len = tail ? sp.len - from : a.sg.len;
   }
   x.nchunks = x.run ? (x.len + kC - 1) / kC : 0;
+  x.none = false;
   return x;
 }
 
@@ -187,7 +191,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
     tc::mbar_init(bar(sm.ufree), kGroup);
     tc::mbar_init(bar(sm.yfree), kGroup);
     tc::mbar_init(bar(sm.clcbar), 1);
-    for (int i = 0; i < kRing; ++i) { tc::mbar_init(bar(sm.rfull[i]), 1); tc::mbar_init(bar(sm.rempty[i]), 2 + 2 * kGroup); }
+    for (int i = 0; i < kRing; ++i) { tc::mbar_init(bar(sm.rfull[i]), 1); tc::mbar_init(bar(sm.rempty[i]), 3 + 2 * kGroup); }
   }
   tc::fence_before();
   __syncthreads();
@@ -195,15 +199,16 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
   const uint32_t tbase = sm.tmem;
   bool ok = true;  // false: a wait gave up; the warp touches only its own CTA's memory and leaves
 
-  // The ring of units, as a consumer (a warp): its place, and the next unit or -1.
+  // The ring of units, as a consumer (a warp): its place, and the next unit (false: none).
   uint32_t ur = 0;
-  auto next_unit = [&]() -> int {
+  auto next_unit = [&](Unit& x) {
     if (ok) ok = tc::mbar_wait_lanes(bar(sm.rfull[ur % kRing]), (ur / kRing) & 1);
-    const int u = ok ? sm.ring[ur % kRing] : -1;
+    if (!ok) return false;
+    x = sm.ring[ur % kRing];
     __syncwarp();
-    if (ok && lane == 0) tc::mbar_arrive(bar(sm.rempty[ur % kRing]));
+    if (lane == 0) tc::mbar_arrive(bar(sm.rempty[ur % kRing]));
     ++ur;
-    return u;
+    return !x.none;
   };
   auto arrive = [&](unsigned long long& b) {
     __syncwarp();
@@ -216,31 +221,53 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
       // ================= units and copies
       uint32_t g = 0;  // chunks so far
       uint32_t asked = 0;
-      bool pending = false;
-      for (int u = blockIdx.x;;) {
-        // the next unit is asked for before this one's copies
-        if (ok && u >= 0) {
-          if (lane == 0) {
-            tc::mbar_arrive_expect_tx(bar(sm.clcbar), 16);
-            asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
-                         ::"r"(tc::smem_u32(&sm.clc)), "r"(bar(sm.clcbar)) : "memory");
-          }
-          __syncwarp();
-          pending = true;
-        }
-        if (ur >= kRing && ok) ok = tc::mbar_wait_lanes(bar(sm.rempty[ur % kRing]), (ur / kRing - 1) & 1);
-        if (lane == 0) {
-          sm.ring[ur % kRing] = ok ? u : -1;
+      auto push = [&](const Unit& x) {
+        if (ok && ur >= kRing) ok = tc::mbar_wait_lanes(bar(sm.rempty[ur % kRing]), (ur / kRing - 1) & 1);
+        if (ok && lane == 0) {
+          sm.ring[ur % kRing] = x;
           tc::mbar_arrive(bar(sm.rfull[ur % kRing]));
         }
         __syncwarp();
         ++ur;
-        if (!ok || u < 0) break;
-        const Unit x = unit_of<kRev, kState>(a, u);
-        for (int64_t c = 0; c < x.nchunks && ok; ++c, ++g) {
+      };
+      auto ask = [&] {  // for the next unit
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(bar(sm.clcbar), 16);
+          asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                       ::"r"(tc::smem_u32(&sm.clc)), "r"(bar(sm.clcbar)) : "memory");
+        }
+        __syncwarp();
+      };
+      Unit x = unit_of<kRev, kState>(a, (int)blockIdx.x), next;
+      push(x);
+      ask();
+      for (;;) {
+        next.none = true;
+        for (int64_t c = 0;; ++c) {
+          if (c == (x.nchunks < kStages ? x.nchunks : kStages)) {
+            // the next unit, told to everybody while this one's first chunks are under way
+            const bool came = tc::mbar_wait_lanes(bar(sm.clcbar), asked & 1);
+            ++asked;
+            ok = ok && came;
+            uint32_t more = 0, nx = 0;
+            if (came) {
+              asm volatile(
+                  "{\n .reg .b128 r;\n .reg .pred p;\n ld.shared.b128 r, [%2];\n"
+                  " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+                  " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}\n"
+                  : "=r"(more), "=r"(nx) : "r"(tc::smem_u32(&sm.clc)) : "memory");
+              tc::fence_async_smem();  // read before the next response is written
+            }
+            __syncwarp();
+            if (more) next = unit_of<kRev, kState>(a, (int)nx);
+            push(next);
+            if (ok && more) ask();
+          }
+          if (!ok || c == x.nchunks) break;
           const int s = g % kStages;
           if (g >= kStages) ok = tc::mbar_wait_lanes(bar(sm.empty[s]), (g / kStages - 1) & 1);
-          if (ok && lane == 0) {
+          if (!ok) break;
+          if (lane == 0) {
             const int t = (int)(x.t0 + (kRev ? x.nchunks - 1 - c : c) * kC);
             tc::mbar_arrive_expect_tx(bar(sm.full[s]), (kState ? 2 : 3) * kTile);
 #pragma unroll
@@ -252,35 +279,22 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
             }
           }
           __syncwarp();
-          if (!ok) break;
+          ++g;
         }
-        const bool came = tc::mbar_wait_lanes(bar(sm.clcbar), asked & 1);
-        ++asked;
-        pending = false;
-        ok = ok && came;
-        uint32_t more = 0, nx = 0;
-        if (came) {
-          asm volatile(
-              "{\n .reg .b128 r;\n .reg .pred p;\n ld.shared.b128 r, [%2];\n"
-              " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
-              " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}\n"
-              : "=r"(more), "=r"(nx) : "r"(tc::smem_u32(&sm.clc)) : "memory");
-          tc::fence_async_smem();  // read before the next response is written
-        }
-        __syncwarp();
-        u = more ? (int)nx : -1;
+        if (!ok || next.none) break;
+        x = next;
       }
       if (!ok) {
-        // flag it, and let this CTA's copies (and the response) land before its memory is given back
+        // flag it, and let this CTA's copies (and a response) land before its memory is given back
         if (lane == 0) atomicOr(P.status, 1);
-        if (pending) tc::mbar_wait_lanes(bar(sm.clcbar), asked & 1);
+        tc::mbar_wait_lanes(bar(sm.clcbar), asked & 1, 1ll << 22);
         for (uint32_t k = g > kStages ? g - kStages : 0; k < g; ++k)
           tc::mbar_wait_lanes(bar(sm.full[k % kStages]), (k / kStages) & 1);
       }
     } else if (warp == kWarpMma) {
       // ================= products
       uint32_t g = 0;
-      // scores of the chunk numbered k, if its tiles are there (wait: wait for them)
+      // the scores of chunk k
       auto scores = [&](uint32_t k) {
         if (ok && tc::elect_one()) {
           const uint64_t dq = tc::kmajor(tc::smem_u32(sm.tile[k % kStages][0]));
@@ -298,70 +312,77 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         if (ok) ok = tc::mbar_wait_lanes(bar(sm.full[k % kStages]), (k / kStages) & 1);
         tc::fence_after();
       };
-      for (int u; (u = next_unit()) >= 0;) {
-        const Unit x = unit_of<kRev, kState>(a, u);
-        if (!kState && x.nchunks) {
-          tiles(g);
-          scores(g);
+      int64_t left = 0;  // chunks of this unit from g on; any unit's are alike here
+      auto any = [&] {   // is there a chunk g?
+        Unit x;
+        while (left == 0) {
+          if (!next_unit(x)) return false;
+          left = x.nchunks;
         }
-        for (int64_t c = 0; c < x.nchunks; ++c, ++g) {
-          const int s = g % kStages;
-          const uint64_t dv = tc::mnmajor(tc::smem_u32(sm.tile[s][2]), kPanel);
-          if (kState) {
-            tiles(g);
-          } else if (c + 1 < x.nchunks) {  // the next chunk's scores (its buffer was read before the last aready)
-            tiles(g + 1);
-            scores(g + 1);
-          }
-          // U, once K~ is there and the last U is read
-          if (ok) ok = tc::mbar_wait_lanes(bar(sm.aready[g & 1]), (g >> 1) & 1);
-          if (ok && g > 0) ok = tc::mbar_wait_lanes(bar(sm.ufree), (g - 1) & 1);
-          tc::fence_after();
-          if (ok && tc::elect_one()) {
-            const uint64_t dh = tc::mnmajor(tc::smem_u32(sm.tile[s][1]), kPanel);
-            const uint64_t dl = tc::mnmajor(tc::smem_u32(sm.lo[g & 1]), kPanel);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc::mma_bf16_ss(tbase + kColU, dv + 128 * k, dh + 128 * k, tc::idesc_bf16(128, 128, true, true), k > 0);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc::mma_bf16_ss(tbase + kColU, dv + 128 * k, dl + 128 * k, tc::idesc_bf16(128, 128, true, true), 1);
-            tc::mma_commit(bar(sm.gu));
-            if (kState) tc::mma_commit(bar(sm.empty[s]));
-          }
-          __syncwarp();
-          if (kState) continue;
-          // Y, once the state is there and the last Y is read
-          if (ok) ok = tc::mbar_wait_lanes(bar(sm.sready[g & 1]), (g >> 1) & 1);
-          if (ok && g > 0) ok = tc::mbar_wait_lanes(bar(sm.yfree), (g - 1) & 1);
-          tc::fence_after();
-          if (ok && tc::elect_one()) {
-            const uint64_t dq = tc::kmajor(tc::smem_u32(sm.tile[s][0]));
-            const uint64_t dp = tc::kmajor(tc::smem_u32(sm.P[g & 1][0])), dr = tc::kmajor(tc::smem_u32(sm.P[g & 1][1]));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t off = (i >> 2) * (kPanel >> 4) + (i & 3) * 2;
-              tc::mma_bf16_ts(tbase + kColO, tbase + kColS + (kSplit ? 0 : 64 * (g & 1)) + 8 * i, dq + off,
-                              tc::idesc_bf16(128, 64, false, false), i > 0);
-              if (kSplit)
-                tc::mma_bf16_ts(tbase + kColO, tbase + kColS + 64 + 8 * i, dq + off, tc::idesc_bf16(128, 64, false, false), 1);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              tc::mma_bf16_ss(tbase + kColO + 64, dv + 128 * k, dp + 2 * k, tc::idesc_bf16(128, 64, true, false), k > 0);
-              tc::mma_bf16_ss(tbase + kColO + 64, dv + 128 * k, dr + 2 * k, tc::idesc_bf16(128, 64, true, false), 1);
-            }
-            tc::mma_commit(bar(sm.gy));
-            tc::mma_commit(bar(sm.empty[s]));
-          }
-          __syncwarp();
+        return true;
+      };
+      bool more = any();
+      if (!kState && more) {
+        tiles(0);
+        scores(0);
+      }
+      for (; more; ++g) {
+        const int s = g % kStages;
+        const uint64_t dv = tc::mnmajor(tc::smem_u32(sm.tile[s][2]), kPanel);
+        if (kState) tiles(g);
+        --left;
+        more = any();
+        if (!kState && more) {  // the next chunk's scores (its buffer was read before the last aready)
+          tiles(g + 1);
+          scores(g + 1);
         }
+        // U, once K~ is there and the last U is read
+        if (ok) ok = tc::mbar_wait_lanes(bar(sm.aready[g & 1]), (g >> 1) & 1);
+        if (ok && g > 0) ok = tc::mbar_wait_lanes(bar(sm.ufree), (g - 1) & 1);
+        tc::fence_after();
+        if (ok && tc::elect_one()) {
+          const uint64_t dh = tc::mnmajor(tc::smem_u32(sm.tile[s][1]), kPanel);
+          const uint64_t dl = tc::mnmajor(tc::smem_u32(sm.lo[g & 1]), kPanel);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc::mma_bf16_ss(tbase + kColU, dv + 128 * k, dh + 128 * k, tc::idesc_bf16(128, 128, true, true), k > 0);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc::mma_bf16_ss(tbase + kColU, dv + 128 * k, dl + 128 * k, tc::idesc_bf16(128, 128, true, true), 1);
+          tc::mma_commit(bar(sm.gu));
+          if (kState) tc::mma_commit(bar(sm.empty[s]));
+        }
+        __syncwarp();
+        if (kState) continue;
+        // Y, once the state is there and the last Y is read
+        if (ok) ok = tc::mbar_wait_lanes(bar(sm.sready[g & 1]), (g >> 1) & 1);
+        if (ok && g > 0) ok = tc::mbar_wait_lanes(bar(sm.yfree), (g - 1) & 1);
+        tc::fence_after();
+        if (ok && tc::elect_one()) {
+          const uint64_t dq = tc::kmajor(tc::smem_u32(sm.tile[s][0]));
+          const uint64_t dp = tc::kmajor(tc::smem_u32(sm.P[g & 1][0])), dr = tc::kmajor(tc::smem_u32(sm.P[g & 1][1]));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t off = (i >> 2) * (kPanel >> 4) + (i & 3) * 2;
+            tc::mma_bf16_ts(tbase + kColO, tbase + kColS + (kSplit ? 0 : 64 * (g & 1)) + 8 * i, dq + off,
+                            tc::idesc_bf16(128, 64, false, false), i > 0);
+            if (kSplit)
+              tc::mma_bf16_ts(tbase + kColO, tbase + kColS + 64 + 8 * i, dq + off, tc::idesc_bf16(128, 64, false, false), 1);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            tc::mma_bf16_ss(tbase + kColO + 64, dv + 128 * k, dp + 2 * k, tc::idesc_bf16(128, 64, true, false), k > 0);
+            tc::mma_bf16_ss(tbase + kColO + 64, dv + 128 * k, dr + 2 * k, tc::idesc_bf16(128, 64, true, false), 1);
+          }
+          tc::mma_commit(bar(sm.gy));
+          tc::mma_commit(bar(sm.empty[s]));
+        }
+        __syncwarp();
       }
     } else if (warp == kWarpDecay) {
       // ================= decays, two tokens a lane
       uint32_t g = 0;
-      for (int u; (u = next_unit()) >= 0;) {
-        const Unit x = unit_of<kRev, kState>(a, u);
+      for (Unit x; next_unit(x);) {
         float total = 0.f, n0 = 0.f, n1 = 0.f;
         auto fetch = [&](int64_t c) {
           const int64_t j = (kRev ? x.nchunks - 1 - c : c) * kC + 2 * lane;
@@ -401,6 +422,15 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         }
         if (kState && x.run && lane == 31) a.sg.decay[x.sslot * P.Hv + x.h] = total;
       }
+    } else {
+      // ================= the next unit's initial state, on its way to L2
+      for (Unit x; next_unit(x);) {
+        if (kState || !x.run || (!a.sg.len && !a.st.in)) continue;
+        const char* src = a.sg.len ? reinterpret_cast<const char*>(a.sg.state + (x.sslot * P.Hv + x.h) * kDim * kDim)
+                                   : reinterpret_cast<const char*>(a.st.in) + (x.slot * P.Hv + x.h) * kDim * kDim * (a.st.bf16 ? 2 : 4);
+        const int lines = kDim * kDim * (!a.sg.len && a.st.bf16 ? 2 : 4) / 128;
+        for (int i = lane; i < lines; i += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 128 * i));
+      }
     }
   } else if (warp < kWarpB) {
     // ================= K~ and P
@@ -409,8 +439,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
     const uint32_t tl = tbase + ((uint32_t)(32 * wq) << 16);
     const float2 scale = make_float2(a.s_intra, a.s_intra);
     uint32_t g = 0;
-    for (int u; (u = next_unit()) >= 0;) {
-      const Unit x = unit_of<kRev, kState>(a, u);
+    for (Unit x; next_unit(x);) {
       for (int64_t c = 0; c < x.nchunks; ++c, ++g) {
         const int s = g % kStages, d = g % kDecs;
         const int64_t left = x.len - (kRev ? x.nchunks - 1 - c : c) * kC;
@@ -487,8 +516,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
     const int v = 32 * wq + lane;  // state row of this thread, its columns 64 half .. + 63; value of Y, tokens 32 half .. + 31
     const uint32_t tl = tbase + ((uint32_t)(32 * wq) << 16);
     uint32_t g = 0;
-    for (int u; (u = next_unit()) >= 0;) {
-      const Unit x = unit_of<kRev, kState>(a, u);
+    for (Unit x; next_unit(x);) {
       if (!x.run) {
         // a device slot index outside the pool (it no longer matches the host mirror the call was checked
         // against, as in a replayed graph): flagged, and the pool is not touched
