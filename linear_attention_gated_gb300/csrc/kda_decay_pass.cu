@@ -25,15 +25,18 @@
 //   warp 0   copies: Q, K, V tiles by tiled copies (128-byte swizzle), three stages; the next unit's
 //            number (cluster launch control: the grid has a CTA for each unit and a running CTA takes
 //            over the next one that has not started)
-//   warp 1   products (tcgen05.mma kind::f16, BF16 operands, FP32 accumulators in tensor memory)
+//   warps 1, 3   products (tcgen05.mma kind::f16, BF16 operands, FP32 accumulators in tensor memory): scores and U;
+//            S Q^T and V^T P^T. Starting a product takes as long as the tensor core is busy with the ones
+//            before, so two warps start them: while one waits for an operand, the other's products run
 //   warp 2   decays of each chunk: sums from both ends, so that the exponents that matter most in
 //            each, the small ones, are sums of few terms
-//   warp 3   the next unit's initial state, on its way to L2
 //   warps 4-11   K~ (over K and beside) and P
 //   warps 12-19  the state, 64 of a row's 128 values a thread in registers, S = e^{b_C} S + U with U = V^T K~
 //            from tensor memory, and as A operand back there; Y
-// K~, P and S are operands in two BF16 parts, hi + lo: 16 mantissa bits. The carried state then keeps FP32-level
-// accuracy, and Y is off by little more than its own rounding also where heads or long sums cancel.
+// K~ is an operand in two BF16 parts, hi + lo, 16 mantissa bits: the carried state keeps FP32-level accuracy.
+// P and S, which feed Y alone, are rounded to BF16 once (as Y itself is) where Y is an output; where Y is FP32 and
+// summed further, over heads or, for the decays' gradient, over the sequence, so that errors of its terms would
+// outlive a cancelling sum, they too are in two parts (kSplit).
 // A unit is one (sequence, head), longest sequences first, or one segment of it.
 //
 // Long axis, few units: each sequence is cut into segments. A first pass runs the state part alone
@@ -51,7 +54,7 @@ namespace {
 
 constexpr int kC = kDecayChunk;
 constexpr int kStages = 3, kDecs = 4, kRing = 4;
-constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpDecay = 2, kWarpA = 4, kWarpB = 12;
+constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpDecay = 2, kWarpMma2 = 3, kWarpA = 4, kWarpB = 12;
 constexpr int kGroup = 8;                  // warps of A and of B
 constexpr int kThreads = 32 * 20;
 // Registers a thread of the control, A and B warps (setmaxnreg): 128 x 40 + 256 x 72 + 256 x 144 = 60,416 of the
@@ -77,7 +80,8 @@ struct Unit {
 struct Smem {
   unsigned char tile[kStages][3][kTile];  // Q, K, V
   unsigned char lo[2][kTile];             // low parts of K~
-  unsigned char P[2][2][kC * kC * 2];     // high and low parts of P
+  unsigned char P[2][kC * kC * 2];
+  unsigned char extra[kTile];             // in two parts: the low parts of P (twice 8 KiB); else: Y on its way out
   float b[kDecs][kC];    // cumulative log2 decay of the chunk
   float eb[kDecs][kC];   // factor of S q_i
   float w[kDecs][kC];    // factor of k_j in K~
@@ -94,7 +98,7 @@ constexpr int kSmemBytes = (int)sizeof(Smem) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
 struct Maps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, y;
 };
 
 struct Segments {
@@ -166,8 +170,8 @@ __device__ __forceinline__ Unit unit_of(const PassArgs& a, int u) {
   return x;
 }
 
-// kRev: backwards in time. kState: the first pass over segments (states alone). kSplit: S Q^T with the state in
-// two BF16 parts.
+// kRev: backwards in time. kState: the first pass over segments (states alone). kSplit: P and S in two
+// BF16 parts and Y in FP32.
 template <bool kRev, bool kState, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
 kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PassArgs a) {
@@ -179,7 +183,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
 
   if (warp == kWarpMma) tc::tmem_alloc(tc::smem_u32(&sm.tmem), 512);
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) { tc::mbar_init(bar(sm.full[i]), 1); tc::mbar_init(bar(sm.empty[i]), 1); }
+    for (int i = 0; i < kStages; ++i) { tc::mbar_init(bar(sm.full[i]), 1); tc::mbar_init(bar(sm.empty[i]), kState ? 1 : 2); }
     for (int i = 0; i < kDecs; ++i) tc::mbar_init(bar(sm.dec[i]), 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar(sm.g0[i]), 1);
@@ -191,7 +195,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
     tc::mbar_init(bar(sm.ufree), kGroup);
     tc::mbar_init(bar(sm.yfree), kGroup);
     tc::mbar_init(bar(sm.clcbar), 1);
-    for (int i = 0; i < kRing; ++i) { tc::mbar_init(bar(sm.rfull[i]), 1); tc::mbar_init(bar(sm.rempty[i]), 3 + 2 * kGroup); }
+    for (int i = 0; i < kRing; ++i) { tc::mbar_init(bar(sm.rfull[i]), 1); tc::mbar_init(bar(sm.rempty[i]), (kState ? 2 : 3) + 2 * kGroup); }
   }
   tc::fence_before();
   __syncthreads();
@@ -209,6 +213,15 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
     if (lane == 0) tc::mbar_arrive(bar(sm.rempty[ur % kRing]));
     ++ur;
     return !x.none;
+  };
+  // A consumer that sees chunks alone: is there one more, `left` those of the unit at hand?
+  auto any_chunk = [&](int64_t& left) {
+    Unit x;
+    while (left == 0) {
+      if (!next_unit(x)) return false;
+      left = x.nchunks;
+    }
+    return true;
   };
   auto arrive = [&](unsigned long long& b) {
     __syncwarp();
@@ -292,10 +305,14 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           tc::mbar_wait_lanes(bar(sm.full[k % kStages]), (k / kStages) & 1);
       }
     } else if (warp == kWarpMma) {
-      // ================= products
+      // ================= products that need no state: the scores and U
       uint32_t g = 0;
-      // the scores of chunk k
+      auto tiles = [&](uint32_t k) {
+        if (ok) ok = tc::mbar_wait_lanes(bar(sm.full[k % kStages]), (k / kStages) & 1);
+        tc::fence_after();
+      };
       auto scores = [&](uint32_t k) {
+        tiles(k);
         if (ok && tc::elect_one()) {
           const uint64_t dq = tc::kmajor(tc::smem_u32(sm.tile[k % kStages][0]));
           const uint64_t dk = tc::kmajor(tc::smem_u32(sm.tile[k % kStages][1]));
@@ -308,81 +325,84 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         }
         __syncwarp();
       };
-      auto tiles = [&](uint32_t k) {
-        if (ok) ok = tc::mbar_wait_lanes(bar(sm.full[k % kStages]), (k / kStages) & 1);
-        tc::fence_after();
-      };
-      int64_t left = 0;  // chunks of this unit from g on; any unit's are alike here
-      auto any = [&] {   // is there a chunk g?
-        Unit x;
-        while (left == 0) {
-          if (!next_unit(x)) return false;
-          left = x.nchunks;
-        }
-        return true;
-      };
-      bool more = any();
-      if (!kState && more) {
-        tiles(0);
-        scores(0);
-      }
+      int64_t left = 0;
+      bool more = any_chunk(left);
+      if (!kState && more) scores(0);
       for (; more; ++g) {
         const int s = g % kStages;
-        const uint64_t dv = tc::mnmajor(tc::smem_u32(sm.tile[s][2]), kPanel);
         if (kState) tiles(g);
         --left;
-        more = any();
-        if (!kState && more) {  // the next chunk's scores (its buffer was read before the last aready)
-          tiles(g + 1);
-          scores(g + 1);
-        }
+        more = any_chunk(left);
+        if (!kState && more) scores(g + 1);  // (its buffer was read before the last aready)
         // U, once K~ is there and the last U is read
         if (ok) ok = tc::mbar_wait_lanes(bar(sm.aready[g & 1]), (g >> 1) & 1);
         if (ok && g > 0) ok = tc::mbar_wait_lanes(bar(sm.ufree), (g - 1) & 1);
         tc::fence_after();
         if (ok && tc::elect_one()) {
+          const uint64_t dv = tc::mnmajor(tc::smem_u32(sm.tile[s][2]), kPanel);
           const uint64_t dh = tc::mnmajor(tc::smem_u32(sm.tile[s][1]), kPanel);
           const uint64_t dl = tc::mnmajor(tc::smem_u32(sm.lo[g & 1]), kPanel);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc::mma_bf16_ss(tbase + kColU, dv + 128 * k, dh + 128 * k, tc::idesc_bf16(128, 128, true, true), k > 0);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc::mma_bf16_ss(tbase + kColU, dv + 128 * k, dl + 128 * k, tc::idesc_bf16(128, 128, true, true), 1);
-          tc::mma_commit(bar(sm.gu));
-          if (kState) tc::mma_commit(bar(sm.empty[s]));
-        }
-        __syncwarp();
-        if (kState) continue;
-        // Y, once the state is there and the last Y is read
-        if (ok) ok = tc::mbar_wait_lanes(bar(sm.sready[g & 1]), (g >> 1) & 1);
-        if (ok && g > 0) ok = tc::mbar_wait_lanes(bar(sm.yfree), (g - 1) & 1);
-        tc::fence_after();
-        if (ok && tc::elect_one()) {
-          const uint64_t dq = tc::kmajor(tc::smem_u32(sm.tile[s][0]));
-          const uint64_t dp = tc::kmajor(tc::smem_u32(sm.P[g & 1][0])), dr = tc::kmajor(tc::smem_u32(sm.P[g & 1][1]));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t off = (i >> 2) * (kPanel >> 4) + (i & 3) * 2;
-            tc::mma_bf16_ts(tbase + kColO, tbase + kColS + (kSplit ? 0 : 64 * (g & 1)) + 8 * i, dq + off,
-                            tc::idesc_bf16(128, 64, false, false), i > 0);
-            if (kSplit)
-              tc::mma_bf16_ts(tbase + kColO, tbase + kColS + 64 + 8 * i, dq + off, tc::idesc_bf16(128, 64, false, false), 1);
-          }
-#pragma unroll
           for (int k = 0; k < 4; ++k) {
-            tc::mma_bf16_ss(tbase + kColO + 64, dv + 128 * k, dp + 2 * k, tc::idesc_bf16(128, 64, true, false), k > 0);
-            tc::mma_bf16_ss(tbase + kColO + 64, dv + 128 * k, dr + 2 * k, tc::idesc_bf16(128, 64, true, false), 1);
+            tc::mma_bf16_ss(tbase + kColU, dv + 128 * k, dh + 128 * k, tc::idesc_bf16(128, 128, true, true), k > 0);
+            tc::mma_bf16_ss(tbase + kColU, dv + 128 * k, dl + 128 * k, tc::idesc_bf16(128, 128, true, true), 1);
           }
-          tc::mma_commit(bar(sm.gy));
+          tc::mma_commit(bar(sm.gu));
           tc::mma_commit(bar(sm.empty[s]));
         }
         __syncwarp();
+      }
+    } else if (warp == kWarpMma2) {
+      // ================= products for Y, by a warp of their own: while one waits, the other's run
+      if (!kState) {
+        uint32_t g = 0;
+        int64_t left = 0;
+        for (; any_chunk(left); ++g, --left) {
+          const int s = g % kStages;
+          if (ok) ok = tc::mbar_wait_lanes(bar(sm.full[s]), (g / kStages) & 1);
+          // once the state is there and the last Y is read
+          if (ok) ok = tc::mbar_wait_lanes(bar(sm.sready[g & 1]), (g >> 1) & 1);
+          if (ok && g > 0) ok = tc::mbar_wait_lanes(bar(sm.yfree), (g - 1) & 1);
+          tc::fence_after();
+          if (ok && tc::elect_one()) {
+            const uint64_t dq = tc::kmajor(tc::smem_u32(sm.tile[s][0]));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t off = (i >> 2) * (kPanel >> 4) + (i & 3) * 2;
+              tc::mma_bf16_ts(tbase + kColO, tbase + kColS + (kSplit ? 0 : 64 * (g & 1)) + 8 * i, dq + off,
+                              tc::idesc_bf16(128, 64, false, false), i > 0);
+              if (kSplit)
+                tc::mma_bf16_ts(tbase + kColO, tbase + kColS + 64 + 8 * i, dq + off, tc::idesc_bf16(128, 64, false, false), 1);
+            }
+          }
+          __syncwarp();
+          if (ok) ok = tc::mbar_wait_lanes(bar(sm.aready[g & 1]), (g >> 1) & 1);
+          tc::fence_after();
+          if (ok && tc::elect_one()) {
+            const uint64_t dv = tc::mnmajor(tc::smem_u32(sm.tile[s][2]), kPanel);
+            const uint64_t dp = tc::kmajor(tc::smem_u32(sm.P[g & 1])), dr = tc::kmajor(tc::smem_u32(sm.extra) + (g & 1) * (kTile / 2));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              tc::mma_bf16_ss(tbase + kColO + 64, dv + 128 * k, dp + 2 * k, tc::idesc_bf16(128, 64, true, false), k > 0);
+              if (kSplit)
+                tc::mma_bf16_ss(tbase + kColO + 64, dv + 128 * k, dr + 2 * k, tc::idesc_bf16(128, 64, true, false), 1);
+            }
+            tc::mma_commit(bar(sm.gy));
+            tc::mma_commit(bar(sm.empty[s]));
+          }
+          __syncwarp();
+        }
       }
     } else if (warp == kWarpDecay) {
       // ================= decays, two tokens a lane
       uint32_t g = 0;
       for (Unit x; next_unit(x);) {
+        if (!kState && x.run && (a.sg.len || a.st.in)) {  // its initial state, on its way to L2
+          const char* src = a.sg.len ? reinterpret_cast<const char*>(a.sg.state + (x.sslot * P.Hv + x.h) * kDim * kDim)
+                                     : reinterpret_cast<const char*>(a.st.in) + (x.slot * P.Hv + x.h) * kDim * kDim * (a.st.bf16 ? 2 : 4);
+          const int lines = kDim * kDim * (!a.sg.len && a.st.bf16 ? 2 : 4) / 128;
+          for (int i = lane; i < lines; i += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 128 * i));
+        }
         float total = 0.f, n0 = 0.f, n1 = 0.f;
         auto fetch = [&](int64_t c) {
           const int64_t j = (kRev ? x.nchunks - 1 - c : c) * kC + 2 * lane;
@@ -422,15 +442,6 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         }
         if (kState && x.run && lane == 31) a.sg.decay[x.sslot * P.Hv + x.h] = total;
       }
-    } else {
-      // ================= the next unit's initial state, on its way to L2
-      for (Unit x; next_unit(x);) {
-        if (kState || !x.run || (!a.sg.len && !a.st.in)) continue;
-        const char* src = a.sg.len ? reinterpret_cast<const char*>(a.sg.state + (x.sslot * P.Hv + x.h) * kDim * kDim)
-                                   : reinterpret_cast<const char*>(a.st.in) + (x.slot * P.Hv + x.h) * kDim * kDim * (a.st.bf16 ? 2 : 4);
-        const int lines = kDim * kDim * (!a.sg.len && a.st.bf16 ? 2 : 4) / 128;
-        for (int i = lane; i < lines; i += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 128 * i));
-      }
     }
   } else if (warp < kWarpB) {
     // ================= K~ and P
@@ -448,12 +459,9 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         unsigned char* Ls = sm.lo[g & 1];
         if (ok) ok = tc::mbar_wait_lanes(bar(sm.dec[d]), (g / kDecs) & 1);
         if (ok) ok = tc::mbar_wait_lanes(bar(sm.full[s]), (g / kStages) & 1);
-        // K is free once the scores are done; they follow chunk g - 2's products, which read lo and P of this parity
-        if (!kState) {
-          if (ok) ok = tc::mbar_wait_lanes(bar(sm.g0[g & 1]), (g >> 1) & 1);
-        } else if (g >= 2) {
-          if (ok) ok = tc::mbar_wait_lanes(bar(sm.empty[(g - 2) % kStages]), ((g - 2) / kStages) & 1);
-        }
+        // lo and P of this parity are free once chunk g - 2's products are done, K once this one's scores are
+        if (ok && g >= 2) ok = tc::mbar_wait_lanes(bar(sm.empty[(g - 2) % kStages]), ((g - 2) / kStages) & 1);
+        if (ok && !kState) ok = tc::mbar_wait_lanes(bar(sm.g0[g & 1]), (g >> 1) & 1);
         tc::fence_after();
 #pragma unroll
         for (int m = 0; m < 4; ++m) {  // 16-byte chunks i
@@ -466,7 +474,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           split2(tc::mul2(unpack2(r.y), w), hi.y, lo.y);
           split2(tc::mul2(unpack2(r.z), w), hi.z, lo.z);
           split2(tc::mul2(unpack2(r.w), w), hi.w, lo.w);
-          if (row >= nt) hi = lo = make_uint4(0u, 0u, 0u, 0u);  // rows past the end hold other tokens
+          if (nt < kC && row >= nt) hi = lo = make_uint4(0u, 0u, 0u, 0u);  // rows past the end hold other tokens
           *reinterpret_cast<uint4*>(Ks + 16 * i) = hi;
           *reinterpret_cast<uint4*>(Ls + 16 * i) = lo;
         }
@@ -477,30 +485,39 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         if (!kState) {
           // rows i = 16 wq + lane / 4 (+ 8), columns 32 half + 8 m + 2 (lane % 4) (+ 1)
           const int i0 = 16 * wq + (lane >> 2), j0 = 32 * half + 2 * (lane & 3);
-          const float b0 = sm.b[d][i0], b1 = sm.b[d][i0 + 8];
-          unsigned char* Pt = sm.P[g & 1][0];
-          float p[16];  // (nothing between the load and its wait, where a register could be moved too early)
-          tc::tmem_ld16x256(tl + kColP + 64 * (g & 1) + 32 * half, p);
-          tc::tmem_wait_ld(p);
+          unsigned char* Pt = sm.P[g & 1];
+          unsigned char* Pl = sm.extra + (g & 1) * (kTile / 2);
+          auto at_of = [&](int i, int m) { return i * 128 + (((4 * half + m) ^ (i & 7)) << 4) + 4 * (lane & 3); };
+          if (kRev ? half == 0 && wq >= 2 : half == 1 && wq < 2) {  // all on the masked side
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const int j = j0 + 8 * m;
-            const float2 bj = *reinterpret_cast<const float2*>(&sm.b[d][j]);
+            for (int m = 0; m < 8; ++m) {
+              *reinterpret_cast<uint32_t*>(Pt + at_of(i0 + 8 * (m & 1), m >> 1)) = 0u;
+              if (kSplit) *reinterpret_cast<uint32_t*>(Pl + at_of(i0 + 8 * (m & 1), m >> 1)) = 0u;
+            }
+          } else {
+            const float b0 = sm.b[d][i0], b1 = sm.b[d][i0 + 8];
+            float p[16];  // (nothing between the load and its wait, where a register could be moved too early)
+            tc::tmem_ld16x256(tl + kColP + 64 * (g & 1) + 32 * half, p);
+            tc::tmem_wait_ld(p);
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              const int i = i0 + 8 * v;
-              const float bi = v ? b1 : b0;
-              const float2 e = kRev ? make_float2(fast_exp2(bj.x - bi), fast_exp2(bj.y - bi))
-                                    : make_float2(fast_exp2(bi - bj.x), fast_exp2(bi - bj.y));
-              float2 y = tc::mul2(tc::mul2(make_float2(p[4 * m + 2 * v], p[4 * m + 2 * v + 1]), scale), e);
-              // (selected, not multiplied: rows past the end may hold anything)
-              y.x = (kRev ? j >= i && j < nt : j <= i && i < nt) ? y.x : 0.f;
-              y.y = (kRev ? j + 1 >= i && j + 1 < nt : j < i && i < nt) ? y.y : 0.f;
-              uint32_t hi, lo;
-              split2(y, hi, lo);
-              uint32_t* dst = reinterpret_cast<uint32_t*>(Pt + i * 128 + (((4 * half + m) ^ (i & 7)) << 4) + 4 * (lane & 3));
-              dst[0] = hi;
-              dst[kC * kC / 2] = lo;
+            for (int m = 0; m < 4; ++m) {
+              const int j = j0 + 8 * m;
+              const float2 bj = *reinterpret_cast<const float2*>(&sm.b[d][j]);
+#pragma unroll
+              for (int v = 0; v < 2; ++v) {
+                const int i = i0 + 8 * v;
+                const float bi = v ? b1 : b0;
+                const float2 e = kRev ? make_float2(fast_exp2(bj.x - bi), fast_exp2(bj.y - bi))
+                                      : make_float2(fast_exp2(bi - bj.x), fast_exp2(bi - bj.y));
+                float2 y = tc::mul2(tc::mul2(make_float2(p[4 * m + 2 * v], p[4 * m + 2 * v + 1]), scale), e);
+                // (selected, not multiplied: rows past the end may hold anything)
+                y.x = (kRev ? j >= i && j < nt : j <= i && i < nt) ? y.x : 0.f;
+                y.y = (kRev ? j + 1 >= i && j + 1 < nt : j < i && i < nt) ? y.y : 0.f;
+                uint32_t hi, lo;
+                split2(y, hi, lo);
+                *reinterpret_cast<uint32_t*>(Pt + at_of(i, m)) = hi;
+                if (kSplit) *reinterpret_cast<uint32_t*>(Pl + at_of(i, m)) = lo;
+              }
             }
           }
         }
@@ -516,7 +533,18 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
     const int v = 32 * wq + lane;  // state row of this thread, its columns 64 half .. + 63; value of Y, tokens 32 half .. + 31
     const uint32_t tl = tbase + ((uint32_t)(32 * wq) << 16);
     uint32_t g = 0;
-    for (Unit x; next_unit(x);) {
+    // The warps that fill a tile of Y together leave together: a barrier among them is not bounded.
+    auto agree = [&] {
+      uint32_t all;
+      asm volatile(
+          "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.and.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+          : "=r"(all) : "r"((uint32_t)ok), "n"(32 * kGroup) : "memory");
+      ok = all != 0;
+    };
+    for (Unit x;;) {
+      const bool more = next_unit(x);
+      if (!kState && !kSplit) agree();
+      if (!ok || !more) break;
       if (!x.run) {
         // a device slot index outside the pool (it no longer matches the host mirror the call was checked
         // against, as in a replayed graph): flagged, and the pool is not touched
@@ -597,44 +625,74 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         if (ok) ok = tc::mbar_wait_lanes(bar(sm.gy), g & 1);
         tc::fence_after();
         if (kSplit && c + 1 < x.nchunks) put_state(g + 1);
-        const int64_t row = (x.t0 + ci * kC + 32 * half) * P.Hv + x.h;
-        uint32_t packed[16];  // pairs of tokens
+        if (kSplit) {  // FP32, straight from the registers: thread v holds one value of each token
+          float* dst = a.y32 + ((x.t0 + ci * kC + 32 * half) * P.Hv + x.h) * kDim + v;
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          float r[16], y[16];
-          tc::tmem_ld16_nowait(tl + kColO + 32 * half + 16 * m, r);
-          tc::tmem_ld16_nowait(tl + kColO + 64 + 32 * half + 16 * m, y);
-          tc::tmem_wait_ld2(r, y);
-#pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 e = *reinterpret_cast<const float4*>(&sm.eb[d][32 * half + 16 * m + j]);
-            const float2 p = tc::fma2(make_float2(e.x, e.y), make_float2(r[j], r[j + 1]), make_float2(y[j], y[j + 1]));
-            const float2 q = tc::fma2(make_float2(e.z, e.w), make_float2(r[j + 2], r[j + 3]), make_float2(y[j + 2], y[j + 3]));
-            packed[8 * m + j / 2] = pack2(p);
-            packed[8 * m + j / 2 + 1] = pack2(q);
-            y[j] = p.x; y[j + 1] = p.y; y[j + 2] = q.x; y[j + 3] = q.y;
-          }
-          if (a.y32) {
-            float* dst = a.y32 + (row + 16 * m * (int64_t)P.Hv) * kDim + v;
+          for (int m = 0; m < 2; ++m) {
+            float r[16], y[16];
+            tc::tmem_ld16_nowait(tl + kColO + 32 * half + 16 * m, r);
+            tc::tmem_ld16_nowait(tl + kColO + 64 + 32 * half + 16 * m, y);
+            tc::tmem_wait_ld2(r, y);
             const int left = nt - 32 * half - 16 * m;
 #pragma unroll
-            for (int j = 0; j < 16; ++j, dst += (int64_t)P.Hv * kDim)
-              if (j < left) *dst = y[j];
-          }
-        }
-        tc::fence_before();
-        arrive(sm.yfree);
-        if (a.y) {
-          // neighbours exchange, so that each stores two values of a token
-          const int odd = lane & 1;
-          const uint32_t pick = odd ? 0x3276u : 0x5410u;  // (own low, neighbour's low) or (neighbour's high, own high)
-          __nv_bfloat16* dst = a.y + (row + odd * P.Hv) * kDim + (v & ~1);
-          const int64_t step = 2 * (int64_t)P.Hv * kDim;
-          const int left = nt - 32 * half - odd;
+            for (int j = 0; j < 16; j += 4) {
+              const float4 e = *reinterpret_cast<const float4*>(&sm.eb[d][32 * half + 16 * m + j]);
+              const float2 p = tc::fma2(make_float2(e.x, e.y), make_float2(r[j], r[j + 1]), make_float2(y[j], y[j + 1]));
+              const float2 q = tc::fma2(make_float2(e.z, e.w), make_float2(r[j + 2], r[j + 3]), make_float2(y[j + 2], y[j + 3]));
+              const float z[4] = {p.x, p.y, q.x, q.y};
 #pragma unroll
-          for (int j = 0; j < 16; ++j, dst += step) {
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, packed[j], 1);
-            if (2 * j < left) *reinterpret_cast<uint32_t*>(dst) = __byte_perm(packed[j], got, pick);
+              for (int i = 0; i < 4; ++i, dst += (int64_t)P.Hv * kDim)
+                if (j + i < left) *dst = z[i];
+            }
+          }
+          tc::fence_before();
+          arrive(sm.yfree);
+        } else {
+          // transposed by matrix stores into a tile of shared memory, copied out from there
+          if (warp == kWarpB && lane == 0) tc::bulk_wait_read();  // the last one has left
+          agree();
+          const uint32_t out = tc::smem_u32(sm.extra);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {  // values 32 wq + 16 q + 8 j + lane / 4, tokens 32 half + 8 m + 2 (lane % 4) (+ 1)
+            float r[16], y[16];
+            tc::tmem_ld16x256(tl + (16u * q << 16) + kColO + 32 * half, r);
+            tc::tmem_ld16x256(tl + (16u * q << 16) + kColO + 64 + 32 * half, y);
+            tc::tmem_wait_ld2(r, y);
+            uint32_t z[8];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const float2 e = *reinterpret_cast<const float2*>(&sm.eb[d][32 * half + 8 * m + 2 * (lane & 3)]);
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                z[2 * m + j] = pack2(tc::fma2(e, make_float2(r[4 * m + 2 * j], r[4 * m + 2 * j + 1]),
+                                              make_float2(y[4 * m + 2 * j], y[4 * m + 2 * j + 1])));
+            }
+            // matrix (m, j): lanes 8 (2 (m & 1) + j) + i give token 32 half + 8 m + i
+            const int col = 32 * wq + 16 * q + 8 * ((lane >> 3) & 1), chunk = (col & 63) >> 3;
+#pragma unroll
+            for (int m = 0; m < 4; m += 2) {
+              const int t = 32 * half + 8 * (m + (lane >> 4)) + (lane & 7);
+              tc::stmatrix4_trans(out + (col >> 6) * kPanel + t * 128 + ((chunk ^ (t & 7)) << 4), z[2 * m], z[2 * m + 1],
+                                  z[2 * m + 2], z[2 * m + 3]);
+            }
+          }
+          tc::fence_before();
+          arrive(sm.yfree);
+          tc::fence_async_smem();
+          asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * kGroup) : "memory");
+          const int64_t t0 = x.t0 + ci * kC;
+          if (nt == kC) {
+            if (warp == kWarpB && lane == 0) {
+              tc::tma_store3(&maps.y, out, 0, x.h, (int)t0);
+              tc::tma_store3(&maps.y, out + kPanel, 64, x.h, (int)t0);
+              tc::bulk_commit();
+            }
+          } else {  // (a whole tile would run into the next sequence)
+            for (int i = tid - 32 * kWarpB; i < nt * 16; i += 32 * kGroup) {
+              const int t = i >> 4, k = i & 15;
+              *reinterpret_cast<uint4*>(a.y + ((t0 + t) * P.Hv + x.h) * kDim + 8 * k) =
+                  *reinterpret_cast<const uint4*>(sm.extra + (k >> 3) * kPanel + t * 128 + (((k & 7) ^ (t & 7)) << 4));
+            }
           }
         }
       }
@@ -660,6 +718,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         }
       }
     }
+    if (!kState && !kSplit && warp == kWarpB && lane == 0) tc::bulk_wait();
     if (!ok && lane == 0) atomicOr(P.status, 1);
   }
   tc::fence_before();
@@ -874,6 +933,7 @@ cudaError_t pass(const DecayProblem& P, const Role& q, const Role& k, const Role
     if ((e = token_map(&maps.q, q.p, q.heads, P.Ttot, q.h, q.t, kC)) != cudaSuccess) return e;
     if ((e = token_map(&maps.k, k.p, k.heads, P.Ttot, k.h, k.t, kC)) != cudaSuccess) return e;
     if ((e = token_map(&maps.v, v.p, v.heads, P.Ttot, v.h, v.t, kC)) != cudaSuccess) return e;
+    if (y && (e = token_map(&maps.y, y, P.Hv, P.Ttot, kDim, (int64_t)P.Hv * kDim, kC)) != cudaSuccess) return e;
   }
   a.P = P;
   a.qdiv = P.Hv / q.heads;
