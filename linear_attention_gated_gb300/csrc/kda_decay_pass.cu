@@ -300,7 +300,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
       if (!ok) {
         // flag it, and let this CTA's copies (and a response) land before its memory is given back
         if (lane == 0) atomicOr(P.status, 1);
-        tc::mbar_wait_lanes(bar(sm.clcbar), asked & 1, 1ll << 22);
+        tc::mbar_wait_lanes(bar(sm.clcbar), asked & 1, 1u << 16);
         for (uint32_t k = g > kStages ? g - kStages : 0; k < g; ++k)
           tc::mbar_wait_lanes(bar(sm.full[k % kStages]), (k / kStages) & 1);
       }

@@ -193,9 +193,10 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t mbar, uint32_t parity, l
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-// The same bounded wait with every lane of the warp polling, and no clock read unless the first try fails: 217
-// cycles of mbar_wait_warp on a phase that is already complete (measured) are most of a step in a
-// pipeline of short steps. The result is the warp's.
+// The same bounded wait with every lane of the warp polling, a limit on the tries in place of the clock, and little
+// code: 217 cycles of mbar_wait_warp on a phase that is already complete (measured) are much of a step
+// in a pipeline of short steps, and so are instruction fetches where warps run different code. 2^20 tries took
+// seconds (the hardware suspends each for a while). The result is the warp's.
 __device__ __forceinline__ bool mbar_try(uint32_t mbar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -206,17 +207,12 @@ __device__ __forceinline__ bool mbar_try(uint32_t mbar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool mbar_wait_lanes(uint32_t mbar, uint32_t parity, long long limit = 1ll << 32) {
-  bool ok = mbar_try(mbar, parity);
-  if (!__all_sync(0xffffffffu, ok)) {
-    const long long t0 = clock64();
-    while (!ok) {
-      ok = mbar_try(mbar, parity);
-      if (clock64() - t0 > limit) break;
-    }
-    ok = __all_sync(0xffffffffu, ok);
-  }
-  return ok;
+__device__ __forceinline__ bool mbar_wait_lanes(uint32_t mbar, uint32_t parity, uint32_t tries = 1u << 20) {
+  bool ok;
+  do {
+    ok = mbar_try(mbar, parity);
+  } while (!ok && --tries);
+  return __all_sync(0xffffffffu, ok);
 }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
