@@ -422,16 +422,16 @@ kda_status kda_prefill(const kda_bf16* q, const kda_bf16* k, const kda_bf16* v, 
  * _WORKSPACE_TOO_SMALL, _CUDA), all before any launch; nothing is allocated; calls
  * only launch kernels on `stream` and may be captured into a CUDA graph. */
 
-/* Bytes of device workspace (256-byte aligned) for this problem: `training` 1
- * for kda_decay_attn_fwd and _bwd, 0 for kda_decay_attn_prefill (which may need
- * none). The packed layout's mirror is read for the sequences' lengths. */
+/* Bytes of device workspace (256-byte aligned, possibly 0) for this problem:
+ * `training` 1 for kda_decay_attn_fwd and _bwd, 0 for kda_decay_attn_prefill. The
+ * packed layout's mirror is read for the sequences' lengths. */
 kda_status kda_decay_attn_workspace_bytes(int64_t B, int64_t T, int64_t Hqk, int64_t Hv,
                                           const int64_t* cu_seqlens_host, int64_t num_seqs,
-                                          int32_t training, size_t* bytes);
+                                          int32_t decay_per_token, int32_t training, size_t* bytes);
 
 /* Training forward: o BF16 [B, T, Hv, 128] and h_T FP32 [N, Hv, 128, 128] from
- * h0 FP32 (NULL for zeros). Leaves in the workspace what kda_decay_attn_bwd reads:
- * pass it there untouched, with the same inputs. */
+ * h0 FP32 (NULL for zeros). Nothing is saved for kda_decay_attn_bwd but its inputs
+ * and h_T; the workspace is scratch of each call. */
 kda_status kda_decay_attn_fwd(const kda_bf16* q, const kda_bf16* k, const kda_bf16* v,
                               const void* log_decay, int32_t decay_per_token, const float* h0,
                               const int64_t* cu_seqlens_dev, const int64_t* cu_seqlens_host,
@@ -440,7 +440,8 @@ kda_status kda_decay_attn_fwd(const kda_bf16* q, const kda_bf16* k, const kda_bf
                               float* h_T, void* workspace, size_t workspace_bytes,
                               int32_t* device_status, struct CUstream_st* stream);
 
-/* Training backward of the kda_decay_attn_fwd call that filled the workspace.
+/* Training backward: the inputs of kda_decay_attn_fwd, its h_T (read only where
+ * dlog_decay and d_hT are given, else it may be NULL) and the adjoints.
  * d_o BF16 [B, T, Hv, 128], d_hT FP32 [N, Hv, 128, 128] or NULL (zeros); dq, dk BF16
  * [B, T, Hqk, 128] (sums over the value heads of the group, rounded once), dv BF16
  * [B, T, Hv, 128], dlog_decay BF16 [B, T, Hv] (NULL with a fixed decay, which
@@ -450,7 +451,7 @@ kda_status kda_decay_attn_bwd(const kda_bf16* q, const kda_bf16* k, const kda_bf
                               const int64_t* cu_seqlens_dev, const int64_t* cu_seqlens_host,
                               int64_t num_seqs, int64_t B, int64_t T, int64_t Hqk, int64_t Hv,
                               int64_t head_dim, float scale, const int64_t* strides,
-                              const kda_bf16* d_o, const float* d_hT, kda_bf16* dq, kda_bf16* dk,
+                              const float* h_T, const kda_bf16* d_o, const float* d_hT, kda_bf16* dq, kda_bf16* dk,
                               kda_bf16* dv, kda_bf16* dlog_decay, float* dh0, void* workspace,
                               size_t workspace_bytes, int32_t* device_status,
                               struct CUstream_st* stream);

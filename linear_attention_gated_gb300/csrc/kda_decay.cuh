@@ -79,10 +79,9 @@ __device__ __forceinline__ float decay_g(const DecayProblem& P, int64_t tok, int
 // Tokens of the segments sequences are cut into, 0 for none. cu: host offsets or null.
 int64_t decay_segment_tokens(const int64_t* cu, int64_t N, int64_t T, int64_t Hv);
 // Workspace: the segments' states, then (training) what the backward needs.
-size_t decay_workspace_bytes(int64_t N, int64_t Ttot, int64_t Hqk, int64_t Hv, int64_t seg, bool training);
-cudaError_t launch_decay_forward(const DecayProblem& P, const DecayStates& st, __nv_bfloat16* o, void* ws,
-                                 bool training, cudaStream_t s);
-cudaError_t launch_decay_backward(const DecayProblem& P, const float* h0, const DecayGrads& g, void* ws,
+size_t decay_workspace_bytes(int64_t N, int64_t Ttot, int64_t Hqk, int64_t Hv, int64_t seg, bool training, bool per_token);
+cudaError_t launch_decay_forward(const DecayProblem& P, const DecayStates& st, __nv_bfloat16* o, void* ws, cudaStream_t s);
+cudaError_t launch_decay_backward(const DecayProblem& P, const float* h0, const float* hT, const DecayGrads& g, void* ws,
                                   cudaStream_t s);
 
 }  // namespace kda

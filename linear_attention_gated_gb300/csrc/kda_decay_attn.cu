@@ -122,7 +122,7 @@ kda_status check_tokens(const void* q, const void* k, const void* v, const void*
 }
 
 kda_status check_workspace(const kda::DecayProblem& P, void* ws, size_t bytes, bool training) {
-  const size_t need = kda::decay_workspace_bytes(P.N, P.Ttot, P.Hqk, P.Hv, P.seg, training);
+  const size_t need = kda::decay_workspace_bytes(P.N, P.Ttot, P.Hqk, P.Hv, P.seg, training, P.per_token);
   if (need && (!ws || bytes < need))
     return fail(KDA_ERR_WORKSPACE_TOO_SMALL, "workspace below kda_decay_attn_workspace_bytes()");
   if ((uintptr_t)ws & 255u) return fail(KDA_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
@@ -146,13 +146,13 @@ kda_status check_device(int32_t* device_status, int32_t** status) {
 
 extern "C" kda_status kda_decay_attn_workspace_bytes(int64_t B, int64_t T, int64_t Hqk, int64_t Hv,
                                                      const int64_t* cu_seqlens_host, int64_t num_seqs,
-                                                     int32_t training, size_t* bytes) {
+                                                     int32_t decay_per_token, int32_t training, size_t* bytes) {
   return kda::guarded([&]() -> kda_status {
     if (!bytes) return fail(KDA_ERR_INVALID_ARGUMENT, "bytes is NULL");
     Shape s{};
     const kda_status st = check_shape(B, T, Hqk, Hv, cu_seqlens_host, num_seqs, &s);
     if (st != KDA_OK) return st;
-    *bytes = kda::decay_workspace_bytes(s.N, s.Ttot, Hqk, Hv, s.seg, training != 0);
+    *bytes = kda::decay_workspace_bytes(s.N, s.Ttot, Hqk, Hv, s.seg, training != 0, decay_per_token != 0);
     return KDA_OK;
   });
 }
@@ -180,7 +180,7 @@ extern "C" kda_status kda_decay_attn_fwd(const kda_bf16* q, const kda_bf16* k, c
     if (aliasing(outs, ins)) return fail(KDA_ERR_ALIASING, "an output overlaps an input or another output");
     if ((st = check_device(device_status, &P.status)) != KDA_OK) return st;
     const kda::DecayStates S{h0, h_T, 0, nullptr, P.N};
-    const cudaError_t e = kda::launch_decay_forward(P, S, reinterpret_cast<__nv_bfloat16*>(o), workspace, true, stream);
+    const cudaError_t e = kda::launch_decay_forward(P, S, reinterpret_cast<__nv_bfloat16*>(o), workspace, stream);
     return e == cudaSuccess ? KDA_OK : fail(KDA_ERR_CUDA, cudaGetErrorString(e));
   });
 }
@@ -189,7 +189,8 @@ extern "C" kda_status kda_decay_attn_bwd(const kda_bf16* q, const kda_bf16* k, c
                                          int32_t decay_per_token, const float* h0, const int64_t* cu_seqlens_dev,
                                          const int64_t* cu_seqlens_host, int64_t num_seqs, int64_t B, int64_t T,
                                          int64_t Hqk, int64_t Hv, int64_t head_dim, float scale,
-                                         const int64_t* strides, const kda_bf16* d_o, const float* d_hT, kda_bf16* dq,
+                                         const int64_t* strides, const float* h_T, const kda_bf16* d_o,
+                                         const float* d_hT, kda_bf16* dq,
                                          kda_bf16* dk, kda_bf16* dv, kda_bf16* dlog_decay, float* dh0, void* workspace,
                                          size_t workspace_bytes, int32_t* device_status, struct CUstream_st* stream) {
   return kda::guarded([&]() -> kda_status {
@@ -201,14 +202,16 @@ extern "C" kda_status kda_decay_attn_bwd(const kda_bf16* q, const kda_bf16* k, c
     if (P.Ttot && (!d_o || !dq || !dk || !dv)) return fail(KDA_ERR_INVALID_ARGUMENT, "null gradient pointer");
     if (dlog_decay && !decay_per_token)
       return fail(KDA_ERR_UNSUPPORTED, "a fixed decay for each head has no gradient: dlog_decay must be NULL");
-    if (((uintptr_t)d_o | (uintptr_t)d_hT | (uintptr_t)dq | (uintptr_t)dk | (uintptr_t)dv | (uintptr_t)h0 | (uintptr_t)dh0) & 15u)
+    if (dlog_decay && d_hT && !h_T)
+      return fail(KDA_ERR_INVALID_ARGUMENT, "the decays' gradient needs the forward's h_T where there is a d_hT");
+    if (((uintptr_t)h_T | (uintptr_t)d_o | (uintptr_t)d_hT | (uintptr_t)dq | (uintptr_t)dk | (uintptr_t)dv | (uintptr_t)h0 | (uintptr_t)dh0) & 15u)
       return fail(KDA_ERR_INVALID_ARGUMENT, "state, adjoint and gradient tensors must be 16-byte aligned");
     if ((st = check_workspace(P, workspace, workspace_bytes, true)) != KDA_OK) return st;
     const size_t states = 4 * (size_t)P.N * Hv * kda::kDim * kda::kDim;
     const size_t tq = 2 * (size_t)P.Ttot * Hqk * kda::kDim, tv = 2 * (size_t)P.Ttot * Hv * kda::kDim;
     const Span outs[] = {{dq, tq}, {dk, tq}, {dv, tv}, {dlog_decay, 2 * (size_t)P.Ttot * Hv}, {dh0, states},
                          {workspace, workspace_bytes}, {device_status, 4}};
-    const Span ins[] = {in[0], in[1], in[2], in[3], in[4], {h0, states}, {d_o, tv}, {d_hT, states}};
+    const Span ins[] = {in[0], in[1], in[2], in[3], in[4], {h0, states}, {h_T, states}, {d_o, tv}, {d_hT, states}};
     if (aliasing(outs, ins)) return fail(KDA_ERR_ALIASING, "an output overlaps an input or another output");
     if ((st = check_device(device_status, &P.status)) != KDA_OK) return st;
     kda::DecayGrads G{};
@@ -219,7 +222,7 @@ extern "C" kda_status kda_decay_attn_bwd(const kda_bf16* q, const kda_bf16* k, c
     G.dv = reinterpret_cast<__nv_bfloat16*>(dv);
     G.dg = reinterpret_cast<__nv_bfloat16*>(dlog_decay);
     G.dh0 = dh0;
-    const cudaError_t e = kda::launch_decay_backward(P, h0, G, workspace, stream);
+    const cudaError_t e = kda::launch_decay_backward(P, h0, h_T, G, workspace, stream);
     return e == cudaSuccess ? KDA_OK : fail(KDA_ERR_CUDA, cudaGetErrorString(e));
   });
 }
@@ -266,7 +269,7 @@ extern "C" kda_status kda_decay_attn_prefill(const kda_bf16* q, const kda_bf16* 
     if (aliasing(outs, ins)) return fail(KDA_ERR_ALIASING, "an output overlaps an input or another output");
     if ((st = check_device(device_status, &P.status)) != KDA_OK) return st;
     const kda::DecayStates S{state, state, state_dtype == KDA_STATE_BF16, state_indices, num_slots};
-    const cudaError_t e = kda::launch_decay_forward(P, S, reinterpret_cast<__nv_bfloat16*>(o), workspace, false, stream);
+    const cudaError_t e = kda::launch_decay_forward(P, S, reinterpret_cast<__nv_bfloat16*>(o), workspace, stream);
     return e == cudaSuccess ? KDA_OK : fail(KDA_ERR_CUDA, cudaGetErrorString(e));
   });
 }

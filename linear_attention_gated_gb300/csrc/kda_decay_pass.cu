@@ -779,94 +779,135 @@ __global__ void __launch_bounds__(256) kda_decay_chain_kernel(const __grid_const
   }
 }
 
-// Sums of a query/key head's value heads, rounded once.
-__global__ void __launch_bounds__(256) kda_decay_group_sum_kernel(const float* x, __nv_bfloat16* y, int64_t rows, int r) {
-  const int64_t at = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) * 4;
-  if (at >= rows * kDim) return;
-  const int64_t row = at / kDim, d = at % kDim;
-  const float* src = x + row * r * kDim + d;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j = 0; j < r; ++j) {
-    const float4 v = *reinterpret_cast<const float4*>(src + (int64_t)j * kDim);
-    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+// dq and dk from the value heads' FP32 parts: sums over a group's heads, rounded once; and, for the decays' gradient,
+// what crosses each token in each value head, q . dq - k . dk. A warp takes a (token, query/key head), the
+// parts' loads four heads ahead; bandwidth bounds it (1 KiB read for each value head and token).
+template <bool kCross>
+__global__ void __launch_bounds__(256) kda_decay_group_sum_kernel(const DecayProblem P, const float* dq32, const float* dk32,
+                                                                  __nv_bfloat16* dq, __nv_bfloat16* dk, float* z) {
+  // a block takes eight consecutive tokens of a head (so that its eight z share a sector)
+  const int hq = blockIdx.x % P.Hqk;
+  const int64_t tok = (int64_t)(blockIdx.x / P.Hqk) * 8 + (threadIdx.x >> 5), row = tok * P.Hqk + hq;
+  if (tok >= P.Ttot) return;
+  const int lane = threadIdx.x & 31;
+  float4 q, k;
+  if (kCross) {
+    const uint2 rq = *reinterpret_cast<const uint2*>(P.q + tok * P.qt + hq * P.qh + 4 * lane);
+    const uint2 rk = *reinterpret_cast<const uint2*>(P.k + tok * P.kt + hq * P.kh + 4 * lane);
+    const float2 q0 = unpack2(rq.x), q1 = unpack2(rq.y), k0 = unpack2(rk.x), k1 = unpack2(rk.y);
+    q = make_float4(q0.x, q0.y, q1.x, q1.y);
+    k = make_float4(k0.x, k0.y, k1.x, k1.y);
   }
-  *reinterpret_cast<uint2*>(y + at) = make_uint2(pack2(s.x, s.y), pack2(s.z, s.w));
+  float4 sq = make_float4(0.f, 0.f, 0.f, 0.f), sk = sq;
+  const int64_t at = row * P.r * kDim + 4 * lane;
+  for (int j0 = 0; j0 < P.r; j0 += 4) {
+    float4 a[4], b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j0 + j < P.r) {
+        a[j] = __ldcs(reinterpret_cast<const float4*>(dq32 + at + (int64_t)(j0 + j) * kDim));
+        b[j] = __ldcs(reinterpret_cast<const float4*>(dk32 + at + (int64_t)(j0 + j) * kDim));
+      }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j0 + j < P.r) {
+        sq.x += a[j].x; sq.y += a[j].y; sq.z += a[j].z; sq.w += a[j].w;
+        sk.x += b[j].x; sk.y += b[j].y; sk.z += b[j].z; sk.w += b[j].w;
+        if (kCross) {
+          float x = q.x * a[j].x + q.y * a[j].y + q.z * a[j].z + q.w * a[j].w -
+                    (k.x * b[j].x + k.y * b[j].y + k.z * b[j].z + k.w * b[j].w);
+#pragma unroll
+          for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+          // heads first: the sums that follow run over tokens
+          if (lane == 0) z[((int64_t)hq * P.r + j0 + j) * P.Ttot + tok] = x;
+        }
+      }
+  }
+  *reinterpret_cast<uint2*>(dq + row * kDim + 4 * lane) = make_uint2(pack2(sq.x, sq.y), pack2(sq.z, sq.w));
+  *reinterpret_cast<uint2*>(dk + row * kDim + 4 * lane) = make_uint2(pack2(sk.x, sk.y), pack2(sk.z, sk.w));
 }
 
-// What crosses each token, q . dq - k . dk of one value head: a warp a row.
-__global__ void __launch_bounds__(256) kda_decay_cross_kernel(const DecayProblem P, const float* dq, const float* dk, float* z) {
-  const int64_t row = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= P.Ttot * P.Hv) return;
-  const int lane = threadIdx.x & 31;
-  const int64_t tok = row / P.Hv;
-  const int hq = (int)(row - tok * P.Hv) / P.r;
-  const uint2 q = *reinterpret_cast<const uint2*>(P.q + tok * P.qt + hq * P.qh + 4 * lane);
-  const uint2 k = *reinterpret_cast<const uint2*>(P.k + tok * P.kt + hq * P.kh + 4 * lane);
-  const float4 a = *reinterpret_cast<const float4*>(dq + row * kDim + 4 * lane);
-  const float4 b = *reinterpret_cast<const float4*>(dk + row * kDim + 4 * lane);
-  const float2 q0 = unpack2(q.x), q1 = unpack2(q.y), k0 = unpack2(k.x), k1 = unpack2(k.y);
-  float x = q0.x * a.x + q0.y * a.y + q1.x * a.z + q1.y * a.w - (k0.x * b.x + k0.y * b.y + k1.x * b.z + k1.y * b.w);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  if (lane == 0) z[row] = x;
-}
+// A sum in two FP32 numbers, 48 bits.
+struct Sum2 {
+  float hi, lo;
+  __device__ __forceinline__ void add(float x) {
+    const float s = hi + x, t = s - hi;
+    lo += (hi - (s - t)) + (x - t);
+    hi = s;
+  }
+  __device__ __forceinline__ void add(Sum2 x) {
+    add(x.hi);
+    lo += x.lo;
+  }
+  __device__ __forceinline__ Sum2 from(int lane_delta) const {
+    return Sum2{__shfl_up_sync(0xffffffffu, hi, lane_delta), __shfl_up_sync(0xffffffffu, lo, lane_delta)};
+  }
+};
 
 // dg of one (sequence, head): a decay scales all that crosses its token, so
 //   dg_t = sum_{i >= t} (q_i . dq_i - k_i . dk_i) + <S_T, dS_T>.
-// The sums cancel over long sequences: FP64. 256 threads, from the end in runs of 1024 tokens.
-__global__ void __launch_bounds__(256) kda_decay_gate_grad_kernel(const DecayProblem P, const float* z, const float* hT,
-                                                                 const float* dhT, __nv_bfloat16* dg) {
-  __shared__ double part[8];
+// The sums cancel over long sequences: 48 bits. 512 threads, from the end in runs of 4096 tokens.
+constexpr int kGateThreads = 512, kGateEach = 8;
+__global__ void __launch_bounds__(kGateThreads) kda_decay_gate_grad_kernel(const DecayProblem P, const float* z, const float* hT,
+                                                                          const float* dhT, __nv_bfloat16* dg) {
+  constexpr int kWarps = kGateThreads / 32;
+  __shared__ Sum2 part[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t n = blockIdx.x / P.Hv;
   const int h = (int)(blockIdx.x % P.Hv);
   const DecaySpan sp = decay_span(P, n);
-  auto block_sum = [&](double x) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    __syncthreads();
-    if (lane == 0) part[warp] = x;
-    __syncthreads();
-    double s = 0.0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) s += part[k];
-    return s;
-  };
-  double acc = 0.0;
-  if (dhT) {
+  z += (int64_t)h * P.Ttot + sp.t0;
+  Sum2 acc{0.f, 0.f};  // of what lies behind the run
+  if (dhT && sp.len) {
     const int64_t base = (n * P.Hv + h) * kDim * kDim;
-    float x = 0.f;  // (64 products a thread)
-    for (int j = tid; j < kDim * kDim; j += 256) x = fmaf(hT[base + j], dhT[base + j], x);
-    acc = block_sum((double)x);
-  }
-  for (int64_t end = sp.len; end > 0; end -= 1024) {
-    // this thread's four tokens, the last first
-    const int64_t t = end - 1 - 4 * tid;
-    double s[4], run = 0.0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      run += t - j >= 0 ? (double)z[(sp.t0 + t - j) * P.Hv + h] : 0.0;
-      s[j] = run;
+    Sum2 x{0.f, 0.f};
+#pragma unroll 8
+    for (int j = 4 * tid; j < kDim * kDim; j += 4 * kGateThreads) {
+      const float4 a = *reinterpret_cast<const float4*>(hT + base + j), b = *reinterpret_cast<const float4*>(dhT + base + j);
+      x.add(a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w);
     }
-    double pre = run;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const double p = __shfl_up_sync(0xffffffffu, pre, d);
-      if (lane >= d) pre += p;
+      const Sum2 p = x.from(d);
+      if (lane >= d) x.add(p);
     }
+    if (lane == 31) part[warp] = x;
     __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) acc.add(part[k]);
+    __syncthreads();
+  }
+  for (int64_t end = sp.len; end > 0; end -= kGateThreads * kGateEach) {
+    const int64_t t = end - 1 - kGateEach * tid;  // this thread's tokens, the last first
+    float v[kGateEach];
+#pragma unroll
+    for (int j = 0; j < kGateEach; ++j) v[j] = t - j >= 0 ? z[t - j] : 0.f;
+    Sum2 run{0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < kGateEach; ++j) run.add(v[j]);
+    Sum2 pre = run;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const Sum2 p = pre.from(d);
+      if (lane >= d) pre.add(p);
+    }
     if (lane == 31) part[warp] = pre;
+    Sum2 mine = pre.from(1);
+    if (lane == 0) mine = Sum2{0.f, 0.f};
     __syncthreads();
-    double before = acc + pre - run, all = 0.0;
+    Sum2 before = acc;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (k < warp) before += part[k];
-      all += part[k];
+    for (int k = 0; k < kWarps; ++k) {
+      if (k < warp) before.add(part[k]);
+      acc.add(part[k]);
     }
+    before.add(mine);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (t - j >= 0) dg[(sp.t0 + t - j) * P.Hv + h] = __float2bfloat16_rn((float)(before + s[j]));
-    acc += all;
+    for (int j = 0; j < kGateEach; ++j) {
+      before.add(v[j]);
+      if (t - j >= 0) dg[(sp.t0 + t - j) * P.Hv + h] = __float2bfloat16_rn(before.hi + before.lo);
+    }
+    __syncthreads();
   }
 }
 
@@ -885,24 +926,17 @@ SegWs carve_segments(int64_t N, int64_t Ttot, int64_t Hv, int64_t seg) {
   return w;
 }
 
-// After the segments: the final state (for the decays' gradient), FP32 dq and dk of each value head, and
-// what crosses each token and head.
+// After the segments: FP32 dq and dk of each value head, and what crosses each token and head.
 struct GradWs {
-  size_t hT, dq, dk, z, total;
+  size_t dq, dk, z, total;
 };
-GradWs carve_grads(int64_t N, int64_t Ttot, int64_t Hqk, int64_t Hv, bool per_token) {
-  GradWs w{0, 0, 0, 0, 0};
-  size_t at = 0;
+GradWs carve_grads(int64_t Ttot, int64_t Hqk, int64_t Hv, bool per_token) {
+  GradWs w{0, 0, 0, 0};
+  if (!per_token && Hqk == Hv) return w;
   const size_t rows = (size_t)Ttot * Hv;
-  if (per_token) at = ctx_align_up(sizeof(float) * (size_t)N * Hv * kDim * kDim);
-  w.dq = w.dk = w.z = at;
-  if (per_token || Hqk != Hv) {
-    w.dk = ctx_align_up(w.dq + sizeof(float) * rows * kDim);
-    w.z = ctx_align_up(w.dk + sizeof(float) * rows * kDim);
-    at = w.z;
-  }
-  if (per_token) at = ctx_align_up(w.z + sizeof(float) * rows);
-  w.total = at;
+  w.dk = ctx_align_up(sizeof(float) * rows * kDim);
+  w.z = ctx_align_up(w.dk + sizeof(float) * rows * kDim);
+  w.total = ctx_align_up(w.z + (per_token ? sizeof(float) * rows : 0));
   return w;
 }
 
@@ -983,25 +1017,19 @@ int64_t decay_segment_tokens(const int64_t* cu, int64_t N, int64_t T, int64_t Hv
   return longest <= 3 * seg ? 0 : seg * kC;
 }
 
-size_t decay_workspace_bytes(int64_t N, int64_t Ttot, int64_t Hqk, int64_t Hv, int64_t seg, bool training) {
-  // (the larger of the two kinds of decay: the size does not depend on which a call uses)
-  return carve_segments(N, Ttot, Hv, seg).total + (training ? carve_grads(N, Ttot, Hqk, Hv, true).total : 0);
+size_t decay_workspace_bytes(int64_t N, int64_t Ttot, int64_t Hqk, int64_t Hv, int64_t seg, bool training, bool per_token) {
+  return carve_segments(N, Ttot, Hv, seg).total + (training ? carve_grads(Ttot, Hqk, Hv, per_token).total : 0);
 }
 
-cudaError_t launch_decay_forward(const DecayProblem& P, const DecayStates& st, __nv_bfloat16* o, void* ws,
-                                 bool training, cudaStream_t s) {
+cudaError_t launch_decay_forward(const DecayProblem& P, const DecayStates& st, __nv_bfloat16* o, void* ws, cudaStream_t s) {
   const Role q{P.q, P.qt, P.qh, P.Hqk}, k{P.k, P.kt, P.kh, P.Hqk}, v{P.v, P.vt, P.vh, P.Hv};
-  cudaError_t e = pass<false>(P, q, k, v, P.scale, P.scale, 1.f, st, false, o, nullptr, ws, s);
-  if (e == cudaSuccess && training && P.per_token)
-    e = cudaMemcpyAsync(reinterpret_cast<char*>(ws) + carve_segments(P.N, P.Ttot, P.Hv, P.seg).total, st.out,
-                        sizeof(float) * P.N * P.Hv * kDim * kDim, cudaMemcpyDeviceToDevice, s);
-  return e;
+  return pass<false>(P, q, k, v, P.scale, P.scale, 1.f, st, false, o, nullptr, ws, s);
 }
 
-cudaError_t launch_decay_backward(const DecayProblem& P, const float* h0, const DecayGrads& g, void* ws,
+cudaError_t launch_decay_backward(const DecayProblem& P, const float* h0, const float* hT, const DecayGrads& g, void* ws,
                                   cudaStream_t s) {
   char* base = reinterpret_cast<char*>(ws) + carve_segments(P.N, P.Ttot, P.Hv, P.seg).total;
-  const GradWs w = carve_grads(P.N, P.Ttot, P.Hqk, P.Hv, P.per_token);
+  const GradWs w = carve_grads(P.Ttot, P.Hqk, P.Hv, P.per_token);
   // summed over a group's heads, and in the decays' gradient over the whole sequence (differences of large numbers):
   // dq and dk stay FP32 until then
   const bool f32 = g.dg || P.r > 1;
@@ -1019,17 +1047,14 @@ cudaError_t launch_decay_backward(const DecayProblem& P, const float* h0, const 
   if ((e = pass<true>(P, k, q, d, 1.f, c, c, DecayStates{g.d_hT, g.dh0, 0, nullptr, P.N}, false, g.dv, nullptr, ws,
                       s)) != cudaSuccess) return e;
   if (P.Ttot == 0 || !f32) return cudaSuccess;
-  if (g.dg) {
-    float* z = reinterpret_cast<float*>(base + w.z);
-    kda_decay_cross_kernel<<<(unsigned)((P.Ttot * P.Hv + 7) / 8), 256, 0, s>>>(P, dq, dk, z);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    kda_decay_gate_grad_kernel<<<(unsigned)(P.N * P.Hv), 256, 0, s>>>(P, z, reinterpret_cast<const float*>(base), g.d_hT, g.dg);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
-  const int64_t rows = P.Ttot * P.Hqk;
-  const unsigned grid = (unsigned)((rows * kDim / 4 + 255) / 256);
-  kda_decay_group_sum_kernel<<<grid, 256, 0, s>>>(dq, g.dq, rows, P.r);
-  kda_decay_group_sum_kernel<<<grid, 256, 0, s>>>(dk, g.dk, rows, P.r);
+  float* z = reinterpret_cast<float*>(base + w.z);
+  const int64_t blocks = (P.Ttot + 7) / 8 * P.Hqk;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  const unsigned grid = (unsigned)blocks;
+  if (g.dg) kda_decay_group_sum_kernel<true><<<grid, 256, 0, s>>>(P, dq, dk, g.dq, g.dk, z);
+  else kda_decay_group_sum_kernel<false><<<grid, 256, 0, s>>>(P, dq, dk, g.dq, g.dk, nullptr);
+  if ((e = cudaGetLastError()) != cudaSuccess || !g.dg) return e;
+  kda_decay_gate_grad_kernel<<<(unsigned)(P.N * P.Hv), kGateThreads, 0, s>>>(P, z, hT, g.d_hT, g.dg);
   return cudaGetLastError();
 }
 

@@ -149,20 +149,20 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def decay_workspace_bytes(B, T, Hqk, Hv, cu_seqlens_cpu=None, training=True) -> int:
+def decay_workspace_bytes(B, T, Hqk, Hv, cu_seqlens_cpu=None, per_token=True, training=True) -> int:
     """Device bytes that kda_decay_attn_fwd and _bwd (or, training False, kda_decay_attn_prefill)
-    need for this problem."""
+    need for this problem, with decays for each token or fixed for each head."""
     lib = load_library()
     out = ctypes.c_size_t(0)
     n = 0 if cu_seqlens_cpu is None else cu_seqlens_cpu.numel() - 1
-    _check(lib.kda_decay_attn_workspace_bytes(B, T, Hqk, Hv, _p(cu_seqlens_cpu), n, int(training), ctypes.byref(out)))
+    _check(lib.kda_decay_attn_workspace_bytes(B, T, Hqk, Hv, _p(cu_seqlens_cpu), n, int(per_token), int(training), ctypes.byref(out)))
     return out.value
 
 
 class DecayContext:
-    """What the backward of one forward call needs: the borrowed inputs with their tensor versions
-    (they must not change before the backward) and the workspace the forward filled. Passing it back
-    as ``context_out`` reuses the workspace for another call of the same shapes."""
+    """What the backward of one forward call needs: the borrowed inputs and final state with their tensor
+    versions (they must not change before the backward), and a workspace. Passing it back as
+    ``context_out`` uses the workspace again for another call of the same shapes and lengths."""
 
     def __init__(self, key, nbytes, device):
         self.key = key
@@ -181,7 +181,7 @@ class DecayContext:
         if not self.inputs:
             raise KdaError(4, "the context holds no forward")
         if self.versions != tuple(t._version for t in self.inputs if t is not None):
-            raise KdaError(4, "an input of the forward was modified before the backward")
+            raise KdaError(4, "an input or the final state of the forward was modified before the backward")
 
     def status(self):
         """Waits for the device and raises if a bounded device wait of these calls gave up."""
@@ -209,11 +209,15 @@ def kda_decay_attn_fwd(q, k, v, log_decay, initial_state=None, cu_seqlens=None, 
     if initial_state is not None:
         _want(initial_state, "initial_state", _F32, (N, Hv, D, D), dev)
     ctx = context_out
-    key = (B, T, Hqk, Hv, N)
+    key = (B, T, Hqk, Hv, N, per_token)
     if ctx is None:
-        ctx = DecayContext(key, decay_workspace_bytes(B, T, Hqk, Hv, cu_host), dev)
+        ctx = DecayContext(key, decay_workspace_bytes(B, T, Hqk, Hv, cu_host, per_token), dev)
     elif ctx.key != key or ctx.device != dev:
-        raise KdaError(4, "context reuse needs the same shapes and device")
+        raise KdaError(4, "context reuse needs the same shapes, kind of decay and device")
+    elif cu_host is not None and cu_host is not ctx.cu:
+        nbytes = decay_workspace_bytes(B, T, Hqk, Hv, cu_host, per_token)  # other lengths may need more
+        if nbytes > ctx.workspace.numel():
+            ctx.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     o = torch.empty((B, T, Hv, D), dtype=_BF16, device=dev) if out is None else out
     hT = torch.empty((N, Hv, D, D), dtype=_F32, device=dev) if final_state_out is None else final_state_out
     if out is not None:
@@ -227,7 +231,7 @@ def kda_decay_attn_fwd(q, k, v, log_decay, initial_state=None, cu_seqlens=None, 
     with _on(dev) as stream:
         _check(lib.kda_decay_attn_fwd(*call, o.data_ptr(), hT.data_ptr(), ws.data_ptr(), ws.numel(),
                                       ctx.device_status.data_ptr(), stream))
-    ctx._snapshot((q, k, v, log_decay, initial_state, cu_seqlens), call, cu_host,
+    ctx._snapshot((q, k, v, log_decay, initial_state, cu_seqlens, hT), call, cu_host,
                   (q.shape, v.shape, (N, Hv, D, D), per_token))
     return o, hT, ctx
 
@@ -261,7 +265,7 @@ def kda_decay_attn_bwd(ctx: DecayContext, do, dfinal_state=None, out=None):
                 _want(t, ("dq", "dk", "dv", "dlog_decay", "dinitial_state")[i], _F32 if i == 4 else _BF16, s, dev)
     ws = ctx.workspace
     with _on(dev) as stream:
-        _check(lib.kda_decay_attn_bwd(*ctx.call, do.data_ptr(), _p(dfinal_state), *[_p(t) for t in out], ws.data_ptr(),
+        _check(lib.kda_decay_attn_bwd(*ctx.call, ctx.inputs[6].data_ptr(), do.data_ptr(), _p(dfinal_state), *[_p(t) for t in out], ws.data_ptr(),
                                       ws.numel(), ctx.device_status.data_ptr(), stream))
     return tuple(out)
 
@@ -288,7 +292,7 @@ def kda_decay_attn_prefill(q, k, v, log_decay, state, cu_seqlens=None, state_ind
     if device_status is not None:
         _want(device_status, "device_status", _I32, device_status.shape, dev)
     if workspace is None:
-        nbytes = decay_workspace_bytes(B, T, Hqk, Hv, cu_host, False)
+        nbytes = decay_workspace_bytes(B, T, Hqk, Hv, cu_host, per_token, False)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     else:
         _want(workspace, "workspace", torch.uint8, workspace.shape, dev)

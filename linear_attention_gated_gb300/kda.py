@@ -95,9 +95,9 @@ def load_library(path: str = LIB_PATH):
     i32 = ctypes.c_int32
     decay = [P] * 4 + [i32]  # q, k, v, log_decay, decay_per_token
     shape = [P, P, I, I, I, I, I, I, F, P]  # cu_seqlens, its mirror, N, B, T, Hqk, Hv, head_dim, scale, strides
-    lib.kda_decay_attn_workspace_bytes.argtypes = [I, I, I, I, P, I, i32, ctypes.POINTER(S)]
+    lib.kda_decay_attn_workspace_bytes.argtypes = [I, I, I, I, P, I, i32, i32, ctypes.POINTER(S)]
     lib.kda_decay_attn_fwd.argtypes = decay + [P] + shape + [P, P, P, S, P, P]
-    lib.kda_decay_attn_bwd.argtypes = decay + [P] + shape + [P] * 7 + [P, S, P, P]
+    lib.kda_decay_attn_bwd.argtypes = decay + [P] + shape + [P] * 8 + [P, S, P, P]
     lib.kda_decay_attn_prefill.argtypes = decay + shape + [P, i32, P, P, I, P, P, S, P, P]
     lib.kda_decay_attn_decode.argtypes = decay + [P, i32, P, P, I, I, I, I, I, F, P, P, P]
     rope = [i32, P, P, P, P, I, I, I, I, I, F, i32, P, P, P]  # dtype to the two outputs

@@ -32,7 +32,7 @@ def arr(values, kind=ctypes.c_int64):
 
 def ws_bytes(lib, B=1, T=64, hqk=2, hv=4, cu=None, training=1):
     n = ctypes.c_size_t(0)
-    rc = lib.kda_decay_attn_workspace_bytes(B, T, hqk, hv, arr(cu), 0 if cu is None else len(cu) - 1, training, ctypes.byref(n))
+    rc = lib.kda_decay_attn_workspace_bytes(B, T, hqk, hv, arr(cu), 0 if cu is None else len(cu) - 1, 1, training, ctypes.byref(n))
     return rc, n.value
 
 
@@ -51,7 +51,7 @@ def fwd(lib, B=1, T=64, hqk=2, hv=4, cu=None, cu_dev=0, per_token=1, head_dim=12
     (dict(B=0), 1), (dict(T=-1), 1), (dict(hqk=0), 1), (dict(hqk=3, hv=4), 1),
     (dict(head_dim=64), 2), (dict(per_token=2), 1), (dict(scale=float("inf")), 1),
     (dict(q=None), 1), (dict(g=None), 1), (dict(o=None), 1), (dict(hT=None), 1),
-    (dict(q=at(0) + 2), 1), (dict(h0=at(4) + 8), 1), (dict(ws=at(8) + 16), 1), (dict(less=1), 7),
+    (dict(q=at(0) + 2), 1), (dict(h0=at(4) + 8), 1), (dict(ws=at(8) + 16), 1), (dict(less=1, hqk=2, hv=4), 7),
     (dict(cu=[0, 30, 60]), 1), (dict(cu=[1, 30, 64]), 1), (dict(cu=[0, 40, 30, 64]), 1), (dict(cu=[0]), 1),
     (dict(cu=[0, 64], B=2), 1), (dict(cu=[0, 64], cu_dev=1, o=at(0)), 3),
     (dict(o=at(2) + 1024), 3), (dict(hT=at(4)), 3), (dict(ws=at(6)), 3),
@@ -75,14 +75,14 @@ def test_valid_forwards_reach_the_device_check(lib):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(dq=None), 1), (dict(dg=at(13), per_token=0), 2), (dict(dv=at(9)), 3), (dict(dh0=at(12)), 3), (dict(dq=at(10) + 2), 1),
-    (dict(ws=None), 7),
+    (dict(ws=None), 7), (dict(hT=None), 1), (dict(hT=at(15)), 3),
 ])
 def test_backward_refuses(lib, kw, status):
     per_token = kw.pop("per_token", 1)
-    a = dict(do=at(9), dhT=at(14), dq=at(10), dk=at(11), dv=at(12), dg=at(13) if per_token else None, dh0=at(15), ws=at(16))
+    a = dict(hT=at(17), do=at(9), dhT=at(14), dq=at(10), dk=at(11), dv=at(12), dg=at(13) if per_token else None, dh0=at(15), ws=at(16))
     a.update(kw)
     rc = lib.kda_decay_attn_bwd(at(0), at(1), at(2), at(3), per_token, at(4), None, None, 0, 1, 64, 2, 4, 128, NAN, None,
-                                a["do"], a["dhT"], a["dq"], a["dk"], a["dv"], a["dg"], a["dh0"], a["ws"], 1 << 30, None, None)
+                                a["hT"], a["do"], a["dhT"], a["dq"], a["dk"], a["dv"], a["dg"], a["dh0"], a["ws"], 1 << 30, None, None)
     assert rc == status, lib.kda_last_error_message()
 
 
