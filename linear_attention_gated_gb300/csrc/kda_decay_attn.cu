@@ -7,7 +7,6 @@
 
 #include <cmath>
 #include <cstdio>
-#include <unordered_set>
 
 namespace {
 
@@ -252,12 +251,9 @@ extern "C" kda_status kda_decay_attn_prefill(const kda_bf16* q, const kda_bf16* 
     if ((state_indices == nullptr) != (state_indices_host == nullptr))
       return fail(KDA_ERR_INVALID_ARGUMENT, "state_indices needs its host mirror (and the reverse)");
     if (state_indices_host) {
-      std::unordered_set<int32_t> seen;
-      for (int64_t i = 0; i < P.N; ++i) {
-        const int32_t sl = state_indices_host[i];
-        if (sl < 0 || sl >= num_slots) return fail(KDA_ERR_INVALID_ARGUMENT, "state index out of range");
-        if (!seen.insert(sl).second) return fail(KDA_ERR_INVALID_ARGUMENT, "two sequences share a state slot");
-      }
+      const int fault = kda::slot_fault(state_indices_host, P.N, num_slots);
+      if (fault == 1) return fail(KDA_ERR_INVALID_ARGUMENT, "state index out of range");
+      if (fault == 2) return fail(KDA_ERR_INVALID_ARGUMENT, "two sequences share a state slot");
     } else if (num_slots < P.N) {
       return fail(KDA_ERR_INVALID_ARGUMENT, "without state_indices the pool needs a slot per sequence");
     }

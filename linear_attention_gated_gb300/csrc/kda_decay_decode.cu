@@ -15,7 +15,6 @@
 #include "kda_host.h"
 
 #include <cmath>
-#include <unordered_set>
 
 namespace kda {
 namespace {
@@ -137,13 +136,9 @@ extern "C" kda_status kda_decay_attn_decode(const kda_bf16* q, const kda_bf16* k
     if (N && (!q || !k || !v || !log_decay || !state || !o))
       return dfail(KDA_ERR_INVALID_ARGUMENT, "decay_attn decode: null tensor pointer");
     if (state_indices_host) {
-      std::unordered_set<int32_t> seen;
-      for (int64_t i = 0; i < N; ++i) {
-        const int32_t s = state_indices_host[i];
-        if (s < 0 || s >= num_slots) return dfail(KDA_ERR_INVALID_ARGUMENT, "decay_attn decode: state index out of range");
-        if (!seen.insert(s).second)
-          return dfail(KDA_ERR_INVALID_ARGUMENT, "decay_attn decode: two sequences share a state slot");
-      }
+      const int fault = kda::slot_fault(state_indices_host, N, num_slots);
+      if (fault == 1) return dfail(KDA_ERR_INVALID_ARGUMENT, "decay_attn decode: state index out of range");
+      if (fault == 2) return dfail(KDA_ERR_INVALID_ARGUMENT, "decay_attn decode: two sequences share a state slot");
     } else if (num_slots < N) {
       return dfail(KDA_ERR_INVALID_ARGUMENT, "decay_attn decode: without state_indices the pool needs a slot per sequence");
     }

@@ -5,6 +5,7 @@
 
 #include <cstdint>
 #include <new>
+#include <vector>
 
 #include "../../include/kda.h"
 
@@ -24,6 +25,30 @@ inline const char* size_limit_violation(int64_t B, int64_t T, int64_t Hv, int64_
   if (B * T > kMaxTokens / Hv) return "more than 2^40 token-heads";
   if (num_seqs > B * T) return "more sequences than tokens";
   return nullptr;
+}
+
+// The first fault of N slot indices of a pool of `slots`: 1 out of range, 2 a slot used twice, 0 none. (A bit for
+// each slot in a buffer kept per thread; only the words touched are cleared again.)
+inline int slot_fault(const int32_t* idx, int64_t N, int64_t slots) {
+  static thread_local std::vector<uint64_t> seen;
+  for (int64_t i = 0; i < N; ++i)
+    if (idx[i] < 0 || idx[i] >= slots) return 1;
+  if (N < 2) return 0;
+  const size_t words = (size_t)(slots + 63) / 64;
+  if (seen.size() < words) seen.resize(words, 0);
+  int64_t n = 0;
+  int fault = 0;
+  for (; n < N; ++n) {
+    uint64_t& w = seen[(size_t)idx[n] >> 6];
+    const uint64_t bit = uint64_t(1) << (idx[n] & 63);
+    if (w & bit) {
+      fault = 2;
+      break;
+    }
+    w |= bit;
+  }
+  for (int64_t i = 0; i < n; ++i) seen[(size_t)idx[i] >> 6] = 0;
+  return fault;
 }
 
 // Runs the body of a C entry point. A host exception (std::bad_alloc while

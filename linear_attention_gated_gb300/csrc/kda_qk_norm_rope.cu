@@ -11,8 +11,8 @@
 // Memory bound: 10 to 20 flops per value moved. A row belongs to a group of
 // G = 4, 8 or 16 lanes (the power of two at or above D / 16); each lane holds
 // the two 8-value vectors whose elements rotate into each other, so the rotation
-// needs no exchange and the norm log2(G) shuffles. A CTA takes a tile of whole
-// tokens of one tensor (queries or keys), keeps that tensor's weight in
+// needs no exchange and the norm log2(G) shuffles. The next row's loads are under way while a row is worked on. A CTA takes a tile of whole
+// tokens of one tensor (queries or keys) at a time, keeps that tensor's weight in
 // registers and computes each token's cosines and sines once for all its heads.
 //
 // Angles: p f is reduced modulo one turn in 64-bit fixed point, f / 2 pi scaled
@@ -21,6 +21,7 @@
 #include "../../include/kda.h"
 #include "kda_common.cuh"
 #include "kda_host.h"
+#include "tc.cuh"
 
 #include <cuda_fp16.h>
 
@@ -30,7 +31,7 @@
 namespace kda {
 namespace {
 
-constexpr int kNrThreads = 256;
+constexpr int kNrThreads = 128;
 constexpr int kNrTokens = 64;  // most tokens of one tile
 
 struct NrTensor {
@@ -55,52 +56,60 @@ struct NrArgs {
   int ctas0;             // CTAs of the queries
 };
 
+// 8 values of a row: raw as they come from memory, and as four FP32 pairs.
 template <typename T>
 struct Vec8;
 template <>
 struct Vec8<__nv_bfloat16> {
   uint4 r;
+  __device__ __forceinline__ void zero() { r = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void load(const void* p) { r = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void get(float* x) const { unpack_bf16x8(r, x); }
-  static __device__ __forceinline__ void store(void* p, const float* x) {
-    store_bf16x8(reinterpret_cast<__nv_bfloat16*>(p), x);
+  __device__ __forceinline__ void get(float2* x) const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  static __device__ __forceinline__ void store(void* p, const float2* x) {
+    uint4 v;
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(x[i].x, x[i].y);
+    *reinterpret_cast<uint4*>(p) = v;
   }
 };
 template <>
 struct Vec8<__half> {
   uint4 r;
+  __device__ __forceinline__ void zero() { r = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void load(const void* p) { r = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void get(float* x) const {
+  __device__ __forceinline__ void get(float2* x) const {
     const __half2* h = reinterpret_cast<const __half2*>(&r);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(h[i]);
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
+    for (int i = 0; i < 4; ++i) x[i] = __half22float2(h[i]);
   }
-  static __device__ __forceinline__ void store(void* p, const float* x) {
+  static __device__ __forceinline__ void store(void* p, const float2* x) {
     uint4 v;
     __half2* h = reinterpret_cast<__half2*>(&v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(x[i].x, x[i].y);
     *reinterpret_cast<uint4*>(p) = v;
   }
 };
 template <>
 struct Vec8<float> {
   float4 a, b;
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void load(const void* p) {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
   }
-  __device__ __forceinline__ void get(float* x) const {
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  __device__ __forceinline__ void get(float2* x) const {
+    x[0] = make_float2(a.x, a.y); x[1] = make_float2(a.z, a.w);
+    x[2] = make_float2(b.x, b.y); x[3] = make_float2(b.z, b.w);
   }
-  static __device__ __forceinline__ void store(void* p, const float* x) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  static __device__ __forceinline__ void store(void* p, const float2* x) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
   }
 };
 
@@ -126,41 +135,47 @@ __device__ __forceinline__ uint64_t fixed_turns(double f) {
   return t >= 1.0 ? 0ull : (uint64_t)(t * 18446744073709551616.0);
 }
 
-// Rotates the lane's 8 pairs by (cos, sin) (sgn = -1: back). Half pairs: (a[e], b[e]).
-// Interleaved: neighbours inside a (pairs 0..3) and b (pairs 4..7).
-template <bool kInter>
-__device__ __forceinline__ void rotate8(float* a, float* b, const float2* cs, float sgn) {
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// Rotates the lane's 8 pairs by c[d], s[d] (kBack: back), d = 0..7, two FP32 operations to an instruction. Half pairs: value d of a
+// with value d of b. Interleaved: neighbours inside a (pairs 0..3) and b (pairs 4..7).
+template <bool kInter, bool kBack>
+__device__ __forceinline__ void rotate8(float2* a, float2* b, const float* c, const float* s) {
   if constexpr (kInter) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float s0 = sgn * cs[e].y, s1 = sgn * cs[4 + e].y;
-      const float x0 = a[2 * e], y0 = a[2 * e + 1], x1 = b[2 * e], y1 = b[2 * e + 1];
-      a[2 * e] = x0 * cs[e].x - y0 * s0;
-      a[2 * e + 1] = y0 * cs[e].x + x0 * s0;
-      b[2 * e] = x1 * cs[4 + e].x - y1 * s1;
-      b[2 * e + 1] = y1 * cs[4 + e].x + x1 * s1;
+    for (int e = 0; e < 8; ++e) {
+      float2& x = e < 4 ? a[e] : b[e - 4];
+      const float2 turned = kBack ? make_float2(s[e], -s[e]) : make_float2(-s[e], s[e]);
+      x = tc::fma2(make_float2(x.y, x.x), turned, tc::mul2(x, both(c[e])));
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float s = sgn * cs[e].y, x = a[e], y = b[e];
-      a[e] = x * cs[e].x - y * s;
-      b[e] = y * cs[e].x + x * s;
+    for (int e = 0; e < 4; ++e) {
+      const float2 ce = make_float2(c[2 * e], c[2 * e + 1]), se = make_float2(s[2 * e], s[2 * e + 1]);
+      const float2 minus = make_float2(-se.x, -se.y);
+      const float2 x = a[e], y = b[e];
+      a[e] = tc::fma2(y, kBack ? se : minus, tc::mul2(x, ce));
+      b[e] = tc::fma2(x, kBack ? minus : se, tc::mul2(y, ce));
     }
   }
 }
 
+// CTAs an SM: what the registers of two rows in flight leave room for.
+template <typename T, bool kBwd>
+constexpr int kNrBlocks = sizeof(T) == 4 ? (kBwd ? 2 : 4) : (kBwd ? 4 : 6);
+
 template <typename T, int G, bool kInter, bool kBwd>
-__global__ void __launch_bounds__(kNrThreads, kBwd ? 3 : 4) kda_qk_norm_rope_kernel(const NrArgs a) {
+__global__ void __launch_bounds__(kNrThreads, kNrBlocks<T, kBwd>) kda_qk_norm_rope_kernel(const NrArgs a) {
   extern __shared__ __align__(16) unsigned char nr_smem[];
-  float2* cs = reinterpret_cast<float2*>(nr_smem);  // [tokens of the tile][R / 2]
   constexpr int kGroups = kNrThreads / G;
   const int which = (int)blockIdx.x >= a.ctas0;
   const NrTensor& t = a.t[which];
   const int64_t first = which ? (int64_t)blockIdx.x - a.ctas0 : blockIdx.x;
   const int64_t step = which ? (int64_t)gridDim.x - a.ctas0 : a.ctas0;
   const int tid = threadIdx.x, lane = tid % G, group = tid / G;
-  const int R = a.R, half = R / 2;
+  const int R = a.R, half = R / 2, H = t.H;
+  uint64_t* turns_of = reinterpret_cast<uint64_t*>(nr_smem);               // [R / 2] fixed-point frequencies
+  float* cs = reinterpret_cast<float*>(nr_smem + half * sizeof(uint64_t));  // [tokens of the tile][cos, sin][R / 2]
   const bool active = lane < a.D / 16;
   const bool turns = active && 16 * lane < R;
   // the lane's two vectors: the halves of its pairs, or 16 neighbouring values
@@ -169,112 +184,138 @@ __global__ void __launch_bounds__(kNrThreads, kBwd ? 3 : 4) kda_qk_norm_rope_ker
     c0 = 8 * lane;
     c1 = 8 * lane + half;
   }
-  float w0[8], w1[8];
+  auto tokens_of = [&](int64_t tile) {
+    if (tile >= t.tiles) return 0;
+    const int64_t left = a.n - tile * t.tokens;
+    return (int)(left < t.tokens ? left : t.tokens);
+  };
+  // The next row: its token in the tile (with `ntok` or more: none) and head, and its values, on their way. From row to
+  // row of a group: kGroups rows on.
+  const int head0 = group % H, token0 = group / H, head_step = kGroups % H, token_step = kGroups / H;
+  int token = token0, head = head0, ntok = tokens_of(first);
+  int64_t tile = first, tok0 = first * t.tokens;
+  Vec8<T> na, nb, nda, ndb;
+  na.zero(); nb.zero(); nda.zero(); ndb.zero();
+  auto fetch = [&] {
+    if (!active || token >= ntok) return;
+    const T* src = reinterpret_cast<const T*>(t.x) + (tok0 + token) * t.xt + head * t.xh;
+    na.load(src + c0);
+    nb.load(src + c1);
+    if constexpr (kBwd) {
+      const T* sd = reinterpret_cast<const T*>(t.dy) + (tok0 + token) * t.dt + head * t.dh;
+      nda.load(sd + c0);
+      ndb.load(sd + c1);
+    }
+  };
+  fetch();
+  for (int d = tid; d < half; d += kNrThreads) turns_of[d] = fixed_turns(a.freq[d]);
+  float2 w0[4], w1[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w0[e] = w1[e] = 1.f;
+  for (int e = 0; e < 4; ++e) w0[e] = w1[e] = both(1.f);
   if (active && t.w) {
     Vec8<float> v;
     v.load(t.w + c0); v.get(w0);
     v.load(t.w + c1); v.get(w1);
   }
-  float g0[8], g1[8];  // backward: this lane's share of dw
+  float2 g0[4], g1[4];  // backward: this lane's share of dw
 #pragma unroll
-  for (int e = 0; e < 8; ++e) g0[e] = g1[e] = 0.f;
+  for (int e = 0; e < 4; ++e) g0[e] = g1[e] = both(0.f);
   const float inv_d = 1.f / (float)a.D;
-  const T* x = reinterpret_cast<const T*>(t.x);
-  const T* dy = reinterpret_cast<const T*>(t.dy);
-  T* y = reinterpret_cast<T*>(t.y);
 
-  for (int64_t tile = first; tile < t.tiles; tile += step) {
-    const int64_t tok0 = tile * t.tokens;
-    const int ntok = (int)(a.n - tok0 < t.tokens ? a.n - tok0 : t.tokens);
+  while (tile < t.tiles) {
     if (R) {
-      __syncthreads();  // the last tile's rows are done with cs
+      __syncthreads();  // the last tile's rows are done with cs (and the frequencies are there)
       for (int i = tid; i < ntok * half; i += kNrThreads) {
         const int tt = i / half, d = i - tt * half;
-        cs[i] = cos_sin(a.pos[tok0 + tt], fixed_turns(a.freq[d]));
+        const float2 v = cos_sin(a.pos[tok0 + tt], turns_of[d]);
+        cs[tt * R + d] = v.x;
+        cs[tt * R + half + d] = v.y;
       }
       __syncthreads();
     }
-    const int rows = ntok * t.H;
     // all lanes of a warp make the same number of rounds: the shuffles are warp wide
-    for (int row0 = 0; row0 < rows; row0 += kGroups) {
-      const int row = row0 + group;
-      const bool live = active && row < rows;
-      int tt = 0, h = row;
-      if (t.tokens > 1) {
-        tt = row / t.H;
-        h = row - tt * t.H;
+    const int rounds = (ntok * H + kGroups - 1) / kGroups;
+    for (int i = 0; i < rounds; ++i) {
+      const bool live = active && token < ntok;
+      float2 p[4], q[4], u[4], v[4];
+      na.get(p);
+      nb.get(q);
+      if constexpr (kBwd) {
+        nda.get(u);
+        ndb.get(v);
       }
-      const int64_t tok = tok0 + tt;
-      float p[8], q[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) p[e] = q[e] = 0.f;
-      Vec8<T> va, vb, da, db;
-      if (live) {
-        const T* src = x + tok * t.xt + h * t.xh;
-        va.load(src + c0);
-        vb.load(src + c1);
-        if constexpr (kBwd) {
-          const T* sd = dy + tok * t.dt + h * t.dh;
-          da.load(sd + c0);
-          db.load(sd + c1);
-        }
-        va.get(p);
-        vb.get(q);
+      T* out = reinterpret_cast<T*>(t.y) + (tok0 + token) * t.yt + head * t.yh;
+      const float* angle = cs + (live && turns ? token * R + 8 * lane : 0);
+      // the next row is on its way while this one is worked on
+      head += head_step;
+      token += token_step;
+      if (head >= H) {
+        head -= H;
+        ++token;
       }
-      float ss = 0.f;
+      if (i == rounds - 1) {
+        tile += step;
+        tok0 = tile * t.tokens;
+        ntok = tokens_of(tile);
+        token = token0;
+        head = head0;
+      }
+      fetch();
+      float2 s2 = tc::mul2(p[0], p[0]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss += p[e] * p[e] + q[e] * q[e];
-      const float r = rsqrtf(group_sum<G>(ss) * inv_d + a.eps);
-      float2 c[8];
+      for (int e = 1; e < 4; ++e) s2 = tc::fma2(p[e], p[e], s2);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s2 = tc::fma2(q[e], q[e], s2);
+      const float r = rsqrtf(group_sum<G>(s2.x + s2.y) * inv_d + a.eps);
+      float c[8], s[8];
       if (turns) {
-        const float4* src = reinterpret_cast<const float4*>(cs + (live ? tt : 0) * half + 8 * lane);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 v = src[e];
-          c[2 * e] = make_float2(v.x, v.y);
-          c[2 * e + 1] = make_float2(v.z, v.w);
+        for (int e = 0; e < 8; e += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(angle + e), y = *reinterpret_cast<const float4*>(angle + half + e);
+          c[e] = x.x; c[e + 1] = x.y; c[e + 2] = x.z; c[e + 3] = x.w;
+          s[e] = y.x; s[e + 1] = y.y; s[e + 2] = y.z; s[e + 3] = y.w;
         }
+      }
+      const float2 rr = both(r);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        p[e] = tc::mul2(p[e], rr);
+        q[e] = tc::mul2(q[e], rr);
       }
       if constexpr (!kBwd) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          p[e] = p[e] * r * w0[e];
-          q[e] = q[e] * r * w1[e];
+        for (int e = 0; e < 4; ++e) {
+          p[e] = tc::mul2(p[e], w0[e]);
+          q[e] = tc::mul2(q[e], w1[e]);
         }
-        if (turns) rotate8<kInter>(p, q, c, 1.f);
+        if (turns) rotate8<kInter, false>(p, q, c, s);
       } else {
-        float u[8], v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] = v[e] = 0.f;
+        if (turns) rotate8<kInter, true>(u, v, c, s);
         if (live) {
-          da.get(u);
-          db.get(v);
-        }
-        if (turns) rotate8<kInter>(u, v, c, -1.f);
-        float dot = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          p[e] *= r;
-          q[e] *= r;
-          g0[e] = fmaf(u[e], p[e], g0[e]);
-          g1[e] = fmaf(v[e], q[e], g1[e]);
-          u[e] *= w0[e];
-          v[e] *= w1[e];
-          dot += u[e] * p[e] + v[e] * q[e];
+          for (int e = 0; e < 4; ++e) {
+            g0[e] = tc::fma2(u[e], p[e], g0[e]);
+            g1[e] = tc::fma2(v[e], q[e], g1[e]);
+          }
         }
-        dot = group_sum<G>(dot) * inv_d;
+        float2 d2 = both(0.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          p[e] = r * (u[e] - p[e] * dot);
-          q[e] = r * (v[e] - q[e] * dot);
+        for (int e = 0; e < 4; ++e) {
+          u[e] = tc::mul2(u[e], w0[e]);
+          v[e] = tc::mul2(v[e], w1[e]);
+          d2 = tc::fma2(u[e], p[e], d2);
+          d2 = tc::fma2(v[e], q[e], d2);
+        }
+        const float2 minus = both(-group_sum<G>(d2.x + d2.y) * inv_d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[e] = tc::mul2(rr, tc::fma2(p[e], minus, u[e]));
+          q[e] = tc::mul2(rr, tc::fma2(q[e], minus, v[e]));
         }
       }
       if (live) {
-        T* dst = y + tok * t.yt + h * t.yh;
-        Vec8<T>::store(dst + c0, p);
-        Vec8<T>::store(dst + c1, q);
+        Vec8<T>::store(out + c0, p);
+        Vec8<T>::store(out + c1, q);
       }
     }
   }
@@ -282,20 +323,22 @@ __global__ void __launch_bounds__(kNrThreads, kBwd ? 3 : 4) kda_qk_norm_rope_ker
     // the CTA's share of dw: the groups' sums in a fixed order
     float* acc = reinterpret_cast<float*>(nr_smem);  // [groups of a warp summed: warps][16 G]
     __syncthreads();
+    float* f0 = reinterpret_cast<float*>(g0);
+    float* f1 = reinterpret_cast<float*>(g1);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
 #pragma unroll
       for (int o = G; o < 32; o <<= 1) {
-        g0[e] += __shfl_xor_sync(0xffffffffu, g0[e], o);
-        g1[e] += __shfl_xor_sync(0xffffffffu, g1[e], o);
+        f0[e] += __shfl_xor_sync(0xffffffffu, f0[e], o);
+        f1[e] += __shfl_xor_sync(0xffffffffu, f1[e], o);
       }
     }
     const int warp = tid >> 5;
     if ((tid & 31) < G && active) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        acc[warp * a.D + c0 + e] = g0[e];
-        acc[warp * a.D + c1 + e] = g1[e];
+        acc[warp * a.D + c0 + e] = f0[e];
+        acc[warp * a.D + c1 + e] = f1[e];
       }
     }
     __syncthreads();
@@ -308,21 +351,21 @@ __global__ void __launch_bounds__(kNrThreads, kBwd ? 3 : 4) kda_qk_norm_rope_ker
   }
 }
 
-// dw of queries (block y 0) and keys (1): 32 columns a CTA, eight partial sums each.
-__global__ void __launch_bounds__(256) kda_norm_weight_grad_kernel(const float* part, int ctas0, int ctas, int D,
+// dw of queries (block y 0) and keys (1): 32 columns a CTA, 32 partial sums each.
+__global__ void __launch_bounds__(1024) kda_norm_weight_grad_kernel(const float* part, int ctas0, int ctas, int D,
                                                                    float* dqw, float* dkw) {
-  __shared__ float s[8][32];
+  __shared__ float s[32][32];
   const int col = threadIdx.x & 31, lane = threadIdx.x >> 5, d = blockIdx.x * 32 + col;
   const int lo = blockIdx.y ? ctas0 : 0, hi = blockIdx.y ? ctas : ctas0;
   float* out = blockIdx.y ? dkw : dqw;
   float x = 0.f;
   if (d < D && out)
-    for (int i = lo + lane; i < hi; i += 8) x += part[(int64_t)i * D + d];
+    for (int i = lo + lane; i < hi; i += 32) x += part[(int64_t)i * D + d];
   s[lane][col] = x;
   __syncthreads();
   if (lane == 0 && d < D && out) {
 #pragma unroll
-    for (int k = 1; k < 8; ++k) x += s[k][col];
+    for (int k = 1; k < 32; ++k) x += s[k][col];
     out[d] = x;
   }
 }
@@ -332,7 +375,7 @@ kda_status nfail(kda_status st, const char* msg) {
   return st;
 }
 
-constexpr int64_t kNrMaxCtas = 152 * 4;  // CTAs of one tensor in the backward: rows of dw_part
+constexpr int64_t kNrMaxCtas = 152 * 6;  // most CTAs (backward: rows of dw_part)
 
 // A strided [tokens, heads, D] view in bytes.
 struct View {
@@ -481,6 +524,9 @@ kda_status nr_run(const NrCall& c) {
   a.D = (int)c.D;
   a.R = (int)c.R;
   a.eps = c.eps;
+  const bool wide = c.dtype == KDA_DTYPE_FP32;
+  const int64_t resident = 152 * (wide ? (c.bwd ? kNrBlocks<float, true> : kNrBlocks<float, false>)
+                                       : (c.bwd ? kNrBlocks<__half, true> : kNrBlocks<__half, false>));
   int64_t ctas[2];
   int most = 1;
   for (int i = 0; i < 2; ++i) {
@@ -493,17 +539,20 @@ kda_status nr_run(const NrCall& c) {
     t.yt = st[4 + 2 * i]; t.yh = st[5 + 2 * i];
     t.dt = c.bwd ? st[8 + 2 * i] : 0; t.dh = c.bwd ? st[9 + 2 * i] : 0;
     t.H = (int)heads[i];
-    // whole tokens, at least 64 rows a tile where there are as many
-    int64_t tt = (63 + t.H) / t.H;
+    // whole tokens: 256 rows a tile (barriers and angles count less) where that leaves every CTA one, else 64
+    const int64_t want = c.n * (c.Hq + c.Hk) >= 256 * resident ? 256 : 64;
+    int64_t tt = (want - 1 + t.H) / t.H;
     if (tt > kNrTokens) tt = kNrTokens;
     t.tokens = (int)tt;
     t.tiles = (c.n + tt - 1) / tt;
-    ctas[i] = c.bwd && t.tiles > kNrMaxCtas ? kNrMaxCtas : t.tiles;
-    if (ctas[i] > INT32_MAX / 4) return nfail(KDA_ERR_UNSUPPORTED, "qk_norm_rope: too many tokens");
+    // the CTAs that run at once, shared out by rows; each takes its tiles in turn
+    ctas[i] = resident * t.H / (c.Hq + c.Hk);
+    if (ctas[i] < 1) ctas[i] = 1;
+    if (ctas[i] > t.tiles) ctas[i] = t.tiles;
     if (t.tokens > most) most = t.tokens;
   }
   a.ctas0 = (int)ctas[0];
-  size_t smem = (size_t)most * (c.R / 2) * sizeof(float2);
+  size_t smem = (size_t)(c.R / 2) * (sizeof(uint64_t) + most * 2 * sizeof(float));
   if (c.bwd && smem < sizeof(float) * 8 * c.D) smem = sizeof(float) * 8 * c.D;
   const int64_t grid = ctas[0] + ctas[1];
   if (grid > 0) {
@@ -513,7 +562,7 @@ kda_status nr_run(const NrCall& c) {
     if (e != cudaSuccess) return nfail(KDA_ERR_CUDA, cudaGetErrorString(e));
   }
   if (c.bwd && (c.dqw || c.dkw)) {
-    kda_norm_weight_grad_kernel<<<dim3((unsigned)((c.D + 31) / 32), 2), 256, 0, c.stream>>>(
+    kda_norm_weight_grad_kernel<<<dim3((unsigned)((c.D + 31) / 32), 2), 1024, 0, c.stream>>>(
         c.part, (int)ctas[0], (int)grid, (int)c.D, c.dqw, c.dkw);
     if ((e = cudaGetLastError()) != cudaSuccess) return nfail(KDA_ERR_CUDA, cudaGetErrorString(e));
   }
@@ -544,7 +593,7 @@ extern "C" kda_status kda_qk_norm_rope_fwd(const void* q, const void* k, int32_t
 extern "C" kda_status kda_qk_norm_rope_workspace_bytes(int64_t head_dim, size_t* bytes) {
   if (!bytes || head_dim < 16 || head_dim > 256 || head_dim % 16)
     return kda::nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: bytes is NULL or head_dim unsupported");
-  *bytes = 2 * kda::kNrMaxCtas * (size_t)head_dim * sizeof(float);
+  *bytes = kda::kNrMaxCtas * (size_t)head_dim * sizeof(float);
   return KDA_OK;
 }
 
@@ -566,7 +615,7 @@ extern "C" kda_status kda_qk_norm_rope_bwd(const void* dq, const void* dk, const
     c.part = reinterpret_cast<float*>(workspace);
     c.bwd = true;
     c.stream = stream;
-    if (workspace && workspace_bytes < 2 * kda::kNrMaxCtas * (size_t)(head_dim > 0 ? head_dim : 0) * sizeof(float))
+    if (workspace && workspace_bytes < kda::kNrMaxCtas * (size_t)(head_dim > 0 ? head_dim : 0) * sizeof(float))
       return kda::nfail(KDA_ERR_WORKSPACE_TOO_SMALL, "qk_norm_rope: workspace below kda_qk_norm_rope_workspace_bytes()");
     if ((uintptr_t)workspace & 15u) return kda::nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: workspace must be 16-byte aligned");
     return kda::nr_run(c);

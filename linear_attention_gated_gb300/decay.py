@@ -17,35 +17,34 @@ from .kda import KdaError, _check, load_library
 
 DIM = 128
 _NAN = float("nan")
+_UNCUT = 1536  # sequences up to this long are never cut into segments: prefill needs no workspace for them
 _BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 _STATE = {torch.bfloat16: 0, torch.float32: 1}
 _ROPE_TYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 
 
-class _on:
-    """The device of the call's tensors made current, where it is not already, and its stream."""
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
 
-    __slots__ = ("device", "index", "before")
 
-    def __init__(self, device):
-        if device.type != "cuda":
-            raise ValueError("tensors must be CUDA tensors")
-        self.index = device.index
-        self.before = None
-
-    def __enter__(self):
-        now = torch.cuda.current_device()
-        if now != self.index:
-            self.before = now
-            torch.cuda.set_device(self.index)
-        return torch.cuda.current_stream(self.index).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.before is not None:
-            torch.cuda.set_device(self.before)
+def _call(f, device, *args):
+    """f(*args, stream) with `device` current, its status checked. (The small calls are host-bound: torch's stream and
+    device objects would cost as much as the launch.)"""
+    if device.type != "cuda":
+        raise ValueError("tensors must be CUDA tensors")
+    index = device.index
+    stream = torch.cuda.current_stream(index).cuda_stream if _raw_stream is None else _raw_stream(index)
+    if torch.cuda.current_device() == index:
+        rc = f(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            rc = f(*args, stream)
+    if rc:
+        _check(rc)
 
 
 def _typed(t, name, dtype, shape, device):
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device:
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -228,9 +227,8 @@ def kda_decay_attn_fwd(q, k, v, log_decay, initial_state=None, cu_seqlens=None, 
     call = (q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), per_token, _p(initial_state), _p(cu_seqlens),
             _p(cu_host), N, B, T, Hqk, Hv, D, s, strides)
     ws = ctx.workspace
-    with _on(dev) as stream:
-        _check(lib.kda_decay_attn_fwd(*call, o.data_ptr(), hT.data_ptr(), ws.data_ptr(), ws.numel(),
-                                      ctx.device_status.data_ptr(), stream))
+    _call(lib.kda_decay_attn_fwd, dev, *call, o.data_ptr(), hT.data_ptr(), ws.data_ptr(), ws.numel(),
+          ctx.device_status.data_ptr())
     ctx._snapshot((q, k, v, log_decay, initial_state, cu_seqlens, hT), call, cu_host,
                   (q.shape, v.shape, (N, Hv, D, D), per_token))
     return o, hT, ctx
@@ -264,9 +262,8 @@ def kda_decay_attn_bwd(ctx: DecayContext, do, dfinal_state=None, out=None):
             else:
                 _want(t, ("dq", "dk", "dv", "dlog_decay", "dinitial_state")[i], _F32 if i == 4 else _BF16, s, dev)
     ws = ctx.workspace
-    with _on(dev) as stream:
-        _check(lib.kda_decay_attn_bwd(*ctx.call, ctx.inputs[6].data_ptr(), do.data_ptr(), _p(dfinal_state), *[_p(t) for t in out], ws.data_ptr(),
-                                      ws.numel(), ctx.device_status.data_ptr(), stream))
+    _call(lib.kda_decay_attn_bwd, dev, *ctx.call, ctx.inputs[6].data_ptr(), do.data_ptr(), _p(dfinal_state),
+          *[_p(t) for t in out], ws.data_ptr(), ws.numel(), ctx.device_status.data_ptr())
     return tuple(out)
 
 
@@ -292,16 +289,15 @@ def kda_decay_attn_prefill(q, k, v, log_decay, state, cu_seqlens=None, state_ind
     if device_status is not None:
         _want(device_status, "device_status", _I32, device_status.shape, dev)
     if workspace is None:
-        nbytes = decay_workspace_bytes(B, T, Hqk, Hv, cu_host, per_token, False)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        if T > _UNCUT:
+            nbytes = decay_workspace_bytes(B, T, Hqk, Hv, cu_host, per_token, False)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     else:
         _want(workspace, "workspace", torch.uint8, workspace.shape, dev)
-    with _on(dev) as stream:
-        _check(lib.kda_decay_attn_prefill(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), per_token, _p(cu_seqlens), _p(cu_host), N, B, T,
-            Hqk, Hv, D, _NAN if scale is None else float(scale), strides, state.data_ptr(), sdt, _p(state_indices),
-            _p(idx_host), state.shape[0], out.data_ptr(), _p(workspace), 0 if workspace is None else workspace.numel(),
-            _p(device_status), stream))
+    _call(lib.kda_decay_attn_prefill, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), per_token,
+          _p(cu_seqlens), _p(cu_host), N, B, T, Hqk, Hv, D, _NAN if scale is None else float(scale), strides, state.data_ptr(),
+          sdt, _p(state_indices), _p(idx_host), state.shape[0], out.data_ptr(), _p(workspace),
+          0 if workspace is None else workspace.numel(), _p(device_status))
     return out
 
 
@@ -319,14 +315,12 @@ def kda_decay_attn_decode(q, k, v, log_decay, state, state_indices=None, scale=N
     sdt = _pool(state, Hv, D, dev)
     idx_host = _slots(state_indices, state_indices_cpu, N, dev)
     if out is None:
-        out = torch.empty((N, 1, Hv, D), dtype=_BF16, device=dev)
+        out = torch.empty_like(v) if v.is_contiguous() else torch.empty((N, 1, Hv, D), dtype=_BF16, device=dev)
     else:
         _want(out, "out", _BF16, (N, 1, Hv, D), dev)
-    with _on(dev) as stream:
-        _check(lib.kda_decay_attn_decode(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), per_token, state.data_ptr(), sdt,
-            _p(state_indices), _p(idx_host), state.shape[0], N, Hqk, Hv, D, _NAN if scale is None else float(scale), strides,
-            out.data_ptr(), stream))
+    _call(lib.kda_decay_attn_decode, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), per_token,
+          state.data_ptr(), sdt, _p(state_indices), _p(idx_host), state.shape[0], N, Hqk, Hv, D,
+          _NAN if scale is None else float(scale), strides, out.data_ptr())
     return out
 
 
@@ -360,18 +354,17 @@ def kda_qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6
     lib = load_library()
     B, T, Hq, Hk, D, R, dev = _rope_inputs(q, k, q_weight, k_weight, positions, inv_freq)
     if q_out is None:
-        q_out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=dev)
+        q_out = torch.empty_like(q) if q.is_contiguous() else torch.empty((B, T, Hq, D), dtype=q.dtype, device=dev)
     else:
         _typed(q_out, "q_out", q.dtype, q.shape, dev)
     if k_out is None:
-        k_out = torch.empty((B, T, Hk, D), dtype=q.dtype, device=dev)
+        k_out = torch.empty_like(k) if k.is_contiguous() else torch.empty((B, T, Hk, D), dtype=q.dtype, device=dev)
     else:
         _typed(k_out, "k_out", q.dtype, k.shape, dev)
     strides = _all_strides((("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out)))
-    with _on(dev) as stream:
-        _check(lib.kda_qk_norm_rope_fwd(q.data_ptr(), k.data_ptr(), _ROPE_TYPES[q.dtype], _p(q_weight), _p(k_weight),
-                                        _p(positions) if R else None, _p(inv_freq) if R else None, B * T, Hq, Hk, D, R,
-                                        eps, int(bool(interleaved)), strides, q_out.data_ptr(), k_out.data_ptr(), stream))
+    _call(lib.kda_qk_norm_rope_fwd, dev, q.data_ptr(), k.data_ptr(), _ROPE_TYPES[q.dtype], _p(q_weight), _p(k_weight),
+          _p(positions) if R else None, _p(inv_freq) if R else None, B * T, Hq, Hk, D, R, eps, int(bool(interleaved)),
+          strides, q_out.data_ptr(), k_out.data_ptr())
     return q_out, k_out
 
 
@@ -400,10 +393,8 @@ def kda_qk_norm_rope_bwd(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, 
     elif workspace is not None:
         _want(workspace, "workspace", torch.uint8, workspace.shape, dev)
     strides = _all_strides((("q", q), ("k", k), ("out[0]", gq), ("out[1]", gk), ("dq", dq), ("dk", dk)))
-    with _on(dev) as stream:
-        _check(lib.kda_qk_norm_rope_bwd(dq.data_ptr(), dk.data_ptr(), q.data_ptr(), k.data_ptr(), _ROPE_TYPES[q.dtype],
-                                        _p(q_weight), _p(k_weight), _p(positions) if R else None, _p(inv_freq) if R else None,
-                                        B * T, Hq, Hk, D, R, eps, int(bool(interleaved)), strides, gq.data_ptr(),
-                                        gk.data_ptr(), _p(gqw), _p(gkw), _p(workspace),
-                                        0 if workspace is None else workspace.numel(), stream))
+    _call(lib.kda_qk_norm_rope_bwd, dev, dq.data_ptr(), dk.data_ptr(), q.data_ptr(), k.data_ptr(), _ROPE_TYPES[q.dtype],
+          _p(q_weight), _p(k_weight), _p(positions) if R else None, _p(inv_freq) if R else None, B * T, Hq, Hk, D, R, eps,
+          int(bool(interleaved)), strides, gq.data_ptr(), gk.data_ptr(), _p(gqw), _p(gkw), _p(workspace),
+          0 if workspace is None else workspace.numel())
     return gq, gk, gqw, gkw
