@@ -53,7 +53,7 @@ namespace kda {
 namespace {
 
 constexpr int kC = kDecayChunk;
-constexpr int kStages = 3, kDecs = 4, kRing = 4;
+constexpr int kStages = 3, kDecs = 8, kRing = 4;
 constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpDecay = 2, kWarpMma2 = 3, kWarpA = 4, kWarpB = 12;
 constexpr int kGroup = 8;                  // warps of A and of B
 constexpr int kThreads = 32 * 20;
@@ -88,9 +88,9 @@ struct Smem {
   float lam[kDecs];      // e^{b_C}
   uint4 clc;             // response: the next unit
   Unit ring[kRing];      // units to come
-  // full, empty: a stage's tiles are there / read by all products; dec: a chunk's decays; g0, gu, gy: products done
+  // full, empty: a stage's tiles are there / read by all products; dec, decfree: a chunk's decays are there / read by the last who does; g0, gu, gy: products done
   // (scores, U, Y); aready: K~ and P are there; ufree, yfree: U, Y are read; sready: the state is there
-  unsigned long long full[kStages], empty[kStages], dec[kDecs], g0[2], gu, gy, aready[2], ufree, sready[2], yfree;
+  unsigned long long full[kStages], empty[kStages], dec[kDecs], decfree[kDecs], g0[2], gu, gy, aready[2], ufree, sready[2], yfree;
   unsigned long long clcbar, rfull[kRing], rempty[kRing];
   uint32_t tmem;
 };
@@ -184,7 +184,10 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
   if (warp == kWarpMma) tc::tmem_alloc(tc::smem_u32(&sm.tmem), 512);
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) { tc::mbar_init(bar(sm.full[i]), 1); tc::mbar_init(bar(sm.empty[i]), kState ? 1 : 2); }
-    for (int i = 0; i < kDecs; ++i) tc::mbar_init(bar(sm.dec[i]), 1);
+    for (int i = 0; i < kDecs; ++i) {
+      tc::mbar_init(bar(sm.dec[i]), 1);
+      tc::mbar_init(bar(sm.decfree[i]), kGroup);
+    }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar(sm.g0[i]), 1);
       tc::mbar_init(bar(sm.aready[i]), kGroup);
@@ -403,41 +406,53 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           const int lines = kDim * kDim * (!a.sg.len && a.st.bf16 ? 2 : 4) / 128;
           for (int i = lane; i < lines; i += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 128 * i));
         }
-        float total = 0.f, n0 = 0.f, n1 = 0.f;
+        float total = 0.f;  // lane 31's: log2 of the unit's decay
+        // two chunks ahead: a chunk takes less time than a load
         auto fetch = [&](int64_t c) {
           const int64_t j = (kRev ? x.nchunks - 1 - c : c) * kC + 2 * lane;
-          n0 = c < x.nchunks && j < x.len ? decay_g(P, x.t0 + j, x.h) : 0.f;
-          n1 = c < x.nchunks && j + 1 < x.len ? decay_g(P, x.t0 + j + 1, x.h) : 0.f;
+          return make_float2(c < x.nchunks && j < x.len ? decay_g(P, x.t0 + j, x.h) : 0.f,
+                             c < x.nchunks && j + 1 < x.len ? decay_g(P, x.t0 + j + 1, x.h) : 0.f);
         };
-        fetch(0);
+        float2 next = fetch(0), next2 = fetch(1);
         // backwards: the decay of the token that follows the chunk
         float follow = kRev && x.nchunks && x.t0 + x.len < x.end ? decay_log2(decay_g(P, x.t0 + x.len, x.h)) : 0.f;
+        float whole = 0.f;
         for (int64_t c = 0; c < x.nchunks; ++c, ++g) {
-          float g0 = decay_log2(n0);
-          const float g1 = decay_log2(n1);
-          const float lead = __shfl_sync(0xffffffffu, g0, 0);
-          if (kRev && lane == 0) g0 = 0.f;
-          fetch(c + 1);
-          float pre = g0 + g1, suf = pre;
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const float p = __shfl_up_sync(0xffffffffu, pre, d), q = __shfl_down_sync(0xffffffffu, suf, d);
-            if (lane >= d) pre += p;
-            if (lane + d < 32) suf += q;
-          }
-          const float before = __shfl_up_sync(0xffffffffu, pre, 1), after = __shfl_down_sync(0xffffffffu, suf, 1);
-          const float p0 = (lane ? before : 0.f) + g0, s1 = (lane < 31 ? after : 0.f) + follow;
-          const float2 up = make_float2(exp2f(p0), exp2f(pre)), down = make_float2(exp2f(s1 + g1), exp2f(s1));
-          const float2 e = kRev ? down : up, w = kRev ? up : down;
-          // the slot was last read for chunk g - 4: its Y was read before chunk g - 3's products began
-          if (ok && g >= kStages) ok = tc::mbar_wait_lanes(bar(sm.empty[g % kStages]), (g / kStages - 1) & 1);
           const int d = g % kDecs;
-          *reinterpret_cast<float2*>(&sm.b[d][2 * lane]) = make_float2(p0, pre);
-          *reinterpret_cast<float2*>(&sm.eb[d][2 * lane]) = make_float2(a.s_inter * e.x, a.s_inter * e.y);
-          *reinterpret_cast<float2*>(&sm.w[d][2 * lane]) = make_float2(a.s_w * w.x, a.s_w * w.y);
-          if (lane == 31) sm.lam[d] = exp2f(pre + follow);
-          total += pre + follow;  // lane 31's is the chunk's
-          if (kRev) follow = lead;
+          // of a fixed decay every whole chunk has the same numbers, and the slot has them already
+          const bool again = !P.per_token && c > kDecs && (kRev || (c + 1) * kC <= x.len);
+          if (!again) {
+            float g0 = decay_log2(next.x);
+            const float g1 = decay_log2(next.y);
+            next = next2;
+            next2 = fetch(c + 2);
+            const float lead = __shfl_sync(0xffffffffu, g0, 0);
+            if (kRev && lane == 0) g0 = 0.f;
+            float pre = g0 + g1, suf = pre;
+#pragma unroll
+            for (int k = 1; k < 32; k <<= 1) {
+              const float p = __shfl_up_sync(0xffffffffu, pre, k), q = __shfl_down_sync(0xffffffffu, suf, k);
+              if (lane >= k) pre += p;
+              if (lane + k < 32) suf += q;
+            }
+            const float before = __shfl_up_sync(0xffffffffu, pre, 1), after = __shfl_down_sync(0xffffffffu, suf, 1);
+            const float p0 = (lane ? before : 0.f) + g0, s1 = (lane < 31 ? after : 0.f) + follow;
+            const float2 up = make_float2(fast_exp2(p0), fast_exp2(pre)), down = make_float2(fast_exp2(s1 + g1), fast_exp2(s1));
+            const float2 e = kRev ? down : up, w = kRev ? up : down;
+            whole = pre + follow;
+            const float lam = fast_exp2(whole);
+            if (ok && g >= kDecs) ok = tc::mbar_wait_lanes(bar(sm.decfree[d]), (g / kDecs - 1) & 1);
+            *reinterpret_cast<float2*>(&sm.b[d][2 * lane]) = make_float2(p0, pre);
+            *reinterpret_cast<float2*>(&sm.eb[d][2 * lane]) = make_float2(a.s_inter * e.x, a.s_inter * e.y);
+            *reinterpret_cast<float2*>(&sm.w[d][2 * lane]) = make_float2(a.s_w * w.x, a.s_w * w.y);
+            if (lane == 31) sm.lam[d] = lam;
+            if (kRev) follow = lead;
+          } else {
+            next = next2;
+            next2 = fetch(c + 2);
+            if (ok) ok = tc::mbar_wait_lanes(bar(sm.decfree[d]), (g / kDecs - 1) & 1);
+          }
+          total += whole;
           arrive(sm.dec[d]);
         }
         if (kState && x.run && lane == 31) a.sg.decay[x.sslot * P.Hv + x.h] = total;
@@ -533,6 +548,10 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
     const int v = 32 * wq + lane;  // state row of this thread, its columns 64 half .. + 63; value of Y, tokens 32 half .. + 31
     const uint32_t tl = tbase + ((uint32_t)(32 * wq) << 16);
     uint32_t g = 0;
+    // 32 rows of four 16-byte pieces in the warp's part of `extra`; rows two apart keep out of each other's banks
+    auto turn = [&](int row, int piece) {
+      return reinterpret_cast<float4*>(sm.extra + 2048 * (warp - kWarpB) + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
+    };
     // The warps that fill a tile of Y together leave together: a barrier among them is not bounded.
     auto agree = [&] {
       uint32_t all;
@@ -556,32 +575,48 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
       if (kState || (!a.sg.len && !a.st.in)) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) S[j] = make_float2(0.f, 0.f);
-      } else if (a.sg.len) {  // (the segments' states are kept as S is)
-        const float4* src = reinterpret_cast<const float4*>(a.sg.state + ((x.sslot * P.Hv + x.h) * kDim + v) * kDim + 64 * half);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float4 r = src[j];
-          S[2 * j] = make_float2(r.x, r.y);
-          S[2 * j + 1] = make_float2(r.z, r.w);
-        }
-      } else if (a.transposed) {
+      } else if (a.transposed && !a.sg.len) {
         const float* src = reinterpret_cast<const float*>(a.st.in) + at + (int64_t)64 * half * kDim + v;
 #pragma unroll
         for (int j = 0; j < 32; ++j) S[j] = make_float2(src[2 * j * kDim], src[(2 * j + 1) * kDim]);
-      } else if (a.st.bf16) {
-        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.st.in) + at + v * kDim + 64 * half);
+      } else if (a.sg.len || !a.st.bf16) {  // (the segments' states are kept as S is)
+        const float* src32 = a.sg.len ? a.sg.state + (x.sslot * P.Hv + x.h) * kDim * kDim : reinterpret_cast<const float*>(a.st.in) + at;
+        float4* f = reinterpret_cast<float4*>(S);
+        if (kSplit) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 r = src[j];
-          S[4 * j] = unpack2(r.x); S[4 * j + 1] = unpack2(r.y); S[4 * j + 2] = unpack2(r.z); S[4 * j + 3] = unpack2(r.w);
+          for (int j = 0; j < 16; ++j) f[j] = reinterpret_cast<const float4*>(src32 + v * kDim + 64 * half)[j];
+        } else {  // 16 columns at a time: four lanes to a row in memory, turned through the warp's part of `extra`
+          const float4* src = reinterpret_cast<const float4*>(src32 + (32 * wq + (lane >> 2)) * kDim + 64 * half) + (lane & 3);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) f[j] = src[(j & 3) * 2 * kDim + 4 * (j >> 2)];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *turn(8 * j + (lane >> 2), lane & 3) = f[4 * q + j];
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[4 * q + j] = *turn(lane, j);
+            __syncwarp();
+          }
         }
-      } else {
-        const float4* src = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.st.in) + at + v * kDim + 64 * half);
+      } else {  // BF16, 32 columns at a time
+        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.st.in) + at +
+                                                          (32 * wq + (lane >> 2)) * kDim + 64 * half) + (lane & 3);
+        uint4 f[8];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float4 r = src[j];
-          S[2 * j] = make_float2(r.x, r.y);
-          S[2 * j + 1] = make_float2(r.z, r.w);
+        for (int j = 0; j < 8; ++j) f[j] = src[(j & 3) * kDim + 4 * (j >> 2)];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(turn(8 * j + (lane >> 2), lane & 3)) = f[4 * q + j];
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 r = *reinterpret_cast<const uint4*>(turn(lane, j));
+            float2* z = S + 16 * q + 4 * j;
+            z[0] = unpack2(r.x); z[1] = unpack2(r.y); z[2] = unpack2(r.z); z[3] = unpack2(r.w);
+          }
+          __syncwarp();
         }
       }
       auto put_state = [&](uint32_t k) {  // as chunk k's A operand
@@ -619,7 +654,10 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         }
         tc::fence_before();
         arrive(sm.ufree);
-        if (kState) continue;
+        if (kState) {
+          arrive(sm.decfree[d]);
+          continue;
+        }
         // (in one part, the last chunk's S Q^T has left the other columns: its Y was waited for)
         if (!kSplit && c + 1 < x.nchunks) put_state(g + 1);
         if (ok) ok = tc::mbar_wait_lanes(bar(sm.gy), g & 1);
@@ -647,6 +685,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           }
           tc::fence_before();
           arrive(sm.yfree);
+          arrive(sm.decfree[d]);
         } else {
           // transposed by matrix stores into a tile of shared memory, copied out from there
           if (warp == kWarpB && lane == 0) tc::bulk_wait_read();  // the last one has left
@@ -678,6 +717,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           }
           tc::fence_before();
           arrive(sm.yfree);
+          arrive(sm.decfree[d]);
           tc::fence_async_smem();
           asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * kGroup) : "memory");
           const int64_t t0 = x.t0 + ci * kC;
@@ -696,25 +736,45 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           }
         }
       }
+      if (!kState && !kSplit) {  // `extra` is the copy's until the last Y has left
+        if (warp == kWarpB && lane == 0) tc::bulk_wait_read();
+        agree();
+      }
       if (!ok) break;
-      if (kState) {
-        float4* dst = reinterpret_cast<float4*>(a.sg.state + ((x.sslot * P.Hv + x.h) * kDim + v) * kDim + 64 * half);
+      if (kSplit) continue;  // (no final state is asked for)
+      float* dst32 = kState ? a.sg.state + (x.sslot * P.Hv + x.h) * kDim * kDim
+                     : x.last && a.st.out && !a.st.bf16 ? reinterpret_cast<float*>(a.st.out) + at : nullptr;  // (never transposed)
+      if (kRev && !kState && x.last && x.nchunks) {  // the initial state's adjoint: through the first token's decay
+        const float e = exp2f(decay_log2(decay_g(P, x.t0, x.h)));
 #pragma unroll
-        for (int j = 0; j < 16; ++j) dst[j] = make_float4(S[2 * j].x, S[2 * j].y, S[2 * j + 1].x, S[2 * j + 1].y);
-      } else if (x.last && a.st.out) {  // (never transposed)
-        if (kRev && x.nchunks) {  // the initial state's adjoint: through the first token's decay
-          const float e = exp2f(decay_log2(decay_g(P, x.t0, x.h)));
+        for (int j = 0; j < 32; ++j) S[j] = tc::mul2(S[j], make_float2(e, e));
+      }
+      if (dst32) {
+        float4* dst = reinterpret_cast<float4*>(dst32 + (32 * wq + (lane >> 2)) * kDim + 64 * half) + (lane & 3);
+        const float4* f = reinterpret_cast<const float4*>(S);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) S[j] = tc::mul2(S[j], make_float2(e, e));
+        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) *turn(lane, j) = f[4 * q + j];
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) dst[j * 2 * kDim + 4 * q] = *turn(8 * j + (lane >> 2), lane & 3);
+          __syncwarp();
         }
-        if (a.st.bf16) {
-          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.st.out) + at + v * kDim + 64 * half);
+      } else if (!kState && x.last && a.st.out) {
+        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.st.out) + at +
+                                              (32 * wq + (lane >> 2)) * kDim + 64 * half) + (lane & 3);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dst[j] = make_uint4(pack2(S[4 * j]), pack2(S[4 * j + 1]), pack2(S[4 * j + 2]), pack2(S[4 * j + 3]));
-        } else {
-          float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.st.out) + at + v * kDim + 64 * half);
+        for (int q = 0; q < 2; ++q) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) dst[j] = make_float4(S[2 * j].x, S[2 * j].y, S[2 * j + 1].x, S[2 * j + 1].y);
+          for (int j = 0; j < 4; ++j) {
+            const float2* z = S + 16 * q + 4 * j;
+            *reinterpret_cast<uint4*>(turn(lane, j)) = make_uint4(pack2(z[0]), pack2(z[1]), pack2(z[2]), pack2(z[3]));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) dst[j * kDim + 4 * q] = *reinterpret_cast<const uint4*>(turn(8 * j + (lane >> 2), lane & 3));
+          __syncwarp();
         }
       }
     }
@@ -998,6 +1058,7 @@ cudaError_t pass(const DecayProblem& P, const Role& q, const Role& k, const Role
     kda_decay_chain_kernel<kRev><<<dim3((unsigned)(P.N * P.Hv), 16), 256, 0, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
+  if (y32 && st.out) return cudaErrorInvalidValue;
   return y32 ? launch<kRev, false, true>(maps, a, s) : launch<kRev, false, false>(maps, a, s);
 }
 
@@ -1012,9 +1073,16 @@ int64_t decay_segment_tokens(const int64_t* cu, int64_t N, int64_t T, int64_t Hv
   }
   if (!cu) chunks *= N;
   // an even share of the chunks for each of kUnits units, 8 chunks at least
-  const int64_t seg = std::max<int64_t>((chunks * Hv + kUnits - 1) / kUnits, 8);
+  int64_t seg = std::max<int64_t>((chunks * Hv + kUnits - 1) / kUnits, 8);
   // cutting adds a pass over keys and values: only where the longest sequence alone takes well over an SM's share
-  return longest <= 3 * seg ? 0 : seg * kC;
+  if (longest <= 3 * seg) return 0;
+  // not a few units more than the SMs take in two turns (a third turn for them alone)
+  for (int64_t tries = 0; N * Hv < kUnits && tries < 64; ++tries, ++seg) {
+    int64_t units = 0;
+    for (int64_t n = 0; n < (cu ? N : 1); ++n) units += std::max<int64_t>((chunks_of(n) + seg - 1) / seg, 1);
+    if ((cu ? units : units * N) * Hv <= kUnits) break;
+  }
+  return longest <= seg ? 0 : seg * kC;
 }
 
 size_t decay_workspace_bytes(int64_t N, int64_t Ttot, int64_t Hqk, int64_t Hv, int64_t seg, bool training, bool per_token) {
