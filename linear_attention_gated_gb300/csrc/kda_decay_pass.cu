@@ -407,13 +407,16 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           for (int i = lane; i < lines; i += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 128 * i));
         }
         float total = 0.f;  // lane 31's: log2 of the unit's decay
-        // two chunks ahead: a chunk takes less time than a load
+        // two chunks ahead, as the bits that come (a conversion here would wait for the load)
+        auto bits = [&](int64_t tok) -> uint32_t {
+          return P.per_token ? reinterpret_cast<const uint16_t*>(P.g)[tok * P.Hv + x.h] : reinterpret_cast<const uint32_t*>(P.g)[x.h];
+        };
+        auto number = [&](uint32_t b) { return decay_log2(__uint_as_float(P.per_token ? b << 16 : b)); };
         auto fetch = [&](int64_t c) {
           const int64_t j = (kRev ? x.nchunks - 1 - c : c) * kC + 2 * lane;
-          return make_float2(c < x.nchunks && j < x.len ? decay_g(P, x.t0 + j, x.h) : 0.f,
-                             c < x.nchunks && j + 1 < x.len ? decay_g(P, x.t0 + j + 1, x.h) : 0.f);
+          return make_uint2(c < x.nchunks && j < x.len ? bits(x.t0 + j) : 0u, c < x.nchunks && j + 1 < x.len ? bits(x.t0 + j + 1) : 0u);
         };
-        float2 next = fetch(0), next2 = fetch(1);
+        uint2 next = fetch(0), next2 = fetch(1);
         // backwards: the decay of the token that follows the chunk
         float follow = kRev && x.nchunks && x.t0 + x.len < x.end ? decay_log2(decay_g(P, x.t0 + x.len, x.h)) : 0.f;
         float whole = 0.f;
@@ -422,8 +425,8 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           // of a fixed decay every whole chunk has the same numbers, and the slot has them already
           const bool again = !P.per_token && c > kDecs && (kRev || (c + 1) * kC <= x.len);
           if (!again) {
-            float g0 = decay_log2(next.x);
-            const float g1 = decay_log2(next.y);
+            float g0 = number(next.x);
+            const float g1 = number(next.y);
             next = next2;
             next2 = fetch(c + 2);
             const float lead = __shfl_sync(0xffffffffu, g0, 0);
