@@ -89,8 +89,8 @@ struct Smem {
   uint4 clc;             // response: the next unit
   Unit ring[kRing];      // units to come
   // full, empty: a stage's tiles are there / read by all products; dec, decfree: a chunk's decays are there / read by the last who does; g0, gu, gy: products done
-  // (scores, U, Y); aready: K~ and P are there; ufree, yfree: U, Y are read; sready: the state is there
-  unsigned long long full[kStages], empty[kStages], dec[kDecs], decfree[kDecs], g0[2], gu, gy, aready[2], ufree, sready[2], yfree;
+  // (scores, U, Y); kready, pready: K~, P are there; ufree, yfree: U, Y are read; sready: the state is there
+  unsigned long long full[kStages], empty[kStages], dec[kDecs], decfree[kDecs], g0[2], gu, gy, kready[2], pready[2], ufree, sready[2], yfree;
   unsigned long long clcbar, rfull[kRing], rempty[kRing];
   uint32_t tmem;
 };
@@ -190,7 +190,8 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar(sm.g0[i]), 1);
-      tc::mbar_init(bar(sm.aready[i]), kGroup);
+      tc::mbar_init(bar(sm.kready[i]), kGroup);
+      tc::mbar_init(bar(sm.pready[i]), kGroup);
       tc::mbar_init(bar(sm.sready[i]), kGroup);
     }
     tc::mbar_init(bar(sm.gu), 1);
@@ -336,9 +337,13 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         if (kState) tiles(g);
         --left;
         more = any_chunk(left);
-        if (!kState && more) scores(g + 1);  // (its buffer was read before the last aready)
+        if (!kState && more) {
+          // (chunk g - 1's scores have been read)
+          if (ok && g > 0) ok = tc::mbar_wait_lanes(bar(sm.pready[(g - 1) & 1]), ((g - 1) >> 1) & 1);
+          scores(g + 1);
+        }
         // U, once K~ is there and the last U is read
-        if (ok) ok = tc::mbar_wait_lanes(bar(sm.aready[g & 1]), (g >> 1) & 1);
+        if (ok) ok = tc::mbar_wait_lanes(bar(sm.kready[g & 1]), (g >> 1) & 1);
         if (ok && g > 0) ok = tc::mbar_wait_lanes(bar(sm.ufree), (g - 1) & 1);
         tc::fence_after();
         if (ok && tc::elect_one()) {
@@ -379,7 +384,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
             }
           }
           __syncwarp();
-          if (ok) ok = tc::mbar_wait_lanes(bar(sm.aready[g & 1]), (g >> 1) & 1);
+          if (ok) ok = tc::mbar_wait_lanes(bar(sm.pready[g & 1]), (g >> 1) & 1);
           tc::fence_after();
           if (ok && tc::elect_one()) {
             const uint64_t dv = tc::mnmajor(tc::smem_u32(sm.tile[s][2]), kPanel);
@@ -476,10 +481,13 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         unsigned char* Ks = sm.tile[s][1];
         unsigned char* Ls = sm.lo[g & 1];
         if (ok) ok = tc::mbar_wait_lanes(bar(sm.dec[d]), (g / kDecs) & 1);
-        if (ok) ok = tc::mbar_wait_lanes(bar(sm.full[s]), (g / kStages) & 1);
-        // lo and P of this parity are free once chunk g - 2's products are done, K once this one's scores are
-        if (ok && g >= 2) ok = tc::mbar_wait_lanes(bar(sm.empty[(g - 2) % kStages]), ((g - 2) / kStages) & 1);
-        if (ok && !kState) ok = tc::mbar_wait_lanes(bar(sm.g0[g & 1]), (g >> 1) & 1);
+        if (kState) {
+          if (ok) ok = tc::mbar_wait_lanes(bar(sm.full[s]), (g / kStages) & 1);
+          if (ok && g >= 2) ok = tc::mbar_wait_lanes(bar(sm.empty[(g - 2) % kStages]), ((g - 2) / kStages) & 1);
+        } else if (ok) {
+          // K is free once its scores are done; they are started after chunk g - 2's U, which reads this parity's low parts
+          ok = tc::mbar_wait_lanes(bar(sm.g0[g & 1]), (g >> 1) & 1);
+        }
         tc::fence_after();
 #pragma unroll
         for (int m = 0; m < 4; ++m) {  // 16-byte chunks i
@@ -500,7 +508,11 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           for (int i = at; i < (kC - nt) * 16; i += 32 * kGroup)
             *reinterpret_cast<uint4*>(sm.tile[s][2] + ((i >> 3) & 1) * kPanel + (nt + (i >> 4)) * 128 + (i & 7) * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
+        tc::fence_async_smem();
+        arrive(sm.kready[g & 1]);
         if (!kState) {
+          // P's buffer is free once chunk g - 2's products are done
+          if (ok && g >= 2) ok = tc::mbar_wait_lanes(bar(sm.empty[(g - 2) % kStages]), ((g - 2) / kStages) & 1);
           // rows i = 16 wq + lane / 4 (+ 8), columns 32 half + 8 m + 2 (lane % 4) (+ 1)
           const int i0 = 16 * wq + (lane >> 2), j0 = 32 * half + 2 * (lane & 3);
           unsigned char* Pt = sm.P[g & 1];
@@ -529,8 +541,8 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
                                       : make_float2(fast_exp2(bi - bj.x), fast_exp2(bi - bj.y));
                 float2 y = tc::mul2(tc::mul2(make_float2(p[4 * m + 2 * v], p[4 * m + 2 * v + 1]), scale), e);
                 // (selected, not multiplied: rows past the end may hold anything)
-                y.x = (kRev ? j >= i && j < nt : j <= i && i < nt) ? y.x : 0.f;
-                y.y = (kRev ? j + 1 >= i && j + 1 < nt : j < i && i < nt) ? y.y : 0.f;
+                y.x = (kRev ? (j < nt ? j : -1) >= i : j <= (i < nt ? i : -1)) ? y.x : 0.f;
+                y.y = (kRev ? (j + 1 < nt ? j + 1 : -1) >= i : j < (i < nt ? i : -1)) ? y.y : 0.f;
                 uint32_t hi, lo;
                 split2(y, hi, lo);
                 *reinterpret_cast<uint32_t*>(Pt + at_of(i, m)) = hi;
@@ -538,10 +550,10 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
               }
             }
           }
+          tc::fence_async_smem();
+          tc::fence_before();
+          arrive(sm.pready[g & 1]);
         }
-        tc::fence_async_smem();
-        tc::fence_before();
-        arrive(sm.aready[g & 1]);
       }
     }
   } else {
