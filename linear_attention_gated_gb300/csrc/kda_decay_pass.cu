@@ -329,19 +329,29 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         }
         __syncwarp();
       };
+      // The scores run one chunk ahead of U. Only one unit is looked at while a U is still to come: the warps that wait
+      // for that U hold the ring's places, and more empty units than it has places may follow.
       int64_t left = 0;
-      bool more = any_chunk(left);
-      if (!kState && more) scores(0);
-      for (; more; ++g) {
+      bool end = false;
+      for (uint32_t ahead = 0; !end || ahead > g;) {
+        const bool due = ahead > g;
+        if (left == 0 && !end) {
+          Unit x;
+          end = !next_unit(x);
+          left = end ? 0 : x.nchunks;
+        }
+        if (left > 0) {
+          --left;
+          if (!kState) {
+            // (the scores two chunks before have been read)
+            if (ok && ahead > 1) ok = tc::mbar_wait_lanes(bar(sm.pready[ahead & 1]), ((ahead - 2) >> 1) & 1);
+            scores(ahead);
+          }
+          ++ahead;
+        }
+        if (!due) continue;
         const int s = g % kStages;
         if (kState) tiles(g);
-        --left;
-        more = any_chunk(left);
-        if (!kState && more) {
-          // (chunk g - 1's scores have been read)
-          if (ok && g > 0) ok = tc::mbar_wait_lanes(bar(sm.pready[(g - 1) & 1]), ((g - 1) >> 1) & 1);
-          scores(g + 1);
-        }
         // U, once K~ is there and the last U is read
         if (ok) ok = tc::mbar_wait_lanes(bar(sm.kready[g & 1]), (g >> 1) & 1);
         if (ok && g > 0) ok = tc::mbar_wait_lanes(bar(sm.ufree), (g - 1) & 1);
@@ -359,6 +369,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           tc::mma_commit(bar(sm.empty[s]));
         }
         __syncwarp();
+        ++g;
       }
     } else if (warp == kWarpMma2) {
       // ================= products for Y, by a warp of their own: while one waits, the other's run

@@ -202,6 +202,20 @@ def test_many_heads_and_sequences():
     compare(run(x)[0], reference(x, device="cuda"))
 
 
+def test_more_sequences_than_are_put_in_order():
+    """600 sequences of 0 to 5 tokens (512 at most are run longest first)."""
+    lens = [(7 * i) % 6 for i in range(600)]
+    x = make(lens, 1, 2, "head", seed=23)
+    compare(run(x)[0], reference(x))
+
+
+def test_runs_of_empty_sequences():
+    """More empty units in a row than a running block's ring of units has places, before, between and after others."""
+    lens = [0] * 40 + [70] + [0] * 300 + [1] + [0] * 60
+    x = make(lens, 2, 8, "token", seed=25)
+    compare(run(x)[0], reference(x, device="cuda"))
+
+
 def test_context_reuse_and_repeatability():
     from linear_attention_gated_gb300 import KdaError, kda_decay_attn_bwd
     x, y = make((90, 40), 1, 2, "token", seed=12), make((40, 90), 1, 2, "token", seed=13)
