@@ -110,7 +110,8 @@ struct Segments {
 // Slot of a sequence's first segment: floor(t0 / len) + n leaves each sequence ceil(len_n / len) slots.
 __device__ __forceinline__ int64_t seg_slot(const Segments& g, int64_t t0, int64_t n) { return t0 / g.len + n; }
 
-constexpr int kOrder = 512;  // sequences whose order is passed (more run in index order)
+constexpr int kOrder = 512;      // sequences whose order is passed (more run in index order, whole)
+constexpr int kUnits = 2 * 152;  // the units that a cut aims at: two for each SM, so no sequence has more segments
 
 struct PassArgs {
   DecayProblem P;
@@ -123,6 +124,7 @@ struct PassArgs {
   float* y32;
   int ordered;
   uint16_t order[kOrder];             // longest sequence first
+  int32_t first[kUnits + 1];       // segments s of the sequences that have one: pairs first[s] .. first[s + 1] - 1
 };
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -145,8 +147,10 @@ __device__ __forceinline__ Unit unit_of(const PassArgs& a, int u) {
   Unit x;
   const int64_t p = u / P.Hv;
   x.h = u - (int)(p * P.Hv);
-  const int64_t seg = p / P.N;
-  x.n = p - seg * P.N;
+  int64_t seg = 0;
+  if (a.sg.len)
+    while (seg + 1 < a.sg.most && p >= a.first[seg + 1]) ++seg;
+  x.n = a.sg.len ? p - a.first[seg] : p;
   if (a.ordered) x.n = a.order[x.n];
   const DecaySpan sp = decay_span(P, x.n);
   x.t0 = sp.t0;
@@ -997,9 +1001,6 @@ __global__ void __launch_bounds__(kGateThreads) kda_decay_gate_grad_kernel(const
   }
 }
 
-// Aimed at when sequences are cut: units, twice the SMs (the grid hands them out as CTAs get free).
-constexpr int64_t kUnits = 2 * 152;
-
 struct SegWs {
   size_t state, decay, total;
 };
@@ -1031,7 +1032,8 @@ cudaError_t launch(const Maps& maps, const PassArgs& a, cudaStream_t s) {
   auto kern = kda_decay_pass_kernel<kRev, kState, kSplit>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(a.P.N * a.P.Hv * a.sg.most), kThreads, kSmemBytes, s>>>(maps, a);
+  const int64_t units = (a.sg.len ? a.first[a.sg.most] : a.P.N) * a.P.Hv;
+  kern<<<(unsigned)units, kThreads, kSmemBytes, s>>>(maps, a);
   return cudaGetLastError();
 }
 
@@ -1066,18 +1068,22 @@ cudaError_t pass(const DecayProblem& P, const Role& q, const Role& k, const Role
   a.transposed = transposed;
   a.y = y;
   a.y32 = y32;
+  auto len = [&](int64_t n) { return P.cu_host ? P.cu_host[n + 1] - P.cu_host[n] : P.T; };
   if (P.cu_host && P.N > 1 && P.N <= kOrder) {
     a.ordered = 1;
     for (int64_t i = 0; i < P.N; ++i) a.order[i] = (uint16_t)i;
-    std::stable_sort(a.order, a.order + P.N, [&](uint16_t i, uint16_t j) {
-      return P.cu_host[i + 1] - P.cu_host[i] > P.cu_host[j + 1] - P.cu_host[j];
-    });
+    std::stable_sort(a.order, a.order + P.N, [&](uint16_t i, uint16_t j) { return len(i) > len(j); });
   }
   a.sg.most = 1;
   if (P.seg) {
     const SegWs w = carve_segments(P.N, P.Ttot, P.Hv, P.seg);
     a.sg.len = P.seg;
     a.sg.most = (int)((P.longest + P.seg - 1) / P.seg);
+    int64_t have = P.N;  // the sequences that have a segment s (longest first): all have the first
+    for (int t = 0; t < a.sg.most; ++t) {
+      while (t && have && len(a.ordered ? a.order[have - 1] : have - 1) <= t * P.seg) --have;
+      a.first[t + 1] = a.first[t] + (int32_t)have;
+    }
     a.sg.state = reinterpret_cast<float*>(ws);
     a.sg.decay = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + w.decay);
     if ((e = launch<kRev, true, false>(maps, a, s)) != cudaSuccess) return e;
@@ -1091,6 +1097,7 @@ cudaError_t pass(const DecayProblem& P, const Role& q, const Role& k, const Role
 }  // namespace
 
 int64_t decay_segment_tokens(const int64_t* cu, int64_t N, int64_t T, int64_t Hv) {
+  if (N > kOrder) return 0;
   auto chunks_of = [&](int64_t n) { return ((cu ? cu[n + 1] - cu[n] : T) + kC - 1) / kC; };
   int64_t longest = 0, chunks = 0;
   for (int64_t n = 0; n < (cu ? N : 1); ++n) {

@@ -216,6 +216,16 @@ def test_runs_of_empty_sequences():
     compare(run(x)[0], reference(x, device="cuda"))
 
 
+def test_long_sequences_among_short_ones():
+    """Some sequences are cut into segments, others not, out of order."""
+    x = make((3, 3100, 0, 64, 5000, 1, 200), 1, 1, "token", seed=24)
+    got, _ = run(x)
+    compare(got, reference(x, device="cuda"))
+    again, _ = run(x)
+    for n, t in got.items():
+        assert torch.equal(t, again[n]), n
+
+
 def test_context_reuse_and_repeatability():
     from linear_attention_gated_gb300 import KdaError, kda_decay_attn_bwd
     x, y = make((90, 40), 1, 2, "token", seed=12), make((40, 90), 1, 2, "token", seed=13)
