@@ -15,6 +15,7 @@
 #include "kda_host.h"
 
 #include <cmath>
+#include <type_traits>
 
 namespace kda {
 namespace {
@@ -186,14 +187,14 @@ extern "C" kda_status kda_decay_attn_decode(const kda_bf16* q, const kda_bf16* k
     P.r = (int)(Hv / Hqk);
     P.per_token = decay_per_token;
     P.scale = std::isnan(scale) ? 1.0f / std::sqrt(128.0f) : scale;
-    constexpr int kRows = 32;
-    const unsigned grid = (unsigned)(N * Hv * (kda::kDim / kRows));
-    if (state_dtype == KDA_STATE_BF16)
-      kda::kda_decay_decode_kernel<__nv_bfloat16, kRows><<<grid, kda::kDdThreads, 0, stream>>>(
-          P, reinterpret_cast<__nv_bfloat16*>(state), state_indices, num_slots, reinterpret_cast<__nv_bfloat16*>(o));
-    else
-      kda::kda_decay_decode_kernel<float, kRows><<<grid, kda::kDdThreads, 0, stream>>>(
-          P, reinterpret_cast<float*>(state), state_indices, num_slots, reinterpret_cast<__nv_bfloat16*>(o));
+    auto launch = [&](auto* pool, auto rows) {
+      kda::kda_decay_decode_kernel<std::remove_pointer_t<decltype(pool)>, decltype(rows)::value>
+          <<<(unsigned)(N * Hv * (kda::kDim / decltype(rows)::value)), kda::kDdThreads, 0, stream>>>(
+              P, pool, state_indices, num_slots, reinterpret_cast<__nv_bfloat16*>(o));
+    };
+    // 16 KiB of state to a CTA: 32 rows in FP32, 64 in BF16
+    if (state_dtype == KDA_STATE_BF16) launch(reinterpret_cast<__nv_bfloat16*>(state), std::integral_constant<int, 64>{});
+    else launch(reinterpret_cast<float*>(state), std::integral_constant<int, 32>{});
     if ((e = cudaGetLastError()) != cudaSuccess) return dfail(KDA_ERR_CUDA, cudaGetErrorString(e));
     return KDA_OK;
   });

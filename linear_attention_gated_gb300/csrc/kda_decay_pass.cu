@@ -1105,10 +1105,14 @@ int64_t decay_segment_tokens(const int64_t* cu, int64_t N, int64_t T, int64_t Hv
     longest = std::max(longest, chunks_of(n));
   }
   if (!cu) chunks *= N;
-  // an even share of the chunks for each of kUnits units, 8 chunks at least
-  int64_t seg = std::max<int64_t>((chunks * Hv + kUnits - 1) / kUnits, 8);
-  // cutting adds a pass over keys and values: only where the longest sequence alone takes well over an SM's share
-  if (longest <= 3 * seg) return 0;
+  // An even share of the chunks for each of kUnits units, 8 chunks at least. Cutting adds a pass over keys and values
+  // (about 0.6 of the main pass) and the chain: only where the longest sequence takes well over an SM's share, two units.
+  // Measured, cut against whole, one sequence of 8192 or 16384 tokens: 96 heads (3.2 shares) 269 us : 210 us and
+  // 541 : 404, 64 heads (4.8 shares) 206 : 210 and 359 : 395, 48 heads (6.3) 158 : 207, 32 heads (9.5) 128 : 203;
+  // 1600 tokens of 8 heads 55 : 54, 2048 of 8 heads 50 : 66, 20000 of one head 61 : 470.
+  const int64_t share = (chunks * Hv + kUnits - 1) / kUnits;
+  if (longest <= std::max<int64_t>(4 * share, 24)) return 0;
+  int64_t seg = std::max<int64_t>(share, 8);
   // not a few units more than the SMs take in two turns (a third turn for them alone)
   for (int64_t tries = 0; N * Hv < kUnits && tries < 64; ++tries, ++seg) {
     int64_t units = 0;

@@ -32,7 +32,6 @@ namespace kda {
 namespace {
 
 constexpr int kNrThreads = 128;
-constexpr int kNrTokens = 64;  // most tokens of one tile
 
 struct NrTensor {
   const void* x;
@@ -41,8 +40,7 @@ struct NrTensor {
   const float* w;   // [D] or null
   int64_t xt, xh, dt, dh, yt, yh;  // token and head strides of x, dy and y (elements)
   int H;
-  int tokens;       // tokens of one tile
-  int64_t tiles;
+  int rounds;       // for which angles are computed at a time
 };
 
 struct NrArgs {
@@ -54,6 +52,7 @@ struct NrArgs {
   int D, R;
   float eps;
   int ctas0;             // CTAs of the queries
+  int tokens;            // most tokens whose angles are there
 };
 
 // 8 values of a row: raw as they come from memory, and as four FP32 pairs.
@@ -62,8 +61,7 @@ struct Vec8;
 template <>
 struct Vec8<__nv_bfloat16> {
   uint4 r;
-  __device__ __forceinline__ void zero() { r = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void load(const void* p) { r = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load_ring(const uint4* at) { r = *at; }
   __device__ __forceinline__ void get(float2* x) const {
     const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
 #pragma unroll
@@ -80,8 +78,7 @@ struct Vec8<__nv_bfloat16> {
 template <>
 struct Vec8<__half> {
   uint4 r;
-  __device__ __forceinline__ void zero() { r = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void load(const void* p) { r = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load_ring(const uint4* at) { r = *at; }
   __device__ __forceinline__ void get(float2* x) const {
     const __half2* h = reinterpret_cast<const __half2*>(&r);
 #pragma unroll
@@ -98,10 +95,13 @@ struct Vec8<__half> {
 template <>
 struct Vec8<float> {
   float4 a, b;
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void load(const void* p) {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void load_ring(const uint4* at) {  // pieces a thread's stride apart
+    a = *reinterpret_cast<const float4*>(at);
+    b = *reinterpret_cast<const float4*>(at + kNrThreads);
   }
   __device__ __forceinline__ void get(float2* x) const {
     x[0] = make_float2(a.x, a.y); x[1] = make_float2(a.z, a.w);
@@ -160,22 +160,28 @@ __device__ __forceinline__ void rotate8(float2* a, float2* b, const float* c, co
   }
 }
 
-// CTAs an SM: what the registers of two rows in flight leave room for.
+// CTAs an SM, and rows of a group that are on their way (a ring of asynchronous copies in shared memory): registers bound
+// the first, 64 KiB in flight an SM the product.
 template <typename T, bool kBwd>
-constexpr int kNrBlocks = sizeof(T) == 4 ? (kBwd ? 2 : 4) : (kBwd ? 4 : 6);
+constexpr int kNrBlocks = sizeof(T) == 4 ? (kBwd ? 3 : 5) : (kBwd ? 4 : 6);
+template <typename T, bool kBwd>
+constexpr int kNrStages = kBwd ? 3 : 4;
+template <typename T, bool kBwd>
+constexpr int kNrPieces = (int)sizeof(T) * (kBwd ? 2 : 1);  // 16-byte pieces of a lane and row: x (and dy)
 
 template <typename T, int G, bool kInter, bool kBwd>
 __global__ void __launch_bounds__(kNrThreads, kNrBlocks<T, kBwd>) kda_qk_norm_rope_kernel(const NrArgs a) {
   extern __shared__ __align__(16) unsigned char nr_smem[];
-  constexpr int kGroups = kNrThreads / G;
+  constexpr int kGroups = kNrThreads / G, kStages = kNrStages<T, kBwd>, kPieces = kNrPieces<T, kBwd>;
   const int which = (int)blockIdx.x >= a.ctas0;
   const NrTensor& t = a.t[which];
   const int64_t first = which ? (int64_t)blockIdx.x - a.ctas0 : blockIdx.x;
-  const int64_t step = which ? (int64_t)gridDim.x - a.ctas0 : a.ctas0;
+  const int64_t ctas = which ? (int64_t)gridDim.x - a.ctas0 : a.ctas0;
   const int tid = threadIdx.x, lane = tid % G, group = tid / G;
   const int R = a.R, half = R / 2, H = t.H;
   uint64_t* turns_of = reinterpret_cast<uint64_t*>(nr_smem);               // [R / 2] fixed-point frequencies
-  float* cs = reinterpret_cast<float*>(nr_smem + half * sizeof(uint64_t));  // [tokens of the tile][cos, sin][R / 2]
+  float* cs = reinterpret_cast<float*>(nr_smem + half * sizeof(uint64_t));  // [tokens][cos, sin][R / 2]
+  uint4* ring = reinterpret_cast<uint4*>(cs + a.tokens * R) + tid;          // [stages][pieces][threads]
   const bool active = lane < a.D / 16;
   const bool turns = active && 16 * lane < R;
   // the lane's two vectors: the halves of its pairs, or 16 neighbouring values
@@ -184,30 +190,53 @@ __global__ void __launch_bounds__(kNrThreads, kNrBlocks<T, kBwd>) kda_qk_norm_ro
     c0 = 8 * lane;
     c1 = 8 * lane + half;
   }
-  auto tokens_of = [&](int64_t tile) {
-    if (tile >= t.tiles) return 0;
-    const int64_t left = a.n - tile * t.tokens;
-    return (int)(left < t.tokens ? left : t.tokens);
+  // This CTA's rounds of kGroups rows, a row to a group each: rows (token, head) in order, shared out evenly.
+  const int64_t rows = a.n * H, all = (rows + kGroups - 1) / kGroups;
+  const int64_t u0 = all * first / ctas;
+  const int rounds = (int)(all * (first + 1) / ctas - u0);
+  const int64_t start = u0 * kGroups / H;  // the first row's token; the others count from it
+  int head0 = (int)(u0 * kGroups - start * H), token0 = 0;  // the first row of the angles at hand
+  const int64_t left = rows - u0 * kGroups - group;
+  const int mine = left <= 0 ? 0 : left > (int64_t)rounds * kGroups ? rounds : (int)((left + kGroups - 1) / kGroups);  // rounds with a row
+  // the row that is worked on, and the one whose copy starts next
+  struct Row {
+    int token, head;
   };
-  // The next row: its token in the tile (with `ntok` or more: none) and head, and its values, on their way. From row to
-  // row of a group: kGroups rows on.
-  const int head0 = group % H, token0 = group / H, head_step = kGroups % H, token_step = kGroups / H;
-  int token = token0, head = head0, ntok = tokens_of(first);
-  int64_t tile = first, tok0 = first * t.tokens;
-  Vec8<T> na, nb, nda, ndb;
-  na.zero(); nb.zero(); nda.zero(); ndb.zero();
-  auto fetch = [&] {
-    if (!active || token >= ntok) return;
-    const T* src = reinterpret_cast<const T*>(t.x) + (tok0 + token) * t.xt + head * t.xh;
-    na.load(src + c0);
-    nb.load(src + c1);
-    if constexpr (kBwd) {
-      const T* sd = reinterpret_cast<const T*>(t.dy) + (tok0 + token) * t.dt + head * t.dh;
-      nda.load(sd + c0);
-      ndb.load(sd + c1);
+  Row now{(head0 + group) / H, (head0 + group) % H};
+  Row then = now;
+  const int head_step = kGroups % H, token_step = kGroups / H;
+  auto advance = [&](Row& x) {
+    x.head += head_step;
+    x.token += token_step;
+    if (x.head >= H) {
+      x.head -= H;
+      ++x.token;
     }
   };
-  fetch();
+  const T* xs = reinterpret_cast<const T*>(t.x) + start * t.xt;
+  const T* ds = reinterpret_cast<const T*>(t.dy) + start * t.dt;
+  T* ys = reinterpret_cast<T*>(t.y) + start * t.yt;
+  auto fetch = [&](int i) {  // round i's row; past the end: nothing
+    if (active && i < mine) {
+      uint4* to = ring + kNrThreads * kPieces * (i % kStages);
+      const T* src = xs + then.token * t.xt + then.head * t.xh;
+      const T* sd = ds + then.token * t.dt + then.head * t.dh;
+      constexpr int kEach = 16 / (int)sizeof(T);
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {  // x's first vector, its second; dy's
+        const int v = k * kEach / 8, off = k * kEach % 8;
+        tc::cp_async16(to + kNrThreads * k, (v < 2 ? src : sd) + (v & 1 ? c1 : c0) + off, 16);
+      }
+    }
+    tc::cp_async_commit();
+    advance(then);
+  };
+  if (!active) {  // (their part of a row's sum)
+#pragma unroll
+    for (int k = 0; k < kStages * kPieces; ++k) ring[kNrThreads * k] = make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
   for (int d = tid; d < half; d += kNrThreads) turns_of[d] = fixed_turns(a.freq[d]);
   float2 w0[4], w1[4];
 #pragma unroll
@@ -222,45 +251,41 @@ __global__ void __launch_bounds__(kNrThreads, kNrBlocks<T, kBwd>) kda_qk_norm_ro
   for (int e = 0; e < 4; ++e) g0[e] = g1[e] = both(0.f);
   const float inv_d = 1.f / (float)a.D;
 
-  while (tile < t.tiles) {
+  for (int i = 0; i < rounds;) {
+    // angles of the tokens of the next rounds
+    const int end = R && rounds - i > t.rounds ? i + t.rounds : rounds;
     if (R) {
-      __syncthreads();  // the last tile's rows are done with cs (and the frequencies are there)
-      for (int i = tid; i < ntok * half; i += kNrThreads) {
-        const int tt = i / half, d = i - tt * half;
-        const float2 v = cos_sin(a.pos[tok0 + tt], turns_of[d]);
+      __syncthreads();  // the last ones are done with (and the frequencies are there)
+      const int64_t left = a.n - start - token0;
+      const int last = (head0 + (end - i) * kGroups - 1) / H + 1, ntok = last < left ? last : (int)left;
+      for (int j = tid; j < ntok * half; j += kNrThreads) {
+        const int tt = j / half, d = j - tt * half;
+        const float2 v = cos_sin(a.pos[start + token0 + tt], turns_of[d]);
         cs[tt * R + d] = v.x;
         cs[tt * R + half + d] = v.y;
       }
       __syncthreads();
     }
     // all lanes of a warp make the same number of rounds: the shuffles are warp wide
-    const int rounds = (ntok * H + kGroups - 1) / kGroups;
-    for (int i = 0; i < rounds; ++i) {
-      const bool live = active && token < ntok;
+    for (; i < end; ++i) {
+      tc::cp_async_wait<kStages - 2>();
+      const uint4* from = ring + kNrThreads * kPieces * (i % kStages);
+      const bool live = active && i < mine;
       float2 p[4], q[4], u[4], v[4];
-      na.get(p);
-      nb.get(q);
-      if constexpr (kBwd) {
-        nda.get(u);
-        ndb.get(v);
+      {
+        Vec8<T> x;
+        constexpr int kVec = kNrThreads * (int)sizeof(T) / 2;  // from vector to vector
+        x.load_ring(from); x.get(p);
+        x.load_ring(from + kVec); x.get(q);
+        if constexpr (kBwd) {
+          x.load_ring(from + 2 * kVec); x.get(u);
+          x.load_ring(from + 3 * kVec); x.get(v);
+        }
       }
-      T* out = reinterpret_cast<T*>(t.y) + (tok0 + token) * t.yt + head * t.yh;
-      const float* angle = cs + (live && turns ? token * R + 8 * lane : 0);
-      // the next row is on its way while this one is worked on
-      head += head_step;
-      token += token_step;
-      if (head >= H) {
-        head -= H;
-        ++token;
-      }
-      if (i == rounds - 1) {
-        tile += step;
-        tok0 = tile * t.tokens;
-        ntok = tokens_of(tile);
-        token = token0;
-        head = head0;
-      }
-      fetch();
+      fetch(i + kStages - 1);
+      T* out = ys + now.token * t.yt + now.head * t.yh;
+      const float* angle = cs + (live && turns ? (now.token - token0) * R + 8 * lane : 0);
+      advance(now);
       float2 s2 = tc::mul2(p[0], p[0]);
 #pragma unroll
       for (int e = 1; e < 4; ++e) s2 = tc::fma2(p[e], p[e], s2);
@@ -318,10 +343,14 @@ __global__ void __launch_bounds__(kNrThreads, kNrBlocks<T, kBwd>) kda_qk_norm_ro
         Vec8<T>::store(out + c1, q);
       }
     }
+    const int on = head0 + t.rounds * kGroups;
+    token0 += on / H;
+    head0 = on % H;
   }
   if (kBwd && a.dw_part) {  // (no weights, no workspace: nothing to sum)
     // the CTA's share of dw: the groups' sums in a fixed order
     float* acc = reinterpret_cast<float*>(nr_smem);  // [groups of a warp summed: warps][16 G]
+    tc::cp_async_wait<0>();
     __syncthreads();
     float* f0 = reinterpret_cast<float*>(g0);
     float* f1 = reinterpret_cast<float*>(g1);
@@ -375,7 +404,7 @@ kda_status nfail(kda_status st, const char* msg) {
   return st;
 }
 
-constexpr int64_t kNrMaxCtas = 152 * 6;  // most CTAs (backward: rows of dw_part)
+constexpr int64_t kNrMaxCtas = 152 * 6;  // backward: most CTAs, rows of dw_part
 
 // A strided [tokens, heads, D] view in bytes.
 struct View {
@@ -527,8 +556,8 @@ kda_status nr_run(const NrCall& c) {
   const bool wide = c.dtype == KDA_DTYPE_FP32;
   const int64_t resident = 152 * (wide ? (c.bwd ? kNrBlocks<float, true> : kNrBlocks<float, false>)
                                        : (c.bwd ? kNrBlocks<__half, true> : kNrBlocks<__half, false>));
+  const int groups = kNrThreads / (c.D <= 64 ? 4 : c.D <= 128 ? 8 : 16);
   int64_t ctas[2];
-  int most = 1;
   for (int i = 0; i < 2; ++i) {
     NrTensor& t = a.t[i];
     t.x = i ? c.k : c.q;
@@ -539,21 +568,22 @@ kda_status nr_run(const NrCall& c) {
     t.yt = st[4 + 2 * i]; t.yh = st[5 + 2 * i];
     t.dt = c.bwd ? st[8 + 2 * i] : 0; t.dh = c.bwd ? st[9 + 2 * i] : 0;
     t.H = (int)heads[i];
-    // whole tokens: 256 rows a tile (barriers and angles count less) where that leaves every CTA one, else 64
-    const int64_t want = c.n * (c.Hq + c.Hk) >= 256 * resident ? 256 : 64;
-    int64_t tt = (want - 1 + t.H) / t.H;
-    if (tt > kNrTokens) tt = kNrTokens;
-    t.tokens = (int)tt;
-    t.tiles = (c.n + tt - 1) / tt;
-    // the CTAs that run at once, shared out by rows; each takes its tiles in turn
+    // the CTAs that run at once, shared out by rows
+    const int64_t units = (c.n * t.H + groups - 1) / groups;
     ctas[i] = resident * t.H / (c.Hq + c.Hk);
     if (ctas[i] < 1) ctas[i] = 1;
-    if (ctas[i] > t.tiles) ctas[i] = t.tiles;
-    if (t.tokens > most) most = t.tokens;
+    if (ctas[i] > units) ctas[i] = units;
+    // angles at a time: of up to 16 rounds, in 12 KiB (of one round's tokens at least)
+    t.rounds = 16;
+    auto tokens = [&] { return (int)((t.rounds * groups + t.H - 2) / t.H + 1); };  // (a round may start within a token)
+    while (t.rounds > 1 && tokens() * c.R * sizeof(float) > 12 * 1024) --t.rounds;
+    if (tokens() > a.tokens) a.tokens = tokens();
   }
   a.ctas0 = (int)ctas[0];
-  size_t smem = (size_t)(c.R / 2) * (sizeof(uint64_t) + most * 2 * sizeof(float));
-  if (c.bwd && smem < sizeof(float) * 8 * c.D) smem = sizeof(float) * 8 * c.D;
+  const size_t stages = wide ? (c.bwd ? kNrStages<float, true> : kNrStages<float, false>)
+                             : (c.bwd ? kNrStages<__half, true> : kNrStages<__half, false>);
+  size_t smem = (size_t)(c.R / 2) * sizeof(uint64_t) + a.tokens * c.R * sizeof(float) +
+                stages * 16 * kNrThreads * size * (c.bwd ? 2 : 1);
   const int64_t grid = ctas[0] + ctas[1];
   if (grid > 0) {
     if (c.dtype == KDA_DTYPE_BF16) e = nr_by_group<__nv_bfloat16>(a, grid, smem, c.inter, c.bwd, c.stream);

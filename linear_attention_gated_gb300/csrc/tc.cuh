@@ -125,10 +125,6 @@ __device__ __forceinline__ void stmatrix4_trans(uint32_t saddr, uint32_t r0, uin
                : "memory");
 }
 
-__device__ __forceinline__ void tma_prefetch_map(const void* map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
-}
-
 // A operand read from tensor memory (128 lanes x K columns at a_tmem).
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, int acc) {
   asm volatile(
