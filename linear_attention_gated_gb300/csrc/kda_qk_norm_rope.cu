@@ -39,6 +39,7 @@ struct NrTensor {
   void* y;          // forward: y; backward: dx
   const float* w;   // [D] or null
   int64_t xt, xh, dt, dh, yt, yh;  // token and head strides of x, dy and y (elements)
+  int64_t x_step, x_wrap, d_step, d_wrap, y_step, y_wrap;  // from row to row of a group; more where the head wraps round
   int H;
   int rounds;       // for which angles are computed at a time
 };
@@ -152,10 +153,9 @@ __device__ __forceinline__ void rotate8(float2* a, float2* b, const float* c, co
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 ce = make_float2(c[2 * e], c[2 * e + 1]), se = make_float2(s[2 * e], s[2 * e + 1]);
-      const float2 minus = make_float2(-se.x, -se.y);
-      const float2 x = a[e], y = b[e];
-      a[e] = tc::fma2(y, kBack ? se : minus, tc::mul2(x, ce));
-      b[e] = tc::fma2(x, kBack ? minus : se, tc::mul2(y, ce));
+      const float2 x = a[e], y = b[e], minus = tc::mul2(kBack ? x : y, both(-1.f));  // (packed operands have no sign)
+      a[e] = tc::fma2(kBack ? y : minus, se, tc::mul2(x, ce));
+      b[e] = tc::fma2(kBack ? minus : x, se, tc::mul2(y, ce));
     }
   }
 }
@@ -198,38 +198,33 @@ __global__ void __launch_bounds__(kNrThreads, kNrBlocks<T, kBwd>) kda_qk_norm_ro
   int head0 = (int)(u0 * kGroups - start * H), token0 = 0;  // the first row of the angles at hand
   const int64_t left = rows - u0 * kGroups - group;
   const int mine = left <= 0 ? 0 : left > (int64_t)rounds * kGroups ? rounds : (int)((left + kGroups - 1) / kGroups);  // rounds with a row
-  // the row that is worked on, and the one whose copy starts next
-  struct Row {
-    int token, head;
-  };
-  Row now{(head0 + group) / H, (head0 + group) % H};
-  Row then = now;
+  // From row to row of a group, kGroups rows on, by additions alone: the row that is worked on (its output and its
+  // angles) and the one whose copy starts next (its inputs).
   const int head_step = kGroups % H, token_step = kGroups / H;
-  auto advance = [&](Row& x) {
-    x.head += head_step;
-    x.token += token_step;
-    if (x.head >= H) {
-      x.head -= H;
-      ++x.token;
-    }
-  };
-  const T* xs = reinterpret_cast<const T*>(t.x) + start * t.xt;
-  const T* ds = reinterpret_cast<const T*>(t.dy) + start * t.dt;
-  T* ys = reinterpret_cast<T*>(t.y) + start * t.yt;
+  int head = (head0 + group) % H, next_head = head, row_angle = (head0 + group) / H * R;
+  const int64_t token = start + (head0 + group) / H;
+  const T* xs = reinterpret_cast<const T*>(t.x) + token * t.xt + head * t.xh;
+  const T* ds = kBwd ? reinterpret_cast<const T*>(t.dy) + token * t.dt + head * t.dh : nullptr;
+  T* ys = reinterpret_cast<T*>(t.y) + token * t.yt + head * t.yh;
   auto fetch = [&](int i) {  // round i's row; past the end: nothing
     if (active && i < mine) {
       uint4* to = ring + kNrThreads * kPieces * (i % kStages);
-      const T* src = xs + then.token * t.xt + then.head * t.xh;
-      const T* sd = ds + then.token * t.dt + then.head * t.dh;
       constexpr int kEach = 16 / (int)sizeof(T);
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) {  // x's first vector, its second; dy's
         const int v = k * kEach / 8, off = k * kEach % 8;
-        tc::cp_async16(to + kNrThreads * k, (v < 2 ? src : sd) + (v & 1 ? c1 : c0) + off, 16);
+        tc::cp_async16(to + kNrThreads * k, (v < 2 ? xs : ds) + (v & 1 ? c1 : c0) + off, 16);
       }
     }
     tc::cp_async_commit();
-    advance(then);
+    next_head += head_step;
+    xs += t.x_step;
+    if (kBwd) ds += t.d_step;
+    if (next_head >= H) {
+      next_head -= H;
+      xs += t.x_wrap;
+      if (kBwd) ds += t.d_wrap;
+    }
   };
   if (!active) {  // (their part of a row's sum)
 #pragma unroll
@@ -283,9 +278,16 @@ __global__ void __launch_bounds__(kNrThreads, kNrBlocks<T, kBwd>) kda_qk_norm_ro
         }
       }
       fetch(i + kStages - 1);
-      T* out = ys + now.token * t.yt + now.head * t.yh;
-      const float* angle = cs + (live && turns ? (now.token - token0) * R + 8 * lane : 0);
-      advance(now);
+      T* out = ys;
+      const float* angle = cs + (live && turns ? row_angle + 8 * lane : 0);
+      head += head_step;
+      ys += t.y_step;
+      row_angle += token_step * R;
+      if (head >= H) {
+        head -= H;
+        ys += t.y_wrap;
+        row_angle += R;
+      }
       float2 s2 = tc::mul2(p[0], p[0]);
 #pragma unroll
       for (int e = 1; e < 4; ++e) s2 = tc::fma2(p[e], p[e], s2);
@@ -345,6 +347,7 @@ __global__ void __launch_bounds__(kNrThreads, kNrBlocks<T, kBwd>) kda_qk_norm_ro
     }
     const int on = head0 + t.rounds * kGroups;
     token0 += on / H;
+    row_angle -= on / H * R;
     head0 = on % H;
   }
   if (kBwd && a.dw_part) {  // (no weights, no workspace: nothing to sum)
@@ -388,8 +391,11 @@ __global__ void __launch_bounds__(1024) kda_norm_weight_grad_kernel(const float*
   const int lo = blockIdx.y ? ctas0 : 0, hi = blockIdx.y ? ctas : ctas0;
   float* out = blockIdx.y ? dkw : dqw;
   float x = 0.f;
-  if (d < D && out)
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (started while the last kernel ends)
+  if (d < D && out) {
+#pragma unroll 8
     for (int i = lo + lane; i < hi; i += 32) x += part[(int64_t)i * D + d];
+  }
   s[lane][col] = x;
   __syncthreads();
   if (lane == 0 && d < D && out) {
@@ -568,9 +574,16 @@ kda_status nr_run(const NrCall& c) {
     t.yt = st[4 + 2 * i]; t.yh = st[5 + 2 * i];
     t.dt = c.bwd ? st[8 + 2 * i] : 0; t.dh = c.bwd ? st[9 + 2 * i] : 0;
     t.H = (int)heads[i];
-    // the CTAs that run at once, shared out by rows
-    const int64_t units = (c.n * t.H + groups - 1) / groups;
-    ctas[i] = resident * t.H / (c.Hq + c.Hk);
+    auto steps = [&](int64_t ts, int64_t hs, int64_t& step, int64_t& wrap) {
+      step = groups / t.H * ts + groups % t.H * hs;
+      wrap = ts - t.H * hs;
+    };
+    steps(t.xt, t.xh, t.x_step, t.x_wrap);
+    steps(t.dt, t.dh, t.d_step, t.d_wrap);
+    steps(t.yt, t.yh, t.y_step, t.y_wrap);
+    // the CTAs that run at once, shared out by work: a token's angles take about what two of its rows do
+    const int64_t units = (c.n * t.H + groups - 1) / groups, angles = c.R ? 2 : 0;
+    ctas[i] = resident * (t.H + angles) / (c.Hq + c.Hk + 2 * angles);
     if (ctas[i] < 1) ctas[i] = 1;
     if (ctas[i] > units) ctas[i] = units;
     // angles at a time: of up to 16 rounds, in 12 KiB (of one round's tokens at least)
@@ -592,9 +605,18 @@ kda_status nr_run(const NrCall& c) {
     if (e != cudaSuccess) return nfail(KDA_ERR_CUDA, cudaGetErrorString(e));
   }
   if (c.bwd && (c.dqw || c.dkw)) {
-    kda_norm_weight_grad_kernel<<<dim3((unsigned)((c.D + 31) / 32), 2), 1024, 0, c.stream>>>(
-        c.part, (int)ctas[0], (int)grid, (int)c.D, c.dqw, c.dkw);
-    if ((e = cudaGetLastError()) != cudaSuccess) return nfail(KDA_ERR_CUDA, cudaGetErrorString(e));
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((c.D + 31) / 32), 2);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = c.stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    const float* part = c.part;
+    e = cudaLaunchKernelEx(&cfg, kda_norm_weight_grad_kernel, part, (int)ctas[0], (int)grid, (int)c.D, c.dqw, c.dkw);
+    if (e != cudaSuccess) return nfail(KDA_ERR_CUDA, cudaGetErrorString(e));
   }
   return KDA_OK;
 }

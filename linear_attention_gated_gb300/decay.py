@@ -20,6 +20,7 @@ _NAN = float("nan")
 _UNCUT = 1536  # sequences up to this long are never cut into segments: prefill needs no workspace for them
 _BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 _STATE = {torch.bfloat16: 0, torch.float32: 1}
+_ROPE_WORKSPACE = {}  # head_dim -> bytes
 _ROPE_TYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 
 
@@ -379,18 +380,23 @@ def kda_qk_norm_rope_bwd(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, 
     _typed(dq, "dq", q.dtype, q.shape, dev)
     _typed(dk, "dk", q.dtype, k.shape, dev)
     if out is None:
-        gq, gk = (torch.empty(t.shape, dtype=q.dtype, device=dev) for t in (q, k))
+        gq = torch.empty_like(q) if q.is_contiguous() else torch.empty((B, T, Hq, D), dtype=q.dtype, device=dev)
+        gk = torch.empty_like(k) if k.is_contiguous() else torch.empty((B, T, Hk, D), dtype=q.dtype, device=dev)
     else:
         gq, gk = out
         _typed(gq, "out[0]", q.dtype, q.shape, dev)
         _typed(gk, "out[1]", q.dtype, k.shape, dev)
-    gqw = None if q_weight is None else torch.empty(D, dtype=_F32, device=dev)
-    gkw = None if k_weight is None else torch.empty(D, dtype=_F32, device=dev)
-    if workspace is None and (gqw is not None or gkw is not None):
-        n = ctypes.c_size_t(0)
-        _check(lib.kda_qk_norm_rope_workspace_bytes(D, ctypes.byref(n)))
-        workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
-    elif workspace is not None:
+    gqw = None if q_weight is None else torch.empty_like(q_weight)
+    gkw = None if k_weight is None else torch.empty_like(k_weight)
+    if workspace is None:
+        if gqw is not None or gkw is not None:
+            nbytes = _ROPE_WORKSPACE.get(D)
+            if nbytes is None:
+                n = ctypes.c_size_t(0)
+                _check(lib.kda_qk_norm_rope_workspace_bytes(D, ctypes.byref(n)))
+                nbytes = _ROPE_WORKSPACE[D] = n.value
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
         _want(workspace, "workspace", torch.uint8, workspace.shape, dev)
     strides = _all_strides((("q", q), ("k", k), ("out[0]", gq), ("out[1]", gk), ("dq", dq), ("dk", dk)))
     _call(lib.kda_qk_norm_rope_bwd, dev, dq.data_ptr(), dk.data_ptr(), q.data_ptr(), k.data_ptr(), _ROPE_TYPES[q.dtype],

@@ -166,3 +166,41 @@ def test_difference():
     size = (g.double() * step.double()).norm().item()
     # the difference's own error: e^2 / 6 of a third derivative of a few times the gradient
     assert abs((g.double() * step.double()).sum().item() - want) <= 2e-3 * size
+
+
+@pytest.mark.parametrize("dtype,T,hq,hk,dim,rot,interleaved", [
+    (torch.bfloat16, 40001, 7, 3, 64, 64, False),  # rows enough for several runs of angles a block, heads that no run divides
+    (torch.bfloat16, 30011, 1, 17, 128, 96, True),
+    (torch.float32, 12007, 3, 1, 256, 256, False),
+])
+def test_many_rows(dtype, T, hq, hk, dim, rot, interleaved):
+    x = make(1, T, hq, hk, dim, rot, dtype, seed=T)
+    got = run(x, interleaved)
+    ref = reference({n: t.cuda() if t is not None else None for n, t in x.items()}, interleaved)
+    compare(got, {n: t.cpu() for n, t in ref.items()}, dtype, T * max(hq, hk))
+
+
+def test_a_stream_of_its_own_and_a_graph():
+    """Forward and backward on a side stream, captured and replayed with other inputs."""
+    from linear_attention_gated_gb300 import kda_qk_norm_rope_bwd, kda_qk_norm_rope_fwd
+    x, y = make(2, 130, 6, 2, 128, 64, torch.bfloat16, seed=7), make(2, 130, 6, 2, 128, 64, torch.bfloat16, seed=8, far=1000)
+    d = {n: t.cuda() for n, t in x.items()}
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+
+    def step():
+        rest = (d["q"], d["k"], d["qw"], d["kw"], d["pos"], d["freq"])
+        return kda_qk_norm_rope_fwd(*rest) + kda_qk_norm_rope_bwd(d["dq"], d["dk"], *rest)
+
+    with torch.cuda.stream(s):
+        out = step()
+    torch.cuda.synchronize()
+    compare(dict(zip(("q", "k", "dq", "dk", "dqw", "dkw"), out)), reference(x, False), torch.bfloat16, 1560)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        out = step()
+    for n in d:
+        d[n].copy_(y[n])
+    graph.replay()
+    torch.cuda.synchronize()
+    compare(dict(zip(("q", "k", "dq", "dk", "dqw", "dkw"), out)), reference(y, False), torch.bfloat16, 1560)
