@@ -870,51 +870,68 @@ __global__ void __launch_bounds__(256) kda_decay_chain_kernel(const __grid_const
 }
 
 // dq and dk from the value heads' FP32 parts: sums over a group's heads, rounded once; and, for the decays' gradient,
-// what crosses each token in each value head, q . dq - k . dk. A warp takes a (token, query/key head), the
-// parts' loads four heads ahead; bandwidth bounds it (1 KiB read for each value head and token).
-template <bool kCross>
+// what crosses each token in each value head, q . dq - k . dk. A warp takes four (token, value head) at a time: kHeads
+// (1, 2, else 4) heads of 4 / kHeads tokens of a query/key head, all their loads in flight; bandwidth bounds it (1 KiB
+// read for each token and value head).
+template <bool kCross, int kHeads>
 __global__ void __launch_bounds__(256) kda_decay_group_sum_kernel(const DecayProblem P, const float* dq32, const float* dk32,
                                                                   __nv_bfloat16* dq, __nv_bfloat16* dk, float* z) {
-  // a block takes eight consecutive tokens of a head (so that its eight z share a sector)
-  const int hq = blockIdx.x % P.Hqk;
-  const int64_t tok = (int64_t)(blockIdx.x / P.Hqk) * 8 + (threadIdx.x >> 5), row = tok * P.Hqk + hq;
+  constexpr int kTok = 4 / kHeads;
+  // (a block takes consecutive tokens of a head, so that their z share sectors)
+  const int hq = blockIdx.x % P.Hqk, lane = threadIdx.x & 31;
+  const int64_t tok = ((int64_t)(blockIdx.x / P.Hqk) * 8 + (threadIdx.x >> 5)) * kTok;
   if (tok >= P.Ttot) return;
-  const int lane = threadIdx.x & 31;
-  float4 q, k;
-  if (kCross) {
-    const uint2 rq = *reinterpret_cast<const uint2*>(P.q + tok * P.qt + hq * P.qh + 4 * lane);
-    const uint2 rk = *reinterpret_cast<const uint2*>(P.k + tok * P.kt + hq * P.kh + 4 * lane);
-    const float2 q0 = unpack2(rq.x), q1 = unpack2(rq.y), k0 = unpack2(rk.x), k1 = unpack2(rk.y);
-    q = make_float4(q0.x, q0.y, q1.x, q1.y);
-    k = make_float4(k0.x, k0.y, k1.x, k1.y);
-  }
-  float4 sq = make_float4(0.f, 0.f, 0.f, 0.f), sk = sq;
-  const int64_t at = row * P.r * kDim + 4 * lane;
-  for (int j0 = 0; j0 < P.r; j0 += 4) {
+  float4 sq[kTok], sk[kTok];
+#pragma unroll
+  for (int t = 0; t < kTok; ++t) sq[t] = sk[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j0 = 0; j0 < P.r; j0 += kHeads) {
     float4 a[4], b[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j0 + j < P.r) {
-        a[j] = __ldcs(reinterpret_cast<const float4*>(dq32 + at + (int64_t)(j0 + j) * kDim));
-        b[j] = __ldcs(reinterpret_cast<const float4*>(dk32 + at + (int64_t)(j0 + j) * kDim));
+    for (int i = 0; i < 4; ++i) {
+      const int t = i / kHeads, j = j0 + i % kHeads;
+      a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j < P.r && tok + t < P.Ttot) {
+        const int64_t at = (((tok + t) * P.Hqk + hq) * P.r + j) * kDim + 4 * lane;
+        a[i] = __ldcs(reinterpret_cast<const float4*>(dq32 + at));
+        b[i] = __ldcs(reinterpret_cast<const float4*>(dk32 + at));
       }
+    }
+    float x[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j0 + j < P.r) {
-        sq.x += a[j].x; sq.y += a[j].y; sq.z += a[j].z; sq.w += a[j].w;
-        sk.x += b[j].x; sk.y += b[j].y; sk.z += b[j].z; sk.w += b[j].w;
-        if (kCross) {
-          float x = q.x * a[j].x + q.y * a[j].y + q.z * a[j].z + q.w * a[j].w -
-                    (k.x * b[j].x + k.y * b[j].y + k.z * b[j].z + k.w * b[j].w);
-#pragma unroll
-          for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-          // heads first: the sums that follow run over tokens
-          if (lane == 0) z[((int64_t)hq * P.r + j0 + j) * P.Ttot + tok] = x;
+    for (int i = 0; i < 4; ++i) {
+      const int t = i / kHeads;
+      sq[t].x += a[i].x; sq[t].y += a[i].y; sq[t].z += a[i].z; sq[t].w += a[i].w;
+      sk[t].x += b[i].x; sk[t].y += b[i].y; sk[t].z += b[i].z; sk[t].w += b[i].w;
+      if (kCross) {
+        x[i] = 0.f;
+        if (tok + t < P.Ttot) {
+          const uint2 rq = *reinterpret_cast<const uint2*>(P.q + (tok + t) * P.qt + hq * P.qh + 4 * lane);
+          const uint2 rk = *reinterpret_cast<const uint2*>(P.k + (tok + t) * P.kt + hq * P.kh + 4 * lane);
+          const float2 q0 = unpack2(rq.x), q1 = unpack2(rq.y), k0 = unpack2(rk.x), k1 = unpack2(rk.y);
+          x[i] = q0.x * a[i].x + q0.y * a[i].y + q1.x * a[i].z + q1.y * a[i].w -
+                 (k0.x * b[i].x + k0.y * b[i].y + k1.x * b[i].z + k1.y * b[i].w);
         }
       }
+    }
+    if (kCross) {  // the four sums over the lanes at once: after two steps a lane holds one of them, i = 2 (lane / 16) + lane / 8 % 2
+      const bool up = lane & 16, right = lane & 8;
+      float y0 = (up ? x[2] : x[0]) + __shfl_xor_sync(0xffffffffu, up ? x[0] : x[2], 16);
+      float y1 = (up ? x[3] : x[1]) + __shfl_xor_sync(0xffffffffu, up ? x[1] : x[3], 16);
+      float y = (right ? y1 : y0) + __shfl_xor_sync(0xffffffffu, right ? y0 : y1, 8);
+#pragma unroll
+      for (int o = 4; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+      const int i = lane >> 3, t = i / kHeads, j = j0 + i % kHeads;
+      // heads first: the sums that follow run over tokens
+      if ((lane & 7) == 0 && j < P.r && tok + t < P.Ttot) z[((int64_t)hq * P.r + j) * P.Ttot + tok + t] = y;
+    }
   }
-  *reinterpret_cast<uint2*>(dq + row * kDim + 4 * lane) = make_uint2(pack2(sq.x, sq.y), pack2(sq.z, sq.w));
-  *reinterpret_cast<uint2*>(dk + row * kDim + 4 * lane) = make_uint2(pack2(sk.x, sk.y), pack2(sk.z, sk.w));
+#pragma unroll
+  for (int t = 0; t < kTok; ++t)
+    if (tok + t < P.Ttot) {
+      const int64_t at = ((tok + t) * P.Hqk + hq) * kDim + 4 * lane;
+      *reinterpret_cast<uint2*>(dq + at) = make_uint2(pack2(sq[t].x, sq[t].y), pack2(sq[t].z, sq[t].w));
+      *reinterpret_cast<uint2*>(dk + at) = make_uint2(pack2(sk[t].x, sk[t].y), pack2(sk[t].z, sk[t].w));
+    }
 }
 
 // A sum in two FP32 numbers, 48 bits.
@@ -1145,19 +1162,22 @@ cudaError_t launch_decay_backward(const DecayProblem& P, const float* h0, const 
   const float c = P.scale;
   cudaError_t e;
   const DecayStates none{g.d_hT, nullptr, 0, nullptr, P.N};
+  if ((e = pass<true>(P, k, q, d, 1.f, c, c, DecayStates{g.d_hT, g.dh0, 0, nullptr, P.N}, false, g.dv, nullptr, ws,
+                      s)) != cudaSuccess) return e;
+  // (last what is summed over heads: some of it is still in L2 then)
   if ((e = pass<false>(P, d, v, k, c, c, 1.f, DecayStates{h0, nullptr, 0, nullptr, P.N}, true, f32 ? nullptr : g.dq, dq,
                        ws, s)) != cudaSuccess) return e;
   if ((e = pass<true>(P, v, d, q, 1.f, c, c, none, true, f32 ? nullptr : g.dk, dk, ws, s)) != cudaSuccess)
     return e;
-  if ((e = pass<true>(P, k, q, d, 1.f, c, c, DecayStates{g.d_hT, g.dh0, 0, nullptr, P.N}, false, g.dv, nullptr, ws,
-                      s)) != cudaSuccess) return e;
   if (P.Ttot == 0 || !f32) return cudaSuccess;
   float* z = reinterpret_cast<float*>(base + w.z);
-  const int64_t blocks = (P.Ttot + 7) / 8 * P.Hqk;
+  const int heads = P.r == 1 ? 1 : P.r == 2 ? 2 : 4;
+  const int64_t tokens = 8 * (4 / heads), blocks = (P.Ttot + tokens - 1) / tokens * P.Hqk;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  const unsigned grid = (unsigned)blocks;
-  if (g.dg) kda_decay_group_sum_kernel<true><<<grid, 256, 0, s>>>(P, dq, dk, g.dq, g.dk, z);
-  else kda_decay_group_sum_kernel<false><<<grid, 256, 0, s>>>(P, dq, dk, g.dq, g.dk, nullptr);
+  auto sum = [&](auto kern) { kern<<<(unsigned)blocks, 256, 0, s>>>(P, dq, dk, g.dq, g.dk, z); };
+  if (!g.dg) heads == 2 ? sum(kda_decay_group_sum_kernel<false, 2>) : sum(kda_decay_group_sum_kernel<false, 4>);
+  else if (heads == 1) sum(kda_decay_group_sum_kernel<true, 1>);
+  else heads == 2 ? sum(kda_decay_group_sum_kernel<true, 2>) : sum(kda_decay_group_sum_kernel<true, 4>);
   if ((e = cudaGetLastError()) != cudaSuccess || !g.dg) return e;
   kda_decay_gate_grad_kernel<<<(unsigned)(P.N * P.Hv), kGateThreads, 0, s>>>(P, z, hT, g.d_hT, g.dg);
   return cudaGetLastError();
