@@ -57,11 +57,11 @@ constexpr int kStages = 3, kDecs = 8, kRing = 4;
 constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpDecay = 2, kWarpMma2 = 3, kWarpA = 4, kWarpB = 12;
 constexpr int kGroup = 8;                  // warps of A and of B
 constexpr int kThreads = 32 * 20;
-// Registers a thread of the control, A and B warps (setmaxnreg): 128 x 40 + 256 x 72 + 256 x 144 = 60,416 of the
+// Registers a thread of the control, A and B warps (setmaxnreg): 128 x 48 + 256 x 72 + 256 x 144 (kSplit: 64 and 152) = 61,440, all of the
 // 640 x 96 = 61,440 the block is launched with (a split above that would wait for ever).
 constexpr uint32_t kTile = kC * kDim * 2;  // bytes of a Q, K or V tile
 constexpr uint32_t kPanel = kC * 128;      // bytes of its 64-element half
-constexpr uint32_t kColU = 0;              // U: 128 columns
+constexpr uint32_t kColU = 0;              // U: 128 columns (in the pass over states alone, 128 more in the next one's place)
 constexpr uint32_t kColS = 128;            // the state as A operand, 64 + 64: its high and low BF16 parts, or (one part)
                                            // that of two chunks
 constexpr uint32_t kColO = 256;            // S Q^T, then V^T P^T: 64 + 64
@@ -90,7 +90,7 @@ struct Smem {
   Unit ring[kRing];      // units to come
   // full, empty: a stage's tiles are there / read by all products; dec, decfree: a chunk's decays are there / read by the last who does; g0, gu, gy: products done
   // (scores, U, Y); kready, pready: K~, P are there; ufree, yfree: U, Y are read; sready: the state is there
-  unsigned long long full[kStages], empty[kStages], dec[kDecs], decfree[kDecs], g0[2], gu, gy, kready[2], pready[2], ufree, sready[2], yfree;
+  unsigned long long full[kStages], empty[kStages], dec[kDecs], decfree[kDecs], g0[2], gu[2], gy, kready[2], pready[2], ufree[2], sready[2], yfree;
   unsigned long long clcbar, rfull[kRing], rempty[kRing];
   uint32_t tmem;
 };
@@ -194,13 +194,13 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar(sm.g0[i]), 1);
+      tc::mbar_init(bar(sm.gu[i]), 1);
+      tc::mbar_init(bar(sm.ufree[i]), kGroup);
       tc::mbar_init(bar(sm.kready[i]), kGroup);
       tc::mbar_init(bar(sm.pready[i]), kGroup);
       tc::mbar_init(bar(sm.sready[i]), kGroup);
     }
-    tc::mbar_init(bar(sm.gu), 1);
     tc::mbar_init(bar(sm.gy), 1);
-    tc::mbar_init(bar(sm.ufree), kGroup);
     tc::mbar_init(bar(sm.yfree), kGroup);
     tc::mbar_init(bar(sm.clcbar), 1);
     for (int i = 0; i < kRing; ++i) { tc::mbar_init(bar(sm.rfull[i]), 1); tc::mbar_init(bar(sm.rempty[i]), (kState ? 2 : 3) + 2 * kGroup); }
@@ -210,6 +210,10 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
   tc::fence_after();
   const uint32_t tbase = sm.tmem;
   bool ok = true;  // false: a wait gave up; the warp touches only its own CTA's memory and leaves
+
+  // U of chunk k: its place (the pass over states alone has two, so that one is read while the other is summed) and parity
+  auto uplace = [](uint32_t k) { return kState ? k & 1 : 0u; };
+  auto uphase = [](uint32_t k) { return kState ? (k >> 1) & 1 : k & 1; };
 
   // The ring of units, as a consumer (a warp): its place, and the next unit (false: none).
   uint32_t ur = 0;
@@ -237,7 +241,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
   };
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == kWarpLoad) {
       // ================= units and copies
       uint32_t g = 0;  // chunks so far
@@ -358,18 +362,20 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         if (kState) tiles(g);
         // U, once K~ is there and the last U is read
         if (ok) ok = tc::mbar_wait_lanes(bar(sm.kready[g & 1]), (g >> 1) & 1);
-        if (ok && g > 0) ok = tc::mbar_wait_lanes(bar(sm.ufree), (g - 1) & 1);
+        constexpr uint32_t kUs = kState ? 2 : 1;
+        if (ok && g >= kUs) ok = tc::mbar_wait_lanes(bar(sm.ufree[uplace(g)]), uphase(g - kUs));
         tc::fence_after();
         if (ok && tc::elect_one()) {
           const uint64_t dv = tc::mnmajor(tc::smem_u32(sm.tile[s][2]), kPanel);
           const uint64_t dh = tc::mnmajor(tc::smem_u32(sm.tile[s][1]), kPanel);
           const uint64_t dl = tc::mnmajor(tc::smem_u32(sm.lo[g & 1]), kPanel);
+          const uint32_t u = tbase + kColU + 128 * uplace(g);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            tc::mma_bf16_ss(tbase + kColU, dv + 128 * k, dh + 128 * k, tc::idesc_bf16(128, 128, true, true), k > 0);
-            tc::mma_bf16_ss(tbase + kColU, dv + 128 * k, dl + 128 * k, tc::idesc_bf16(128, 128, true, true), 1);
+            tc::mma_bf16_ss(u, dv + 128 * k, dh + 128 * k, tc::idesc_bf16(128, 128, true, true), k > 0);
+            tc::mma_bf16_ss(u, dv + 128 * k, dl + 128 * k, tc::idesc_bf16(128, 128, true, true), 1);
           }
-          tc::mma_commit(bar(sm.gu));
+          tc::mma_commit(bar(sm.gu[uplace(g)]));
           tc::mma_commit(bar(sm.empty[s]));
         }
         __syncwarp();
@@ -483,7 +489,8 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
     }
   } else if (warp < kWarpB) {
     // ================= K~ and P
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int at = tid - 32 * kWarpA, wq = (warp - kWarpA) & 3, half = (warp - kWarpA) >> 2;
     const uint32_t tl = tbase + ((uint32_t)(32 * wq) << 16);
     const float2 scale = make_float2(a.s_intra, a.s_intra);
@@ -504,17 +511,23 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           ok = tc::mbar_wait_lanes(bar(sm.g0[g & 1]), (g >> 1) & 1);
         }
         tc::fence_after();
+        uint4 r[4];  // (all loads first: a store could be to where the next load is from, for all the compiler knows)
+        float w1[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const int i = at + 32 * kGroup * m;
+          r[m] = *reinterpret_cast<const uint4*>(Ks + 16 * i);
+          w1[m] = sm.w[d][(i >> 3) & (kC - 1)];
+        }
 #pragma unroll
         for (int m = 0; m < 4; ++m) {  // 16-byte chunks i
           const int i = at + 32 * kGroup * m, row = (i >> 3) & (kC - 1);
-          const uint4 r = *reinterpret_cast<const uint4*>(Ks + 16 * i);
-          const float w1 = sm.w[d][row];
-          const float2 w = make_float2(w1, w1);
+          const float2 w = make_float2(w1[m], w1[m]);
           uint4 hi, lo;
-          split2(tc::mul2(unpack2(r.x), w), hi.x, lo.x);
-          split2(tc::mul2(unpack2(r.y), w), hi.y, lo.y);
-          split2(tc::mul2(unpack2(r.z), w), hi.z, lo.z);
-          split2(tc::mul2(unpack2(r.w), w), hi.w, lo.w);
+          split2(tc::mul2(unpack2(r[m].x), w), hi.x, lo.x);
+          split2(tc::mul2(unpack2(r[m].y), w), hi.y, lo.y);
+          split2(tc::mul2(unpack2(r[m].z), w), hi.z, lo.z);
+          split2(tc::mul2(unpack2(r[m].w), w), hi.w, lo.w);
           if (nt < kC && row >= nt) hi = lo = make_uint4(0u, 0u, 0u, 0u);  // rows past the end hold other tokens
           *reinterpret_cast<uint4*>(Ks + 16 * i) = hi;
           *reinterpret_cast<uint4*>(Ls + 16 * i) = lo;
@@ -573,7 +586,8 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
     }
   } else {
     // ================= the state and Y
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    if (kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     const int wq = (warp - kWarpB) & 3, half = (warp - kWarpB) >> 2;
     const int v = 32 * wq + lane;  // state row of this thread, its columns 64 half .. + 63; value of Y, tokens 32 half .. + 31
     const uint32_t tl = tbase + ((uint32_t)(32 * wq) << 16);
@@ -673,17 +687,17 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         const int nt = (int)(x.len - ci * kC < kC ? x.len - ci * kC : kC);
         if (ok) ok = tc::mbar_wait_lanes(bar(sm.dec[d]), (g / kDecs) & 1);
         const float2 lam = make_float2(sm.lam[d], sm.lam[d]);
-        if (ok) ok = tc::mbar_wait_lanes(bar(sm.gu), g & 1);
+        if (ok) ok = tc::mbar_wait_lanes(bar(sm.gu[uplace(g)]), uphase(g));
         tc::fence_after();
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           float r[16];
-          tc::tmem_ld16(tl + kColU + 64 * half + 16 * m, r);
+          tc::tmem_ld16(tl + kColU + 128 * uplace(g) + 64 * half + 16 * m, r);
 #pragma unroll
           for (int j = 0; j < 8; ++j) S[8 * m + j] = tc::fma2(lam, S[8 * m + j], make_float2(r[2 * j], r[2 * j + 1]));
         }
         tc::fence_before();
-        arrive(sm.ufree);
+        arrive(sm.ufree[uplace(g)]);
         if (kState) {
           arrive(sm.decfree[d]);
           continue;
