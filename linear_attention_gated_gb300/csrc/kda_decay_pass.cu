@@ -53,7 +53,7 @@ namespace kda {
 namespace {
 
 constexpr int kC = kDecayChunk;
-constexpr int kStages = 3, kDecs = 8, kRing = 4;
+constexpr int kTiles = 9, kStages = 4, kDecs = 8, kRing = 4;
 constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpDecay = 2, kWarpMma2 = 3, kWarpA = 4, kWarpB = 12;
 constexpr int kGroup = 8;                  // warps of A and of B
 constexpr int kThreads = 32 * 20;
@@ -78,7 +78,7 @@ struct Unit {
 };
 
 struct Smem {
-  unsigned char tile[kStages][3][kTile];  // Q, K, V
+  unsigned char tile[kTiles][kTile];      // stages of Q, K, V
   unsigned char lo[2][kTile];             // low parts of K~
   unsigned char P[2][kC * kC * 2];
   unsigned char extra[kTile];             // in two parts: the low parts of P (twice 8 KiB); else: Y on its way out
@@ -184,10 +184,14 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
   const DecayProblem& P = a.P;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto bar = [](unsigned long long& b) { return tc::smem_u32(&b); };
+  // Stages of copies, and a stage's tile of Q (0), K (1) or V (2). The pass over states alone has no Q and four stages:
+  // it takes a stage in half the time.
+  constexpr uint32_t kSt = kState ? 4 : 3;
+  auto tile = [&](uint32_t s, int x) -> unsigned char* { return sm.tile[kState ? 2 * s + x - 1 : 3 * s + x]; };
 
   if (warp == kWarpMma) tc::tmem_alloc(tc::smem_u32(&sm.tmem), 512);
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) { tc::mbar_init(bar(sm.full[i]), 1); tc::mbar_init(bar(sm.empty[i]), kState ? 1 : 2); }
+    for (uint32_t i = 0; i < kSt; ++i) { tc::mbar_init(bar(sm.full[i]), 1); tc::mbar_init(bar(sm.empty[i]), kState ? 1 : 2); }
     for (int i = 0; i < kDecs; ++i) {
       tc::mbar_init(bar(sm.dec[i]), 1);
       tc::mbar_init(bar(sm.decfree[i]), kGroup);
@@ -269,7 +273,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
       for (;;) {
         next.none = true;
         for (int64_t c = 0;; ++c) {
-          if (c == (x.nchunks < kStages ? x.nchunks : kStages)) {
+          if (c == (x.nchunks < kSt ? x.nchunks : kSt)) {
             // the next unit, told to everybody while this one's first chunks are under way
             const bool came = tc::mbar_wait_lanes(bar(sm.clcbar), asked & 1);
             ++asked;
@@ -289,18 +293,18 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
             if (ok && more) ask();
           }
           if (!ok || c == x.nchunks) break;
-          const int s = g % kStages;
-          if (g >= kStages) ok = tc::mbar_wait_lanes(bar(sm.empty[s]), (g / kStages - 1) & 1);
+          const int s = g % kSt;
+          if (g >= kSt) ok = tc::mbar_wait_lanes(bar(sm.empty[s]), (g / kSt - 1) & 1);
           if (!ok) break;
           if (lane == 0) {
             const int t = (int)(x.t0 + (kRev ? x.nchunks - 1 - c : c) * kC);
             tc::mbar_arrive_expect_tx(bar(sm.full[s]), (kState ? 2 : 3) * kTile);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-              tc::tma_load3(tc::smem_u32(sm.tile[s][1]) + p * kPanel, &maps.k, 64 * p, x.h / a.kdiv, t, bar(sm.full[s]));
+              tc::tma_load3(tc::smem_u32(tile(s, 1)) + p * kPanel, &maps.k, 64 * p, x.h / a.kdiv, t, bar(sm.full[s]));
               if (!kState)
-                tc::tma_load3(tc::smem_u32(sm.tile[s][0]) + p * kPanel, &maps.q, 64 * p, x.h / a.qdiv, t, bar(sm.full[s]));
-              tc::tma_load3(tc::smem_u32(sm.tile[s][2]) + p * kPanel, &maps.v, 64 * p, x.h / a.vdiv, t, bar(sm.full[s]));
+                tc::tma_load3(tc::smem_u32(tile(s, 0)) + p * kPanel, &maps.q, 64 * p, x.h / a.qdiv, t, bar(sm.full[s]));
+              tc::tma_load3(tc::smem_u32(tile(s, 2)) + p * kPanel, &maps.v, 64 * p, x.h / a.vdiv, t, bar(sm.full[s]));
             }
           }
           __syncwarp();
@@ -313,21 +317,21 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         // flag it, and let this CTA's copies (and a response) land before its memory is given back
         if (lane == 0) atomicOr(P.status, 1);
         tc::mbar_wait_lanes(bar(sm.clcbar), asked & 1, 1u << 16);
-        for (uint32_t k = g > kStages ? g - kStages : 0; k < g; ++k)
-          tc::mbar_wait_lanes(bar(sm.full[k % kStages]), (k / kStages) & 1);
+        for (uint32_t k = g > kSt ? g - kSt : 0; k < g; ++k)
+          tc::mbar_wait_lanes(bar(sm.full[k % kSt]), (k / kSt) & 1);
       }
     } else if (warp == kWarpMma) {
       // ================= products that need no state: the scores and U
       uint32_t g = 0;
       auto tiles = [&](uint32_t k) {
-        if (ok) ok = tc::mbar_wait_lanes(bar(sm.full[k % kStages]), (k / kStages) & 1);
+        if (ok) ok = tc::mbar_wait_lanes(bar(sm.full[k % kSt]), (k / kSt) & 1);
         tc::fence_after();
       };
       auto scores = [&](uint32_t k) {
         tiles(k);
         if (ok && tc::elect_one()) {
-          const uint64_t dq = tc::kmajor(tc::smem_u32(sm.tile[k % kStages][0]));
-          const uint64_t dk = tc::kmajor(tc::smem_u32(sm.tile[k % kStages][1]));
+          const uint64_t dq = tc::kmajor(tc::smem_u32(tile(k % kSt, 0)));
+          const uint64_t dk = tc::kmajor(tc::smem_u32(tile(k % kSt, 1)));
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t off = (i >> 2) * (kPanel >> 4) + (i & 3) * 2;
@@ -358,7 +362,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           ++ahead;
         }
         if (!due) continue;
-        const int s = g % kStages;
+        const int s = g % kSt;
         if (kState) tiles(g);
         // U, once K~ is there and the last U is read
         if (ok) ok = tc::mbar_wait_lanes(bar(sm.kready[g & 1]), (g >> 1) & 1);
@@ -366,8 +370,8 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         if (ok && g >= kUs) ok = tc::mbar_wait_lanes(bar(sm.ufree[uplace(g)]), uphase(g - kUs));
         tc::fence_after();
         if (ok && tc::elect_one()) {
-          const uint64_t dv = tc::mnmajor(tc::smem_u32(sm.tile[s][2]), kPanel);
-          const uint64_t dh = tc::mnmajor(tc::smem_u32(sm.tile[s][1]), kPanel);
+          const uint64_t dv = tc::mnmajor(tc::smem_u32(tile(s, 2)), kPanel);
+          const uint64_t dh = tc::mnmajor(tc::smem_u32(tile(s, 1)), kPanel);
           const uint64_t dl = tc::mnmajor(tc::smem_u32(sm.lo[g & 1]), kPanel);
           const uint32_t u = tbase + kColU + 128 * uplace(g);
 #pragma unroll
@@ -387,14 +391,14 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         uint32_t g = 0;
         int64_t left = 0;
         for (; any_chunk(left); ++g, --left) {
-          const int s = g % kStages;
-          if (ok) ok = tc::mbar_wait_lanes(bar(sm.full[s]), (g / kStages) & 1);
+          const int s = g % kSt;
+          if (ok) ok = tc::mbar_wait_lanes(bar(sm.full[s]), (g / kSt) & 1);
           // once the state is there and the last Y is read
           if (ok) ok = tc::mbar_wait_lanes(bar(sm.sready[g & 1]), (g >> 1) & 1);
           if (ok && g > 0) ok = tc::mbar_wait_lanes(bar(sm.yfree), (g - 1) & 1);
           tc::fence_after();
           if (ok && tc::elect_one()) {
-            const uint64_t dq = tc::kmajor(tc::smem_u32(sm.tile[s][0]));
+            const uint64_t dq = tc::kmajor(tc::smem_u32(tile(s, 0)));
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const uint32_t off = (i >> 2) * (kPanel >> 4) + (i & 3) * 2;
@@ -408,7 +412,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           if (ok) ok = tc::mbar_wait_lanes(bar(sm.pready[g & 1]), (g >> 1) & 1);
           tc::fence_after();
           if (ok && tc::elect_one()) {
-            const uint64_t dv = tc::mnmajor(tc::smem_u32(sm.tile[s][2]), kPanel);
+            const uint64_t dv = tc::mnmajor(tc::smem_u32(tile(s, 2)), kPanel);
             const uint64_t dp = tc::kmajor(tc::smem_u32(sm.P[g & 1])), dr = tc::kmajor(tc::smem_u32(sm.extra) + (g & 1) * (kTile / 2));
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -497,15 +501,15 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
     uint32_t g = 0;
     for (Unit x; next_unit(x);) {
       for (int64_t c = 0; c < x.nchunks; ++c, ++g) {
-        const int s = g % kStages, d = g % kDecs;
+        const int s = g % kSt, d = g % kDecs;
         const int64_t left = x.len - (kRev ? x.nchunks - 1 - c : c) * kC;
         const int nt = (int)(left < kC ? left : kC);
-        unsigned char* Ks = sm.tile[s][1];
+        unsigned char* Ks = tile(s, 1);
         unsigned char* Ls = sm.lo[g & 1];
         if (ok) ok = tc::mbar_wait_lanes(bar(sm.dec[d]), (g / kDecs) & 1);
         if (kState) {
-          if (ok) ok = tc::mbar_wait_lanes(bar(sm.full[s]), (g / kStages) & 1);
-          if (ok && g >= 2) ok = tc::mbar_wait_lanes(bar(sm.empty[(g - 2) % kStages]), ((g - 2) / kStages) & 1);
+          if (ok) ok = tc::mbar_wait_lanes(bar(sm.full[s]), (g / kSt) & 1);
+          if (ok && g >= 2) ok = tc::mbar_wait_lanes(bar(sm.empty[(g - 2) % kSt]), ((g - 2) / kSt) & 1);
         } else if (ok) {
           // K is free once its scores are done; they are started after chunk g - 2's U, which reads this parity's low parts
           ok = tc::mbar_wait_lanes(bar(sm.g0[g & 1]), (g >> 1) & 1);
@@ -534,13 +538,13 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         }
         if (nt < kC)
           for (int i = at; i < (kC - nt) * 16; i += 32 * kGroup)
-            *reinterpret_cast<uint4*>(sm.tile[s][2] + ((i >> 3) & 1) * kPanel + (nt + (i >> 4)) * 128 + (i & 7) * 16) =
+            *reinterpret_cast<uint4*>(tile(s, 2) + ((i >> 3) & 1) * kPanel + (nt + (i >> 4)) * 128 + (i & 7) * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
         tc::fence_async_smem();
         arrive(sm.kready[g & 1]);
         if (!kState) {
           // P's buffer is free once chunk g - 2's products are done
-          if (ok && g >= 2) ok = tc::mbar_wait_lanes(bar(sm.empty[(g - 2) % kStages]), ((g - 2) / kStages) & 1);
+          if (ok && g >= 2) ok = tc::mbar_wait_lanes(bar(sm.empty[(g - 2) % kSt]), ((g - 2) / kSt) & 1);
           // rows i = 16 wq + lane / 4 (+ 8), columns 32 half + 8 m + 2 (lane % 4) (+ 1)
           const int i0 = 16 * wq + (lane >> 2), j0 = 32 * half + 2 * (lane & 3);
           unsigned char* Pt = sm.P[g & 1];
