@@ -33,15 +33,28 @@
 //   warps 4-11   K~ (over K and beside) and P
 //   warps 12-19  the state, 64 of a row's 128 values a thread in registers, S = e^{b_C} S + U with U = V^T K~
 //            from tensor memory, and as A operand back there; Y
-// K~ is an operand in two BF16 parts, hi + lo, 16 mantissa bits: the carried state keeps FP32-level accuracy.
-// P and S, which feed Y alone, are rounded to BF16 once (as Y itself is) where Y is an output; where Y is FP32 and
-// summed further, over heads or, for the decays' gradient, over the sequence, so that errors of its terms would
-// outlive a cancelling sum, they too are in two parts (kSplit).
-// A unit is one (sequence, head), longest sequences first, or one segment of it.
+// K~ is an operand in two BF16 parts, hi + lo, 16 mantissa bits: FP32 states are off by 2.4e-6 relative to 64 bits
+// (FP32 arithmetic throughout: 2e-7), whatever the length, as each chunk's part is summed in FP32. One part would
+// leave 1.7e-3; a third would take 16 KiB of shared memory that is not there and a quarter more of the products' time.
+// P and S, which feed Y alone, are rounded to BF16 once (as Y itself is) where Y is an output: o is off by 2.3e-3
+// where one rounding of the exact value leaves 1.7e-3. Where Y is FP32 and summed further, over heads or, for the
+// decays' gradient, over the sequence, so that errors of its terms would outlive a cancelling sum, they too are in two
+// parts (kSplit); it costs 80 us against 57 in a pass over 4 x 2048 tokens of 32 heads.
+// A unit is one (sequence, head), longest sequences first (24 sequences of 1 to 4000 tokens, 64 heads: 540 us, in
+// index order 594), or one segment of it.
+//
+// What bounds it: HBM would take 0.9 us for a chunk and SM, shared memory's pipe is busy for about 1 us (operands of
+// the products 1090 cycles, element-wise loads and stores 1300, copies 500 of some 3300), the tensor core for a third;
+// the rest are waits in the chains K~ -> U -> state -> S Q^T -> Y and scores -> P -> V^T P^T, which three stages of 48
+// KiB, two of K~ and P and the double place of S overlap but for a part. Measured: 1.6 us a chunk and SM. 8 x 1024 tokens of
+// 96 heads (856 MB): 167 us, 5.1 TB/s, 77 % of the copy rate, of which the 8 units beyond 5 an SM take a tenth;
+// 24 sequences, 45 k tokens of 64 heads: 481 us, 1.85 GB, 3.9 TB/s. Tried and slower: 24, 28 and 32 warps with other
+// shares of the roles (195 to 232 us against 170 at the time), Y copied out by each warp for its part or by the copying
+// warp (+5 %), tiles prefetched to L2 (+13 %).
 //
 // Long axis, few units: each sequence is cut into segments. A first pass runs the state part alone
 // over every segment but the last in time, a small kernel chains the segments' states, and
-// the main pass starts every segment from its state.
+// the main pass starts every segment from its state: 32771 tokens of 32 heads 99 + 11 + 176 us (whole: 763).
 #include <algorithm>
 
 #include "kda_decay.cuh"
@@ -838,7 +851,8 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
 }
 
 // Chains the segments of one (sequence, head): in, each segment's own state (from zero) but the last's;
-// out, the state each segment starts from. A CTA takes 1024 of the state's values.
+// out, the state each segment starts from. A CTA takes 1024 of the state's values (16 CTAs a head: few heads are cut).
+// Latency bounds it, one load's and the launch's: 11 us for 9 segments of 32 heads (36 MB in L2).
 template <bool kRev>
 __global__ void __launch_bounds__(256) kda_decay_chain_kernel(const __grid_constant__ PassArgs a) {
   const DecayProblem& P = a.P;
@@ -889,8 +903,9 @@ __global__ void __launch_bounds__(256) kda_decay_chain_kernel(const __grid_const
 
 // dq and dk from the value heads' FP32 parts: sums over a group's heads, rounded once; and, for the decays' gradient,
 // what crosses each token in each value head, q . dq - k . dk. A warp takes four (token, value head) at a time: kHeads
-// (1, 2, else 4) heads of 4 / kHeads tokens of a query/key head, all their loads in flight; bandwidth bounds it (1 KiB
-// read for each token and value head).
+// (1, 2, else 4) heads of 4 / kHeads tokens of a query/key head, all their loads in flight (one token and query/key
+// head a warp, whatever the heads: 69 us against 57). Bandwidth bounds it, 1 KiB read for each token and value head:
+// 8192 tokens of 16 and 32 heads, 336 MB, 57 us, 5.9 TB/s, 88 % of the copy rate.
 template <bool kCross, int kHeads>
 __global__ void __launch_bounds__(256) kda_decay_group_sum_kernel(const DecayProblem P, const float* dq32, const float* dk32,
                                                                   __nv_bfloat16* dq, __nv_bfloat16* dk, float* z) {
@@ -971,7 +986,8 @@ struct Sum2 {
 
 // dg of one (sequence, head): a decay scales all that crosses its token, so
 //   dg_t = sum_{i >= t} (q_i . dq_i - k_i . dk_i) + <S_T, dS_T>.
-// The sums cancel over long sequences: 48 bits. 512 threads, from the end in runs of 4096 tokens.
+// The sums cancel over long sequences: 48 bits. 512 threads, from the end in runs of 4096 tokens. Latency bounds it
+// (scans over a block): 11 us for 4 x 2048 tokens of 32 heads, of 345 for the step.
 constexpr int kGateThreads = 512, kGateEach = 8;
 __global__ void __launch_bounds__(kGateThreads) kda_decay_gate_grad_kernel(const DecayProblem P, const float* z, const float* hT,
                                                                           const float* dhT, __nv_bfloat16* dg) {
