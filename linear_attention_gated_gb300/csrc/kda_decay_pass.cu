@@ -39,14 +39,15 @@
 // P and S, which feed Y alone, are rounded to BF16 once (as Y itself is) where Y is an output: o is off by 2.3e-3
 // where one rounding of the exact value leaves 1.7e-3. Where Y is FP32 and summed further, over heads or, for the
 // decays' gradient, over the sequence, so that errors of its terms would outlive a cancelling sum, they too are in two
-// parts (kSplit); it costs 80 us against 57 in a pass over 4 x 2048 tokens of 32 heads.
+// parts (kSplit); it costs 73 to 78 us against 57 in a pass over 4 x 2048 tokens of 32 heads.
 // A unit is one (sequence, head), longest sequences first (24 sequences of 1 to 4000 tokens, 64 heads: 540 us, in
 // index order 594), or one segment of it.
 //
-// What bounds it: HBM would take 0.9 us for a chunk and SM, shared memory's pipe is busy for about 1 us (operands of
-// the products 1090 cycles, element-wise loads and stores 1300, copies 500 of some 3300), the tensor core for a third;
-// the rest are waits in the chains K~ -> U -> state -> S Q^T -> Y and scores -> P -> V^T P^T, which three stages of 48
-// KiB, two of K~ and P and the double place of S overlap but for a part. Measured: 1.6 us a chunk and SM. 8 x 1024 tokens of
+// What bounds it: shared memory's data pipe, which the products' operands (1090 cycles a chunk), the element-wise loads
+// and stores (1450 with the turns they lose to the others) and the copies (500) share: nearly all of some 3150 cycles.
+// The tensor core is busy for a third, HBM would take half. Three stages of 48 KiB, two places of K~ and P and (one
+// part) of S overlap the chains K~ -> U -> state -> S Q^T -> Y and scores -> P -> V^T P^T of neighbouring chunks.
+// Measured: 1.6 us a chunk and SM. 8 x 1024 tokens of
 // 96 heads (856 MB): 167 us, 5.1 TB/s, 77 % of the copy rate, of which the 8 units beyond 5 an SM take a tenth;
 // 24 sequences, 45 k tokens of 64 heads: 481 us, 1.85 GB, 3.9 TB/s. Tried and slower: 24, 28 and 32 warps with other
 // shares of the roles (195 to 232 us against 170 at the time), Y copied out by each warp for its part or by the copying
@@ -987,7 +988,7 @@ struct Sum2 {
 // dg of one (sequence, head): a decay scales all that crosses its token, so
 //   dg_t = sum_{i >= t} (q_i . dq_i - k_i . dk_i) + <S_T, dS_T>.
 // The sums cancel over long sequences: 48 bits. 512 threads, from the end in runs of 4096 tokens. Latency bounds it
-// (scans over a block): 11 us for 4 x 2048 tokens of 32 heads, of 345 for the step.
+// (scans over a block): 11 us for 4 x 2048 tokens of 32 heads, of 338 for the step.
 constexpr int kGateThreads = 512, kGateEach = 8;
 __global__ void __launch_bounds__(kGateThreads) kda_decay_gate_grad_kernel(const DecayProblem P, const float* z, const float* hT,
                                                                           const float* dhT, __nv_bfloat16* dg) {
