@@ -102,9 +102,9 @@ struct Smem {
   float lam[kDecs];      // e^{b_C}
   uint4 clc;             // response: the next unit
   Unit ring[kRing];      // units to come
-  // full, empty: a stage's tiles are there / read by all products; dec, decfree: a chunk's decays are there / read by the last who does; g0, gu, gy: products done
-  // (scores, U, Y); kready, pready: K~, P are there; ufree, yfree: U, Y are read; sready: the state is there
-  unsigned long long full[kStages], empty[kStages], dec[kDecs], decfree[kDecs], g0[2], gu[2], gy, kready[2], pready[2], ufree[2], sready[2], yfree;
+  // full, empty: a stage's tiles are there / read by all products; dec, decfree: a chunk's decays are there / read by the last who does; g0, gu, gy, gq: products done
+  // (scores, U, Y, its S Q^T in two parts); kready, pready: K~, P are there; ufree, yfree: U, Y are read; sready: the state is there
+  unsigned long long full[kStages], empty[kStages], dec[kDecs], decfree[kDecs], g0[2], gu[2], gy, gq, kready[2], pready[2], ufree[2], sready[2], yfree;
   unsigned long long clcbar, rfull[kRing], rempty[kRing];
   uint32_t tmem;
 };
@@ -219,6 +219,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
       tc::mbar_init(bar(sm.sready[i]), kGroup);
     }
     tc::mbar_init(bar(sm.gy), 1);
+    tc::mbar_init(bar(sm.gq), 1);
     tc::mbar_init(bar(sm.yfree), kGroup);
     tc::mbar_init(bar(sm.clcbar), 1);
     for (int i = 0; i < kRing; ++i) { tc::mbar_init(bar(sm.rfull[i]), 1); tc::mbar_init(bar(sm.rempty[i]), (kState ? 2 : 3) + 2 * kGroup); }
@@ -421,6 +422,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
               if (kSplit)
                 tc::mma_bf16_ts(tbase + kColO, tbase + kColS + 64 + 8 * i, dq + off, tc::idesc_bf16(128, 64, false, false), 1);
             }
+            if (kSplit) tc::mma_commit(bar(sm.gq));
           }
           __syncwarp();
           if (ok) ok = tc::mbar_wait_lanes(bar(sm.pready[g & 1]), (g >> 1) & 1);
@@ -720,34 +722,38 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           arrive(sm.decfree[d]);
           continue;
         }
-        // (in one part, the last chunk's S Q^T has left the other columns: its Y was waited for)
-        if (!kSplit && c + 1 < x.nchunks) put_state(g + 1);
+        // in two parts, the columns are those of this chunk's S Q^T; in one, the last chunk's has left the others: its Y
+        // was waited for
+        if (kSplit && c + 1 < x.nchunks) {
+          if (ok) ok = tc::mbar_wait_lanes(bar(sm.gq), g & 1);
+          tc::fence_after();
+        }
+        if (c + 1 < x.nchunks) put_state(g + 1);
         if (ok) ok = tc::mbar_wait_lanes(bar(sm.gy), g & 1);
         tc::fence_after();
-        if (kSplit && c + 1 < x.nchunks) put_state(g + 1);
         if (kSplit) {  // FP32, straight from the registers: thread v holds one value of each token
-          float* dst = a.y32 + ((x.t0 + ci * kC + 32 * half) * P.Hv + x.h) * kDim + v;
+          float2 z[16];
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             float r[16], y[16];
             tc::tmem_ld16_nowait(tl + kColO + 32 * half + 16 * m, r);
             tc::tmem_ld16_nowait(tl + kColO + 64 + 32 * half + 16 * m, y);
             tc::tmem_wait_ld2(r, y);
-            const int left = nt - 32 * half - 16 * m;
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
               const float4 e = *reinterpret_cast<const float4*>(&sm.eb[d][32 * half + 16 * m + j]);
-              const float2 p = tc::fma2(make_float2(e.x, e.y), make_float2(r[j], r[j + 1]), make_float2(y[j], y[j + 1]));
-              const float2 q = tc::fma2(make_float2(e.z, e.w), make_float2(r[j + 2], r[j + 3]), make_float2(y[j + 2], y[j + 3]));
-              const float z[4] = {p.x, p.y, q.x, q.y};
-#pragma unroll
-              for (int i = 0; i < 4; ++i, dst += (int64_t)P.Hv * kDim)
-                if (j + i < left) *dst = z[i];
+              z[8 * m + j / 2] = tc::fma2(make_float2(e.x, e.y), make_float2(r[j], r[j + 1]), make_float2(y[j], y[j + 1]));
+              z[8 * m + j / 2 + 1] = tc::fma2(make_float2(e.z, e.w), make_float2(r[j + 2], r[j + 3]), make_float2(y[j + 2], y[j + 3]));
             }
           }
           tc::fence_before();
           arrive(sm.yfree);
           arrive(sm.decfree[d]);
+          float* dst = a.y32 + ((x.t0 + ci * kC + 32 * half) * P.Hv + x.h) * kDim + v;
+          const int left = nt - 32 * half;
+#pragma unroll
+          for (int j = 0; j < 32; ++j, dst += (int64_t)P.Hv * kDim)
+            if (j < left) *dst = j & 1 ? z[j / 2].y : z[j / 2].x;
         } else {
           // transposed by matrix stores into a tile of shared memory, copied out from there
           if (warp == kWarpB && lane == 0) tc::bulk_wait_read();  // the last one has left
