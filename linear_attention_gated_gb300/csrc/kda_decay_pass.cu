@@ -39,7 +39,7 @@
 // P and S, which feed Y alone, are rounded to BF16 once (as Y itself is) where Y is an output: o is off by 2.3e-3
 // where one rounding of the exact value leaves 1.7e-3. Where Y is FP32 and summed further, over heads or, for the
 // decays' gradient, over the sequence, so that errors of its terms would outlive a cancelling sum, they too are in two
-// parts (kSplit); it costs 73 to 78 us against 57 in a pass over 4 x 2048 tokens of 32 heads.
+// parts (kSplit); it costs 68 us against 56 in a pass over 4 x 2048 tokens of 32 heads.
 // A unit is one (sequence, head), longest sequences first (24 sequences of 1 to 4000 tokens, 64 heads: 540 us, in
 // index order 594), or one segment of it.
 //
@@ -994,7 +994,7 @@ struct Sum2 {
 // dg of one (sequence, head): a decay scales all that crosses its token, so
 //   dg_t = sum_{i >= t} (q_i . dq_i - k_i . dk_i) + <S_T, dS_T>.
 // The sums cancel over long sequences: 48 bits. 512 threads, from the end in runs of 4096 tokens. Latency bounds it
-// (scans over a block): 11 us for 4 x 2048 tokens of 32 heads, of 338 for the step.
+// (scans over a block): 11 us for 4 x 2048 tokens of 32 heads, of 326 for the step.
 constexpr int kGateThreads = 512, kGateEach = 8;
 __global__ void __launch_bounds__(kGateThreads) kda_decay_gate_grad_kernel(const DecayProblem P, const float* z, const float* hT,
                                                                           const float* dhT, __nv_bfloat16* dg) {
