@@ -18,13 +18,14 @@ from .kda import KdaError, _check, load_library
 DIM = 128
 _NAN = float("nan")
 _UNCUT = 1536  # sequences up to this long are never cut into segments: prefill needs no workspace for them
-_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_BF16, _F32, _F64, _I32, _I64 = torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.int64
 _STATE = {torch.bfloat16: 0, torch.float32: 1}
 _ROPE_WORKSPACE = {}  # head_dim -> bytes
 _ROPE_TYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
 def _call(f, device, *args):
@@ -34,7 +35,7 @@ def _call(f, device, *args):
         raise ValueError("tensors must be CUDA tensors")
     index = device.index
     stream = torch.cuda.current_stream(index).cuda_stream if _raw_stream is None else _raw_stream(index)
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         rc = f(*args, stream)
     else:
         with torch.cuda.device(index):
@@ -77,13 +78,8 @@ def _strides(t, name):
     return st, sh
 
 
-def _all_strides(named):
-    """None when every tensor is contiguous, else the token and head strides of all as a C array."""
-    for _, t in named:
-        if not t.is_contiguous():
-            break
-    else:
-        return None
+def _all_strides(*named):
+    """Token and head strides of all as a C array. (Not needed where all are contiguous.)"""
     flat = [s for name, t in named for s in (_strides(t, name) if t.numel() else (t.shape[2] * t.shape[3], t.shape[3]))]
     return (ctypes.c_int64 * len(flat))(*flat)
 
@@ -104,7 +100,8 @@ def _decay_inputs(q, k, v, log_decay):
         _want(log_decay, "log_decay", _BF16, (B, T, Hv), dev)
     else:
         _want(log_decay, "log_decay", _F32, (Hv,), dev)
-    return B, T, Hqk, Hv, D, int(per_token), _all_strides((("q", q), ("k", k), ("v", v)))
+    flat = q.is_contiguous() and k.is_contiguous() and v.is_contiguous()
+    return B, T, Hqk, Hv, D, int(per_token), None if flat else _all_strides(("q", q), ("k", k), ("v", v))
 
 
 def _offsets(cu_seqlens, cu_seqlens_cpu, dev, need_mirror):
@@ -334,15 +331,18 @@ def _rope_inputs(q, k, q_weight, k_weight, positions, inv_freq):
     Hk = k.shape[2]
     dev = q.device
     _typed(k, "k", q.dtype, (B, T, Hk, D), dev)
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _want(w, name, _F32, (D,), dev)
-    R = 0
-    if inv_freq is not None:
-        R = 2 * inv_freq.numel()
-        _want(inv_freq, "inv_freq", torch.float64, (R // 2,), dev)
-        _want(positions, "positions", _I64, (B, T), dev)
-    return B, T, Hq, Hk, D, R, dev
+    if q_weight is not None:
+        _want(q_weight, "q_weight", _F32, (D,), dev)
+    if k_weight is not None:
+        _want(k_weight, "k_weight", _F32, (D,), dev)
+    if inv_freq is None:
+        return B, T, Hq, Hk, D, 0, dev, None, None
+    R = 2 * inv_freq.numel()
+    _want(inv_freq, "inv_freq", _F64, (R // 2,), dev)
+    _want(positions, "positions", _I64, (B, T), dev)
+    if R == 0:
+        return B, T, Hq, Hk, D, 0, dev, None, None
+    return B, T, Hq, Hk, D, R, dev, positions.data_ptr(), inv_freq.data_ptr()
 
 
 def kda_qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interleaved=False, q_out=None, k_out=None):
@@ -353,19 +353,21 @@ def kda_qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6
     (2d, 2d + 1) when interleaved; None for the norm alone. D and R are multiples of 16, D up to 256.
     q_out and k_out may be q and k."""
     lib = load_library()
-    B, T, Hq, Hk, D, R, dev = _rope_inputs(q, k, q_weight, k_weight, positions, inv_freq)
+    B, T, Hq, Hk, D, R, dev, pos, freq = _rope_inputs(q, k, q_weight, k_weight, positions, inv_freq)
+    flat_q, flat_k = q.is_contiguous(), k.is_contiguous()
     if q_out is None:
-        q_out = torch.empty_like(q) if q.is_contiguous() else torch.empty((B, T, Hq, D), dtype=q.dtype, device=dev)
+        q_out = torch.empty_like(q) if flat_q else torch.empty((B, T, Hq, D), dtype=q.dtype, device=dev)
     else:
         _typed(q_out, "q_out", q.dtype, q.shape, dev)
+        flat_q = flat_q and q_out.is_contiguous()
     if k_out is None:
-        k_out = torch.empty_like(k) if k.is_contiguous() else torch.empty((B, T, Hk, D), dtype=q.dtype, device=dev)
+        k_out = torch.empty_like(k) if flat_k else torch.empty((B, T, Hk, D), dtype=q.dtype, device=dev)
     else:
         _typed(k_out, "k_out", q.dtype, k.shape, dev)
-    strides = _all_strides((("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out)))
+        flat_k = flat_k and k_out.is_contiguous()
+    strides = None if flat_q and flat_k else _all_strides(("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out))
     _call(lib.kda_qk_norm_rope_fwd, dev, q.data_ptr(), k.data_ptr(), _ROPE_TYPES[q.dtype], _p(q_weight), _p(k_weight),
-          _p(positions) if R else None, _p(inv_freq) if R else None, B * T, Hq, Hk, D, R, eps, int(bool(interleaved)),
-          strides, q_out.data_ptr(), k_out.data_ptr())
+          pos, freq, B * T, Hq, Hk, D, R, eps, 1 if interleaved else 0, strides, q_out.data_ptr(), k_out.data_ptr())
     return q_out, k_out
 
 
@@ -376,16 +378,20 @@ def kda_qk_norm_rope_bwd(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, 
     where there is no weight. ``out``: (dq_in, dk_in) buffers, which may be dq and dk. ``workspace``: a uint8
     tensor for the weights' partial sums (kda_qk_norm_rope_workspace_bytes); None takes one for the call."""
     lib = load_library()
-    B, T, Hq, Hk, D, R, dev = _rope_inputs(q, k, q_weight, k_weight, positions, inv_freq)
+    B, T, Hq, Hk, D, R, dev, pos, freq = _rope_inputs(q, k, q_weight, k_weight, positions, inv_freq)
     _typed(dq, "dq", q.dtype, q.shape, dev)
     _typed(dk, "dk", q.dtype, k.shape, dev)
+    flat_q, flat_k = q.is_contiguous(), k.is_contiguous()
     if out is None:
-        gq = torch.empty_like(q) if q.is_contiguous() else torch.empty((B, T, Hq, D), dtype=q.dtype, device=dev)
-        gk = torch.empty_like(k) if k.is_contiguous() else torch.empty((B, T, Hk, D), dtype=q.dtype, device=dev)
+        gq = torch.empty_like(q) if flat_q else torch.empty((B, T, Hq, D), dtype=q.dtype, device=dev)
+        gk = torch.empty_like(k) if flat_k else torch.empty((B, T, Hk, D), dtype=q.dtype, device=dev)
+        flat = flat_q and flat_k
     else:
         gq, gk = out
         _typed(gq, "out[0]", q.dtype, q.shape, dev)
         _typed(gk, "out[1]", q.dtype, k.shape, dev)
+        flat = flat_q and flat_k and gq.is_contiguous() and gk.is_contiguous()
+    flat = flat and dq.is_contiguous() and dk.is_contiguous()
     gqw = None if q_weight is None else torch.empty_like(q_weight)
     gkw = None if k_weight is None else torch.empty_like(k_weight)
     if workspace is None:
@@ -398,9 +404,9 @@ def kda_qk_norm_rope_bwd(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, 
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     else:
         _want(workspace, "workspace", torch.uint8, workspace.shape, dev)
-    strides = _all_strides((("q", q), ("k", k), ("out[0]", gq), ("out[1]", gk), ("dq", dq), ("dk", dk)))
+    strides = None if flat else _all_strides(("q", q), ("k", k), ("out[0]", gq), ("out[1]", gk), ("dq", dq), ("dk", dk))
     _call(lib.kda_qk_norm_rope_bwd, dev, dq.data_ptr(), dk.data_ptr(), q.data_ptr(), k.data_ptr(), _ROPE_TYPES[q.dtype],
-          _p(q_weight), _p(k_weight), _p(positions) if R else None, _p(inv_freq) if R else None, B * T, Hq, Hk, D, R, eps,
-          int(bool(interleaved)), strides, gq.data_ptr(), gk.data_ptr(), _p(gqw), _p(gkw), _p(workspace),
+          _p(q_weight), _p(k_weight), pos, freq, B * T, Hq, Hk, D, R, eps, 1 if interleaved else 0, strides,
+          gq.data_ptr(), gk.data_ptr(), _p(gqw), _p(gkw), _p(workspace),
           0 if workspace is None else workspace.numel())
     return gq, gk, gqw, gkw
