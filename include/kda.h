@@ -416,8 +416,9 @@ kda_status kda_prefill(const kda_bf16* q, const kda_bf16* k, const kda_bf16* v, 
  *               pool. NULL uses a word inside the library.
  * Outputs are caller-owned, overwritten, and must not overlap an input, each other
  * or the workspace. Arithmetic: products of BF16 operands with FP32 accumulation;
- * states, decays and sums are FP32, and states that reach an FP32 output keep its
- * accuracy. Results do not depend on the order of execution.
+ * states, decays and sums are FP32; what enters a state is taken in two BF16 parts
+ * (16 bits), so FP32 states are within about 2.4e-6 of the exact ones (relative, in
+ * the 2-norm). Results do not depend on the order of execution.
  * Errors: as above (KDA_ERR_INVALID_ARGUMENT, _UNSUPPORTED, _ALIASING,
  * _WORKSPACE_TOO_SMALL, _CUDA), all before any launch; nothing is allocated; calls
  * only launch kernels on `stream` and may be captured into a CUDA graph. */

@@ -13,7 +13,7 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// The driver's encoder, looked up once (the runtime is linked statically and the driver not at all).
+// The CUDA driver's encoder, looked up once (the runtime is linked statically and the driver not at all).
 inline EncodeTiled encode_tiled() {
   static const EncodeTiled f = [] {
     void* p = nullptr;
