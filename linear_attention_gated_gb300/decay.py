@@ -168,6 +168,7 @@ class DecayContext:
         self.device_status = torch.zeros(1, dtype=_I32, device=device)
         self.inputs = ()
         self.versions = ()
+        self.cu = None  # the context's own copy of the offsets: the caller's mirror may be filled again before the backward
 
     def _snapshot(self, inputs, call, cu, shapes):
         self.inputs = inputs
@@ -207,11 +208,14 @@ def kda_decay_attn_fwd(q, k, v, log_decay, initial_state=None, cu_seqlens=None, 
         _want(initial_state, "initial_state", _F32, (N, Hv, D, D), dev)
     ctx = context_out
     key = (B, T, Hqk, Hv, N, per_token)
+    if ctx is not None and (ctx.key != key or ctx.device != dev):
+        raise KdaError(4, "context reuse needs the same shapes, kind of decay and device")
+    if cu_host is not None:
+        known = ctx is not None and ctx.cu is not None and torch.equal(cu_host, ctx.cu)
+        cu_host = ctx.cu if known else cu_host.clone()
     if ctx is None:
         ctx = DecayContext(key, decay_workspace_bytes(B, T, Hqk, Hv, cu_host, per_token), dev)
-    elif ctx.key != key or ctx.device != dev:
-        raise KdaError(4, "context reuse needs the same shapes, kind of decay and device")
-    elif cu_host is not None and cu_host is not ctx.cu:
+    elif cu_host is not None and not known:
         nbytes = decay_workspace_bytes(B, T, Hqk, Hv, cu_host, per_token)  # other lengths may need more
         if nbytes > ctx.workspace.numel():
             ctx.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
