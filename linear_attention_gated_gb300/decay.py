@@ -159,12 +159,14 @@ def decay_workspace_bytes(B, T, Hqk, Hv, cu_seqlens_cpu=None, per_token=True, tr
 class DecayContext:
     """What the backward of one forward call needs: the borrowed inputs and final state with their tensor
     versions (they must not change before the backward), and a workspace. Passing it back as
-    ``context_out`` uses the workspace again for another call of the same shapes and lengths."""
+    ``context_out`` uses the workspace again for another call of the same shapes; sequences of other lengths may
+    need a larger one. A captured graph of calls on a context needs the context for as long as it is replayed."""
 
     def __init__(self, key, nbytes, device):
         self.key = key
         self.device = device
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.outgrown = []  # smaller ones from before: a captured graph may still write to them
         self.device_status = torch.zeros(1, dtype=_I32, device=device)
         self.inputs = ()
         self.versions = ()
@@ -218,6 +220,7 @@ def kda_decay_attn_fwd(q, k, v, log_decay, initial_state=None, cu_seqlens=None, 
     elif cu_host is not None and not known:
         nbytes = decay_workspace_bytes(B, T, Hqk, Hv, cu_host, per_token)  # other lengths may need more
         if nbytes > ctx.workspace.numel():
+            ctx.outgrown.append(ctx.workspace)
             ctx.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     o = torch.empty((B, T, Hv, D), dtype=_BF16, device=dev) if out is None else out
     hT = torch.empty((N, Hv, D, D), dtype=_F32, device=dev) if final_state_out is None else final_state_out

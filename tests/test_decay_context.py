@@ -84,3 +84,21 @@ def test_reuse_between_fixed_and_packed(calls):
     kda_decay_attn_fwd(*x, cu_seqlens=cu, cu_seqlens_cpu=cu, context_out=ctx)
     kda_decay_attn_fwd(*x, context_out=ctx)
     assert [c.cu for c in calls] == [None, [0, 64], None]
+
+
+def test_a_workspace_that_was_too_small_lives_as_long_as_the_context(calls):
+    """A captured graph, or work in flight, may still write to it."""
+    import weakref
+
+    from linear_attention_gated_gb300 import kda_decay_attn_fwd
+    x = inputs(8192)
+    *_, ctx = kda_decay_attn_fwd(*x, cu_seqlens=offsets(EVEN), cu_seqlens_cpu=offsets(EVEN))
+    first = weakref.ref(ctx.workspace)
+    kda_decay_attn_fwd(*x, cu_seqlens=offsets(LONG), cu_seqlens_cpu=offsets(LONG), context_out=ctx)
+    assert ctx.workspace.numel() >= need(LONG)
+    assert first() is not None and first().data_ptr() == calls[0].workspace
+    second = ctx.workspace.data_ptr()
+    kda_decay_attn_fwd(*x, cu_seqlens=offsets(EVEN), cu_seqlens_cpu=offsets(EVEN), context_out=ctx)
+    assert calls[2].workspace == second  # the largest serves all
+    del ctx
+    assert first() is None
