@@ -28,13 +28,20 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_get
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
+def _stream(device):
+    """The current stream of `device` (0 for the CPU, whose tensors _call refuses)."""
+    if device.type != "cuda":
+        return 0
+    return torch.cuda.current_stream(device.index).cuda_stream if _raw_stream is None else _raw_stream(device.index)
+
+
 def _call(f, device, *args):
     """f(*args, stream) with `device` current, its status checked. (The small calls are host-bound: torch's stream and
     device objects would cost as much as the launch.)"""
     if device.type != "cuda":
         raise ValueError("tensors must be CUDA tensors")
     index = device.index
-    stream = torch.cuda.current_stream(index).cuda_stream if _raw_stream is None else _raw_stream(index)
+    stream = _stream(device)
     if _current_device() == index:
         rc = f(*args, stream)
     else:
@@ -159,12 +166,15 @@ def decay_workspace_bytes(B, T, Hqk, Hv, cu_seqlens_cpu=None, per_token=True, tr
 class DecayContext:
     """What the backward of one forward call needs: the borrowed inputs and final state with their tensor
     versions (they must not change before the backward), and a workspace. Passing it back as
-    ``context_out`` uses the workspace again for another call of the same shapes; sequences of other lengths may
-    need a larger one. A captured graph of calls on a context needs the context for as long as it is replayed."""
+    ``context_out`` uses the workspace again for another call of the same shapes on the same stream; sequences of
+    other lengths may need a larger one. (A backward on another stream shares that workspace: the caller orders it
+    after the forward and before the context's next call.) A captured graph of calls on a context needs the context
+    for as long as it is replayed."""
 
-    def __init__(self, key, nbytes, device):
+    def __init__(self, key, nbytes, device, stream):
         self.key = key
         self.device = device
+        self.stream = stream
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.outgrown = []  # smaller ones from before: a captured graph may still write to them
         self.device_status = torch.zeros(1, dtype=_I32, device=device)
@@ -200,7 +210,7 @@ def kda_decay_attn_fwd(q, k, v, log_decay, initial_state=None, cu_seqlens=None, 
     initial_state FP32 [N, Hv, 128, 128] value-first, None for zeros. Packed sequences (B = 1) have
     cu_seqlens int64 [N + 1] on the device and its CPU mirror; sequences may be empty. scale defaults to
     1 / sqrt(128). ctx goes to kda_decay_attn_bwd; as ``context_out`` of a later call of the same shapes
-    its workspace is used again."""
+    on the same stream its workspace is used again."""
     lib = load_library()
     B, T, Hqk, Hv, D, per_token, strides = _decay_inputs(q, k, v, log_decay)
     dev = q.device
@@ -210,13 +220,14 @@ def kda_decay_attn_fwd(q, k, v, log_decay, initial_state=None, cu_seqlens=None, 
         _want(initial_state, "initial_state", _F32, (N, Hv, D, D), dev)
     ctx = context_out
     key = (B, T, Hqk, Hv, N, per_token)
-    if ctx is not None and (ctx.key != key or ctx.device != dev):
-        raise KdaError(4, "context reuse needs the same shapes, kind of decay and device")
+    stream = _stream(dev)
+    if ctx is not None and (ctx.key != key or ctx.device != dev or ctx.stream != stream):
+        raise KdaError(4, "context reuse needs the same shapes, kind of decay, device and stream")
     if cu_host is not None:
         known = ctx is not None and ctx.cu is not None and torch.equal(cu_host, ctx.cu)
         cu_host = ctx.cu if known else cu_host.clone()
     if ctx is None:
-        ctx = DecayContext(key, decay_workspace_bytes(B, T, Hqk, Hv, cu_host, per_token), dev)
+        ctx = DecayContext(key, decay_workspace_bytes(B, T, Hqk, Hv, cu_host, per_token), dev, stream)
     elif cu_host is not None and not known:
         nbytes = decay_workspace_bytes(B, T, Hqk, Hv, cu_host, per_token)  # other lengths may need more
         if nbytes > ctx.workspace.numel():

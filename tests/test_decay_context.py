@@ -102,3 +102,18 @@ def test_a_workspace_that_was_too_small_lives_as_long_as_the_context(calls):
     assert calls[2].workspace == second  # the largest serves all
     del ctx
     assert first() is None
+
+
+def test_reuse_on_another_stream_is_refused(calls, monkeypatch):
+    """Two steps at once would share one workspace."""
+    from linear_attention_gated_gb300 import KdaError, decay, kda_decay_attn_fwd
+    x = inputs(64)
+    on = [5]
+    monkeypatch.setattr(decay, "_stream", lambda device: on[0], raising=False)
+    *_, ctx = kda_decay_attn_fwd(*x)
+    on[0] = 6
+    with pytest.raises(KdaError, match="stream"):
+        kda_decay_attn_fwd(*x, context_out=ctx)
+    on[0] = 5
+    kda_decay_attn_fwd(*x, context_out=ctx)
+    assert len(calls) == 2
