@@ -117,3 +117,62 @@ def test_reuse_on_another_stream_is_refused(calls, monkeypatch):
     on[0] = 5
     kda_decay_attn_fwd(*x, context_out=ctx)
     assert len(calls) == 2
+
+
+def test_writes_into_the_callers_tensors_count_as_changes(monkeypatch):
+    """Tensors that a call writes get a new version, those that it reads keep theirs."""
+    import linear_attention_gated_gb300 as lib
+    from linear_attention_gated_gb300 import decay
+    monkeypatch.setattr(decay, "_call", lambda *args: None)
+    x = inputs(1, hv=2)
+    q, k, v, g = x
+    f32 = {n: torch.zeros(1, 2, D, D) for n in ("h0", "hT", "pool", "dh0", "dhT")}
+    o, dq, dk, dv, dg, do, q2, k2 = (torch.zeros_like(t) for t in (v, q, k, v, g, v, q, k))
+    pos, freq = torch.zeros(1, 1, dtype=torch.int64), torch.ones(64, dtype=torch.float64)
+
+    def changed(f, *written):
+        every = [*x, *f32.values(), o, dq, dk, dv, dg, do, q2, k2, pos, freq]
+        before = [t._version for t in every]
+        got = f()
+        for t, b in zip(every, before):
+            assert (t._version != b) == any(t is w for w in written), (t.shape, t._version - b)
+        return got
+
+    pool = f32["pool"]
+    *_, ctx = changed(lambda: lib.kda_decay_attn_fwd(*x, f32["h0"], out=o, final_state_out=f32["hT"]), o, f32["hT"])
+    changed(lambda: lib.kda_decay_attn_bwd(ctx, do, f32["dhT"], out=(dq, dk, dv, dg, f32["dh0"])), dq, dk, dv, dg, f32["dh0"])
+    changed(lambda: lib.kda_decay_attn_fwd(*x, f32["h0"]))
+    changed(lambda: lib.kda_decay_attn_prefill(*x, pool, out=o), o, pool)
+    changed(lambda: lib.kda_decay_attn_prefill(*x, pool), pool)
+    changed(lambda: lib.kda_decay_attn_decode(*x, pool, out=o), o, pool)
+    changed(lambda: lib.kda_qk_norm_rope_fwd(q, k, None, None, pos, freq, q_out=q, k_out=k2), q, k2)
+    changed(lambda: lib.kda_qk_norm_rope_bwd(dq, dk, q, k, None, None, pos, freq, out=(dq, k2)), dq, k2)
+    changed(lambda: lib.kda_qk_norm_rope_bwd(dq, dk, q, k, None, None, pos, freq))
+    with torch.inference_mode():  # tensors without versions
+        lib.kda_decay_attn_decode(*x, torch.zeros(1, 2, D, D), out=torch.zeros_like(v))
+
+
+def test_backward_notices_inputs_that_the_package_changed(calls):
+    from linear_attention_gated_gb300 import (KdaError, kda_decay_attn_bwd, kda_decay_attn_fwd, kda_qk_norm_rope_fwd)
+    x, shared = inputs(64), torch.zeros(1, 1, D, D)
+    fixed = x[:3] + [torch.zeros(1)]
+    do, dhT = x[2], torch.zeros(1, 1, D, D)
+    *_, first = kda_decay_attn_fwd(*x, final_state_out=shared)
+    *_, other = kda_decay_attn_fwd(*fixed, final_state_out=shared)
+    *_, last = kda_decay_attn_fwd(*x, final_state_out=shared)
+    with pytest.raises(KdaError):  # the decays' gradient would read another layer's final state
+        kda_decay_attn_bwd(first, do, dhT)
+    kda_decay_attn_bwd(first, do)  # (it is not read here,
+    kda_decay_attn_bwd(other, do, dhT)  # nor here)
+    kda_decay_attn_bwd(last, do, dhT)
+    made = len(calls)
+    # in place on a query that the forward had
+    from linear_attention_gated_gb300 import decay
+    caught, decay._call = decay._call, lambda *args: None
+    try:
+        kda_qk_norm_rope_fwd(x[0], x[1], None, None, None, None, q_out=x[0], k_out=torch.empty_like(x[1]))
+    finally:
+        decay._call = caught
+    with pytest.raises(KdaError):
+        kda_decay_attn_bwd(last, do)
+    assert len(calls) == made
