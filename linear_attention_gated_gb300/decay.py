@@ -156,6 +156,11 @@ def _written(*tensors):
         torch.autograd.graph.increment_version(given)
 
 
+def _versions(tensors):
+    """Their versions, as far as they have some (tensors made in inference mode have none)."""
+    return tuple(None if t is None or t.is_inference() else t._version for t in tensors)
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
@@ -191,14 +196,14 @@ class DecayContext:
 
     def _snapshot(self, inputs, call, cu, shapes):
         self.inputs = inputs
-        self.versions = tuple(t._version for t in inputs if t is not None)
+        self.versions = _versions(inputs)
         self.call, self.cu, self.shapes = call, cu, shapes
 
     def check_unchanged(self, final_state=True):
         """final_state: it is read again too (by the decays' gradient, with an adjoint of its own)."""
         if not self.inputs:
             raise KdaError(4, "the context holds no forward")
-        now = tuple(t._version for t in self.inputs if t is not None)
+        now = _versions(self.inputs)
         if self.versions[:-1] != now[:-1] or (final_state and self.versions[-1] != now[-1]):
             raise KdaError(4, "an input or the final state of the forward was modified before the backward")
 

@@ -176,3 +176,14 @@ def test_backward_notices_inputs_that_the_package_changed(calls):
     with pytest.raises(KdaError):
         kda_decay_attn_bwd(last, do)
     assert len(calls) == made
+
+
+def test_a_training_pair_in_inference_mode(calls):
+    """Tensors made there have no versions to check."""
+    from linear_attention_gated_gb300 import kda_decay_attn_bwd, kda_decay_attn_fwd
+    outside = inputs(64)
+    with torch.inference_mode():
+        for x in (outside, inputs(64)):
+            *_, ctx = kda_decay_attn_fwd(*x)
+            kda_decay_attn_bwd(ctx, x[2], torch.zeros(1, 1, D, D))
+    assert len(calls) == 4
