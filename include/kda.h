@@ -513,7 +513,8 @@ kda_status kda_qk_norm_rope_workspace_bytes(int64_t head_dim, size_t* bytes);
 /* Its gradients: from the outputs' (dq, dk) and the forward's inputs to dq_out, dk_out
  * (of dtype) and dq_weight, dk_weight (FP32 [head_dim], summed over tokens and heads in
  * a fixed order; NULL exactly where the weight is). `strides`: token and head strides of q, k,
- * dq_out, dk_out, dq, dk (12 numbers). dq_out may be q or dq, dk_out may be k or dk.
+ * dq_out, dk_out, dq, dk (12 numbers). dq_out may be q or dq, dk_out may be k or dk; other
+ * overlaps of what is written (the workspace too) are refused.
  * workspace may be NULL when there is no weight. */
 kda_status kda_qk_norm_rope_bwd(const void* dq, const void* dk, const void* q, const void* k,
                                 int32_t dtype, const float* q_weight, const float* k_weight,

@@ -541,18 +541,29 @@ kda_status nr_run(const NrCall& c) {
   const int64_t in_hs[4] = {st[1], st[3], c.bwd ? st[9] : 0, c.bwd ? st[11] : 0};
   const View out[2] = {view_of(c.q_out, st[4], st[5], c.Hq, c.D, c.n, size), view_of(c.k_out, st[6], st[7], c.Hk, c.D, c.n, size)};
   const int64_t out_hs[2] = {st[5], st[7]};
+  auto span = [](const void* p, int64_t bytes) { return View{(uintptr_t)p, 0, bytes, p && bytes ? 1 : 0}; };
+  const View flat[4] = {span(c.qw, 4 * c.D), span(c.kw, 4 * c.D), span(c.R ? c.pos : nullptr, 8 * c.n), span(c.R ? c.freq : nullptr, 4 * c.R)};
   for (int i = 0; i < 2; ++i) {
     for (int j = 0; j < 4; ++j) {
       const bool same = (j & 1) == i && in[j].p == out[i].p && in[j].token == out[i].token && in_hs[j] == out_hs[i];
       if (!same && may_overlap(in[j], out[i]))
         return nfail(KDA_ERR_ALIASING, "qk_norm_rope: an output overlaps an input that is not its own");
     }
-    const View flat[] = {View{(uintptr_t)c.qw, 0, 4 * c.D, c.qw ? 1 : 0}, View{(uintptr_t)c.kw, 0, 4 * c.D, c.kw ? 1 : 0},
-                         View{(uintptr_t)c.pos, 0, 8 * c.n, c.R ? 1 : 0}, View{(uintptr_t)c.freq, 0, 4 * c.R, c.R ? 1 : 0}};
     for (const View& f : flat)
       if (may_overlap(f, out[i])) return nfail(KDA_ERR_ALIASING, "qk_norm_rope: an output overlaps an input");
   }
   if (may_overlap(out[0], out[1])) return nfail(KDA_ERR_ALIASING, "qk_norm_rope: the outputs overlap");
+  const View sums[3] = {span(c.dqw, 4 * c.D), span(c.dkw, 4 * c.D), span(c.part, kNrMaxCtas * 4 * c.D)};
+  for (int i = 0; i < 3; ++i) {
+    for (const View& x : in)
+      if (may_overlap(x, sums[i])) return nfail(KDA_ERR_ALIASING, "qk_norm_rope: a weight's gradient or the workspace overlaps an input");
+    for (const View& x : flat)
+      if (may_overlap(x, sums[i])) return nfail(KDA_ERR_ALIASING, "qk_norm_rope: a weight's gradient or the workspace overlaps an input");
+    for (const View& x : out)
+      if (may_overlap(x, sums[i])) return nfail(KDA_ERR_ALIASING, "qk_norm_rope: a weight's gradient or the workspace overlaps an output");
+    for (int j = 0; j < i; ++j)
+      if (may_overlap(sums[j], sums[i])) return nfail(KDA_ERR_ALIASING, "qk_norm_rope: the weights' gradients or the workspace overlap");
+  }
 
   int dev = -1, major = 0, minor = 0;
   cudaError_t e = cudaGetDevice(&dev);
