@@ -80,6 +80,8 @@ __device__ __forceinline__ float decay_g(const DecayProblem& P, int64_t tok, int
 int64_t decay_segment_tokens(const int64_t* cu, int64_t N, int64_t T, int64_t Hv);
 // Workspace: the segments' states, then (training) what the backward needs.
 size_t decay_workspace_bytes(int64_t N, int64_t Ttot, int64_t Hqk, int64_t Hv, int64_t seg, bool training, bool per_token);
+// Blocks of the kernel that sums dq and dk over a group's heads.
+int64_t decay_group_sum_blocks(const DecayProblem& P);
 cudaError_t launch_decay_forward(const DecayProblem& P, const DecayStates& st, __nv_bfloat16* o, void* ws, cudaStream_t s);
 cudaError_t launch_decay_backward(const DecayProblem& P, const float* h0, const float* hT, const DecayGrads& g, void* ws,
                                   cudaStream_t s);

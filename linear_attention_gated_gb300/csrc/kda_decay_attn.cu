@@ -93,9 +93,10 @@ kda_status check_tokens(const void* q, const void* k, const void* v, const void*
   const void* ptrs[3] = {q, k, v};
   for (int i = 0; i < 3; ++i) {
     const int64_t ts = x[2 * i], hs = x[2 * i + 1];
-    if (hs < D || ts < (heads[i] - 1) * hs + D || hs % 8 || ts % 8)
+    bool too_large;
+    if (!kda::view_rows_apart(s.Ttot, heads[i], D, ts, hs, &too_large) || hs % 8 || ts % 8)
       return fail(KDA_ERR_INVALID_ARGUMENT, "token and head strides must be multiples of 8 elements and keep rows apart");
-    if (ts > (int64_t(1) << 38)) return fail(KDA_ERR_UNSUPPORTED, "token stride too large");
+    if (too_large || ts > (int64_t(1) << 38)) return fail(KDA_ERR_UNSUPPORTED, "strides too large");
     spans[i] = Span{ptrs[i], s.Ttot ? 2 * (size_t)((s.Ttot - 1) * ts + (heads[i] - 1) * hs + D) : 0};
   }
   spans[3] = Span{g, per_token ? 2 * (size_t)s.Ttot * Hv : 4 * (size_t)Hv};
@@ -198,6 +199,8 @@ extern "C" kda_status kda_decay_attn_bwd(const kda_bf16* q, const kda_bf16* k, c
     kda_status st = check_tokens(q, k, v, log_decay, decay_per_token, cu_seqlens_dev, cu_seqlens_host, num_seqs, B, T,
                                  Hqk, Hv, head_dim, scale, strides, &P, in);
     if (st != KDA_OK) return st;
+    if ((dlog_decay || P.r > 1) && kda::decay_group_sum_blocks(P) > INT32_MAX)
+      return fail(KDA_ERR_UNSUPPORTED, "problem too large for the sums over heads (2^31 blocks)");
     if (P.Ttot && (!d_o || !dq || !dk || !dv)) return fail(KDA_ERR_INVALID_ARGUMENT, "null gradient pointer");
     if (dlog_decay && !decay_per_token)
       return fail(KDA_ERR_UNSUPPORTED, "a fixed decay for each head has no gradient: dlog_decay must be NULL");
@@ -246,8 +249,8 @@ extern "C" kda_status kda_decay_attn_prefill(const kda_bf16* q, const kda_bf16* 
     if (!state || (P.Ttot && !o)) return fail(KDA_ERR_INVALID_ARGUMENT, "null tensor pointer");
     if (((uintptr_t)o | (uintptr_t)state) & 15u)
       return fail(KDA_ERR_INVALID_ARGUMENT, "state and output tensors must be 16-byte aligned");
-    if (num_slots < 1 || num_slots > (int64_t(1) << 31))
-      return fail(KDA_ERR_UNSUPPORTED, "the pool needs 1 to 2^31 slots");
+    if (num_slots < 1 || num_slots > (int64_t(1) << 31) || kda::pool_too_large(num_slots, Hv))
+      return fail(KDA_ERR_UNSUPPORTED, "the pool needs 1 to 2^31 slots, and at most 2^40 states");
     if ((state_indices == nullptr) != (state_indices_host == nullptr))
       return fail(KDA_ERR_INVALID_ARGUMENT, "state_indices needs its host mirror (and the reverse)");
     if (state_indices_host) {

@@ -128,8 +128,8 @@ extern "C" kda_status kda_decay_attn_decode(const kda_bf16* q, const kda_bf16* k
     if (kda::size_limit_violation(1, N ? N : 1, Hv, 0) || N > INT32_MAX / 4 / Hv)
       return dfail(KDA_ERR_UNSUPPORTED, "decay_attn decode: too many (sequence, head) units");
     if (head_dim != kda::kDim) return dfail(KDA_ERR_UNSUPPORTED, "decay_attn decode: head_dim must be 128");
-    if (num_slots < 0 || num_slots > (int64_t(1) << 31))
-      return dfail(KDA_ERR_UNSUPPORTED, "decay_attn decode: more than 2^31 pool slots");
+    if (num_slots < 0 || num_slots > (int64_t(1) << 31) || kda::pool_too_large(num_slots, Hv))
+      return dfail(KDA_ERR_UNSUPPORTED, "decay_attn decode: more than 2^31 pool slots or 2^40 states");
     if (decay_per_token != 0 && decay_per_token != 1)
       return dfail(KDA_ERR_INVALID_ARGUMENT, "decay_attn decode: decay_per_token must be 0 or 1");
     if (std::isinf(scale)) return dfail(KDA_ERR_INVALID_ARGUMENT, "decay_attn decode: scale must be finite");
@@ -156,7 +156,8 @@ extern "C" kda_status kda_decay_attn_decode(const kda_bf16* q, const kda_bf16* k
     Span ins[5];
     for (int i = 0; i < 3; ++i) {
       const int64_t ts = x[2 * i], hs = x[2 * i + 1];
-      if (hs < D || ts < (heads[i] - 1) * hs + D || hs % 8 || ts % 8 || ts > (int64_t(1) << 38))
+      bool too_large;
+      if (!kda::view_rows_apart(N, heads[i], D, ts, hs, &too_large) || too_large || hs % 8 || ts % 8 || ts > (int64_t(1) << 38))
         return dfail(KDA_ERR_INVALID_ARGUMENT,
                      "decay_attn decode: token and head strides must be multiples of 8 elements and keep rows apart");
       ins[i] = Span{ptrs[i], N ? 2 * (size_t)((N - 1) * ts + (heads[i] - 1) * hs + D) : 0};

@@ -1184,6 +1184,13 @@ size_t decay_workspace_bytes(int64_t N, int64_t Ttot, int64_t Hqk, int64_t Hv, i
   return carve_segments(N, Ttot, Hv, seg).total + (training ? carve_grads(Ttot, Hqk, Hv, per_token).total : 0);
 }
 
+// Heads that a warp of kda_decay_group_sum_kernel takes of each of its 4 / heads tokens.
+static int group_sum_heads(const DecayProblem& P) { return P.r == 1 ? 1 : P.r == 2 ? 2 : 4; }
+int64_t decay_group_sum_blocks(const DecayProblem& P) {
+  const int64_t tokens = 8 * (4 / group_sum_heads(P));
+  return (P.Ttot + tokens - 1) / tokens * P.Hqk;
+}
+
 cudaError_t launch_decay_forward(const DecayProblem& P, const DecayStates& st, __nv_bfloat16* o, void* ws, cudaStream_t s) {
   const Role q{P.q, P.qt, P.qh, P.Hqk}, k{P.k, P.kt, P.kh, P.Hqk}, v{P.v, P.vt, P.vh, P.Hv};
   return pass<false>(P, q, k, v, P.scale, P.scale, 1.f, st, false, o, nullptr, ws, s);
@@ -1212,10 +1219,9 @@ cudaError_t launch_decay_backward(const DecayProblem& P, const float* h0, const 
     return e;
   if (P.Ttot == 0 || !f32) return cudaSuccess;
   float* z = reinterpret_cast<float*>(base + w.z);
-  const int heads = P.r == 1 ? 1 : P.r == 2 ? 2 : 4;
-  const int64_t tokens = 8 * (4 / heads), blocks = (P.Ttot + tokens - 1) / tokens * P.Hqk;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  auto sum = [&](auto kern) { kern<<<(unsigned)blocks, 256, 0, s>>>(P, dq, dk, g.dq, g.dk, z); };
+  const int heads = group_sum_heads(P);
+  const unsigned blocks = (unsigned)decay_group_sum_blocks(P);  // (checked before the first launch)
+  auto sum = [&](auto kern) { kern<<<blocks, 256, 0, s>>>(P, dq, dk, g.dq, g.dk, z); };
   if (!g.dg) heads == 2 ? sum(kda_decay_group_sum_kernel<false, 2>) : sum(kda_decay_group_sum_kernel<false, 4>);
   else if (heads == 1) sum(kda_decay_group_sum_kernel<true, 1>);
   else heads == 2 ? sum(kda_decay_group_sum_kernel<true, 2>) : sum(kda_decay_group_sum_kernel<true, 4>);

@@ -27,6 +27,15 @@ inline const char* size_limit_violation(int64_t B, int64_t T, int64_t Hv, int64_
   return nullptr;
 }
 
+// Bounds on a strided [tokens, heads, D] view (token and head strides ts, hs in elements, hs >= D >= 1 checked here) and
+// on a state pool, for the same reason: views of at most 2^56 elements, pools of 2^40 states.
+inline bool view_rows_apart(int64_t tokens, int64_t heads, int64_t D, int64_t ts, int64_t hs, bool* too_large) {
+  constexpr int64_t kMaxElements = int64_t(1) << 56;
+  *too_large = hs > kMaxElements / heads || ts > kMaxElements / (tokens > 0 ? tokens : 1);
+  return *too_large || (hs >= D && ts >= (heads - 1) * hs + D);
+}
+inline bool pool_too_large(int64_t slots, int64_t Hv) { return slots > (int64_t(1) << 40) / Hv; }
+
 // The first fault of N slot indices of a pool of `slots`: 1 out of range, 2 a slot used twice, 0 none. (A bit for
 // each slot in a buffer kept per thread; only the words touched are cleared again.)
 inline int slot_fault(const int32_t* idx, int64_t N, int64_t slots) {

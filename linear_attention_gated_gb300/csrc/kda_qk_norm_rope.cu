@@ -514,11 +514,12 @@ kda_status nr_run(const NrCall& c) {
   for (int i = 0; i < nst; ++i)
     st[i] = c.strides ? c.strides[i] : (i & 1 ? c.D : heads[i / 2] * c.D);
   for (int i = 0; i < nst; i += 2) {
-    if (st[i + 1] < c.D || st[i] < (heads[i / 2] - 1) * st[i + 1] + c.D)
+    bool too_large;
+    if (!view_rows_apart(c.n, heads[i / 2], c.D, st[i], st[i + 1], &too_large))
       return nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: heads or tokens of a tensor overlap (strides too small)");
+    if (too_large || st[i] > (int64_t(1) << 40)) return nfail(KDA_ERR_UNSUPPORTED, "qk_norm_rope: strides too large");
     if ((st[i] * size) % 16 || (st[i + 1] * size) % 16)
       return nfail(KDA_ERR_INVALID_ARGUMENT, "qk_norm_rope: token and head strides must be multiples of 16 bytes");
-    if (st[i] > (int64_t(1) << 40)) return nfail(KDA_ERR_UNSUPPORTED, "qk_norm_rope: token stride too large");
   }
   if (c.n) {
     const void* ptrs[] = {c.q, c.k, c.q_out, c.k_out, c.bwd ? c.dq : c.q, c.bwd ? c.dk : c.k};
