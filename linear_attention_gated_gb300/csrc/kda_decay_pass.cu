@@ -34,7 +34,7 @@
 //   warps 12-19  the state, 64 of a row's 128 values a thread in registers, S = e^{b_C} S + U with U = V^T K~
 //            from tensor memory, and as A operand back there; Y
 // K~ is an operand in two BF16 parts, hi + lo, 16 mantissa bits: FP32 states are off by 2.4e-6 relative to 64 bits
-// (FP32 arithmetic throughout: 2e-7), whatever the length, as each chunk's part is summed in FP32. One part would
+// (FP32 arithmetic throughout: 2e-7), and by one FP32 rounding a chunk of what they were before (StateFactor). One part would
 // leave 1.7e-3; a third would take 16 KiB of shared memory that is not there and a quarter more of the products' time.
 // P and S, which feed Y alone, are rounded to BF16 once (as Y itself is) where Y is an output: o is off by 2.3e-3
 // where one rounding of the exact value leaves 1.7e-3. Where Y is FP32 and summed further, over heads or, for the
@@ -149,6 +149,22 @@ __device__ __forceinline__ uint32_t pack2(float2 x) { return pack2(x.x, x.y); }
 __device__ __forceinline__ float2 unpack2(uint32_t x) {
   return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
 }
+// The factors 2^x that a state is multiplied by one after the other. Each rounded to FP32 by itself, a slow fixed decay's would
+// be off by the same part of a step every time (states 6e-5 off after 1536 chunks). So what a rounding leaves goes
+// into the next factor, and their product stays within a step of the exact one. |x| >= 1/2 is forgotten too soon for that.
+struct StateFactor {
+  float left = 0.f;
+  __device__ __forceinline__ float next(float x) {
+    if (!(fabsf(x) < 0.5f)) {
+      left = 0.f;
+      return fast_exp2(x);
+    }
+    const float m = expm1f(x * 0.6931471805599453f), e = 1.f + m;  // (2^-23 of m off: little where 2^x is next to 1)
+    const float more = fmaf(left, e, m - (e - 1.f)), f = e + more;
+    left = __fdividef(more - (f - e), f);
+    return f;
+  }
+};
 // x as BF16 pairs hi + lo: 16 mantissa bits together
 __device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
   hi = pack2(x);
@@ -453,6 +469,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           for (int i = lane; i < lines; i += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 128 * i));
         }
         float total = 0.f;  // lane 31's: log2 of the unit's decay
+        StateFactor factor;
         // two chunks ahead, as the bits that come (a conversion here would wait for the load)
         auto bits = [&](int64_t tok) -> uint32_t {
           return P.per_token ? reinterpret_cast<const uint16_t*>(P.g)[tok * P.Hv + x.h] : reinterpret_cast<const uint32_t*>(P.g)[x.h];
@@ -468,7 +485,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
         float whole = 0.f;
         for (int64_t c = 0; c < x.nchunks; ++c, ++g) {
           const int d = g % kDecs;
-          // of a fixed decay every whole chunk has the same numbers, and the slot has them already
+          // of a fixed decay every whole chunk has the same numbers (but the state's factor), and the slot has them already
           const bool again = !P.per_token && c > kDecs && (kRev || (c + 1) * kC <= x.len);
           if (!again) {
             float g0 = number(next.x);
@@ -489,7 +506,7 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
             const float2 up = make_float2(fast_exp2(p0), fast_exp2(pre)), down = make_float2(fast_exp2(s1 + g1), fast_exp2(s1));
             const float2 e = kRev ? down : up, w = kRev ? up : down;
             whole = pre + follow;
-            const float lam = fast_exp2(whole);
+            const float lam = factor.next(whole);
             if (ok && g >= kDecs) ok = tc::mbar_wait_lanes(bar(sm.decfree[d]), (g / kDecs - 1) & 1);
             *reinterpret_cast<float2*>(&sm.b[d][2 * lane]) = make_float2(p0, pre);
             *reinterpret_cast<float2*>(&sm.eb[d][2 * lane]) = make_float2(a.s_inter * e.x, a.s_inter * e.y);
@@ -499,7 +516,9 @@ kda_decay_pass_kernel(const __grid_constant__ Maps maps, const __grid_constant__
           } else {
             next = next2;
             next2 = fetch(c + 2);
+            const float lam = factor.next(whole);
             if (ok) ok = tc::mbar_wait_lanes(bar(sm.decfree[d]), (g / kDecs - 1) & 1);
+            if (lane == 31) sm.lam[d] = lam;
           }
           total += whole;
           arrive(sm.dec[d]);
@@ -885,6 +904,7 @@ __global__ void __launch_bounds__(256) kda_decay_chain_kernel(const __grid_const
   const int64_t base = seg_slot(sg, sp.t0, n);
   const int64_t m = sp.len > sg.len ? (sp.len + sg.len - 1) / sg.len : 1;
   auto slot_of = [&](int64_t i) { return (base + (kRev ? m - 1 - i : i)) * P.Hv + h; };
+  StateFactor factor;
   constexpr int kAhead = 8;  // loads in flight: none waits for the chain
   for (int64_t i = 0; i < m; i += kAhead) {
     float4 u[kAhead];
@@ -900,7 +920,7 @@ __global__ void __launch_bounds__(256) kda_decay_chain_kernel(const __grid_const
       if (i + j >= m) break;
       *reinterpret_cast<float4*>(sg.state + slot_of(i + j) * kDim * kDim + at) = x;
       if (i + j + 1 < m) {
-        const float e = exp2f(d[j]);
+        const float e = factor.next(d[j]);
         x.x = fmaf(e, x.x, u[j].x); x.y = fmaf(e, x.y, u[j].y);
         x.z = fmaf(e, x.z, u[j].z); x.w = fmaf(e, x.w, u[j].w);
       }
