@@ -11,6 +11,7 @@ struct kda_ctx;  // the saved-forward context of the C ABI (kda_api.cu)
 namespace kda {
 
 constexpr int kDim = 128;      // K = V = 128 (flashinfer.kda_training, module description)
+constexpr int kSms = 152;  // of a GB300
 constexpr int kChunk = 16;     // tokens per sub-chunk of the chunked (WY / UT) form
 constexpr int kCkTokens = 16;  // tokens between saved state checkpoints (multiple of kChunk)
 constexpr int kLds = 132;      // padded shared-memory row stride (floats) of 128-wide tiles

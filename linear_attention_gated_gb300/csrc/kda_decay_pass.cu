@@ -125,7 +125,7 @@ struct Segments {
 __device__ __forceinline__ int64_t seg_slot(const Segments& g, int64_t t0, int64_t n) { return t0 / g.len + n; }
 
 constexpr int kOrder = 512;      // sequences whose order is passed (more run in index order, whole)
-constexpr int kUnits = 2 * 152;  // the units that a cut aims at: two for each SM, so no sequence has more segments
+constexpr int kUnits = 2 * kSms;  // the units that a cut aims at: two for each SM, so no sequence has more segments
 
 struct PassArgs {
   DecayProblem P;
@@ -1187,7 +1187,8 @@ int64_t decay_segment_tokens(const int64_t* cu, int64_t N, int64_t T, int64_t Hv
   // (about 0.6 of the main pass) and the chain: only where the longest sequence takes well over an SM's share, two units.
   // Measured, cut against whole, one sequence of 8192 or 16384 tokens: 96 heads (3.2 shares) 269 us : 210 us and
   // 541 : 404, 64 heads (4.8 shares) 206 : 210 and 359 : 395, 48 heads (6.3) 158 : 207, 32 heads (9.5) 128 : 203;
-  // 1600 tokens of 8 heads 55 : 54, 2048 of 8 heads 50 : 66, 20000 of one head 61 : 470.
+  // 1600 tokens of 8 heads 55 : 54, 2048 of 8 heads 50 : 66, 20000 of one head 61 : 470. (The Python binding knows that
+  // up to 24 chunks are never cut.)
   const int64_t share = (chunks * Hv + kUnits - 1) / kUnits;
   if (longest <= std::max<int64_t>(4 * share, 24)) return 0;
   int64_t seg = std::max<int64_t>(share, 8);

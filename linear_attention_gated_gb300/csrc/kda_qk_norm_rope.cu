@@ -420,7 +420,7 @@ kda_status nfail(kda_status st, const char* msg) {
   return st;
 }
 
-constexpr int64_t kNrMaxCtas = 152 * 6;  // backward: most CTAs, rows of dw_part
+constexpr int64_t kNrMaxCtas = kSms * 6;  // backward: most CTAs, rows of dw_part
 
 // A strided [tokens, heads, D] view in bytes.
 struct View {
@@ -582,7 +582,7 @@ kda_status nr_run(const NrCall& c) {
   a.R = (int)c.R;
   a.eps = c.eps;
   const bool wide = c.dtype == KDA_DTYPE_FP32;
-  const int64_t resident = 152 * (wide ? (c.bwd ? kNrBlocks<float, true> : kNrBlocks<float, false>)
+  const int64_t resident = kSms * (wide ? (c.bwd ? kNrBlocks<float, true> : kNrBlocks<float, false>)
                                        : (c.bwd ? kNrBlocks<__half, true> : kNrBlocks<__half, false>));
   const int groups = kNrThreads / (c.D <= 64 ? 4 : c.D <= 128 ? 8 : 16);
   int64_t ctas[2];

@@ -17,7 +17,7 @@ from .kda import KdaError, _check, load_library
 
 DIM = 128
 _NAN = float("nan")
-_UNCUT = 1536  # sequences up to this long are never cut into segments: prefill needs no workspace for them
+_UNCUT = 1536  # sequences up to this long are never cut into segments (24 chunks in csrc/kda_decay_pass.cu): prefill needs no workspace for them
 _BF16, _F32, _F64, _I32, _I64 = torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.int64
 _STATE = {torch.bfloat16: 0, torch.float32: 1}
 _ROPE_WORKSPACE = {}  # head_dim -> bytes

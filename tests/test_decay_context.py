@@ -187,3 +187,14 @@ def test_a_training_pair_in_inference_mode(calls):
             *_, ctx = kda_decay_attn_fwd(*x)
             kda_decay_attn_bwd(ctx, x[2], torch.zeros(1, 1, D, D))
     assert len(calls) == 4
+
+
+def test_prefill_without_a_workspace_is_for_sequences_that_are_never_cut():
+    """The length up to which the binding does not ask the library, against the library."""
+    from linear_attention_gated_gb300 import decay, decay_workspace_bytes
+    for hv in (1, 2, 8, 96):
+        for B in (1, 3, 40):
+            assert decay_workspace_bytes(B, decay._UNCUT, hv, hv, training=False) == 0
+        for lens in ([decay._UNCUT], [decay._UNCUT - 1, 1], [1] * 100 + [decay._UNCUT - 100]):
+            assert decay_workspace_bytes(1, sum(lens), hv, hv, offsets(lens), training=False) == 0
+    assert decay_workspace_bytes(1, decay._UNCUT + 1, 1, 1, training=False) > 0
