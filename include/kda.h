@@ -418,8 +418,17 @@ kda_status kda_prefill(const kda_bf16* q, const kda_bf16* k, const kda_bf16* v, 
  * or the workspace. Arithmetic: products of BF16 operands with FP32 accumulation;
  * states, decays and sums are FP32; what enters a state is taken in two BF16 parts
  * (16 bits), so what a call adds to FP32 states is within 4.3e-6 of the exact (relative,
- * in the 2-norm; 2.2e-6 to 2.5e-6 measured), and each 64 tokens round the state once more
- * (a state carried over 98,304 tokens: 2e-6). Results do not depend on the order of execution.
+ * in the 2-norm; 1.8e-6 to 2.7e-6 measured), and each 64 tokens round the state once more
+ * (a state carried over 98,304 tokens at decays of 3e-6 to 1e-4 a token: 1e-6 to 4e-6
+ * measured). A decode step is FP32 throughout and rounds the state for each token.
+ * The state's copy that o is read from, the masked product of queries and keys and o
+ * itself are rounded to BF16 once: o, dv, and with fixed decays and Hqk = Hv dq and dk too,
+ * are within 3.9e-3 (2.4e-3 measured; the exact values rounded to BF16: 1.7e-3); else dq
+ * and dk are rounded to BF16 at the end alone. Results do not depend on the order of
+ * execution.
+ * A NaN or infinity in v or in an output's gradient stays in its sequence, but may reach the
+ * results of all tokens of its chunk (64 tokens from the sequence's or a segment's first), also of
+ * those before it.
  * Errors: as above (KDA_ERR_INVALID_ARGUMENT, _UNSUPPORTED, _ALIASING,
  * _WORKSPACE_TOO_SMALL, _CUDA), all before any launch; nothing is allocated; calls
  * only launch kernels on `stream` and may be captured into a CUDA graph. */

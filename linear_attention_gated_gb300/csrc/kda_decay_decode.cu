@@ -11,8 +11,9 @@
 // request are 128 CTAs). A thread has all its rows' loads in flight before it
 // touches the token's vectors; a half-warp owns a row, 8 keys a lane.
 //
-// Measured: 256 sequences x 96 heads, BF16 states, 1.64 GB: 255 us, 6.4 TB/s, 96 % of the
-// copy rate; 128 x 96 in FP32 236 us; one sequence of 32 heads 5.6 us on the GPU.
+// Measured: 256 sequences x 96 heads, BF16 states, 1.64 GB: a call among others through the Python
+// binding 255 us, 6.4 TB/s, 96 % of the copy rate (in a captured graph 251 us); 128 x 96 in FP32
+// 235 us; one sequence of 32 heads 5.6 us on the GPU with nothing in its caches.
 #include "../../include/kda.h"
 #include "kda_decay.cuh"
 #include "kda_host.h"
@@ -196,8 +197,14 @@ extern "C" kda_status kda_decay_attn_decode(const kda_bf16* q, const kda_bf16* k
           <<<(unsigned)(N * Hv * (kda::kDim / decltype(rows)::value)), kda::kDdThreads, 0, stream>>>(
               P, pool, state_indices, num_slots, reinterpret_cast<__nv_bfloat16*>(o));
     };
-    // 16 KiB of state to a CTA, 32 rows in FP32 and 64 in BF16, fill the loads in flight. With 16, 32, 64, 128 rows:
-    // BF16, 256 x 96 heads: 283, 257, 243, 238 us; FP32, 128 x 96: 235, 236, 237, 239, 1 x 32: 11.3, 7.8, 8.4, 9.9.
+    // 16 KiB of state to a CTA, 32 rows in FP32 and 64 in BF16: fewer rows spread few requests over more SMs, more of them
+    // have more loads in flight. us in a captured graph of calls on pools in turn, 600 MB together, with 16, 32, 64, 128 rows:
+    //   BF16  1 x 32 heads 1.99, 2.04, 2.25, 2.60;  3 x 64 4.83, 4.82, 4.81, 5.46;  7 x 64 7.92, 7.70, 6.78, 7.04;
+    //         16 x 64 14.5, 13.3, 13.0, 13.0;  64 x 96 76.5, 68.3, 65.2, 63.4;  256 x 96 297, 264, 251, 242
+    //   FP32  1 x 32 3.04, 3.19, 3.62, 5.29;  3 x 64 5.94, 5.99, 6.86, 8.33;  4 x 64 7.30, 7.07, 8.08, 8.65;
+    //         16 x 64 22.0, 22.4, 23.3, 24.8;  128 x 96 234, 235, 237, 239
+    // One count serves all sizes: it is the best or within 5 % of it but for a single request, whose call takes
+    // longer on the host (18 us), and which another count would win at most 0.3 us.
     if (state_dtype == KDA_STATE_BF16) launch(reinterpret_cast<__nv_bfloat16*>(state), std::integral_constant<int, 64>{});
     else launch(reinterpret_cast<float*>(state), std::integral_constant<int, 32>{});
     if ((e = cudaGetLastError()) != cudaSuccess) return dfail(KDA_ERR_CUDA, cudaGetErrorString(e));

@@ -17,8 +17,8 @@
 //   dq:  Q = do, K = v,  V = k     forward,   S = the state, transposed
 //   dk:  Q = v,  K = do, V = q     backwards, S = the state's adjoint, transposed
 //   dv:  Q = k,  K = q,  V = do    backwards, S = the state's adjoint            (its end is dh0)
-// Nothing is saved by the forward: what the backward needs of the states it carries again, which moves
-// fewer bytes than a state stored and read for every chunk would (32 KiB against the 16 KiB of a tile).
+// Nothing is saved by the forward: what the backward needs of the states it carries again, from the 48 KiB of a
+// chunk's three tiles, which a pass reads anyway. A state stored and read for every chunk would be 128 KiB more.
 //
 // One CTA an SM, 20 warps with roles, so that the copies, the products and the element-wise work of
 // neighbouring chunks (and units) run side by side; only the state's update is a chain.
@@ -36,15 +36,15 @@
 // K~ is an operand in two BF16 parts, hi + lo, 16 mantissa bits: FP32 states are off by 2.4e-6 relative to 64 bits
 // (FP32 arithmetic throughout: 2e-7), and by one FP32 rounding a chunk of what they were before (StateFactor). One part would
 // leave 1.7e-3; a third would take 16 KiB of shared memory that is not there and a quarter more of the products' time.
-// P and S, which feed Y alone, are rounded to BF16 once (as Y itself is) where Y is an output: o is off by 2.3e-3
-// where one rounding of the exact value leaves 1.7e-3. Where Y is FP32 and summed further, over heads or, for the
+// P and S, which feed Y alone, are rounded to BF16 once (as Y itself is) where Y is an output: o and dv (dq and dk too with
+// fixed decays and no groups) are off by 2.4e-3 where one rounding of the exact value leaves 1.7e-3. Where Y is FP32 and summed further, over heads or, for the
 // decays' gradient, over the sequence, so that errors of its terms would outlive a cancelling sum, they too are in two
 // parts (kSplit); it costs 68 us against 56 in a pass over 4 x 2048 tokens of 32 heads.
 // A unit is one (sequence, head), longest sequences first (24 sequences of 1 to 4000 tokens, 64 heads: 540 us, in
 // index order 594), or one segment of it.
 //
-// What bounds it: shared memory's data pipe, which the products' operands (1090 cycles a chunk), the element-wise loads
-// and stores (1450 with the turns they lose to the others) and the copies (500) share: nearly all of some 3150 cycles.
+// What bounds it: shared memory's data pipe, which the products' operands (34 % of a chunk's some 3150 cycles), the
+// element-wise loads and stores (39 %, and 7 % for the turns they lose to the others) and the copies (15 %) share.
 // The tensor core is busy for a third, HBM would take half. Three stages of 48 KiB, two places of K~ and P and (one
 // part) of S overlap the chains K~ -> U -> state -> S Q^T -> Y and scores -> P -> V^T P^T of neighbouring chunks.
 // Measured: 1.6 us a chunk and SM. 8 x 1024 tokens of
