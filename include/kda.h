@@ -426,9 +426,8 @@ kda_status kda_prefill(const kda_bf16* q, const kda_bf16* k, const kda_bf16* v, 
  * are within 3.9e-3 (2.4e-3 measured; the exact values rounded to BF16: 1.7e-3); else dq
  * and dk are rounded to BF16 at the end alone. Results do not depend on the order of
  * execution.
- * A NaN or infinity in v or in an output's gradient stays in its sequence, but may reach the
- * results of all tokens of its chunk (64 tokens from the sequence's or a segment's first), also of
- * those before it.
+ * A NaN or infinity of a token stays in its sequence, but may reach the results of all
+ * tokens of its chunk (64 tokens, counted from the sequence's first), also of those before it.
  * Errors: as above (KDA_ERR_INVALID_ARGUMENT, _UNSUPPORTED, _ALIASING,
  * _WORKSPACE_TOO_SMALL, _CUDA), all before any launch; nothing is allocated; calls
  * only launch kernels on `stream` and may be captured into a CUDA graph. */

@@ -203,8 +203,8 @@ extern "C" kda_status kda_decay_attn_decode(const kda_bf16* q, const kda_bf16* k
     //         16 x 64 14.5, 13.3, 13.0, 13.0;  64 x 96 76.5, 68.3, 65.2, 63.4;  256 x 96 297, 264, 251, 242
     //   FP32  1 x 32 3.04, 3.19, 3.62, 5.29;  3 x 64 5.94, 5.99, 6.86, 8.33;  4 x 64 7.30, 7.07, 8.08, 8.65;
     //         16 x 64 22.0, 22.4, 23.3, 24.8;  128 x 96 234, 235, 237, 239
-    // One count serves all sizes: it is the best or within 5 % of it but for a single request, whose call takes
-    // longer on the host (18 us), and which another count would win at most 0.3 us.
+    // One count serves all sizes: it is the best or within 8 % of it but for a single request, whose call takes
+    // longer on the host (18 us) and would gain 0.4 us at most from another.
     if (state_dtype == KDA_STATE_BF16) launch(reinterpret_cast<__nv_bfloat16*>(state), std::integral_constant<int, 64>{});
     else launch(reinterpret_cast<float*>(state), std::integral_constant<int, 32>{});
     if ((e = cudaGetLastError()) != cudaSuccess) return dfail(KDA_ERR_CUDA, cudaGetErrorString(e));

@@ -25,6 +25,8 @@ _ROPE_TYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+# Tensors that a call wrote get a new version, as torch's own writes in place give them: _written((t, ...))
+_written = getattr(torch._C, "_increment_version", torch.autograd.graph.increment_version)
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
@@ -41,7 +43,7 @@ def _call(f, device, *args):
     if device.type != "cuda":
         raise ValueError("tensors must be CUDA tensors")
     index = device.index
-    stream = _stream(device)
+    stream = torch.cuda.current_stream(index).cuda_stream if _raw_stream is None else _raw_stream(index)
     if _current_device() == index:
         rc = f(*args, stream)
     else:
@@ -149,13 +151,6 @@ def _pool(state, Hv, D, dev):
     return _STATE[state.dtype]
 
 
-def _written(*tensors):
-    """These tensors of the caller were written to: a new version, as torch's own writes in place give them."""
-    given = [t for t in tensors if t is not None]
-    if given:
-        torch.autograd.graph.increment_version(given)
-
-
 def _versions(tensors):
     """Their versions, as far as they have some (tensors made in inference mode have none)."""
     return tuple(None if t is None or t.is_inference() else t._version for t in tensors)
@@ -259,7 +254,7 @@ def kda_decay_attn_fwd(q, k, v, log_decay, initial_state=None, cu_seqlens=None, 
     ws = ctx.workspace
     _call(lib.kda_decay_attn_fwd, dev, *call, o.data_ptr(), hT.data_ptr(), ws.data_ptr(), ws.numel(),
           ctx.device_status.data_ptr())
-    _written(out, final_state_out)
+    _written((o, hT))
     ctx._snapshot((q, k, v, log_decay, initial_state, cu_seqlens, hT), call, cu_host,
                   (q.shape, v.shape, (N, Hv, D, D), per_token))
     return o, hT, ctx
@@ -280,7 +275,6 @@ def kda_decay_attn_bwd(ctx: DecayContext, do, dfinal_state=None, out=None):
     if dfinal_state is not None:
         _want(dfinal_state, "dfinal_state", _F32, ss, dev)
     shapes = (qs, qs, vs, vs[:3] if per_token else None, ss if ctx.inputs[4] is not None else None)
-    given = out or ()
     if out is None:
         out = tuple(None if s is None else torch.empty(s, dtype=_F32 if i == 4 else _BF16, device=dev)
                     for i, s in enumerate(shapes))
@@ -296,7 +290,7 @@ def kda_decay_attn_bwd(ctx: DecayContext, do, dfinal_state=None, out=None):
     ws = ctx.workspace
     _call(lib.kda_decay_attn_bwd, dev, *ctx.call, ctx.inputs[6].data_ptr(), do.data_ptr(), _p(dfinal_state),
           *[_p(t) for t in out], ws.data_ptr(), ws.numel(), ctx.device_status.data_ptr())
-    _written(*given)
+    _written([t for t in out if t is not None])
     return tuple(out)
 
 
@@ -315,7 +309,6 @@ def kda_decay_attn_prefill(q, k, v, log_decay, state, cu_seqlens=None, state_ind
     N = B if cu_host is None else cu_host.numel() - 1
     idx_host = _slots(state_indices, state_indices_cpu, N, dev)
     sdt = _pool(state, Hv, D, dev)
-    given = out
     if out is None:
         out = torch.empty((B, T, Hv, D), dtype=_BF16, device=dev)
     else:
@@ -332,7 +325,7 @@ def kda_decay_attn_prefill(q, k, v, log_decay, state, cu_seqlens=None, state_ind
           _p(cu_seqlens), _p(cu_host), N, B, T, Hqk, Hv, D, _NAN if scale is None else float(scale), strides, state.data_ptr(),
           sdt, _p(state_indices), _p(idx_host), state.shape[0], out.data_ptr(), _p(workspace),
           0 if workspace is None else workspace.numel(), _p(device_status))
-    _written(state, given)
+    _written((state, out))
     return out
 
 
@@ -349,7 +342,6 @@ def kda_decay_attn_decode(q, k, v, log_decay, state, state_indices=None, scale=N
     dev = q.device
     sdt = _pool(state, Hv, D, dev)
     idx_host = _slots(state_indices, state_indices_cpu, N, dev)
-    given = out
     if out is None:
         out = torch.empty_like(v) if v.is_contiguous() else torch.empty((N, 1, Hv, D), dtype=_BF16, device=dev)
     else:
@@ -357,7 +349,7 @@ def kda_decay_attn_decode(q, k, v, log_decay, state, state_indices=None, scale=N
     _call(lib.kda_decay_attn_decode, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), per_token,
           state.data_ptr(), sdt, _p(state_indices), _p(idx_host), state.shape[0], N, Hqk, Hv, D,
           _NAN if scale is None else float(scale), strides, out.data_ptr())
-    _written(state, given)
+    _written((state, out))
     return out
 
 
@@ -394,7 +386,7 @@ def kda_qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6
     lib = load_library()
     B, T, Hq, Hk, D, R, dev, pos, freq = _rope_inputs(q, k, q_weight, k_weight, positions, inv_freq)
     flat_q, flat_k = q.is_contiguous(), k.is_contiguous()
-    given = q_out, k_out
+    fresh = q_out is None and k_out is None
     if q_out is None:
         q_out = torch.empty_like(q) if flat_q else torch.empty((B, T, Hq, D), dtype=q.dtype, device=dev)
     else:
@@ -408,7 +400,8 @@ def kda_qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6
     strides = None if flat_q and flat_k else _all_strides(("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out))
     _call(lib.kda_qk_norm_rope_fwd, dev, q.data_ptr(), k.data_ptr(), _ROPE_TYPES[q.dtype], _p(q_weight), _p(k_weight),
           pos, freq, B * T, Hq, Hk, D, R, eps, 1 if interleaved else 0, strides, q_out.data_ptr(), k_out.data_ptr())
-    _written(*given)
+    if not fresh:
+        _written((q_out, k_out))
     return q_out, k_out
 
 
@@ -451,5 +444,5 @@ def kda_qk_norm_rope_bwd(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, 
           gq.data_ptr(), gk.data_ptr(), _p(gqw), _p(gkw), _p(workspace),
           0 if workspace is None else workspace.numel())
     if out is not None:
-        _written(gq, gk)
+        _written((gq, gk))
     return gq, gk, gqw, gkw
