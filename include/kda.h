@@ -533,6 +533,101 @@ kda_status kda_qk_norm_rope_bwd(const void* dq, const void* dk, const void* q, c
                                 void* dq_out, void* dk_out, float* dq_weight, float* dk_weight,
                                 void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
 
+/* Gated delta rule: a decay and a step size (beta) for each token and head.
+ *
+ * The method: per (sequence, value head h) a value-first FP32 state S[128, 128],
+ *   S' = exp(g_t) S_{t-1},  u_t = v_t - S' k_t,  S_t = S' + beta_t u_t k_t^T,  o_t = scale S_t q_t
+ * with value head h reading query/key head h / (Hv / Hqk). Next to KDA above: one decay
+ * per head (any log decay <= 0, none at all with log_decay NULL), beta as it is, and no
+ * normalisation inside: k of norm 1 and beta in [0, 2] keep the state bounded
+ * (kda_qk_norm_rope_fwd with weights of 1 / sqrt(128) and no rotation gives such k).
+ * Shared by the entry points kda_gated_delta_*:
+ *   q, k, v, strides, cu_seqlens, scale, T, device_status, aliasing and errors as for
+ *               kda_decay_attn_* (sequences may be empty)
+ *   log_decay   g, BF16 [B, T, Hv], or NULL for 0; -inf resets the state
+ *   beta        BF16 [B, T, Hv]
+ * Arithmetic: products of BF16 operands with FP32 accumulation. Each chunk of 64 tokens solves
+ * its triangular system in FP32; what enters a state or is solved from one is taken in two
+ * BF16 parts (16 bits), states are FP32: what a call leaves in FP32 states is within 1e-5 of the
+ * exact (relative, in the 2-norm) for keys of norm 1. o, dq, dk, dv, dlog_decay and dbeta are
+ * rounded to BF16 from operands that were rounded to BF16 once: within 5e-3. A decode step is FP32
+ * throughout. Results do not depend on the order of execution. A NaN or infinity of a token stays
+ * in its sequence, but may reach all tokens of its chunk (64 tokens from the sequence's first). */
+
+/* Bytes of device workspace (256-byte aligned, possibly 0): `training` 1 for
+ * kda_gated_delta_fwd and _bwd, 0 for kda_gated_delta_prefill. */
+kda_status kda_gated_delta_workspace_bytes(int64_t B, int64_t T, int64_t Hqk, int64_t Hv,
+                                           const int64_t* cu_seqlens_host, int64_t num_seqs,
+                                           int32_t training, size_t* bytes);
+
+/* Training forward: o BF16 [B, T, Hv, 128] and h_T FP32 [N, Hv, 128, 128] from h0 FP32 (NULL
+ * for zeros). The workspace holds what kda_gated_delta_bwd needs (each chunk's system and start
+ * state, u) and must not change until then. */
+kda_status kda_gated_delta_fwd(const kda_bf16* q, const kda_bf16* k, const kda_bf16* v,
+                               const kda_bf16* log_decay, const kda_bf16* beta, const float* h0,
+                               const int64_t* cu_seqlens_dev, const int64_t* cu_seqlens_host,
+                               int64_t num_seqs, int64_t B, int64_t T, int64_t Hqk, int64_t Hv,
+                               int64_t head_dim, float scale, const int64_t* strides, kda_bf16* o,
+                               float* h_T, void* workspace, size_t workspace_bytes,
+                               int32_t* device_status, struct CUstream_st* stream);
+
+/* Training backward: the inputs of kda_gated_delta_fwd, its workspace and the adjoints.
+ * d_o BF16 [B, T, Hv, 128], d_hT FP32 [N, Hv, 128, 128] or NULL (zeros); dq, dk BF16
+ * [B, T, Hqk, 128] (sums over the value heads of the group, rounded once), dv BF16
+ * [B, T, Hv, 128], dlog_decay BF16 [B, T, Hv] (or NULL: not wanted; NULL without decays), dbeta BF16
+ * [B, T, Hv], dh0 FP32 or NULL. All gradients contiguous. */
+kda_status kda_gated_delta_bwd(const kda_bf16* q, const kda_bf16* k, const kda_bf16* v,
+                               const kda_bf16* log_decay, const kda_bf16* beta,
+                               const int64_t* cu_seqlens_dev, const int64_t* cu_seqlens_host,
+                               int64_t num_seqs, int64_t B, int64_t T, int64_t Hqk, int64_t Hv,
+                               int64_t head_dim, float scale, const int64_t* strides,
+                               const kda_bf16* d_o, const float* d_hT, kda_bf16* dq, kda_bf16* dk,
+                               kda_bf16* dv, kda_bf16* dlog_decay, kda_bf16* dbeta, float* dh0,
+                               void* workspace, size_t workspace_bytes, int32_t* device_status,
+                               struct CUstream_st* stream);
+
+/* Inference prefill from a state pool and one decode step on it (T = 1), as
+ * kda_decay_attn_prefill and kda_decay_attn_decode. */
+kda_status kda_gated_delta_prefill(const kda_bf16* q, const kda_bf16* k, const kda_bf16* v,
+                                   const kda_bf16* log_decay, const kda_bf16* beta,
+                                   const int64_t* cu_seqlens_dev, const int64_t* cu_seqlens_host,
+                                   int64_t num_seqs, int64_t B, int64_t T, int64_t Hqk, int64_t Hv,
+                                   int64_t head_dim, float scale, const int64_t* strides, void* state,
+                                   int32_t state_dtype, const int32_t* state_indices,
+                                   const int32_t* state_indices_host, int64_t num_slots, kda_bf16* o,
+                                   void* workspace, size_t workspace_bytes, int32_t* device_status,
+                                   struct CUstream_st* stream);
+kda_status kda_gated_delta_decode(const kda_bf16* q, const kda_bf16* k, const kda_bf16* v,
+                                  const kda_bf16* log_decay, const kda_bf16* beta, void* state,
+                                  int32_t state_dtype, const int32_t* state_indices,
+                                  const int32_t* state_indices_host, int64_t num_slots, int64_t N,
+                                  int64_t Hqk, int64_t Hv, int64_t head_dim, float scale,
+                                  const int64_t* strides, kda_bf16* o, struct CUstream_st* stream);
+
+/* Layer norm of each row of x [rows, width] (rows row_stride elements apart, row_stride >= width):
+ *   y = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ *   x, y        of type dtype (KDA_DTYPE_*), aligned to their elements (16 bytes are faster);
+ *               y contiguous, and may be x where x is contiguous
+ *   weight, bias  FP32 [width], or NULL for 1 and 0
+ *   mean, rstd  FP32 [rows], written for the backward
+ * Arithmetic is FP32, y rounded once; eps >= 0. rows may be 0. Other overlaps are refused. */
+kda_status kda_layer_norm_fwd(const void* x, int32_t dtype, const float* weight, const float* bias,
+                              int64_t rows, int64_t width, int64_t row_stride, float eps, void* y,
+                              float* mean, float* rstd, struct CUstream_st* stream);
+
+/* Device bytes that kda_layer_norm_bwd needs for the sums over rows. */
+kda_status kda_layer_norm_workspace_bytes(int64_t rows, int64_t width, size_t* bytes);
+
+/* Its gradients, from dy (rows dy_stride apart), x, weight and the forward's mean and rstd: dx
+ * (contiguous, of dtype; it may be dy or x where those are contiguous and width is at most 12288,
+ * FP32: 8192), dweight and dbias FP32 [width] or NULL (not wanted), summed over the rows in a fixed order
+ * (zeros for no rows). workspace may be NULL without dweight and dbias. */
+kda_status kda_layer_norm_bwd(const void* dy, const void* x, int32_t dtype, const float* weight,
+                              const float* mean, const float* rstd, int64_t rows, int64_t width,
+                              int64_t dy_stride, int64_t row_stride, void* dx, float* dweight,
+                              float* dbias, void* workspace, size_t workspace_bytes,
+                              struct CUstream_st* stream);
+
 /* Self-test of the device-side timeout path (no counterpart on the pages: the
  * kernels' own failure handling). Launches one CTA of 32 threads on `stream`
  * whose mbarrier wait can never complete, because nothing arrives on the

@@ -6,7 +6,9 @@
 ``kda_prefill`` and the single-token ``kda_decode`` call libkda.so; ``HostStep`` runs whole training
 steps from and to host memory (``kda_step_host``). Linear attention with a decay for each head:
 ``kda_decay_attn_fwd`` / ``_bwd`` / ``_prefill`` / ``_decode``, and the norm and position rotation of its
-queries and keys, ``kda_qk_norm_rope_fwd`` / ``_bwd``. See include/kda.h.
+queries and keys, ``kda_qk_norm_rope_fwd`` / ``_bwd``. The gated delta rule with a decay for each token and head:
+``kda_gated_delta_fwd`` / ``_bwd`` / ``_prefill`` / ``_decode``. Layer norm: ``kda_layer_norm_fwd`` / ``_bwd``.
+See include/kda.h.
 """
 
 from .decay import (  # noqa: F401
@@ -18,6 +20,20 @@ from .decay import (  # noqa: F401
     kda_decay_attn_prefill,
     kda_qk_norm_rope_bwd,
     kda_qk_norm_rope_fwd,
+)
+
+from .delta import (  # noqa: F401
+    DeltaContext,
+    gated_delta_workspace_bytes,
+    kda_gated_delta_bwd,
+    kda_gated_delta_decode,
+    kda_gated_delta_fwd,
+    kda_gated_delta_prefill,
+)
+
+from .norm import (  # noqa: F401
+    kda_layer_norm_bwd,
+    kda_layer_norm_fwd,
 )
 
 from .kda import (  # noqa: F401

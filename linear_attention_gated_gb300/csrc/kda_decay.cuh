@@ -3,6 +3,7 @@
 #pragma once
 
 #include "kda_common.cuh"
+#include "tc.cuh"
 
 namespace kda {
 
@@ -75,6 +76,63 @@ __device__ __forceinline__ float decay_g(const DecayProblem& P, int64_t tok, int
   return P.per_token ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(P.g)[tok * P.Hv + h])
                      : reinterpret_cast<const float*>(P.g)[h];
 }
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+__device__ __forceinline__ uint32_t pack2(float2 x) { return pack2(x.x, x.y); }
+__device__ __forceinline__ float2 unpack2(uint32_t x) {
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+// The factors 2^x that a state is multiplied by one after the other. Each rounded to FP32 by itself, a slow fixed decay's would
+// be off by the same part of a step every time (states 6e-5 off after 1536 chunks). So what a rounding leaves goes
+// into the next factor, and their product stays within a step of the exact one. |x| >= 1/2 is forgotten too soon for that.
+struct StateFactor {
+  float left = 0.f;
+  __device__ __forceinline__ float next(float x) {
+    if (!(fabsf(x) < 0.5f)) {
+      left = 0.f;
+      return fast_exp2(x);
+    }
+    const float m = expm1f(x * 0.6931471805599453f), e = 1.f + m;  // (2^-23 of m off: little where 2^x is next to 1)
+    const float more = fmaf(left, e, m - (e - 1.f)), f = e + more;
+    left = __fdividef(more - (f - e), f);
+    return f;
+  }
+};
+// x as BF16 pairs hi + lo: 16 mantissa bits together
+__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
+  hi = pack2(x);
+  lo = pack2(tc::sub2(x, unpack2(hi)));
+}
+
+// Eight values of a state row, as they come from memory.
+template <typename S>
+struct StateVec;
+template <>
+struct StateVec<__nv_bfloat16> {
+  uint4 r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float* x) const { unpack_bf16x8(r, x); }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* x) { store_bf16x8(p, x); }
+};
+template <>
+struct StateVec<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void get(float* x) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+  static __device__ __forceinline__ void store(float* p, const float* x) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+};
 
 // Tokens of the segments sequences are cut into, 0 for none. cu: host offsets or null.
 int64_t decay_segment_tokens(const int64_t* cu, int64_t N, int64_t T, int64_t Hv);

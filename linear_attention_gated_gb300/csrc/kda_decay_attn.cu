@@ -1,124 +1,28 @@
 // kda_decay_attn.cu -- host side of the linear attention with a decay for each
 // head: argument checks, workspace sizes and launches of kda_decay_attn_fwd,
 // kda_decay_attn_bwd and kda_decay_attn_prefill. Nothing is allocated here.
-#include "../../include/kda.h"
-#include "kda_decay.cuh"
-#include "kda_host.h"
-
-#include <cmath>
-#include <cstdio>
+#include "kda_decay_host.h"
 
 namespace {
 
 __device__ int32_t g_decay_status;
 
-kda_status fail(kda_status st, const char* what) {
-  char buf[256];
-  snprintf(buf, sizeof(buf), "decay_attn: %s", what);
-  kda::set_last_error(buf);
-  return st;
-}
+constexpr const char* kOp = "decay_attn";
+using kda::host::aliasing;
+using kda::host::check_shape;
+using kda::host::Shape;
+using kda::host::Span;
 
-struct Span {
-  const void* p;
-  size_t bytes;
-};
+kda_status fail(kda_status st, const char* what) { return kda::host::fail(kOp, st, what); }
 
-bool overlap(const Span& a, const Span& b) {
-  const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
-  return a.p && b.p && a.bytes && b.bytes && a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-template <size_t NO, size_t NI>
-bool aliasing(const Span (&outs)[NO], const Span (&ins)[NI]) {
-  for (size_t i = 0; i < NO; ++i) {
-    for (const Span& in : ins)
-      if (overlap(in, outs[i])) return true;
-    for (size_t j = i + 1; j < NO; ++j)
-      if (overlap(outs[i], outs[j])) return true;
-  }
-  return false;
-}
-
-struct Shape {
-  int64_t N, Ttot, seg, longest;
-};
-
-kda_status check_shape(int64_t B, int64_t T, int64_t Hqk, int64_t Hv, const int64_t* cu, int64_t num_seqs, Shape* s) {
-  if (B < 1 || T < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "B must be >= 1 and T >= 0");
-  if (Hqk < 1 || Hv < 1 || Hv % Hqk) return fail(KDA_ERR_INVALID_ARGUMENT, "Hv must be a positive multiple of Hqk");
-  if (kda::size_limit_violation(B, T ? T : 1, Hv, 0))
-    return fail(KDA_ERR_UNSUPPORTED, "problem too large (over 2^40 tokens or token-heads, or 2^20 heads)");
-  s->Ttot = B * T;
-  s->N = B;
-  if (cu) {
-    if (B != 1) return fail(KDA_ERR_INVALID_ARGUMENT, "packed input needs a physical batch of one");
-    if (num_seqs < 1) return fail(KDA_ERR_INVALID_ARGUMENT, "packed input needs num_seqs >= 1");
-    if (cu[0] != 0 || cu[num_seqs] != T) return fail(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens must run from 0 to T");
-    for (int64_t i = 0; i < num_seqs; ++i)
-      if (cu[i + 1] < cu[i]) return fail(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens decreases");
-    s->N = num_seqs;
-  }
-  if (s->N > INT32_MAX / Hv) return fail(KDA_ERR_UNSUPPORTED, "too many (sequence, head) units");
-  if (s->Ttot >= INT32_MAX) return fail(KDA_ERR_UNSUPPORTED, "problem too large (2^31 tokens)");
-  s->longest = cu ? 0 : T;
-  for (int64_t i = 0; cu && i < s->N; ++i)
-    if (cu[i + 1] - cu[i] > s->longest) s->longest = cu[i + 1] - cu[i];
-  s->seg = kda::decay_segment_tokens(cu, s->N, T, Hv);
-  return KDA_OK;
-}
-
-// Fills and checks what the three entry points share. strides: token and head strides (elements) of
-// q, k, v, or null for contiguous tensors. spans: the bytes that q, k, v and the decays take.
 kda_status check_tokens(const void* q, const void* k, const void* v, const void* g, int32_t per_token,
                         const int64_t* cu_dev, const int64_t* cu_host, int64_t num_seqs, int64_t B, int64_t T,
                         int64_t Hqk, int64_t Hv, int64_t head_dim, float scale, const int64_t* strides,
                         kda::DecayProblem* P, Span (&spans)[5]) {
-  if ((cu_dev == nullptr) != (cu_host == nullptr))
-    return fail(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens needs its host mirror (and the reverse)");
-  Shape s{};
-  const kda_status st = check_shape(B, T, Hqk, Hv, cu_host, num_seqs, &s);
-  if (st != KDA_OK) return st;
-  if (head_dim != kda::kDim) return fail(KDA_ERR_UNSUPPORTED, "head_dim must be 128");
-  if (per_token != 0 && per_token != 1) return fail(KDA_ERR_INVALID_ARGUMENT, "decay_per_token must be 0 or 1");
-  if (std::isinf(scale)) return fail(KDA_ERR_INVALID_ARGUMENT, "scale must be finite (NaN selects 1/sqrt(128))");
-  if ((!g && (s.Ttot || !per_token)) || (s.Ttot && (!q || !k || !v))) return fail(KDA_ERR_INVALID_ARGUMENT, "null tensor pointer");
-  if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v) & 15u)
-    return fail(KDA_ERR_INVALID_ARGUMENT, "token tensors must be 16-byte aligned");
-  const int64_t D = kda::kDim;
-  int64_t x[6] = {Hqk * D, D, Hqk * D, D, Hv * D, D};
-  if (strides)
-    for (int i = 0; i < 6; ++i) x[i] = strides[i];
-  const int64_t heads[3] = {Hqk, Hqk, Hv};
-  const void* ptrs[3] = {q, k, v};
-  for (int i = 0; i < 3; ++i) {
-    const int64_t ts = x[2 * i], hs = x[2 * i + 1];
-    bool too_large;
-    if (!kda::view_rows_apart(s.Ttot, heads[i], D, ts, hs, &too_large) || hs % 8 || ts % 8)
-      return fail(KDA_ERR_INVALID_ARGUMENT, "token and head strides must be multiples of 8 elements and keep rows apart");
-    if (too_large || ts > (int64_t(1) << 38)) return fail(KDA_ERR_UNSUPPORTED, "strides too large");
-    spans[i] = Span{ptrs[i], s.Ttot ? 2 * (size_t)((s.Ttot - 1) * ts + (heads[i] - 1) * hs + D) : 0};
-  }
-  spans[3] = Span{g, per_token ? 2 * (size_t)s.Ttot * Hv : 4 * (size_t)Hv};
-  spans[4] = Span{cu_dev, cu_dev ? 8 * (size_t)(s.N + 1) : 0};
-  P->q = reinterpret_cast<const __nv_bfloat16*>(q);
-  P->k = reinterpret_cast<const __nv_bfloat16*>(k);
-  P->v = reinterpret_cast<const __nv_bfloat16*>(v);
-  P->g = g;
-  P->cu = cu_dev;
-  P->qt = x[0]; P->qh = x[1]; P->kt = x[2]; P->kh = x[3]; P->vt = x[4]; P->vh = x[5];
-  P->N = s.N;
-  P->T = T;
-  P->Ttot = s.Ttot;
-  P->Hqk = (int)Hqk;
-  P->Hv = (int)Hv;
-  P->r = (int)(Hv / Hqk);
-  P->per_token = per_token;
-  P->seg = s.seg;
-  P->longest = s.longest;
-  P->cu_host = cu_host;
-  P->scale = std::isnan(scale) ? 1.0f / std::sqrt(128.0f) : scale;
-  return KDA_OK;
+  const kda_status st = kda::host::check_tokens(kOp, q, k, v, g, true, per_token, cu_dev, cu_host, num_seqs, B, T, Hqk, Hv, head_dim,
+                                                scale, strides, P, spans);
+  if (st == KDA_OK) P->seg = kda::decay_segment_tokens(cu_host, P->N, T, Hv);
+  return st;
 }
 
 kda_status check_workspace(const kda::DecayProblem& P, void* ws, size_t bytes, bool training) {
@@ -130,16 +34,7 @@ kda_status check_workspace(const kda::DecayProblem& P, void* ws, size_t bytes, b
 }
 
 kda_status check_device(int32_t* device_status, int32_t** status) {
-  int dev = -1, major = 0, minor = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  if (e != cudaSuccess) return fail(KDA_ERR_CUDA, cudaGetErrorString(e));
-  if (major != 10 || minor != 3) return fail(KDA_ERR_UNSUPPORTED, "kernels are built for sm_103a");
-  *status = device_status;
-  if (!device_status && (e = cudaGetSymbolAddress(reinterpret_cast<void**>(status), g_decay_status)) != cudaSuccess)
-    return fail(KDA_ERR_CUDA, cudaGetErrorString(e));
-  return KDA_OK;
+  return kda::host::check_device(kOp, device_status, &g_decay_status, status);
 }
 
 }  // namespace
@@ -150,9 +45,9 @@ extern "C" kda_status kda_decay_attn_workspace_bytes(int64_t B, int64_t T, int64
   return kda::guarded([&]() -> kda_status {
     if (!bytes) return fail(KDA_ERR_INVALID_ARGUMENT, "bytes is NULL");
     Shape s{};
-    const kda_status st = check_shape(B, T, Hqk, Hv, cu_seqlens_host, num_seqs, &s);
+    const kda_status st = check_shape(kOp, B, T, Hqk, Hv, cu_seqlens_host, num_seqs, &s);
     if (st != KDA_OK) return st;
-    *bytes = kda::decay_workspace_bytes(s.N, s.Ttot, Hqk, Hv, s.seg, training != 0, decay_per_token != 0);
+    *bytes = kda::decay_workspace_bytes(s.N, s.Ttot, Hqk, Hv, kda::decay_segment_tokens(cu_seqlens_host, s.N, T, Hv), training != 0, decay_per_token != 0);
     return KDA_OK;
   });
 }

@@ -27,32 +27,6 @@ namespace {
 constexpr int kDdThreads = 128;
 constexpr int kDdPerPass = kDdThreads / 16;  // rows of one pass: a half-warp each
 
-template <typename S>
-struct DdVec;
-template <>
-struct DdVec<__nv_bfloat16> {
-  uint4 r;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void get(float* x) const { unpack_bf16x8(r, x); }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* x) { store_bf16x8(p, x); }
-};
-template <>
-struct DdVec<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
-  }
-  __device__ __forceinline__ void get(float* x) const {
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  }
-  static __device__ __forceinline__ void store(float* p, const float* x) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-  }
-};
-
 template <typename S, int kRows>
 __global__ void __launch_bounds__(kDdThreads) kda_decay_decode_kernel(const DecayProblem P, S* pool, const int32_t* idx,
                                                                       int64_t num_slots, __nv_bfloat16* o) {
@@ -70,7 +44,7 @@ __global__ void __launch_bounds__(kDdThreads) kda_decay_decode_kernel(const Deca
     return;
   }
   S* s = pool + (slot * P.Hv + h) * (int64_t)(kDim * kDim) + row0 * kDim + 8 * hl;
-  DdVec<S> raw[kPasses];
+  StateVec<S> raw[kPasses];
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) raw[p].load(s + p * kDdPerPass * kDim);
   float q[8], k[8], v[kPasses];
@@ -91,7 +65,7 @@ __global__ void __launch_bounds__(kDdThreads) kda_decay_decode_kernel(const Deca
       x[e] = fmaf(v[p], k[e], d * x[e]);
       y = fmaf(x[e], q[e], y);
     }
-    DdVec<S>::store(s + p * kDdPerPass * kDim, x);
+    StateVec<S>::store(s + p * kDdPerPass * kDim, x);
     y = row16_sum(y);
     if (hl == 0) out[p * kDdPerPass] = __float2bfloat16_rn(P.scale * y);
   }

@@ -141,36 +141,6 @@ struct PassArgs {
   int32_t first[kUnits + 1];       // segments s of the sequences that have one: pairs first[s] .. first[s + 1] - 1
 };
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&x);
-}
-__device__ __forceinline__ uint32_t pack2(float2 x) { return pack2(x.x, x.y); }
-__device__ __forceinline__ float2 unpack2(uint32_t x) {
-  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-}
-// The factors 2^x that a state is multiplied by one after the other. Each rounded to FP32 by itself, a slow fixed decay's would
-// be off by the same part of a step every time (states 6e-5 off after 1536 chunks). So what a rounding leaves goes
-// into the next factor, and their product stays within a step of the exact one. |x| >= 1/2 is forgotten too soon for that.
-struct StateFactor {
-  float left = 0.f;
-  __device__ __forceinline__ float next(float x) {
-    if (!(fabsf(x) < 0.5f)) {
-      left = 0.f;
-      return fast_exp2(x);
-    }
-    const float m = expm1f(x * 0.6931471805599453f), e = 1.f + m;  // (2^-23 of m off: little where 2^x is next to 1)
-    const float more = fmaf(left, e, m - (e - 1.f)), f = e + more;
-    left = __fdividef(more - (f - e), f);
-    return f;
-  }
-};
-// x as BF16 pairs hi + lo: 16 mantissa bits together
-__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
-  hi = pack2(x);
-  lo = pack2(tc::sub2(x, unpack2(hi)));
-}
-
 template <bool kRev, bool kState>
 __device__ __forceinline__ Unit unit_of(const PassArgs& a, int u) {
   const DecayProblem& P = a.P;

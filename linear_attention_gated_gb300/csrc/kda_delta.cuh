@@ -1,0 +1,65 @@
+// kda_delta.cuh -- launch parameters and the chunks' workspace shared by the kernels of the gated delta rule (kda_delta_*.cu).
+//
+// Per (sequence, value head), value first, with b the running sum of a chunk's log decays, D_ij = e^{b_i - b_j} (all
+// exponents <= 0) and C = 64 tokens a chunk:
+//   (1 + A) U = V - e^{b} K S^T,   A_ij = D_ij k_i . k_j beta_j  (j < i),   T = (1 + A)^-1
+//   O  = s e^{b} Q S^T + P (beta U),   P_ij = s D_ij q_i . k_j  (j <= i)
+//   S <- e^{b_C} S + sum_j w_j beta_j u_j k_j^T,   w_j = e^{b_C - b_j}
+// T and P are a chunk's own and are made for all chunks side by side; the pass over a sequence's chunks has three
+// products in its chain (K S^T, T X, the state's update).
+#pragma once
+
+#include "kda_decay.cuh"
+
+namespace kda {
+
+struct DeltaProblem : DecayProblem {  // (g may be null: no decay)
+  const __nv_bfloat16* beta;          // [Ttot, Hv]
+  int64_t slots;                      // places for chunks: Ttot / 64 + N
+};
+
+// What is kept for each (chunk, head). T and P are BF16 tiles [64][64] in the 128-byte swizzle, in two parts hi + lo
+// (16 mantissa bits); P's low part is for the backward alone.
+constexpr uint32_t kPkT = 0, kPkTlo = 8192, kPkP = 16384, kPkAux = 24576, kPkAux2 = 25600, kPkPlo = 26624;
+constexpr uint32_t kPkForward = kPkAux2, kPkInfer = kPkPlo, kPkTrain = 34816;
+struct DeltaAux {
+  float eb[64];    // e^{b_i}
+  float w[64];     // e^{b_C - b_i}
+  float beta[64];  // 0 past the sequence's end
+  float whole;     // b_C in base 2
+  float pad[63];
+  float bh[64], bl[64];  // b_i in base 2, in two parts
+};
+static_assert(sizeof(DeltaAux) == 1536 && kPkAux2 == kPkAux + 1024, "a chunk's numbers");
+
+constexpr uint32_t kStateTile = 32768, kUTile = 16384;  // a state in BF16 [2][128 rows][64], u [2][64 tokens][64], swizzled
+
+// Place of a sequence's first chunk: leaves each sequence ceil(len / 64) places.
+__host__ __device__ __forceinline__ int64_t delta_slot(int64_t t0, int64_t n) { return t0 / kDecayChunk + n; }
+
+// Device workspace: packets; training: the states at the chunks' starts and u of the forward, the states' adjoints
+// at the chunks' ends.
+struct DeltaWs {
+  size_t packet, states, u, adjoints, total;
+};
+DeltaWs delta_workspace(int64_t slots, int64_t Hv, bool training);
+
+struct DeltaGrads {
+  const __nv_bfloat16* d_o;  // [Ttot, Hv, 128]
+  const float* d_hT;         // [N, Hv, 128, 128] or null (zeros)
+  __nv_bfloat16* dq;         // [Ttot, Hqk, 128]
+  __nv_bfloat16* dk;
+  __nv_bfloat16* dv;         // [Ttot, Hv, 128]
+  __nv_bfloat16* dg;         // [Ttot, Hv] or null
+  __nv_bfloat16* dbeta;      // [Ttot, Hv]
+  float* dh0;                // [N, Hv, 128, 128] or null
+};
+
+cudaError_t launch_delta_prep(const DeltaProblem& P, bool training, void* ws, cudaStream_t s);
+cudaError_t launch_delta_forward(const DeltaProblem& P, const DecayStates& st, __nv_bfloat16* o, bool training, void* ws,
+                                 cudaStream_t s);
+cudaError_t launch_delta_backward(const DeltaProblem& P, const DeltaGrads& g, void* ws, cudaStream_t s);
+// The part of the backward within chunks (after the adjoints' pass).
+cudaError_t launch_delta_grads(const DeltaProblem& P, const DeltaGrads& g, void* ws, cudaStream_t s);
+
+}  // namespace kda

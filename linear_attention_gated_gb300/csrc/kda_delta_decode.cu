@@ -1,0 +1,114 @@
+// kda_delta_decode.cu -- one token per sequence of the gated delta rule, on a state pool, in place:
+//   S' = e^{g} S,  u = v - S' k,  S <- S' + beta u k^T,   o = s S q
+// for the state S [128 x 128] (value-first) of pool slot state_indices[n] and every value head.
+//
+// The step reads and writes each state once and does 10 flops per state value: HBM bandwidth bounds it (64 KiB there
+// and 64 KiB back per FP32 state, against 1 KiB of vectors). The 128 rows of a state are independent, so a CTA takes
+// kRows of them; a half-warp owns a row, 8 keys a lane, and all of a thread's rows are in flight before it touches the
+// token's vectors. A row's two sums over the keys follow one another: the thread's rows hide each other's.
+#include "kda_decay_host.h"
+#include "kda_delta.cuh"
+
+#include <type_traits>
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kPerPass = kThreads / 16;  // rows of one pass: a half-warp each
+
+template <typename S, int kRows>
+__global__ void __launch_bounds__(kThreads) kda_delta_decode_kernel(const DeltaProblem P, S* pool, const int32_t* idx,
+                                                                    int64_t num_slots, __nv_bfloat16* o) {
+  constexpr int kParts = kDim / kRows, kPasses = kRows / kPerPass;
+  const int part = blockIdx.x % kParts;
+  const int64_t unit = blockIdx.x / kParts;
+  const int64_t n = unit / P.Hv;
+  const int h = (int)(unit - n * P.Hv);
+  const int tid = threadIdx.x, hl = tid & 15, row0 = part * kRows + (tid >> 4);
+  const int64_t slot = idx ? idx[n] : n;
+  if (slot < 0 || slot >= num_slots) {
+    // a device index outside the pool (it no longer matches the host mirror the call was checked
+    // against, as in a replayed graph): no state is touched and these values of o read NaN
+    if (tid < kRows) o[(n * P.Hv + h) * kDim + part * kRows + tid] = __ushort_as_bfloat16(0x7fc0);
+    return;
+  }
+  S* s = pool + (slot * P.Hv + h) * (int64_t)(kDim * kDim) + row0 * kDim + 8 * hl;
+  StateVec<S> raw[kPasses];
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) raw[p].load(s + p * kPerPass * kDim);
+  float q[8], k[8], v[kPasses];
+  const int hq = h / P.r;
+  load_bf16x8(P.q + n * P.qt + hq * P.qh + 8 * hl, q);
+  load_bf16x8(P.k + n * P.kt + hq * P.kh + 8 * hl, k);
+  const __nv_bfloat16* vr = P.v + n * P.vt + h * P.vh + row0;
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) v[p] = __bfloat162float(vr[p * kPerPass]);
+  const float d = P.g ? exp2f(decay_log2(decay_g(P, n, h))) : 1.f;
+  const float beta = __bfloat162float(P.beta[n * P.Hv + h]);
+  __nv_bfloat16* out = o + (n * P.Hv + h) * kDim + row0;
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    float x[8], z = 0.f, y = 0.f;
+    raw[p].get(x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] *= d;
+      z = fmaf(x[e], k[e], z);
+    }
+    const float u = beta * (v[p] - row16_sum(z));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = fmaf(u, k[e], x[e]);
+      y = fmaf(x[e], q[e], y);
+    }
+    StateVec<S>::store(s + p * kPerPass * kDim, x);
+    y = row16_sum(y);
+    if (hl == 0) out[p * kPerPass] = __float2bfloat16_rn(P.scale * y);
+  }
+}
+
+__device__ int32_t g_unused_status;  // (decode reports a bad slot in o)
+
+}  // namespace
+}  // namespace kda
+
+extern "C" kda_status kda_gated_delta_decode(const kda_bf16* q, const kda_bf16* k, const kda_bf16* v, const kda_bf16* log_decay,
+                                             const kda_bf16* beta, void* state, int32_t state_dtype,
+                                             const int32_t* state_indices, const int32_t* state_indices_host,
+                                             int64_t num_slots, int64_t N, int64_t Hqk, int64_t Hv, int64_t head_dim,
+                                             float scale, const int64_t* strides, kda_bf16* o, struct CUstream_st* stream) {
+  using namespace kda::host;
+  constexpr const char* op = "gated_delta decode";
+  return kda::guarded([&]() -> kda_status {
+    if (N < 0) return fail(op, KDA_ERR_INVALID_ARGUMENT, "N must be >= 0");
+    kda::DeltaProblem P{};
+    Span in[5];
+    kda_status st = check_tokens(op, q, k, v, log_decay, false, 1, nullptr, nullptr, 0, N ? N : 1, N ? 1 : 0, Hqk, Hv, head_dim, scale,
+                                 strides, &P, in);
+    if (st != KDA_OK) return st;
+    if (N > INT32_MAX / 4 / Hv) return fail(op, KDA_ERR_UNSUPPORTED, "too many (sequence, head) units");
+    if (N && (!beta || !state || !o)) return fail(op, KDA_ERR_INVALID_ARGUMENT, "null tensor pointer");
+    const kda::host::Pool pool{state, state_dtype, state_indices, state_indices_host, num_slots};
+    if ((st = check_pool(op, pool, N, Hv)) != KDA_OK) return st;
+    if ((uintptr_t)o & 15u) return fail(op, KDA_ERR_INVALID_ARGUMENT, "state and output tensors must be 16-byte aligned");
+    const size_t gates = 2 * (size_t)N * Hv;
+    const Span outs[] = {pool_span(pool, Hv), {o, gates * kda::kDim}};
+    const Span ins[] = {in[0], in[1], in[2], {log_decay, gates}, {beta, gates}, {state_indices, 4 * (size_t)N}};
+    if (aliasing(outs, ins)) return fail(op, KDA_ERR_ALIASING, "an output overlaps an input or another output");
+    if ((st = check_device(op, nullptr, &kda::g_unused_status, &P.status)) != KDA_OK) return st;
+    if (N == 0) return KDA_OK;
+    P.N = N;
+    P.beta = reinterpret_cast<const __nv_bfloat16*>(beta);
+    auto launch = [&](auto* states, auto rows) {
+      kda::kda_delta_decode_kernel<std::remove_pointer_t<decltype(states)>, decltype(rows)::value>
+          <<<(unsigned)(N * Hv * (kda::kDim / decltype(rows)::value)), kda::kThreads, 0, stream>>>(
+              P, states, state_indices, num_slots, reinterpret_cast<__nv_bfloat16*>(o));
+    };
+    // 16 KiB of state to a CTA, as in the decay attention's step
+    if (state_dtype == KDA_STATE_BF16) launch(reinterpret_cast<__nv_bfloat16*>(state), std::integral_constant<int, 64>{});
+    else launch(reinterpret_cast<float*>(state), std::integral_constant<int, 32>{});
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? KDA_OK : fail(op, KDA_ERR_CUDA, cudaGetErrorString(e));
+  });
+}

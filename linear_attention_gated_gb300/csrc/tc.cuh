@@ -115,6 +115,8 @@ __device__ __forceinline__ void tma_store3(const void* map, uint32_t src_smem, i
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// (all but the thread's last group)
+__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Four 8 x 8 matrices of 16-bit values, each stored transposed: lane l holds row l / 4, columns 2 (l % 4) and the
@@ -123,6 +125,12 @@ __device__ __forceinline__ void stmatrix4_trans(uint32_t saddr, uint32_t r0, uin
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
                ::"r"(saddr), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
                : "memory");
+}
+
+// The reverse: four 8 x 8 matrices of 16-bit values, each transposed on its way to registers.
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t saddr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(saddr) : "memory");
 }
 
 // A operand read from tensor memory (128 lanes x K columns at a_tmem).
@@ -156,6 +164,11 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst_smem, const void* src, uin
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                ::"r"(dst_smem), "l"(src), "r"(bytes), "r"(mbar)
                : "memory");
+}
+
+// The same the other way; bulk_commit and the waits above are the bookkeeping of the thread that starts it.
+__device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src_smem, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src_smem), "r"(bytes) : "memory");
 }
 
 // Plain arrive (release at CTA scope) on an mbarrier.

@@ -34,7 +34,9 @@ EXPORTED = ("kda_ctx_workspace_bytes", "kda_fwd", "kda_bwd", "kda_ctx_status", "
             "kda_selftest_device_timeout", "kda_step_arena_bytes", "kda_step_host",
             "kda_bwd_standalone_workspace_bytes", "kda_bwd_standalone", "kda_noalloc_status",
             "kda_decay_attn_workspace_bytes", "kda_decay_attn_fwd", "kda_decay_attn_bwd", "kda_decay_attn_prefill",
-            "kda_decay_attn_decode", "kda_qk_norm_rope_fwd", "kda_qk_norm_rope_bwd", "kda_qk_norm_rope_workspace_bytes")
+            "kda_decay_attn_decode", "kda_qk_norm_rope_fwd", "kda_qk_norm_rope_bwd", "kda_qk_norm_rope_workspace_bytes",
+            "kda_gated_delta_workspace_bytes", "kda_gated_delta_fwd", "kda_gated_delta_bwd", "kda_gated_delta_prefill",
+            "kda_gated_delta_decode", "kda_layer_norm_fwd", "kda_layer_norm_bwd", "kda_layer_norm_workspace_bytes")
 
 
 class KdaError(RuntimeError):
@@ -104,8 +106,16 @@ def load_library(path: str = LIB_PATH):
     lib.kda_qk_norm_rope_fwd.argtypes = [P, P] + rope + [P]
     lib.kda_qk_norm_rope_bwd.argtypes = [P] * 4 + rope + [P, P, P, S, P]
     lib.kda_qk_norm_rope_workspace_bytes.argtypes = [I, ctypes.POINTER(S)]
+    lib.kda_gated_delta_workspace_bytes.argtypes = [I, I, I, I, P, I, i32, ctypes.POINTER(S)]
+    lib.kda_gated_delta_fwd.argtypes = [P] * 6 + shape + [P, P, P, S, P, P]
+    lib.kda_gated_delta_bwd.argtypes = [P] * 5 + shape + [P] * 8 + [P, S, P, P]
+    lib.kda_gated_delta_prefill.argtypes = [P] * 5 + shape + [P, i32, P, P, I, P, P, S, P, P]
+    lib.kda_gated_delta_decode.argtypes = [P] * 6 + [i32, P, P, I, I, I, I, I, F, P, P, P]
+    lib.kda_layer_norm_fwd.argtypes = [P, i32, P, P, I, I, I, F, P, P, P, P]
+    lib.kda_layer_norm_bwd.argtypes = [P, P, i32, P, P, P, I, I, I, I, P, P, P, P, S, P]
+    lib.kda_layer_norm_workspace_bytes.argtypes = [I, I, ctypes.POINTER(S)]
     for name in EXPORTED:
-        if name.startswith(("kda_decay", "kda_qk")):
+        if name.startswith(("kda_decay", "kda_qk", "kda_gated", "kda_layer")):
             getattr(lib, name).restype = ctypes.c_int
     lib.kda_chunk_tokens.argtypes = []
     lib.kda_chunk_tokens.restype = ctypes.c_int32
