@@ -3,11 +3,13 @@
 // Per (sequence, value head), value first, with b the running sum of a chunk's log decays, D_ij = e^{b_i - b_j} (all
 // exponents <= 0) and C = 64 tokens a chunk:
 //   (1 + A) U = V - e^{b} K S^T,   A_ij = D_ij k_i . k_j beta_j  (j < i),   T = (1 + A)^-1
-//   O  = s e^{b} Q S^T + P (beta U),   P_ij = s D_ij q_i . k_j  (j <= i)
+//   O  = s (e^{b} Q S^T + P (beta U)),   P_ij = D_ij q_i . k_j  (j <= i)
 //   S <- e^{b_C} S + sum_j w_j beta_j u_j k_j^T,   w_j = e^{b_C - b_j}
 // T and P are a chunk's own and are made for all chunks side by side; the pass over a sequence's chunks has three
 // products in its chain (K S^T, T X, the state's update).
 #pragma once
+
+#include <cstddef>
 
 #include "kda_decay.cuh"
 
@@ -18,27 +20,46 @@ struct DeltaProblem : DecayProblem {  // (g may be null: no decay)
   int64_t slots;                      // places for chunks: Ttot / 64 + N
 };
 
-// What is kept for each (chunk, head). T and P are BF16 tiles [64][64] in the 128-byte swizzle, in two parts hi + lo
+// What is made for each (chunk, head). T and P are BF16 tiles [64][64] in the 128-byte swizzle, in two parts hi + lo
 // (16 mantissa bits); P's low part is for the backward alone.
-constexpr uint32_t kPkT = 0, kPkTlo = 8192, kPkP = 16384, kPkAux = 24576, kPkAux2 = 25600, kPkPlo = 26624;
-constexpr uint32_t kPkForward = kPkAux2, kPkInfer = kPkPlo, kPkTrain = 34816;
+constexpr uint32_t kPkT = 0, kPkTlo = 8192, kPkP = 16384, kPkAux = 24576, kPkPlo = 26624;
+constexpr uint32_t kPkInfer = kPkPlo, kPkTrain = kPkPlo + 8192;
 struct DeltaAux {
   float eb[64];    // e^{b_i}
   float w[64];     // e^{b_C - b_i}
   float beta[64];  // 0 past the sequence's end
   float whole;     // b_C in base 2
   float pad[63];
-  float bh[64], bl[64];  // b_i in base 2, in two parts
+  float a[64];     // decays of the tokens
+  float b[64];     // b_i in base 2
 };
-static_assert(sizeof(DeltaAux) == 1536 && kPkAux2 == kPkAux + 1024, "a chunk's numbers");
+constexpr uint32_t kPkPass = kPkAux + 1024;  // what the forward's pass reads: up to `whole`
+static_assert(sizeof(DeltaAux) <= kPkPlo - kPkAux && offsetof(DeltaAux, a) == 1024, "a chunk's numbers");
 
 constexpr uint32_t kStateTile = 32768, kUTile = 16384;  // a state in BF16 [2][128 rows][64], u [2][64 tokens][64], swizzled
 
 // Place of a sequence's first chunk: leaves each sequence ceil(len / 64) places.
 __host__ __device__ __forceinline__ int64_t delta_slot(int64_t t0, int64_t n) { return t0 / kDecayChunk + n; }
 
-// Device workspace: packets; training: the states at the chunks' starts and u of the forward, the states' adjoints
-// at the chunks' ends.
+// The chunk of a place, as a kernel for all chunks side by side finds it: nt <= 0 where there is none.
+struct DeltaChunk {
+  int64_t t0;
+  int nt;
+};
+__device__ __forceinline__ DeltaChunk delta_chunk(const DeltaProblem& P, int64_t slot) {
+  int64_t lo = 0, hi = P.N;  // the last sequence whose first place is not behind this one
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) / 2;
+    if (delta_slot(decay_span(P, mid).t0, mid) <= slot) lo = mid;
+    else hi = mid;
+  }
+  const DecaySpan sp = decay_span(P, lo);
+  const int64_t c = slot - delta_slot(sp.t0, lo), left = sp.len - c * kDecayChunk;
+  return DeltaChunk{sp.t0 + c * kDecayChunk, c < 0 || left <= 0 ? 0 : left < kDecayChunk ? (int)left : kDecayChunk};
+}
+
+// Workspace: packets; of the training pair, the states at the chunks' starts and u from the forward, the states' adjoints at
+// the chunks' ends from the backward.
 struct DeltaWs {
   size_t packet, states, u, adjoints, total;
 };

@@ -76,17 +76,10 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wq = warp & 3, half = warp >> 2;
   const int64_t slot = blockIdx.x / P.Hqk;
   const int hq = (int)(blockIdx.x - slot * P.Hqk);
-  int64_t lo = 0, hi = P.N;  // the last sequence whose first place is not behind this one
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) / 2;
-    if (delta_slot(decay_span(P, mid).t0, mid) <= slot) lo = mid;
-    else hi = mid;
-  }
-  const DecaySpan sp = decay_span(P, lo);
-  const int64_t ci = slot - delta_slot(sp.t0, lo);
-  if (ci < 0 || ci * kC >= sp.len) return;  // a place without a chunk
-  const int64_t t0 = sp.t0 + ci * kC;
-  const int nt = (int)(sp.len - ci * kC < kC ? sp.len - ci * kC : kC);
+  const DeltaChunk ch = delta_chunk(P, slot);
+  if (ch.nt <= 0) return;  // a place without a chunk
+  const int64_t t0 = ch.t0;
+  const int nt = ch.nt;
   auto bar = [](unsigned long long& b) { return tc::smem_u32(&b); };
   if (warp == 0) tc::tmem_alloc(tc::smem_u32(&sm.tmem), 512);
   if (tid == 0)
@@ -183,7 +176,7 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int i = 32 * (wq & 1) + 16 * q + 8 * j + (lane >> 2);
-          const float bh = sm.aux.bh[i], bl = sm.aux.bl[i];
+          const float bi = sm.aux.b[i];
           float row = 0.f;
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
@@ -193,7 +186,7 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
               const int t = tok0 + 8 * m + e;
               const float beta = sm.aux.beta[t], x = uu[4 * m + 2 * j + e];
               const bool in = first ? t <= i : t < i;
-              const float d = in ? fast_exp2((bh - sm.aux.bh[t]) + (bl - sm.aux.bl[t])) * (first ? P.scale : 1.f) * x : 0.f;
+              const float d = in ? fast_exp2(bi - sm.aux.b[t]) * (first ? P.scale : 1.f) * x : 0.f;
               z[e] = d * beta;
               const float y = in ? d * kk[4 * m + 2 * j + e] : 0.f;
               col[2 * m + e] += y;

@@ -1,5 +1,15 @@
 // kda_delta_prep.cu -- what a chunk of the gated delta rule has of its own, for all chunks side by side: the factors of its
 // decays, P and T = (1 + A)^-1 (kda_delta.cuh).
+//
+// One CTA of four warps a (chunk, head): scores [K; Q] K^T (M = 128, N = 64) on the tensor cores (tcgen05), then A (two warps)
+// and P (the others) element by element, a row a thread. T comes from A's 16 x 16 blocks, by forward substitution in FP32 (a
+// column a thread; powers of A would lose everything where keys are alike), joined to 32 x 32 and then 64 x 64 by
+// T21 = -T22 (A21 T11): products of operands in two parts within a warp (mma.sync: a warp's first product comes out as
+// the second's operand lies, so nothing is exchanged; a tcgen05 product of 16 or 32 rows would use a quarter of its lanes and
+// take a round trip through tensor memory).
+// Made inside the pass that uses them, a chunk ahead of it, T and P cost no traffic, but their chain of some 900 instructions a
+// warp takes longer than a chunk's pass (7000 cycles against 4300), and 91 KiB of code of seven kinds of warps does not stay in the
+// instruction cache: 8 x 1024 tokens of 96 heads 378 us so.
 #include "kda_delta.cuh"
 #include "kda_layout.h"
 #include "kda_tma.h"
@@ -15,168 +25,275 @@ struct Maps {
 };
 
 struct Smem {
-  unsigned char tile[32768];  // [2 panels][64 rows of K, 64 of Q][64]; then T, its low part, P, its low part
-  float At[kC][kC];           // A transposed: At[j][i] = A_ij
+  union {
+    unsigned char kq[32768];      // [2 panels][64 rows of K, 64 of Q][64]
+    struct {
+      unsigned char T[2][8192];   // high, low part
+      unsigned char P[2][8192];
+    } o;
+  };
+  unsigned char A21[2][4096];     // high, low part, 32 rows of 128 bytes
+  float At[2][2][16][16];         // A's 16 x 16 blocks on the diagonal, transposed
   DeltaAux aux;
+  float ones[4];
   unsigned long long full, done;
   uint32_t tmem;
 };
 constexpr int kSmemBytes = (int)sizeof(Smem) + 1024;
 
-// One CTA a (chunk, head): 64 rows of K and of Q, scores [K; Q] K^T (M = 128, N = 64) on the tensor cores, then A and P
-// element by element, and T by forward substitution, a column a thread: t_l -= A_li t_i for l > i once t_i is known, so
-// that the products of a step are independent. All in FP32: powers of A (1 - A + A^2 ...) would lose
-// everything where keys are alike.
+// 2^x, half a step off where it is near 1: products of up to 63 of them are taken.
+__device__ __forceinline__ float token_decay(float x) {
+  return fabsf(x) < 0.5f ? 1.f + expm1f(x * 0.6931471805599453f) : fast_exp2(x);
+}
+
+// acc += A B for a 16 x 8 tile over 16 inner values, BF16 operands each in two parts (low x low left out).
+__device__ __forceinline__ void mma_split(float* c, const uint32_t* ah, const uint32_t* al, const uint32_t* bh, const uint32_t* bl) {
+  auto mma = [&](const uint32_t* a, const uint32_t* b) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+  };
+  mma(ah, bl);
+  mma(al, bh);
+  mma(ah, bh);
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t saddr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(saddr) : "memory");
+}
+// Byte of (row, 16-byte piece) in a tile of 128-byte rows, swizzled.
+__device__ __forceinline__ uint32_t piece(int row, int c) { return row * 128 + ((c ^ (row & 7)) << 4); }
+
+// kTrain: P's low part too.
 template <bool kTrain>
-__global__ void __launch_bounds__(128) kda_delta_prep_kernel(const __grid_constant__ Maps maps, const DeltaProblem P,
-                                                             unsigned char* packets) {
+__global__ void __launch_bounds__(128, 6) kda_delta_prep_kernel(const __grid_constant__ Maps maps, const DeltaProblem P,
+                                                                unsigned char* packets) {
   extern __shared__ unsigned char raw_smem[];
   Smem& sm = *reinterpret_cast<Smem*>(raw_smem + ((1024 - (tc::smem_u32(raw_smem) & 1023)) & 1023));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int64_t slot = blockIdx.x / P.Hv;
   const int h = (int)(blockIdx.x - slot * P.Hv);
-  int64_t lo = 0, hi = P.N;  // the last sequence whose first place is not behind this one
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) / 2;
-    if (delta_slot(decay_span(P, mid).t0, mid) <= slot) lo = mid;
-    else hi = mid;
-  }
-  const DecaySpan sp = decay_span(P, lo);
-  const int64_t c = slot - delta_slot(sp.t0, lo);
-  if (c < 0 || c * kC >= sp.len) return;  // a place without a chunk
-  const int64_t t0 = sp.t0 + c * kC;
-  const int nt = (int)(sp.len - c * kC < kC ? sp.len - c * kC : kC);
+  const DeltaChunk ch = delta_chunk(P, slot);
+  if (ch.nt <= 0) return;  // a place without a chunk
   const uint32_t full = tc::smem_u32(&sm.full), done = tc::smem_u32(&sm.done);
-  if (warp == 0) tc::tmem_alloc(tc::smem_u32(&sm.tmem), 64);
+  if (w == 1) tc::tmem_alloc(tc::smem_u32(&sm.tmem), 64);
   if (tid == 0) {
     tc::mbar_init(full, 1);
     tc::mbar_init(done, 1);
-  }
-  tc::fence_before();
-  __syncthreads();
-  tc::fence_after();
-  if (tid == 0) {
     tc::mbar_arrive_expect_tx(full, 32768);
-    const int hq = h / P.r;
+    const uint32_t kq = tc::smem_u32(sm.kq);
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      tc::tma_load3(tc::smem_u32(sm.tile) + p * 16384, &maps.k, 64 * p, hq, (int)t0, full);
-      tc::tma_load3(tc::smem_u32(sm.tile) + p * 16384 + 8192, &maps.q, 64 * p, hq, (int)t0, full);
+      tc::tma_load3(kq + p * 16384, &maps.k, 64 * p, h / P.r, (int)ch.t0, full);
+      tc::tma_load3(kq + p * 16384 + 8192, &maps.q, 64 * p, h / P.r, (int)ch.t0, full);
     }
   }
-  if (warp == 1) {
-    // Two tokens a lane. The sums are exact in 64-bit fixed point (units of 2^-40): D_ij is a difference of
+  if (tid < 4) sm.ones[tid] = 1.f;
+  const int nt = ch.nt;
+  if (w == 0) {
+    // Decays, two tokens a lane. The sums are exact in 64-bit fixed point (units of 2^-40): factors are of differences of
     // sums that can be thousands of times larger.
-    long long f[2];
-    float be[2];
+    float x[2], be[2];
     bool bad = false;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int j = 2 * lane + e;
-      float x = 0.f;
-      be[e] = 0.f;
+      x[e] = be[e] = 0.f;
       if (j < nt) {
-        if (P.g) x = decay_log2(__bfloat162float(reinterpret_cast<const __nv_bfloat16*>(P.g)[(t0 + j) * P.Hv + h]));
-        be[e] = __bfloat162float(P.beta[(t0 + j) * P.Hv + h]);
+        if (P.g) x[e] = decay_log2(__bfloat162float(reinterpret_cast<const __nv_bfloat16*>(P.g)[(ch.t0 + j) * P.Hv + h]));
+        be[e] = __bfloat162float(P.beta[(ch.t0 + j) * P.Hv + h]);
       }
-      if (!(x < 1048576.f)) { bad = true; x = 0.f; }  // NaN or infinite: so is the chunk
-      f[e] = __float2ll_rn(x * 1099511627776.f);
+      if (!(x[e] < 1048576.f)) { bad = true; x[e] = 0.f; }  // NaN or infinite: so is the chunk
     }
     bad = __any_sync(0xffffffffu, bad);
-    long long sum = f[0] + f[1];
+    const long long f1 = __float2ll_rn(x[1] * 1099511627776.f);
+    long long sum = __float2ll_rn(x[0] * 1099511627776.f) + f1;
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, sum, k);
       if (lane >= k) sum += y;
     }
-    const long long whole = __shfl_sync(0xffffffffu, sum, 31);
+    const long long whole = __shfl_sync(0xffffffffu, sum, 31), b0 = sum - f1;
     const float nan = bad ? __int_as_float(0x7fc00000) : 0.f;
-    auto number = [&](long long x) { return (float)x * 9.094947017729282e-13f + nan; };
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int j = 2 * lane + e;
-      const long long b = e ? sum : sum - f[1];
-      sm.aux.eb[j] = fast_exp2(number(b));
-      sm.aux.w[j] = fast_exp2(number(whole - b));
-      sm.aux.beta[j] = be[e];
-      sm.aux.bh[j] = (float)(b >> 32) * 0.00390625f + nan;
-      sm.aux.bl[j] = (float)(b & 0xffffffffll) * 9.094947017729282e-13f;
-    }
+    auto number = [&](long long y) { return (float)y * 9.094947017729282e-13f + nan; };
+    auto two = [&](float* to, float y0, float y1) { *reinterpret_cast<float2*>(to + 2 * lane) = make_float2(y0, y1); };
+    two(sm.aux.eb, fast_exp2(number(b0)), fast_exp2(number(sum)));
+    two(sm.aux.w, fast_exp2(number(whole - b0)), fast_exp2(number(whole - sum)));
+    two(sm.aux.beta, be[0], be[1]);
+    two(sm.aux.a, token_decay(x[0]) + nan, token_decay(x[1]) + nan);
+    two(sm.aux.b, number(b0), number(sum));
     if (lane == 0) sm.aux.whole = number(whole);
   }
-  bool ok = tc::mbar_wait_lanes(full, 0);
-  if (warp == 0 && ok && tc::elect_one()) {
-    const uint64_t d = tc::kmajor(tc::smem_u32(sm.tile));
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  bool ok = true;
+  if (w == 1) {
+    ok = tc::mbar_wait_lanes(full, 0);
+    if (ok && tc::elect_one()) {
+      const uint64_t d = tc::kmajor(tc::smem_u32(sm.kq));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t off = (i >> 2) * (16384 >> 4) + (i & 3) * 2;
-      tc::mma_bf16_ss(sm.tmem, d + off, d + off, tc::idesc_bf16(128, 64, false, false), i > 0);
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t off = (i >> 2) * (16384 >> 4) + (i & 3) * 2;
+        tc::mma_bf16_ss(sm.tmem, d + off, d + off, tc::idesc_bf16(128, 64, false, false), i > 0);
+      }
+      tc::mma_commit(done);
     }
-    tc::mma_commit(done);
+    __syncwarp();
   }
-  __syncwarp();
   if (ok) ok = tc::mbar_wait_lanes(done, 0);
   tc::fence_after();
-  __syncthreads();  // (the decays are there)
-  const int i = tid & 63;
-  const bool keys = warp < 2;
-  const float bh = sm.aux.bh[i], bl = sm.aux.bl[i];
-  const uint32_t tl = sm.tmem + ((uint32_t)(32 * warp) << 16);
-  unsigned char* out = sm.tile + (keys ? 0 : 16384);
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {
+  const int hw = w & 1, i = 32 * hw + lane;  // this thread's row, of K K^T (w < 2) or Q K^T
+  const bool keys = w < 2;
+  const uint32_t tl = sm.tmem + ((uint32_t)(32 * w) << 16);
+  unsigned char* T = sm.o.T[0];
+  unsigned char* mine = keys ? T : sm.o.P[0];
+  // sixteen columns at a time, from the last: D_ij = D_i,j+1 a_j+1 from D_ii = 1
+  float d = 0.f, a1 = 0.f;
+#pragma unroll 1
+  for (int m = 2 * hw + 1; m >= 0; --m) {
     float r[16];
     tc::tmem_ld16(tl + 16 * m, r);
-    uint32_t ph[8], pl[8];
+    const int last = i < nt ? i - 16 * m - (keys ? 1 : 0) : -1;  // the columns up to it count
 #pragma unroll
-    for (int e = 0; e < 16; e += 2) {
-      float2 y;
+    for (int q = 3; q >= 0; --q) {
+      const float4 a4 = *reinterpret_cast<const float4*>(&sm.aux.a[16 * m + 4 * q]);
+      const float4 b4 = *reinterpret_cast<const float4*>(keys ? &sm.aux.beta[16 * m + 4 * q] : sm.ones);
+      const float av[4] = {a4.x, a4.y, a4.z, a4.w}, bv[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int j = 16 * m + e + x;
-        const float d = fast_exp2((bh - sm.aux.bh[j]) + (bl - sm.aux.bl[j])) * (keys ? sm.aux.beta[j] : P.scale);
+      for (int e = 3; e >= 0; --e) {
+        const int j = 4 * q + e;
+        d = 16 * m + j == i ? 1.f : d * a1;
+        a1 = av[e];
         // (selected, not multiplied: rows past the end may hold anything)
-        const float v = (keys ? j < i : j <= i) && i < nt ? d * r[e + x] : 0.f;
-        if (x) y.y = v;
-        else y.x = v;
-        if (keys) sm.At[j][i] = v;
+        r[j] = j <= last ? r[j] * (bv[e] * d) : 0.f;
       }
-      if (!keys) split2(y, ph[e / 2], pl[e / 2]);
     }
-    if (!keys) {
+    if (keys && (i >> 4) == m) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint32_t at = i * 128 + (((2 * m + x) ^ (i & 7)) << 4);
-        *reinterpret_cast<uint4*>(out + at) = make_uint4(ph[4 * x], ph[4 * x + 1], ph[4 * x + 2], ph[4 * x + 3]);
-        if (kTrain) *reinterpret_cast<uint4*>(out + 8192 + at) = make_uint4(pl[4 * x], pl[4 * x + 1], pl[4 * x + 2], pl[4 * x + 3]);
+      for (int j = 0; j < 16; ++j) sm.At[w][m & 1][j][lane & 15] = r[j];
+    } else {  // (above the diagonal: zeros)
+      uint32_t hi[8], lo[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) split2(make_float2(r[2 * e], r[2 * e + 1]), hi[e], lo[e]);
+      const bool cross = keys && m < 2 * hw;  // a part of A21
+      unsigned char* to = cross ? sm.A21[0] : mine;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t at = piece(cross ? lane : i, 2 * m + q);
+        *reinterpret_cast<uint4*>(to + at) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+        if (keys || kTrain)
+          *reinterpret_cast<uint4*>(to + (cross ? 4096 : 8192) + at) = make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
       }
     }
   }
+  if (!hw)
+#pragma unroll
+    for (int q = 4; q < 8; ++q) {
+      *reinterpret_cast<uint4*>(mine + piece(i, q)) = make_uint4(0u, 0u, 0u, 0u);
+      if (keys || kTrain) *reinterpret_cast<uint4*>(mine + 8192 + piece(i, q)) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  const uint32_t Ts = tc::smem_u32(T);
+  const int r8 = lane & 7, q1 = (lane >> 3) & 1, q2 = lane >> 4;  // row and place of the 8 x 8 matrix whose address this lane gives
   if (keys) {
-    asm volatile("barrier.cta.sync 1, 64;" ::: "memory");
-    float2 t[kC / 2];
+    // the blocks on the diagonal, a column a thread: t_l -= A_lj t_j for l > j once t_j is known
+    __syncwarp();
+    const int blk = lane >> 4, col = lane & 15;
+    float2 t[8];
 #pragma unroll
-    for (int l = 0; l < kC / 2; ++l) t[l] = make_float2(2 * l == i ? 1.f : 0.f, 2 * l + 1 == i ? 1.f : 0.f);
+    for (int l = 0; l < 8; ++l) t[l] = make_float2(2 * l == col ? 1.f : 0.f, 2 * l + 1 == col ? 1.f : 0.f);
 #pragma unroll
-    for (int j = 0; j < kC - 1; ++j) {
+    for (int j = 0; j < 15; ++j) {
       const float tj = -((j & 1) ? t[j / 2].y : t[j / 2].x);
 #pragma unroll
-      for (int l = (j + 1) / 4; l < kC / 4; ++l) {  // rows 4 l .. 4 l + 3 (A is zero on the diagonal and above)
-        const float4 a = *reinterpret_cast<const float4*>(&sm.At[j][4 * l]);
-        if (4 * l + 1 > j) t[2 * l] = tc::fma2(make_float2(a.x, a.y), make_float2(tj, tj), t[2 * l]);
-        t[2 * l + 1] = tc::fma2(make_float2(a.z, a.w), make_float2(tj, tj), t[2 * l + 1]);
+      for (int l = (j + 1) / 4; l < 4; ++l) {  // rows 4 l .. 4 l + 3 (A is zero on the diagonal and above)
+        const float4 y = *reinterpret_cast<const float4*>(&sm.At[w][blk][j][4 * l]);
+        if (4 * l + 1 > j) t[2 * l] = tc::fma2(make_float2(y.x, y.y), make_float2(tj, tj), t[2 * l]);
+        t[2 * l + 1] = tc::fma2(make_float2(y.z, y.w), make_float2(tj, tj), t[2 * l + 1]);
       }
     }
 #pragma unroll
-    for (int l = 0; l < kC / 2; ++l) {
-      uint32_t th, tl2;
-      split2(t[l], th, tl2);
+    for (int l = 0; l < 8; ++l) {
+      uint32_t th, tlo;
+      split2(t[l], th, tlo);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int row = 2 * l + e;
-        const uint32_t at = row * 128 + (((i >> 3) ^ (row & 7)) << 4) + 2 * (i & 7);
-        *reinterpret_cast<uint16_t*>(sm.tile + at) = (uint16_t)(e ? th >> 16 : th & 0xffffu);
-        *reinterpret_cast<uint16_t*>(sm.tile + 8192 + at) = (uint16_t)(e ? tl2 >> 16 : tl2 & 0xffffu);
+        const uint32_t to = piece(32 * w + 16 * blk + 2 * l + e, i >> 3) + 2 * (i & 7);
+        *reinterpret_cast<uint16_t*>(T + to) = (uint16_t)(e ? th >> 16 : th & 0xffffu);
+        *reinterpret_cast<uint16_t*>(T + 8192 + to) = (uint16_t)(e ? tlo >> 16 : tlo & 0xffffu);
+      }
+    }
+    __syncwarp();
+    // joined: Y^T = T00^T A10^T (as its operands lie, Y is the next product's operand), T10 = -T11 Y
+    uint32_t ah[4], al[4], bh[4], bl[4];
+    const uint32_t t00 = Ts + piece(32 * w + 8 * q2 + r8, 4 * w + q1), a10 = Ts + piece(32 * w + 16 + 8 * q2 + r8, 4 * w + q1);
+    const uint32_t t11 = Ts + piece(32 * w + 16 + 8 * q1 + r8, 4 * w + 2 + q2);
+    tc::ldmatrix4_trans(t00, ah);
+    tc::ldmatrix4_trans(t00 + 8192, al);
+    ldmatrix4(a10, bh);
+    ldmatrix4(a10 + 8192, bl);
+    float y[2][4] = {};
+    mma_split(y[0], ah, al, bh, bl);
+    mma_split(y[1], ah, al, bh + 2, bl + 2);
+    ldmatrix4(t11, ah);
+    ldmatrix4(t11 + 8192, al);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      split2(make_float2(y[0][2 * n], y[0][2 * n + 1]), bh[0], bl[0]);
+      split2(make_float2(y[1][2 * n], y[1][2 * n + 1]), bh[1], bl[1]);
+      float z[4] = {};
+      mma_split(z, ah, al, bh, bl);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t th, tlo;
+        split2(make_float2(-z[2 * k], -z[2 * k + 1]), th, tlo);
+        const uint32_t to = piece(32 * w + 16 + 8 * k + (lane >> 2), 4 * w + n) + 4 * (lane & 3);
+        *reinterpret_cast<uint32_t*>(T + to) = th;
+        *reinterpret_cast<uint32_t*>(T + 8192 + to) = tlo;
+      }
+    }
+  }
+  __syncthreads();
+  {
+    // columns 8 w .. of T21, as above over 32 inner values
+    const uint32_t A21 = tc::smem_u32(sm.A21[0]);
+    const int half = w >> 1, n0 = w & 1;  // (sixteen columns make the operand; this warp's eight of them are used)
+    float y[4][4] = {};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t ah[4], al[4];
+      const uint32_t t11 = Ts + piece(16 * k + 8 * q2 + r8, 2 * half + q1);
+      tc::ldmatrix4_trans(t11, ah);
+      tc::ldmatrix4_trans(t11 + 8192, al);
+#pragma unroll
+      for (int n = 0; n < 4; n += 2) {
+        uint32_t bh[4], bl[4];
+        const uint32_t a21 = A21 + piece(8 * n + 8 * q2 + r8, 2 * k + q1);
+        ldmatrix4(a21, bh);
+        ldmatrix4(a21 + 4096, bl);
+        mma_split(y[n], ah, al, bh, bl);
+        mma_split(y[n + 1], ah, al, bh + 2, bl + 2);
+      }
+    }
+    uint32_t bh[4], bl[4];  // inner values in steps of 8
+#pragma unroll
+    for (int k = 0; k < 4; ++k) split2(make_float2(n0 ? y[k][2] : y[k][0], n0 ? y[k][3] : y[k][1]), bh[k], bl[k]);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      float z[4] = {};
+#pragma unroll
+      for (int k = 0; k <= m; ++k) {
+        uint32_t ah[4], al[4];
+        const uint32_t t22 = Ts + piece(32 + 16 * m + 8 * q1 + r8, 4 + 2 * k + q2);
+        ldmatrix4(t22, ah);
+        ldmatrix4(t22 + 8192, al);
+        mma_split(z, ah, al, bh + 2 * k, bl + 2 * k);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t th, tlo;
+        split2(make_float2(-z[2 * k], -z[2 * k + 1]), th, tlo);
+        const uint32_t to = piece(32 + 16 * m + 8 * k + (lane >> 2), w) + 4 * (lane & 3);
+        *reinterpret_cast<uint32_t*>(T + to) = th;
+        *reinterpret_cast<uint32_t*>(T + 8192 + to) = tlo;
       }
     }
   }
@@ -185,10 +302,9 @@ __global__ void __launch_bounds__(128) kda_delta_prep_kernel(const __grid_consta
   __syncthreads();
   if (tid == 0) {
     unsigned char* dst = packets + (slot * P.Hv + h) * (int64_t)(kTrain ? kPkTrain : kPkInfer);
-    const uint32_t src = tc::smem_u32(sm.tile);
-    tc::bulk_s2g(dst, src, kPkAux);
+    tc::bulk_s2g(dst, Ts, kPkAux);
     tc::bulk_s2g(dst + kPkAux, tc::smem_u32(&sm.aux), sizeof(DeltaAux));
-    if (kTrain) tc::bulk_s2g(dst + kPkPlo, src + 24576, 8192);
+    if (kTrain) tc::bulk_s2g(dst + kPkPlo, Ts + 24576, 8192);
     tc::bulk_commit();
     tc::bulk_wait_read();
   }
@@ -196,7 +312,7 @@ __global__ void __launch_bounds__(128) kda_delta_prep_kernel(const __grid_consta
     if (lane == 0) atomicOr(P.status, 1);
     tc::mbar_wait_lanes(full, 0, 1u << 16);
   }
-  if (warp == 0) {
+  if (w == 1) {
     tc::fence_after();
     tc::tmem_dealloc(sm.tmem, 64);
   }
@@ -215,7 +331,7 @@ cudaError_t launch(const Maps& maps, const DeltaProblem& P, void* ws, cudaStream
 
 DeltaWs delta_workspace(int64_t slots, int64_t Hv, bool training) {
   const size_t n = (size_t)slots * Hv;
-  DeltaWs w{0, 0, 0, 0, 0};
+  DeltaWs w{};
   w.states = ctx_align_up(n * (training ? kPkTrain : kPkInfer));
   w.u = w.states + (training ? n * kStateTile : 0);
   w.adjoints = w.u + (training ? n * kUTile : 0);
