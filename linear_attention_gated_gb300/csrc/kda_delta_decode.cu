@@ -5,7 +5,9 @@
 // The step reads and writes each state once and does 10 flops per state value: HBM bandwidth bounds it (64 KiB there
 // and 64 KiB back per FP32 state, against 1 KiB of vectors). The 128 rows of a state are independent, so a CTA takes
 // kRows of them; a half-warp owns a row, 8 keys a lane, and all of a thread's rows are in flight before it touches the
-// token's vectors. A row's two sums over the keys follow one another: the thread's rows hide each other's.
+// token's vectors. Both sums over the keys are taken of the old state, S k and S q, and o = s (e^g S q + beta u k . q): they do not
+// follow one another. The sums of all of a half-warp's rows are exchanged together, each step halving what a lane holds:
+// 15 and 8 shuffles for eight rows, where sums row by row take 64.
 #include "kda_decay_host.h"
 #include "kda_delta.cuh"
 
@@ -37,34 +39,61 @@ __global__ void __launch_bounds__(kThreads) kda_delta_decode_kernel(const DeltaP
   StateVec<S> raw[kPasses];
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) raw[p].load(s + p * kPerPass * kDim);
-  float q[8], k[8], v[kPasses];
+  float q[8], k[8];
   const int hq = h / P.r;
   load_bf16x8(P.q + n * P.qt + hq * P.qh + 8 * hl, q);
   load_bf16x8(P.k + n * P.kt + hq * P.kh + 8 * hl, k);
-  const __nv_bfloat16* vr = P.v + n * P.vt + h * P.vh + row0;
-#pragma unroll
-  for (int p = 0; p < kPasses; ++p) v[p] = __bfloat162float(vr[p * kPerPass]);
+  // after the exchange lane hl holds number hl of 16 (S k of its 8 rows, then S q), or hl / 2 of 8
+  constexpr int kSums = 2 * kPasses;
+  static_assert(kSums == 16 || kSums == 8, "sums of a half-warp");
+  const int mine = kSums == 16 ? hl & 7 : (hl >> 1) & 3, row = mine * kPerPass;  // its row
+  const float v = __bfloat162float(P.v[n * P.vt + h * P.vh + row0 + row]);
   const float d = P.g ? exp2f(decay_log2(decay_g(P, n, h))) : 1.f;
   const float beta = __bfloat162float(P.beta[n * P.Hv + h]);
-  __nv_bfloat16* out = o + (n * P.Hv + h) * kDim + row0;
+  float kq = 0.f, sum[kSums];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) kq = fmaf(k[e], q[e], kq);
+  kq = row16_sum(kq);
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     float x[8], z = 0.f, y = 0.f;
     raw[p].get(x);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      x[e] *= d;
       z = fmaf(x[e], k[e], z);
-    }
-    const float u = beta * (v[p] - row16_sum(z));
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] = fmaf(u, k[e], x[e]);
       y = fmaf(x[e], q[e], y);
     }
+    sum[p] = z;
+    sum[kPasses + p] = y;
+  }
+  int m = kSums;
+#pragma unroll
+  for (int o = 8; o; o >>= 1) {
+    if (m > 1) {
+      m /= 2;
+      const bool up = hl & o;
+#pragma unroll
+      for (int i = 0; i < kSums / 2; ++i)
+        if (i < m) {
+          const float got = __shfl_xor_sync(0xffffffffu, up ? sum[i] : sum[i + m], o);
+          sum[i] = (up ? sum[i + m] : sum[i]) + got;
+        }
+    } else {
+      sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
+    }
+  }
+  const float own = d * sum[0];
+  const float bu = beta * (v - own);  // (of the lanes that hold S k)
+  const float there = __shfl_xor_sync(0xffffffffu, bu, 8);
+  if ((hl & 8) && (kSums == 16 || !(hl & 1))) o[(n * P.Hv + h) * kDim + row0 + row] = __float2bfloat16_rn(P.scale * fmaf(there, kq, own));
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const float u = __shfl_sync(0xffffffffu, bu, (tid & 16) | (kSums == 16 ? p : 2 * p));
+    float x[8];
+    raw[p].get(x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = fmaf(u, k[e], d * x[e]);
     StateVec<S>::store(s + p * kPerPass * kDim, x);
-    y = row16_sum(y);
-    if (hl == 0) out[p * kPerPass] = __float2bfloat16_rn(P.scale * y);
   }
 }
 

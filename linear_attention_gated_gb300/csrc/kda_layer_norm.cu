@@ -4,11 +4,14 @@
 //
 // Bandwidth bounds both: x is read and y written, 16 flops a value at most. kG threads share a row and keep their part of it
 // in registers, so it is read once, and the deviations are taken from the mean itself (a difference of squares
-// would cancel); rows are handed out so that a CTA keeps the same columns: the weights stay in registers for all of its rows,
-// as do the sums of dw and db (a row's share of FP32 weights is twice its BF16 values).
-// The CTAs' sums are joined by a second small kernel in a fixed order.
+// would cancel). Rows are handed out so that a thread keeps the same columns: the weights stay in registers for all of its rows
+// (a row's share of FP32 weights is twice its BF16 values), as do the sums of dw and db. Rows are on their way in a
+// ring of asynchronous copies, each thread's part to its own place: nobody waits for anybody but in the rows' sums. Forward, the
+// sum of the next row and the squares of this one are joined in one exchange.
+// The CTAs' sums of dw and db are joined by a second small kernel in a fixed order.
 #include "../../include/kda.h"
 #include "kda_decay_host.h"
+#include "tc.cuh"
 
 #include <cuda_fp16.h>
 
@@ -44,45 +47,82 @@ __device__ __forceinline__ T from_float(float x) {
   else return __float2bfloat16_rn(x);
 }
 
-// A thread's part of a row: kPer pieces of kE values. Aligned rows: a piece is 16 bytes, the pieces of a row's threads lie
-// side by side; else a thread's values lie kG apart, one load each.
+__device__ __forceinline__ float2 pair_of(uint32_t x, const __nv_bfloat16*) { return unpack2(x); }
+__device__ __forceinline__ float2 pair_of(uint32_t x, const __half*) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
+__device__ __forceinline__ uint32_t of_pair(float2 x, const __nv_bfloat16*) { return pack2(x); }
+__device__ __forceinline__ uint32_t of_pair(float2 x, const __half*) {
+  const __half2 y = __floats2half2_rn(x.x, x.y);
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// A thread's part of a row: kPer pieces of 16 bytes, as pairs of values. Aligned rows: the pieces of a row's threads lie side by
+// side and come through a ring of asynchronous copies; else a thread's values lie kG apart and are loaded one by one.
 template <typename T, bool kAligned, int kG, int kPer>
 struct Part {
-  static constexpr int kE = 16 / (int)sizeof(T);
-  static __device__ __forceinline__ int column(int i, int e, int at) { return kAligned ? (i * kG + at) * kE + e : (i * kE + e) * kG + at; }
-  union Piece {
-    uint4 v;
-    T t[kE];
-    __device__ __forceinline__ Piece() {}
-  };
-  Piece p[kPer];
-  __device__ __forceinline__ void load(const T* row, int at, int D, bool there) {
+  static constexpr int kE = 16 / (int)sizeof(T), kPairs = kPer * kE / 2;
+  static constexpr int kStages = kPer > 3 ? 3 : 4, kRingBytes = kAligned ? kStages * kPer * kThreads * 16 : 0;
+  uint32_t r[kPer * 4];
+  static __device__ __forceinline__ int column(int pair, int e, int at) {
+    return kAligned ? (2 * pair / kE * kG + at) * kE + 2 * pair % kE + e : (2 * pair + e) * kG + at;
+  }
+  static __device__ __forceinline__ uint4* place(uint4* ring, int stage, int i) { return ring + (stage * kPer + i) * kThreads + threadIdx.x; }
+  // (aligned) starts the copy of a row's part, zeros where there is none
+  static __device__ __forceinline__ void start(uint4* ring, int stage, const T* row, int at, int D, bool there) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      if constexpr (kAligned) {
-        const int c = column(i, 0, at);
-        p[i].v = there && c < D ? __ldcs(reinterpret_cast<const uint4*>(row + c)) : make_uint4(0u, 0u, 0u, 0u);
-      } else {
+      const int c = (i * kG + at) * kE;
+      const bool in = there && c < D;
+      tc::cp_async16(place(ring, stage, i), in ? row + c : row, in ? 16u : 0u);
+    }
+  }
+  __device__ __forceinline__ void take(uint4* ring, int stage) {
 #pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          const int c = column(i, e, at);
-          p[i].t[e] = there && c < D ? row[c] : from_float<T>(0.f);
-        }
+    for (int i = 0; i < kPer; ++i) *reinterpret_cast<uint4*>(r + 4 * i) = *place(ring, stage, i);
+  }
+  // (not aligned)
+  __device__ __forceinline__ void load(const T* row, int at, int D, bool there) {
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) {
+      const int c0 = column(p, 0, at), c1 = column(p, 1, at);
+      const T x0 = there && c0 < D ? row[c0] : from_float<T>(0.f), x1 = there && c1 < D ? row[c1] : from_float<T>(0.f);
+      if constexpr (sizeof(T) == 4) {
+        r[2 * p] = __float_as_uint(x0);
+        r[2 * p + 1] = __float_as_uint(x1);
+      } else {
+        r[p] = (uint32_t) * reinterpret_cast<const uint16_t*>(&x0) | (uint32_t) * reinterpret_cast<const uint16_t*>(&x1) << 16;
       }
     }
   }
-  __device__ __forceinline__ float get(int i, int e) const { return to_float(p[i].t[e]); }
-  __device__ __forceinline__ void set(int i, int e, float x) { p[i].t[e] = from_float<T>(x); }
+  __device__ __forceinline__ float2 get(int p) const {
+    if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(r[2 * p]), __uint_as_float(r[2 * p + 1]));
+    else return pair_of(r[p], (const T*)nullptr);
+  }
+  __device__ __forceinline__ void set(int p, float2 x) {
+    if constexpr (sizeof(T) == 4) {
+      r[2 * p] = __float_as_uint(x.x);
+      r[2 * p + 1] = __float_as_uint(x.y);
+    } else {
+      r[p] = of_pair(x, (const T*)nullptr);
+    }
+  }
   __device__ __forceinline__ void store(T* row, int at, int D) const {
+    if constexpr (kAligned) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if constexpr (kAligned) {
-        const int c = column(i, 0, at);
-        if (c < D) *reinterpret_cast<uint4*>(row + c) = p[i].v;
-      } else {
+      for (int i = 0; i < kPer; ++i) {
+        const int c = (i * kG + at) * kE;
+        if (c < D) *reinterpret_cast<uint4*>(row + c) = *reinterpret_cast<const uint4*>(r + 4 * i);
+      }
+    } else {
 #pragma unroll
-        for (int e = 0; e < kE; ++e)
-          if (column(i, e, at) < D) row[column(i, e, at)] = p[i].t[e];
+      for (int p = 0; p < kPairs; ++p) {
+        const int c0 = column(p, 0, at), c1 = column(p, 1, at);
+        if constexpr (sizeof(T) == 4) {
+          if (c0 < D) row[c0] = __uint_as_float(r[2 * p]);
+          if (c1 < D) row[c1] = __uint_as_float(r[2 * p + 1]);
+        } else {
+          if (c0 < D) *reinterpret_cast<uint16_t*>(row + c0) = (uint16_t)r[p];
+          if (c1 < D) *reinterpret_cast<uint16_t*>(row + c1) = (uint16_t)(r[p] >> 16);
+        }
       }
     }
   }
@@ -114,134 +154,192 @@ __device__ __forceinline__ void row_sums(float (&x)[kN], float* buf, int turn) {
   }
 }
 
+// FP32 vectors' values of this thread's columns, `none` where there is no vector.
+template <typename P, int kPairs>
+__device__ __forceinline__ void load_vector(float2 (&to)[kPairs], const float* v, float none, int at, int D) {
+#pragma unroll
+  for (int p = 0; p < kPairs; ++p) {
+    const int c0 = P::column(p, 0, at), c1 = P::column(p, 1, at);
+    to[p] = make_float2(v && c0 < D ? v[c0] : none, v && c1 < D ? v[c1] : none);
+  }
+}
+
 template <typename T, bool kAligned, int kG, int kPer>
 __global__ void __launch_bounds__(kThreads) kda_layer_norm_fwd_kernel(const NormArgs a) {
   using P = Part<T, kAligned, kG, kPer>;
-  constexpr int kE = P::kE, kRows = kThreads / kG;
-  __shared__ float buf[2 * (kThreads / 32)];
+  constexpr int kPairs = P::kPairs, kRows = kThreads / kG, kAhead = P::kStages - 1;
+  extern __shared__ uint4 ring[];
+  __shared__ float buf[4 * (kThreads / 32)];
   const int at = threadIdx.x % kG, group = threadIdx.x / kG, D = a.D;
   const T* x = reinterpret_cast<const T*>(a.x);
-  float w[kPer][kE], b[kPer][kE];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i)
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      const int c = P::column(i, e, at);
-      w[i][e] = a.w && c < D ? a.w[c] : 1.f;
-      b[i][e] = a.b && c < D ? a.b[c] : 0.f;
+  const int64_t first = (int64_t)blockIdx.x * kRows + group, step = (int64_t)gridDim.x * kRows;
+  // row k of this thread's group
+  auto start = [&](int64_t k) {
+    const int64_t row = first + k * step;
+    P::start(ring, (int)(k % P::kStages), x + (row < a.rows ? row : 0) * a.xs, at, D, row < a.rows);
+    tc::cp_async_commit();
+  };
+  auto fetch = [&](P& v, int64_t k) {
+    const int64_t row = first + k * step;
+    if constexpr (kAligned) {
+      tc::cp_async_wait<kAhead - 1>();
+      v.take(ring, (int)(k % P::kStages));
+      start(k + kAhead);  // (to the place that was read last time)
+    } else {
+      v.load(x + (row < a.rows ? row : 0) * a.xs, at, D, row < a.rows);
     }
+  };
+  if constexpr (kAligned)
+    for (int k = 0; k < kAhead; ++k) start(k);
+  float2 w[kPairs], b[kPairs];
+  load_vector<P>(w, a.w, 1.f, at, D);
+  load_vector<P>(b, a.b, 0.f, at, D);
   const float inv = 1.f / (float)D;
-  P next;
-  int64_t row = (int64_t)blockIdx.x * kRows + group;
-  next.load(x + row * a.xs, at, D, row < a.rows);
-  for (; row - group < a.rows; row += (int64_t)gridDim.x * kRows) {
-    P v = next;
-    const int64_t after = row + (int64_t)gridDim.x * kRows;
-    next.load(x + after * a.xs, at, D, after < a.rows);
-    float s[1] = {0.f};
+  auto sum_of = [&](const P& v) {
+    float2 s = make_float2(0.f, 0.f), t = s;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
+    for (int p = 0; p < kPairs; p += 2) {
+      s = tc::add2(s, v.get(p));
+      if (p + 1 < kPairs) t = tc::add2(t, v.get(p + 1));
+    }
+    s = tc::add2(s, t);
+    return s.x + s.y;
+  };
+  P v;
+  fetch(v, 0);
+  float sums[1] = {sum_of(v)};
+  row_sums<kG, 1>(sums, buf, 0);
+  float mean = sums[0] * inv;
+  int turn = 1;
+  for (int64_t k = 0; first - group + k * step < a.rows; ++k, turn ^= 1) {
+    const int64_t row = first + k * step;
+    P next;
+    fetch(next, k + 1);
+    const float2 m2 = make_float2(-mean, -mean);
+    float2 q = make_float2(0.f, 0.f), t = q;
 #pragma unroll
-      for (int e = 0; e < kE; ++e) s[0] += v.get(i, e);
-    row_sums<kG, 1>(s, buf, 0);
-    const float mean = s[0] * inv;
-    s[0] = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        const float d = v.get(i, e) - mean;
-        if (P::column(i, e, at) < D) s[0] = fmaf(d, d, s[0]);
-      }
-    row_sums<kG, 1>(s, buf, 1);
+    for (int p = 0; p < kPairs; ++p) {
+      float2 d = tc::add2(v.get(p), m2);
+      if (P::column(p, 0, at) >= D) d.x = 0.f;
+      if (P::column(p, 1, at) >= D) d.y = 0.f;
+      if (p & 1) t = tc::fma2(d, d, t);
+      else q = tc::fma2(d, d, q);
+    }
+    q = tc::add2(q, t);
+    float s[2] = {q.x + q.y, sum_of(next)};
+    row_sums<kG, 2>(s, buf, turn);
     const float rstd = rsqrtf(fmaf(s[0], inv, a.eps));
     if (row < a.rows) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-#pragma unroll
-        for (int e = 0; e < kE; ++e) v.set(i, e, fmaf((v.get(i, e) - mean) * rstd, w[i][e], b[i][e]));
+      for (int p = 0; p < kPairs; ++p)
+        v.set(p, tc::fma2(tc::mul2(tc::add2(v.get(p), m2), make_float2(rstd, rstd)), w[p], b[p]));
       v.store(reinterpret_cast<T*>(a.out) + row * D, at, D);
       if (at == 0) {
         a.mean[row] = mean;
         a.rstd[row] = rstd;
       }
     }
+    v = next;
+    mean = s[1] * inv;
   }
+  if constexpr (kAligned) tc::cp_async_wait_all();
 }
 
 template <typename T, bool kAligned, int kG, int kPer>
 __global__ void __launch_bounds__(kThreads) kda_layer_norm_bwd_kernel(const NormArgs a) {
   using P = Part<T, kAligned, kG, kPer>;
-  constexpr int kE = P::kE, kRows = kThreads / kG;
+  constexpr int kPairs = P::kPairs, kRows = kThreads / kG, kAhead = P::kStages - 1;
+  extern __shared__ uint4 ring[];  // x, then dy; at last the groups' sums
   __shared__ float buf[4 * (kThreads / 32)];
-  __shared__ float join[kRows > 1 ? kThreads * kE : 1];
   const int at = threadIdx.x % kG, group = threadIdx.x / kG, D = a.D;
   const T* x = reinterpret_cast<const T*>(a.x);
   const T* dy = reinterpret_cast<const T*>(a.dy);
-  float w[kPer][kE], dw[kPer][kE], db[kPer][kE];
+  const int64_t first = (int64_t)blockIdx.x * kRows + group, step = (int64_t)gridDim.x * kRows;
+  constexpr int kHalf = P::kStages * kPer * kThreads;
+  auto start = [&](int64_t k) {
+    const int64_t row = first + k * step, in = row < a.rows ? row : 0;
+    P::start(ring, (int)(k % P::kStages), x + in * a.xs, at, D, row < a.rows);
+    P::start(ring + kHalf, (int)(k % P::kStages), dy + in * a.dys, at, D, row < a.rows);
+    tc::cp_async_commit();
+  };
+  if constexpr (kAligned)
+    for (int k = 0; k < kAhead; ++k) start(k);
+  float2 w[kPairs], dw[kPairs], db[kPairs];
+  load_vector<P>(w, a.w, 1.f, at, D);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      const int c = P::column(i, e, at);
-      w[i][e] = a.w && c < D ? a.w[c] : 1.f;
-      dw[i][e] = db[i][e] = 0.f;
-    }
+  for (int p = 0; p < kPairs; ++p) dw[p] = db[p] = make_float2(0.f, 0.f);
   const float inv = 1.f / (float)D;
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * kRows + group; row - group < a.rows; row += (int64_t)gridDim.x * kRows, turn ^= 1) {
-    const bool there = row < a.rows;
+  float mean = first < a.rows ? a.mean[first] : 0.f, rstd = first < a.rows ? a.rstd[first] : 0.f;
+  for (int64_t k = 0; first - group + k * step < a.rows; ++k, turn ^= 1) {
+    const int64_t row = first + k * step;
+    const bool there = row < a.rows, more = row + step < a.rows;
     P v, g;
-    v.load(x + row * a.xs, at, D, there);
-    g.load(dy + row * a.dys, at, D, there);
-    const float mean = there ? a.mean[row] : 0.f, rstd = there ? a.rstd[row] : 0.f;
-    float s[2] = {0.f, 0.f};
+    if constexpr (kAligned) {
+      tc::cp_async_wait<kAhead - 1>();
+      v.take(ring, (int)(k % P::kStages));
+      g.take(ring + kHalf, (int)(k % P::kStages));
+      start(k + kAhead);
+    } else {
+      v.load(x + (there ? row : 0) * a.xs, at, D, there);
+      g.load(dy + (there ? row : 0) * a.dys, at, D, there);
+    }
+    const float mean1 = more ? a.mean[row + step] : 0.f, rstd1 = more ? a.rstd[row + step] : 0.f;
+    const float2 m2 = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
+    float2 s0 = make_float2(0.f, 0.f), s1 = s0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {  // (columns past the end: dy is zero)
-        const float d = g.get(i, e), n = (v.get(i, e) - mean) * rstd, t = d * w[i][e];
-        s[0] += t;
-        s[1] = fmaf(t, n, s[1]);
-        dw[i][e] = fmaf(d, n, dw[i][e]);
-        db[i][e] += d;
-      }
+    for (int p = 0; p < kPairs; ++p) {  // (columns past the end: dy is zero)
+      const float2 d = g.get(p), n = tc::mul2(tc::add2(v.get(p), m2), r2), t = tc::mul2(d, w[p]);
+      s0 = tc::add2(s0, t);
+      s1 = tc::fma2(t, n, s1);
+      dw[p] = tc::fma2(d, n, dw[p]);
+      db[p] = tc::add2(db[p], d);
+    }
+    float s[2] = {s0.x + s0.y, s1.x + s1.y};
     row_sums<kG, 2>(s, buf, turn);
     if (there) {
-      const float mt = s[0] * inv, mn = s[1] * inv;
+      const float2 mt = make_float2(-s[0] * inv, -s[0] * inv), mn = make_float2(-s[1] * inv, -s[1] * inv);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          const float n = (v.get(i, e) - mean) * rstd, t = g.get(i, e) * w[i][e];
-          v.set(i, e, rstd * (t - mt - n * mn));
-        }
+      for (int p = 0; p < kPairs; ++p) {
+        const float2 n = tc::mul2(tc::add2(v.get(p), m2), r2);
+        v.set(p, tc::mul2(r2, tc::fma2(n, mn, tc::fma2(g.get(p), w[p], mt))));
+      }
       v.store(reinterpret_cast<T*>(a.out) + row * D, at, D);
     }
+    mean = mean1;
+    rstd = rstd1;
   }
+  if constexpr (kAligned) tc::cp_async_wait_all();
   if (!a.part) return;
   float* to = a.part + (int64_t)blockIdx.x * 2 * D;
+  if constexpr (kRows == 1) {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
+    for (int p = 0; p < kPairs; ++p)
 #pragma unroll
-    for (int x2 = 0; x2 < 2; ++x2) {
-      if constexpr (kRows > 1) {
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < kE; ++e) join[e * kThreads + threadIdx.x] = x2 ? db[i][e] : dw[i][e];
-        __syncthreads();
-      }
-      if (group == 0)
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          float s = x2 ? db[i][e] : dw[i][e];
-          if constexpr (kRows > 1) {
-            s = 0.f;
-            for (int r = 0; r < kRows; ++r) s += join[e * kThreads + r * kG + at];
-          }
-          const int c = P::column(i, e, at);
-          if (c < D) to[(int64_t)x2 * D + c] = s;
+      for (int e = 0; e < 2; ++e) {
+        const int c = P::column(p, e, at);
+        if (c < D) {
+          to[c] = e ? dw[p].y : dw[p].x;
+          to[D + c] = e ? db[p].y : db[p].x;
         }
+      }
+  } else {
+    // the groups' sums, a few columns at a time
+    float2* join = reinterpret_cast<float2*>(ring);
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) {
+      __syncthreads();
+      join[threadIdx.x] = dw[p];
+      join[kThreads + threadIdx.x] = db[p];
+      __syncthreads();
+      for (int i = threadIdx.x; i < 2 * kG; i += kThreads) {
+        const int k = i % kG, which = i / kG;
+        float2 s = make_float2(0.f, 0.f);
+        for (int r = 0; r < kRows; ++r) s = tc::add2(s, join[which * kThreads + r * kG + k]);
+        const int c0 = P::column(p, 0, k), c1 = P::column(p, 1, k);
+        if (c0 < D) to[(int64_t)which * D + c0] = s.x;
+        if (c1 < D) to[(int64_t)which * D + c1] = s.y;
+      }
     }
   }
 }
@@ -327,30 +425,41 @@ __global__ void __launch_bounds__(256) kda_layer_norm_join_kernel(const float* p
   }
 }
 
-constexpr int kParts = kSms;  // most CTAs of the backward: each leaves sums of its own
+constexpr int kParts = kSms;  // most CTAs: one an SM; each of the backward leaves sums of its own
 
 // Threads that share a row: the fewest (of 8, 32, 128, 256, 512) that keep it in 16 values each.
 template <typename T, bool kAligned, bool kBwd>
 cudaError_t launch_rows(const NormArgs& a, int* parts, cudaStream_t s) {
-  constexpr int kE = 16 / (int)sizeof(T), k16 = 16 / kE, kWide = kBwd ? (sizeof(T) == 2 ? 3 : 4) : 32 / kE;
-  auto go = [&](auto G, auto per) {
-    constexpr int g = decltype(G)::value, n = decltype(per)::value, rows = kThreads / g;
+  constexpr int kE = 16 / (int)sizeof(T);
+  auto go = [&](auto G, auto values) {
+    constexpr int g = decltype(G)::value, n = decltype(values)::value / kE, rows = kThreads / g;
+    using P = Part<T, kAligned, g, n>;
+    constexpr int bytes = kBwd ? std::max(2 * P::kRingBytes, g < kThreads ? 16 * kThreads : 0) : P::kRingBytes;
     const int64_t need = (a.rows + rows - 1) / rows;
-    const unsigned grid = (unsigned)std::min<int64_t>(need, kBwd ? kParts : 2 * kSms);
+    const unsigned grid = (unsigned)std::min<int64_t>(need, kParts);
     *parts = (int)grid;
-    if constexpr (kBwd) kda_layer_norm_bwd_kernel<T, kAligned, g, n><<<grid, kThreads, 0, s>>>(a);
-    else kda_layer_norm_fwd_kernel<T, kAligned, g, n><<<grid, kThreads, 0, s>>>(a);
+    auto kern = [] {
+      if constexpr (kBwd) return kda_layer_norm_bwd_kernel<T, kAligned, g, n>;
+      else return kda_layer_norm_fwd_kernel<T, kAligned, g, n>;
+    }();
+    if (bytes > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      if (e != cudaSuccess) return e;
+    }
+    kern<<<grid, kThreads, bytes, s>>>(a);
     return cudaGetLastError();
   };
   using std::integral_constant;
-  constexpr integral_constant<int, k16> per{};
-  if (a.D <= 128) return go(integral_constant<int, 8>{}, per);
-  if (a.D <= 512) return go(integral_constant<int, 32>{}, per);
-  if (a.D <= 2048) return go(integral_constant<int, 128>{}, per);
-  if (a.D <= 4096) return go(integral_constant<int, 256>{}, per);
-  if (a.D <= 8192) return go(integral_constant<int, 512>{}, per);
-  if constexpr (kWide > k16)
-    if (a.D <= 512 * kE * kWide) return go(integral_constant<int, 512>{}, integral_constant<int, kWide>{});
+  constexpr integral_constant<int, 16> v16{};
+  if (a.D <= 128) return go(integral_constant<int, 8>{}, v16);
+  if (a.D <= 512) return go(integral_constant<int, 32>{}, v16);
+  if (a.D <= 2048) return go(integral_constant<int, 128>{}, v16);
+  if (a.D <= 4096) return go(integral_constant<int, 256>{}, v16);
+  if (a.D <= 8192) return go(integral_constant<int, 512>{}, v16);
+  if constexpr (sizeof(T) == 2)
+    if (a.D <= 12288) return go(integral_constant<int, 512>{}, integral_constant<int, 24>{});
+  if constexpr (!kBwd && sizeof(T) == 2)
+    if (a.D <= 16384) return go(integral_constant<int, 512>{}, integral_constant<int, 32>{});
   if constexpr (kBwd) {
     kda_layer_norm_wide_bwd_kernel<T><<<(unsigned)a.rows, kThreads, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
