@@ -372,6 +372,14 @@ __device__ __forceinline__ void tmem_ld16x256(uint32_t taddr, float* v) {
       : "r"(taddr));
 }
 
+// The same, two repeats (16 columns).
+__device__ __forceinline__ void tmem_ld16x256x2(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
 // Two FP32 operations in one instruction, on register pairs.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
