@@ -24,6 +24,8 @@ struct Maps {
   CUtensorMap q, k;
 };
 
+// (Six CTAs an SM: T holds what makes it where it is empty so far. A21's parts lie in its upper right quarter, and A's blocks
+// on the diagonal, FP32 and transposed, in the lower left one: those of a warp's 16 rows in 16 rows of T's high or low part.)
 struct Smem {
   union {
     unsigned char kq[32768];      // [2 panels][64 rows of K, 64 of Q][64]
@@ -32,8 +34,6 @@ struct Smem {
       unsigned char P[2][8192];
     } o;
   };
-  unsigned char A21[2][4096];     // high, low part, 32 rows of 128 bytes
-  float At[2][2][16][16];         // A's 16 x 16 blocks on the diagonal, transposed
   DeltaAux aux;
   float ones[4];
   unsigned long long full, done;
@@ -169,27 +169,25 @@ __global__ void __launch_bounds__(128, 6) kda_delta_prep_kernel(const __grid_con
     }
     if (keys && (i >> 4) == m) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) sm.At[w][m & 1][j][lane & 15] = r[j];
+      for (int j = 0; j < 16; ++j) *reinterpret_cast<float*>(T + 8192 * w + piece(32 + 16 * (m & 1) + j, (lane & 15) >> 2) + 4 * (lane & 3)) = r[j];
     } else {  // (above the diagonal: zeros)
       uint32_t hi[8], lo[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) split2(make_float2(r[2 * e], r[2 * e + 1]), hi[e], lo[e]);
       const bool cross = keys && m < 2 * hw;  // a part of A21
-      unsigned char* to = cross ? sm.A21[0] : mine;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const uint32_t at = piece(cross ? lane : i, 2 * m + q);
-        *reinterpret_cast<uint4*>(to + at) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-        if (keys || kTrain)
-          *reinterpret_cast<uint4*>(to + (cross ? 4096 : 8192) + at) = make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+        const uint32_t at = piece(cross ? lane : i, 2 * m + q + (cross ? 4 : 0));
+        *reinterpret_cast<uint4*>(mine + at) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+        if (keys || kTrain) *reinterpret_cast<uint4*>(mine + 8192 + at) = make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
       }
     }
   }
-  if (!hw)
+  if (!keys && !hw)
 #pragma unroll
     for (int q = 4; q < 8; ++q) {
       *reinterpret_cast<uint4*>(mine + piece(i, q)) = make_uint4(0u, 0u, 0u, 0u);
-      if (keys || kTrain) *reinterpret_cast<uint4*>(mine + 8192 + piece(i, q)) = make_uint4(0u, 0u, 0u, 0u);
+      if (kTrain) *reinterpret_cast<uint4*>(mine + 8192 + piece(i, q)) = make_uint4(0u, 0u, 0u, 0u);
     }
   const uint32_t Ts = tc::smem_u32(T);
   const int r8 = lane & 7, q1 = (lane >> 3) & 1, q2 = lane >> 4;  // row and place of the 8 x 8 matrix whose address this lane gives
@@ -205,7 +203,7 @@ __global__ void __launch_bounds__(128, 6) kda_delta_prep_kernel(const __grid_con
       const float tj = -((j & 1) ? t[j / 2].y : t[j / 2].x);
 #pragma unroll
       for (int l = (j + 1) / 4; l < 4; ++l) {  // rows 4 l .. 4 l + 3 (A is zero on the diagonal and above)
-        const float4 y = *reinterpret_cast<const float4*>(&sm.At[w][blk][j][4 * l]);
+        const float4 y = *reinterpret_cast<const float4*>(T + 8192 * w + piece(32 + 16 * blk + j, l));
         if (4 * l + 1 > j) t[2 * l] = tc::fma2(make_float2(y.x, y.y), make_float2(tj, tj), t[2 * l]);
         t[2 * l + 1] = tc::fma2(make_float2(y.z, y.w), make_float2(tj, tj), t[2 * l + 1]);
       }
@@ -254,7 +252,6 @@ __global__ void __launch_bounds__(128, 6) kda_delta_prep_kernel(const __grid_con
   __syncthreads();
   {
     // columns 8 w .. of T21, as above over 32 inner values
-    const uint32_t A21 = tc::smem_u32(sm.A21[0]);
     const int half = w >> 1, n0 = w & 1;  // (sixteen columns make the operand; this warp's eight of them are used)
     float y[4][4] = {};
 #pragma unroll
@@ -266,13 +263,16 @@ __global__ void __launch_bounds__(128, 6) kda_delta_prep_kernel(const __grid_con
 #pragma unroll
       for (int n = 0; n < 4; n += 2) {
         uint32_t bh[4], bl[4];
-        const uint32_t a21 = A21 + piece(8 * n + 8 * q2 + r8, 2 * k + q1);
+        const uint32_t a21 = Ts + piece(8 * n + 8 * q2 + r8, 4 + 2 * k + q1);
         ldmatrix4(a21, bh);
-        ldmatrix4(a21 + 4096, bl);
+        ldmatrix4(a21 + 8192, bl);
         mma_split(y[n], ah, al, bh, bl);
         mma_split(y[n + 1], ah, al, bh + 2, bl + 2);
       }
     }
+    __syncthreads();  // A21 is read
+    for (int k = tid; k < 256; k += 128)
+      *reinterpret_cast<uint4*>(T + 8192 * (k >> 7) + piece((k >> 2) & 31, 4 + (k & 3))) = make_uint4(0u, 0u, 0u, 0u);
     uint32_t bh[4], bl[4];  // inner values in steps of 8
 #pragma unroll
     for (int k = 0; k < 4; ++k) split2(make_float2(n0 ? y[k][2] : y[k][0], n0 ? y[k][3] : y[k][1]), bh[k], bl[k]);
