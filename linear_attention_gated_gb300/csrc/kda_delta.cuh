@@ -59,11 +59,14 @@ __device__ __forceinline__ DeltaChunk delta_chunk(const DeltaProblem& P, int64_t
 }
 
 // Workspace: packets; of the training pair, the states at the chunks' starts and u from the forward, the states' adjoints at
-// the chunks' ends from the backward.
+// the chunks' ends from the backward; where sequences are cut, what the segments make of zero and of the identity.
 struct DeltaWs {
-  size_t packet, states, u, adjoints, total;
+  size_t packet, states, u, adjoints, segments, through, total;
 };
-DeltaWs delta_workspace(int64_t slots, int64_t Hv, bool training);
+DeltaWs delta_workspace(const DeltaProblem& P, bool training);  // (goes by N, Ttot, Hv, slots and seg)
+
+// Tokens of the segments that the forward cuts sequences into, 0 for none. cu: host offsets or null.
+int64_t delta_segment_tokens(const int64_t* cu, int64_t N, int64_t T, int64_t Hv);
 
 struct DeltaGrads {
   const __nv_bfloat16* d_o;  // [Ttot, Hv, 128]

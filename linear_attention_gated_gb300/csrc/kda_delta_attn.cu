@@ -29,11 +29,12 @@ kda_status check(const void* q, const void* k, const void* v, const void* g, con
   for (int i = 0; i < 5; ++i) spans[i] = in[i];
   spans[5] = Span{beta, 2 * (size_t)P->Ttot * Hv};
   P->beta = reinterpret_cast<const __nv_bfloat16*>(beta);
+  P->seg = kda::delta_segment_tokens(cu_host, P->N, T, Hv);
   return set_slots(Shape{P->N, P->Ttot, 0}, Hv, &P->slots);
 }
 
 kda_status check_workspace(const kda::DeltaProblem& P, void* ws, size_t bytes, bool training) {
-  const size_t need = P.Ttot ? kda::delta_workspace(P.slots, P.Hv, training).total : 0;
+  const size_t need = P.Ttot ? kda::delta_workspace(P, training).total : 0;
   if (need && (!ws || bytes < need))
     return fail(KDA_ERR_WORKSPACE_TOO_SMALL, "workspace below kda_gated_delta_workspace_bytes()");
   if ((uintptr_t)ws & 255u) return fail(KDA_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
@@ -48,9 +49,13 @@ extern "C" kda_status kda_gated_delta_workspace_bytes(int64_t B, int64_t T, int6
     if (!bytes) return fail(KDA_ERR_INVALID_ARGUMENT, "bytes is NULL");
     Shape s{};
     kda_status st = check_shape(kOp, B, T, Hqk, Hv, cu_seqlens_host, num_seqs, &s);
-    int64_t slots = 0;
-    if (st != KDA_OK || (st = set_slots(s, Hv, &slots)) != KDA_OK) return st;
-    *bytes = s.Ttot ? kda::delta_workspace(slots, Hv, training != 0).total : 0;
+    kda::DeltaProblem P{};
+    if (st != KDA_OK || (st = set_slots(s, Hv, &P.slots)) != KDA_OK) return st;
+    P.N = s.N;
+    P.Ttot = s.Ttot;
+    P.Hv = (int)Hv;
+    P.seg = kda::delta_segment_tokens(cu_seqlens_host, s.N, T, Hv);
+    *bytes = s.Ttot ? kda::delta_workspace(P, training != 0).total : 0;
     return KDA_OK;
   });
 }

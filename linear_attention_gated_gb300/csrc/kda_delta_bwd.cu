@@ -475,7 +475,7 @@ cudaError_t launch_delta_backward(const DeltaProblem& P, const DeltaGrads& g, vo
   a.P = P;
   a.d_hT = g.d_hT;
   a.dh0 = g.dh0;
-  const DeltaWs w = delta_workspace(P.slots, P.Hv, true);
+  const DeltaWs w = delta_workspace(P, true);
   unsigned char* base = reinterpret_cast<unsigned char*>(ws);
   a.packets = base + w.packet;
   a.adjoints = base + w.adjoints;

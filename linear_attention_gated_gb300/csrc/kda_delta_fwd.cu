@@ -12,6 +12,10 @@
 // tokens, T being lower triangular: the first half's u does not wait for the second's x. So does the update, in halves of
 // the state's columns, and S K^T starts with the first of them. What is off the chain (S Q^T, beta u for the output) is put where
 // the tensor core and the warps would wait.
+//
+// Long axis, few units: each sequence is cut into segments. A pass over every segment but the last goes from a state of zero
+// and, without values, from the identity (a chunk takes S to S M + N, whatever S is: so does a segment); a small kernel
+// chains them, and the main pass starts every segment from its state.
 #include <algorithm>
 
 #include "kda_delta.cuh"
@@ -39,11 +43,13 @@ constexpr uint32_t kColO = 384;  // 64: (beta U)^T P^T
 constexpr uint32_t kColU = 448;  // 64: T x
 
 struct Unit {
-  int64_t n, t0, len;
-  int64_t slot;   // of its state
-  int64_t place;  // of its first chunk
+  int64_t n, t0, len;  // sequence; first token and tokens of the unit
+  int64_t slot, sslot; // of its state, and of its segment's
+  int64_t place;       // of its first chunk
   int nchunks, h;
-  bool run, none;  // the slot is in the pool; no unit: the end
+  bool run, last;      // there is something to do (the slot is in the pool); the sequence's last segment
+  bool identity;       // pass over segments: from the identity, without values
+  bool none;           // no unit: the end
 };
 
 struct Smem {
@@ -61,12 +67,25 @@ struct Smem {
 constexpr int kSmemBytes = (int)sizeof(Smem) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
-constexpr int kOrder = 512;  // sequences whose order is passed (more run in index order)
+constexpr int kOrder = 512;      // sequences whose order is passed (more run in index order, whole)
+constexpr int kMost = 4 * kSms;  // most segments of a sequence
+
+struct Segments {
+  int64_t len;     // tokens of a segment (a multiple of kC), 0: sequences are not cut
+  int most;        // most segments of a sequence
+  float* state;    // [slots, Hv, 128, 128]: what a segment makes of zero, then the state it starts from
+  float* through;  // [slots, Hv, 128, 128]: what it makes of the identity
+};
+// Slot of a sequence's first segment: leaves each sequence ceil(len_n / len) slots.
+__device__ __forceinline__ int64_t seg_slot(const Segments& g, int64_t t0, int64_t n) { return t0 / g.len + n; }
 
 struct PassArgs {
   DeltaProblem P;
   DecayStates st;
+  Segments sg;
+  int32_t first[kMost + 1];  // segments s of the sequences that have one: pairs first[s] .. first[s + 1] - 1
   const unsigned char* packets;
+  uint32_t stride;         // from packet to packet
   unsigned char* states;   // training: BF16 states at the chunks' starts
   unsigned char* u;
   __nv_bfloat16* o;
@@ -79,11 +98,18 @@ struct Maps {
 
 __device__ __forceinline__ float* regs(uint32_t* x) { return reinterpret_cast<float*>(x); }
 
+template <bool kState>
 __device__ __forceinline__ Unit unit_of(const PassArgs& a, int u) {
   const DeltaProblem& P = a.P;
   Unit x;
-  x.n = u / P.Hv;
-  x.h = u - (int)(x.n * P.Hv);
+  x.identity = kState && (u & 1);
+  if (kState) u >>= 1;
+  const int64_t p = u / P.Hv;
+  x.h = u - (int)(p * P.Hv);
+  int64_t seg = 0;
+  if (a.sg.len)
+    while (seg + 1 < a.sg.most && p >= a.first[seg + 1]) ++seg;
+  x.n = a.sg.len ? p - a.first[seg] : p;
   if (a.ordered) x.n = a.order[x.n];
   const DecaySpan sp = decay_span(P, x.n);
   x.t0 = sp.t0;
@@ -91,12 +117,24 @@ __device__ __forceinline__ Unit unit_of(const PassArgs& a, int u) {
   x.slot = a.st.slots ? a.st.slots[x.n] : x.n;
   x.run = x.slot >= 0 && x.slot < a.st.num_slots;
   x.place = delta_slot(sp.t0, x.n);
+  x.sslot = 0;
+  x.last = true;
+  if (a.sg.len) {
+    const int64_t from = seg * a.sg.len;
+    x.sslot = seg_slot(a.sg, sp.t0, x.n) + seg;
+    x.last = from + a.sg.len >= sp.len;
+    if ((seg > 0 && from >= sp.len) || (kState && x.last)) x.run = false;
+    x.t0 += from;
+    x.len = x.last ? sp.len - from : a.sg.len;
+    x.place += from / kC;
+  }
   x.nchunks = x.run ? (int)((x.len + kC - 1) / kC) : 0;
   x.none = false;
   return x;
 }
 
-template <bool kTrain>
+// kTrain: states and u are saved. kState: the pass over segments (states alone).
+template <bool kTrain, bool kState>
 __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PassArgs a) {
   extern __shared__ unsigned char raw_smem[];
   Smem& sm = *reinterpret_cast<Smem*>(raw_smem + ((1024 - (tc::smem_u32(raw_smem) & 1023)) & 1023));
@@ -108,13 +146,13 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
   if (tid == 0) {
     auto init = [&](unsigned long long& b, uint32_t n) { tc::mbar_init(bar(b), n); };
     for (int i = 0; i < 2; ++i) {
-      init(sm.full[i], 1); init(sm.empty[i], 1 + 16);
+      init(sm.full[i], 1); init(sm.empty[i], kState ? 9 : 17);
       init(sm.sready[i], 4); init(sm.xready[i], 4); init(sm.wready[i], 4);
       init(sm.gu[i], 1); init(sm.gs[i], 1);
     }
     init(sm.raw, 1); init(sm.gx, 1); init(sm.gq, 1); init(sm.vready, 8); init(sm.go, 1); init(sm.ofree, 8); init(sm.ufree, 8);
     init(sm.scopied, 8); init(sm.clcbar, 1);
-    for (int i = 0; i < kRing; ++i) { init(sm.rfull[i], 1); init(sm.rempty[i], 17); }
+    for (int i = 0; i < kRing; ++i) { init(sm.rfull[i], 1); init(sm.rempty[i], kState ? 9 : 17); }
   }
   tc::fence_before();
   __syncthreads();
@@ -171,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
         }
         __syncwarp();
       };
-      Unit x = unit_of(a, (int)blockIdx.x), next;
+      Unit x = unit_of<kState>(a, (int)blockIdx.x), next;
       push(x);
       ask();
       for (;;) {
@@ -192,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
               tc::fence_async_smem();  // read before the next response is written
             }
             __syncwarp();
-            if (more) next = unit_of(a, (int)nx);
+            if (more) next = unit_of<kState>(a, (int)nx);
             push(next);
             if (ok && more) ask();
           }
@@ -207,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
             tc::mbar_arrive_expect_tx(f, 3 * kTile + kPkPass);
 #pragma unroll
             for (int p = 0; p < 2; ++p) tc::tma_load3(tc::smem_u32(sm.tok[s][0]) + p * kPanel, &maps.k, 64 * p, x.h / P.r, t, f);
-            tc::bulk_g2s(tc::smem_u32(sm.packet[s]), a.packets + ((x.place + c) * P.Hv + x.h) * (int64_t)(kTrain ? kPkTrain : kPkInfer), kPkPass, f);
+            tc::bulk_g2s(tc::smem_u32(sm.packet[s]), a.packets + ((x.place + c) * P.Hv + x.h) * (int64_t)a.stride, kPkPass, f);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
               tc::tma_load3(tc::smem_u32(sm.tok[s][2]) + p * kPanel, &maps.v, 64 * p, x.h, t, f);
@@ -265,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
         }
         if (!ok) break;
         // S Q^T
-        if (g && !wait(sm.ofree, g - 1)) break;
-        if (tc::elect_one()) {
+        if (!kState && g && !wait(sm.ofree, g - 1)) break;
+        if (!kState && tc::elect_one()) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             tc::mma_bf16_ts(tbase + kColQ, tbase + kColS + 64 * (i >> 2) + 8 * (i & 3), qk + (i >> 2) * (kPanel >> 4) + (i & 3) * 2, kN64, i > 0);
@@ -293,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
         }
         if (!ok) break;
         // the state's update, in place of the operand (once that is read), the last of it for one half of the columns after the other
-        if (!wait(sm.gq, g)) break;
+        if (!kState && !wait(sm.gq, g)) break;
         if (kTrain && !wait(sm.scopied, g)) break;
         if (!wait(sm.wready[0], g)) break;
         if (tc::elect_one())
@@ -314,11 +352,12 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
                 tc::mma_bf16_ts(tbase + kColS + 64 * h, tbase + kColA + 8 * i + 32 * part, kn + h * (kPanel >> 4) + 128 * i,
                                 tc::idesc_bf16(128, 64, false, true), 1);
             tc::mma_commit(bar(sm.gs[h]));
+            if (kState && h) tc::mma_commit(bar(sm.empty[s]));
           }
         __syncwarp();
         // beta u's part of the output
-        if (!wait(sm.vready, g)) break;
-        if (tc::elect_one()) {
+        if (!kState && !wait(sm.vready, g)) break;
+        if (!kState && tc::elect_one()) {
           const uint64_t p = tc::kmajor(T + kPkP);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -355,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
       }
     };
     uint32_t g = 0;
-    for (Unit x;;) {
+    for (Unit x; !kState;) {
       const bool more = next_unit(x);
       if (!agree() || !more) break;
       for (int c = 0; c < x.nchunks; ++c, ++g) {
@@ -468,14 +507,24 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
     uint32_t g = 0;
     for (Unit x; next_unit(x);) {
       if (!x.run) {
+        if (kState) continue;
         // a device slot index outside the pool (it no longer matches the host mirror the call was checked
         // against, as in a replayed graph): flagged, and the pool is not touched
-        if (warp == kWarpChain && lane == 0) atomicOr(P.status, 4);
+        if ((x.slot < 0 || x.slot >= a.st.num_slots) && warp == kWarpChain && lane == 0) atomicOr(P.status, 4);
         continue;
       }
       const int64_t at = (x.slot * P.Hv + x.h) * kDim * kDim + v * kDim + 64 * half;
+      const int64_t sat = (x.sslot * P.Hv + x.h) * kDim * kDim + v * kDim + 64 * half;
       float2 S[32];
-      if (!a.st.in) {
+      if (kState) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          S[j] = make_float2(x.identity && v == 64 * half + 2 * j ? 1.f : 0.f, x.identity && v == 64 * half + 2 * j + 1 ? 1.f : 0.f);
+      } else if (a.sg.len) {
+        const float4* src = reinterpret_cast<const float4*>(a.sg.state + sat);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) reinterpret_cast<float4*>(S)[j] = src[j];
+      } else if (!a.st.in) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) S[j] = make_float2(0.f, 0.f);
       } else if (!a.st.bf16) {
@@ -513,6 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
         // x = v - e^b (S k)
         uint32_t r[2][8];
         float2 e[4], f[4];
+        const uint32_t keep = kState && x.identity ? 0u : 0xffffffffu;
         // 4 x 2 blocks [8 tokens][8 values], transposed: r[2 i + j] holds tokens j0 + 8 i (+ 1) of value 8 j + lane / 4
 #pragma unroll
         for (int q = 0; q < 2; ++q)
@@ -521,6 +571,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
             const int t = 32 * half + 8 * (i + (lane >> 4)) + (lane & 7), d = 32 * wq + 16 * q + 8 * ((lane >> 3) & 1);
             tc::ldmatrix4_trans(tc::smem_u32(sm.tok[s][2]) + (d >> 6) * kPanel + t * 128 + ((((d & 63) >> 3) ^ (t & 7)) << 4), r[q] + 2 * i);
           }
+        if (kState)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) r[i >> 3][i & 7] &= keep;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           e[i] = *reinterpret_cast<const float2*>(&aux.eb[j0 + 8 * i]);
@@ -579,18 +632,20 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
         tc::fence_before();
         arrive(sm.wready[half]);
         arrive(sm.empty[s]);
+        if (!kState) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t hi[8], lo[8];
+          for (int q = 0; q < 2; ++q) {
+            uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) split2(y[q][i], hi[i], lo[i]);
-          const uint32_t col = tl + (16u * q << 16) + kColA + 64 + 16 * half;
-          tc::tmem_st16x128(col, regs(hi));
-          tc::tmem_st16x128(col + 32, regs(lo));
+            for (int i = 0; i < 8; ++i) split2(y[q][i], hi[i], lo[i]);
+            const uint32_t col = tl + (16u * q << 16) + kColA + 64 + 16 * half;
+            tc::tmem_st16x128(col, regs(hi));
+            tc::tmem_st16x128(col + 32, regs(lo));
+          }
+          tc::tmem_wait_st();
+          tc::fence_before();
+          arrive(sm.vready);
         }
-        tc::tmem_wait_st();
-        tc::fence_before();
-        arrive(sm.vready);
         if (!wait(sm.gs[half], g)) break;
         const float2 lam = make_float2(lam1, lam1);
 #pragma unroll
@@ -608,7 +663,12 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
         if (c + 1 < x.nchunks) put_state();
       }
       if (!ok) break;
-      if (a.st.out && !a.st.bf16) {
+      if (kState) {
+        float4* dst = reinterpret_cast<float4*>((x.identity ? a.sg.through : a.sg.state) + sat);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) dst[j] = reinterpret_cast<const float4*>(S)[j];
+      } else if (!x.last) {
+      } else if (a.st.out && !a.st.bf16) {
         float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.st.out) + at);
 #pragma unroll
         for (int j = 0; j < 16; ++j) dst[j] = reinterpret_cast<const float4*>(S)[j];
@@ -628,6 +688,92 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
   }
 }
 
+// Chains the segments of one (sequence, head), x <- x M + N: in, each segment's N and M but the last's; out, the state each
+// segment starts from, in N's place. A CTA takes 16 of the state's 128 rows (independent of each other) and multiplies them with M in
+// four parts of 32 rows, which come through a ring of asynchronous copies. FP32.
+constexpr int kChainRows = 16, kChainThreads = 256, kPart = 32, kParts = kDim / kPart, kChainStages = 3;
+constexpr int kChainSmem = (kChainStages * kPart * kDim + kDim * kChainRows) * 4;
+__global__ void __launch_bounds__(kChainThreads) kda_delta_chain_kernel(const __grid_constant__ PassArgs a) {
+  extern __shared__ float chain_smem[];
+  float* M = chain_smem;                                   // [stages][32][128]
+  float* xs = chain_smem + kChainStages * kPart * kDim;    // [128][16]: the rows, transposed
+  const DeltaProblem& P = a.P;
+  const Segments& sg = a.sg;
+  const int64_t n = blockIdx.x / P.Hv;
+  const int h = (int)(blockIdx.x % P.Hv);
+  const DecaySpan sp = decay_span(P, n);
+  const int64_t slot = a.st.slots ? a.st.slots[n] : n;
+  if (slot < 0 || slot >= a.st.num_slots) return;  // the main pass flags it
+  // rows row .. row + 3, columns col and the next
+  const int tid = threadIdx.x, col = 2 * (tid & 63), r0 = 4 * (tid >> 6), row = kChainRows * blockIdx.y + r0;
+  const int64_t base = seg_slot(sg, sp.t0, n);
+  const int64_t m = sp.len > sg.len ? (sp.len + sg.len - 1) / sg.len : 1;
+  auto at = [&](int64_t i) { return ((base + i) * P.Hv + h) * kDim * kDim; };
+  auto fetch = [&](int64_t p) {  // part p of all
+    if (p < (m - 1) * kParts) {
+      const float* src = sg.through + at(p / kParts) + (p % kParts) * kPart * kDim;
+#pragma unroll
+      for (int k = 0; k < kPart * kDim / 4 / kChainThreads; ++k)
+        tc::cp_async16(M + (p % kChainStages) * kPart * kDim + 4 * (tid + k * kChainThreads), src + 4 * (tid + k * kChainThreads), 16);
+    }
+    tc::cp_async_commit();
+  };
+  for (int p = 0; p < kChainStages - 1; ++p) fetch(p);
+  float2 x[4];
+  const int64_t from = (slot * P.Hv + h) * kDim * kDim;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int64_t k = from + (row + r) * kDim + col;
+    if (!a.st.in) x[r] = make_float2(0.f, 0.f);
+    else if (a.st.bf16) x[r] = unpack2(*reinterpret_cast<const uint32_t*>(reinterpret_cast<const __nv_bfloat16*>(a.st.in) + k));
+    else x[r] = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(a.st.in) + k);
+  }
+  for (int64_t i = 0; i < m; ++i) {
+    float* s = sg.state + at(i) + row * kDim + col;
+    float2 y[4];
+    if (i + 1 < m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) y[r] = *reinterpret_cast<const float2*>(s + r * kDim);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) *reinterpret_cast<float2*>(s + r * kDim) = x[r];
+    if (i + 1 == m) break;
+    *reinterpret_cast<float4*>(xs + col * kChainRows + r0) = make_float4(x[0].x, x[1].x, x[2].x, x[3].x);
+    *reinterpret_cast<float4*>(xs + (col + 1) * kChainRows + r0) = make_float4(x[0].y, x[1].y, x[2].y, x[3].y);
+#pragma unroll 1
+    for (int p = 0; p < kParts; ++p) {
+      const int64_t at_part = i * kParts + p;
+      tc::cp_async_wait<kChainStages - 2>();
+      __syncthreads();  // the part is there for all (and xs); the one before is read
+      fetch(at_part + kChainStages - 1);
+      const float* Mp = M + (at_part % kChainStages) * kPart * kDim + col;
+      const float* xp = xs + p * kPart * kChainRows + r0;
+#pragma unroll 16
+      for (int k = 0; k < kPart; ++k) {
+        const float4 q = *reinterpret_cast<const float4*>(xp + k * kChainRows);
+        const float2 w = *reinterpret_cast<const float2*>(Mp + k * kDim);
+        y[0] = tc::fma2(make_float2(q.x, q.x), w, y[0]);
+        y[1] = tc::fma2(make_float2(q.y, q.y), w, y[1]);
+        y[2] = tc::fma2(make_float2(q.z, q.z), w, y[2]);
+        y[3] = tc::fma2(make_float2(q.w, q.w), w, y[3]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] = y[r];
+    __syncthreads();  // xs is read
+  }
+  tc::cp_async_wait_all();
+}
+
+template <bool kTrain, bool kState>
+cudaError_t launch(const Maps& maps, const PassArgs& a, cudaStream_t s) {
+  auto kern = kda_delta_fwd_kernel<kTrain, kState>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  const int64_t units = (a.sg.len ? a.first[a.sg.most] : a.P.N) * a.P.Hv * (kState ? 2 : 1);
+  kern<<<(unsigned)units, kThreads, kSmemBytes, s>>>(maps, a);
+  return cudaGetLastError();
+}
+
 template <bool kTrain>
 cudaError_t forward(const DeltaProblem& P, const DecayStates& st, __nv_bfloat16* o, unsigned char* ws, cudaStream_t s) {
   Maps maps{};
@@ -642,24 +788,54 @@ cudaError_t forward(const DeltaProblem& P, const DecayStates& st, __nv_bfloat16*
   }
   a.P = P;
   a.st = st;
-  const DeltaWs w = delta_workspace(P.slots, P.Hv, kTrain);
+  const DeltaWs w = delta_workspace(P, kTrain);
   a.packets = ws + w.packet;
+  a.stride = kTrain ? kPkTrain : kPkInfer;
   a.states = ws + w.states;
   a.u = ws + w.u;
   a.o = o;
+  auto len = [&](int64_t n) { return P.cu_host ? P.cu_host[n + 1] - P.cu_host[n] : P.T; };
   if (P.cu_host && P.N > 1 && P.N <= kOrder) {
     a.ordered = 1;
     for (int64_t i = 0; i < P.N; ++i) a.order[i] = (uint16_t)i;
-    auto len = [&](int64_t n) { return P.cu_host[n + 1] - P.cu_host[n]; };
     std::stable_sort(a.order, a.order + P.N, [&](uint16_t i, uint16_t j) { return len(i) > len(j); });
   }
-  auto kern = kda_delta_fwd_kernel<kTrain>;
-  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes)) != cudaSuccess) return e;
-  kern<<<(unsigned)(P.N * P.Hv), kThreads, kSmemBytes, s>>>(maps, a);
-  return cudaGetLastError();
+  a.sg.most = 1;
+  if (P.seg) {
+    a.sg.len = P.seg;
+    a.sg.most = (int)((P.longest + P.seg - 1) / P.seg);
+    int64_t have = P.N;  // the sequences that have a segment s (longest first): all have the first
+    for (int t = 0; t < a.sg.most; ++t) {
+      while (t && have && len(a.ordered ? a.order[have - 1] : have - 1) <= t * P.seg) --have;
+      a.first[t + 1] = a.first[t] + (int32_t)have;
+    }
+    a.sg.state = reinterpret_cast<float*>(ws + w.segments);
+    a.sg.through = reinterpret_cast<float*>(ws + w.through);
+    if ((e = launch<false, true>(maps, a, s)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(kda_delta_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kChainSmem)) != cudaSuccess) return e;
+    kda_delta_chain_kernel<<<dim3((unsigned)(P.N * P.Hv), kDim / kChainRows), kChainThreads, kChainSmem, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  return launch<kTrain, false>(maps, a, s);
 }
 
 }  // namespace
+
+int64_t delta_segment_tokens(const int64_t* cu, int64_t N, int64_t T, int64_t Hv) {
+  if (N > kOrder) return 0;
+  auto chunks_of = [&](int64_t n) { return ((cu ? cu[n + 1] - cu[n] : T) + kC - 1) / kC; };
+  int64_t longest = 0, chunks = 0;
+  for (int64_t n = 0; n < (cu ? N : 1); ++n) {
+    chunks += chunks_of(n);
+    longest = std::max(longest, chunks_of(n));
+  }
+  if (!cu) chunks *= N;
+  const int64_t share = (chunks * Hv + kSms - 1) / kSms;  // an SM's even share of the chunks
+  if (longest <= 4 * share + 40) return 0;
+  // a quarter of it, so that the last turn is short, 8 chunks at least (and no more segments than are passed)
+  const int64_t seg = std::max({(share + 3) / 4, (int64_t)8, (longest + kMost - 1) / kMost});
+  return seg * kC;
+}
 
 cudaError_t launch_delta_forward(const DeltaProblem& P, const DecayStates& st, __nv_bfloat16* o, bool training, void* ws,
                                  cudaStream_t s) {

@@ -409,7 +409,7 @@ cudaError_t launch_delta_grads(const DeltaProblem& P, const DeltaGrads& g, void*
   if ((e = token_map(&maps.d_o, g.d_o, P.Hv, P.Ttot, kDim, (int64_t)P.Hv * kDim, kC)) != cudaSuccess) return e;
   if ((e = token_map(&maps.dv, g.dv, P.Hv, P.Ttot, kDim, (int64_t)P.Hv * kDim, kC)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(kda_delta_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes)) != cudaSuccess) return e;
-  const DeltaWs w = delta_workspace(P.slots, P.Hv, true);
+  const DeltaWs w = delta_workspace(P, true);
   unsigned char* b = reinterpret_cast<unsigned char*>(ws);
   const int64_t units = P.slots * P.Hqk;
   kda_delta_grad_kernel<<<(unsigned)(units < kSms ? units : kSms), kThreads, kSmemBytes, s>>>(maps, P, b + w.packet, b + w.states, b + w.adjoints, b + w.u, g);

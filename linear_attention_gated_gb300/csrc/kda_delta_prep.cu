@@ -35,7 +35,7 @@ struct Smem {
     } o;
   };
   DeltaAux aux;
-  float ones[4];
+  float far[2][kC];               // e^{-b_j} beta_j, e^{-b_j}
   unsigned long long full, done;
   uint32_t tmem;
 };
@@ -86,7 +86,6 @@ __global__ void __launch_bounds__(128, 6) kda_delta_prep_kernel(const __grid_con
       tc::tma_load3(kq + p * 16384 + 8192, &maps.q, 64 * p, h / P.r, (int)ch.t0, full);
     }
   }
-  if (tid < 4) sm.ones[tid] = 1.f;
   const int nt = ch.nt;
   if (w == 0) {
     // Decays, two tokens a lane. The sums are exact in 64-bit fixed point (units of 2^-40): factors are of differences of
@@ -121,6 +120,9 @@ __global__ void __launch_bounds__(128, 6) kda_delta_prep_kernel(const __grid_con
     two(sm.aux.a, token_decay(x[0]) + nan, token_decay(x[1]) + nan);
     two(sm.aux.b, number(b0), number(sum));
     if (lane == 0) sm.aux.whole = number(whole);
+    const float f0 = fast_exp2(number(-b0)), f1f = fast_exp2(number(-sum));
+    two(sm.far[0], f0 * be[0], f1f * be[1]);
+    two(sm.far[1], f0, f1f);
   }
   tc::fence_before();
   __syncthreads();
@@ -146,25 +148,43 @@ __global__ void __launch_bounds__(128, 6) kda_delta_prep_kernel(const __grid_con
   const uint32_t tl = sm.tmem + ((uint32_t)(32 * w) << 16);
   unsigned char* T = sm.o.T[0];
   unsigned char* mine = keys ? T : sm.o.P[0];
-  // sixteen columns at a time, from the last: D_ij = D_i,j+1 a_j+1 from D_ii = 1
+  // D_ij = e^{b_i} e^{-b_j} where both stay in range (decays to 2^-100 over the chunk); else, sixteen columns at a time from the
+  // last, D_ij = D_i,j+1 a_j+1 from D_ii = 1.
+  const bool range = sm.aux.whole > -100.f && nt == kC;
+  const float bi = sm.aux.eb[i];
   float d = 0.f, a1 = 0.f;
 #pragma unroll 1
   for (int m = 2 * hw + 1; m >= 0; --m) {
     float r[16];
     tc::tmem_ld16(tl + 16 * m, r);
     const int last = i < nt ? i - 16 * m - (keys ? 1 : 0) : -1;  // the columns up to it count
+    if (range) {
+      const float4* f = reinterpret_cast<const float4*>(&sm.far[keys ? 0 : 1][16 * m]);
+      const float2 b2 = make_float2(bi, bi);
 #pragma unroll
-    for (int q = 3; q >= 0; --q) {
-      const float4 a4 = *reinterpret_cast<const float4*>(&sm.aux.a[16 * m + 4 * q]);
-      const float4 b4 = *reinterpret_cast<const float4*>(keys ? &sm.aux.beta[16 * m + 4 * q] : sm.ones);
-      const float av[4] = {a4.x, a4.y, a4.z, a4.w}, bv[4] = {b4.x, b4.y, b4.z, b4.w};
+      for (int q = 0; q < 4; ++q) {
+        const float4 y = f[q];
+        const float2 lo = tc::mul2(make_float2(r[4 * q], r[4 * q + 1]), tc::mul2(make_float2(y.x, y.y), b2));
+        const float2 hi = tc::mul2(make_float2(r[4 * q + 2], r[4 * q + 3]), tc::mul2(make_float2(y.z, y.w), b2));
+        r[4 * q] = lo.x; r[4 * q + 1] = lo.y; r[4 * q + 2] = hi.x; r[4 * q + 3] = hi.y;
+      }
+      if (m >= 2 * hw)  // (the other half lies before all of its rows)
 #pragma unroll
-      for (int e = 3; e >= 0; --e) {
-        const int j = 4 * q + e;
-        d = 16 * m + j == i ? 1.f : d * a1;
-        a1 = av[e];
-        // (selected, not multiplied: rows past the end may hold anything)
-        r[j] = j <= last ? r[j] * (bv[e] * d) : 0.f;
+        for (int j = 0; j < 16; ++j) r[j] = j <= last ? r[j] : 0.f;
+    } else {
+#pragma unroll
+      for (int q = 3; q >= 0; --q) {
+        const float4 a4 = *reinterpret_cast<const float4*>(&sm.aux.a[16 * m + 4 * q]);
+        const float4 b4 = keys ? *reinterpret_cast<const float4*>(&sm.aux.beta[16 * m + 4 * q]) : make_float4(1.f, 1.f, 1.f, 1.f);
+        const float av[4] = {a4.x, a4.y, a4.z, a4.w}, bv[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+        for (int e = 3; e >= 0; --e) {
+          const int j = 4 * q + e;
+          d = 16 * m + j == i ? 1.f : d * a1;
+          a1 = av[e];
+          // (selected, not multiplied: rows past the end may hold anything)
+          r[j] = j <= last ? r[j] * (bv[e] * d) : 0.f;
+        }
       }
     }
     if (keys && (i >> 4) == m) {
@@ -251,49 +271,61 @@ __global__ void __launch_bounds__(128, 6) kda_delta_prep_kernel(const __grid_con
   }
   __syncthreads();
   {
-    // columns 8 w .. of T21, as above over 32 inner values
-    const int half = w >> 1, n0 = w & 1;  // (sixteen columns make the operand; this warp's eight of them are used)
-    float y[4][4] = {};
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      uint32_t ah[4], al[4];
-      const uint32_t t11 = Ts + piece(16 * k + 8 * q2 + r8, 2 * half + q1);
-      tc::ldmatrix4_trans(t11, ah);
-      tc::ldmatrix4_trans(t11 + 8192, al);
-#pragma unroll
-      for (int n = 0; n < 4; n += 2) {
-        uint32_t bh[4], bl[4];
-        const uint32_t a21 = Ts + piece(8 * n + 8 * q2 + r8, 4 + 2 * k + q1);
-        ldmatrix4(a21, bh);
-        ldmatrix4(a21 + 8192, bl);
-        mma_split(y[n], ah, al, bh, bl);
-        mma_split(y[n + 1], ah, al, bh + 2, bl + 2);
-      }
-    }
-    __syncthreads();  // A21 is read
-    for (int k = tid; k < 256; k += 128)
-      *reinterpret_cast<uint4*>(T + 8192 * (k >> 7) + piece((k >> 2) & 31, 4 + (k & 3))) = make_uint4(0u, 0u, 0u, 0u);
-    uint32_t bh[4], bl[4];  // inner values in steps of 8
-#pragma unroll
-    for (int k = 0; k < 4; ++k) split2(make_float2(n0 ? y[k][2] : y[k][0], n0 ? y[k][3] : y[k][1]), bh[k], bl[k]);
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      float z[4] = {};
-#pragma unroll
-      for (int k = 0; k <= m; ++k) {
-        uint32_t ah[4], al[4];
-        const uint32_t t22 = Ts + piece(32 + 16 * m + 8 * q1 + r8, 4 + 2 * k + q2);
-        ldmatrix4(t22, ah);
-        ldmatrix4(t22 + 8192, al);
-        mma_split(z, ah, al, bh + 2 * k, bl + 2 * k);
-      }
+    // columns 16 hw .. of T21, as above over 32 inner values, by two warps
+    uint32_t bh[2][4], bl[2][4];  // [8 columns][inner values in steps of 8]
+    if (!keys) {
+      float y[4][4] = {};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        uint32_t th, tlo;
-        split2(make_float2(-z[2 * k], -z[2 * k + 1]), th, tlo);
-        const uint32_t to = piece(32 + 16 * m + 8 * k + (lane >> 2), w) + 4 * (lane & 3);
-        *reinterpret_cast<uint32_t*>(T + to) = th;
-        *reinterpret_cast<uint32_t*>(T + 8192 + to) = tlo;
+        uint32_t ah[4], al[4];
+        const uint32_t t11 = Ts + piece(16 * k + 8 * q2 + r8, 2 * hw + q1);
+        tc::ldmatrix4_trans(t11, ah);
+        tc::ldmatrix4_trans(t11 + 8192, al);
+#pragma unroll
+        for (int n = 0; n < 4; n += 2) {
+          uint32_t ch[4], cl[4];
+          const uint32_t a21 = Ts + piece(8 * n + 8 * q2 + r8, 4 + 2 * k + q1);
+          ldmatrix4(a21, ch);
+          ldmatrix4(a21 + 8192, cl);
+          mma_split(y[n], ah, al, ch, cl);
+          mma_split(y[n + 1], ah, al, ch + 2, cl + 2);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) split2(make_float2(y[k][2 * n], y[k][2 * n + 1]), bh[n][k], bl[n][k]);
+    }
+    __syncthreads();  // A21 is read
+    if (keys) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int x = tid + 64 * k;
+        *reinterpret_cast<uint4*>(T + 8192 * (x >> 7) + piece((x >> 2) & 31, 4 + (x & 3))) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    } else {
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        float z[2][4] = {};
+#pragma unroll
+        for (int k = 0; k <= m; ++k) {
+          uint32_t ah[4], al[4];
+          const uint32_t t22 = Ts + piece(32 + 16 * m + 8 * q1 + r8, 4 + 2 * k + q2);
+          ldmatrix4(t22, ah);
+          ldmatrix4(t22 + 8192, al);
+#pragma unroll
+          for (int n = 0; n < 2; ++n) mma_split(z[n], ah, al, bh[n] + 2 * k, bl[n] + 2 * k);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t th, tlo;
+            split2(make_float2(-z[n][2 * k], -z[n][2 * k + 1]), th, tlo);
+            const uint32_t to = piece(32 + 16 * m + 8 * k + (lane >> 2), 2 * hw + n) + 4 * (lane & 3);
+            *reinterpret_cast<uint32_t*>(T + to) = th;
+            *reinterpret_cast<uint32_t*>(T + 8192 + to) = tlo;
+          }
       }
     }
   }
@@ -329,13 +361,16 @@ cudaError_t launch(const Maps& maps, const DeltaProblem& P, void* ws, cudaStream
 
 }  // namespace
 
-DeltaWs delta_workspace(int64_t slots, int64_t Hv, bool training) {
-  const size_t n = (size_t)slots * Hv;
+DeltaWs delta_workspace(const DeltaProblem& P, bool training) {
+  const size_t n = (size_t)P.slots * P.Hv;
   DeltaWs w{};
   w.states = ctx_align_up(n * (training ? kPkTrain : kPkInfer));
   w.u = w.states + (training ? n * kStateTile : 0);
   w.adjoints = w.u + (training ? n * kUTile : 0);
-  w.total = w.adjoints + (training ? n * kStateTile : 0);
+  w.segments = w.adjoints + (training ? n * kStateTile : 0);
+  const size_t cut = P.seg ? sizeof(float) * (size_t)(P.Ttot / P.seg + P.N) * P.Hv * kDim * kDim : 0;
+  w.through = w.segments + cut;
+  w.total = w.through + cut;
   return w;
 }
 

@@ -83,6 +83,11 @@ def kda_gated_delta_fwd(q, k, v, log_decay, beta, initial_state=None, cu_seqlens
         cu_host = ctx.cu if known else cu_host.clone()
     if ctx is None:
         ctx = DeltaContext(key, gated_delta_workspace_bytes(B, T, Hqk, Hv, cu_host), dev, stream)
+    elif cu_host is not None and not known:
+        nbytes = gated_delta_workspace_bytes(B, T, Hqk, Hv, cu_host)  # other lengths may need more
+        if nbytes > ctx.workspace.numel():
+            ctx.outgrown.append(ctx.workspace)
+            ctx.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     if out is None:
         out = torch.empty((B, T, Hv, D), dtype=_BF16, device=dev)
     else:

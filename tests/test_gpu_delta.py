@@ -166,3 +166,16 @@ def test_no_tokens():
     got, _ = run(x)
     assert got["o"].shape == (1, 0, 2, D) and got["dq"].shape == (1, 0, 1, D)
     assert torch.equal(got["hT"].cpu(), x["h0"]) and torch.equal(got["dh0"].cpu(), x["dhT"])
+
+
+@pytest.mark.parametrize("lens,hqk,hv,gate", [((3100,), 1, 1, True), ((2900, 0, 77, 3400), 1, 2, False)], ids=str)
+def test_sequences_cut_into_segments(lens, hqk, hv, gate):
+    """Long sequences of few heads: each is cut, and the segments' states are chained."""
+    from linear_attention_gated_gb300 import gated_delta_workspace_bytes
+    x = make(lens, hqk, hv, seed=11, gate=gate)
+    places = (sum(lens) // 64 + len(lens)) * hv
+    assert gated_delta_workspace_bytes(1, sum(lens), hqk, hv, x["cu"], False) > places * 26624 + 256  # (what uncut ones take)
+    if gate:  # decays that leave something of the state over a segment
+        x["g"] = (x["g"].float() * 0.02).bfloat16()
+    got, _ = run(x)
+    compare(got, reference(x, device="cuda"))
