@@ -5,7 +5,8 @@
 //   warp 0   copies: K, Q and V tiles by tiled copies (128-byte swizzle), T, P and the decays' factors; the next unit's number
 //            (cluster launch control: the grid has a CTA for each unit, one (sequence, head), longest first, and a running
 //            CTA takes over the next one that has not started)
-//   warp 1   products (tcgen05.mma kind::f16, BF16 operands, FP32 accumulators in tensor memory)
+//   warps 1, 2   products (tcgen05.mma kind::f16, BF16 operands, FP32 accumulators in tensor memory): the chain's, and o's (a
+//            warp that waits for room for o does not hold up the chain: 257 -> 249 us)
 //   warps 4-11   o (and u) on their way out
 //   warps 12-19  the state, 64 of a row's 128 values a thread in registers, and the elements between the chain's products
 // The chain of a chunk: S K^T -> x = v - e^b S k -> T x -> w beta u -> the state's update. Elements go in two halves of the
@@ -27,7 +28,7 @@ namespace kda {
 namespace {
 
 constexpr int kC = kDecayChunk;
-constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpOut = 4, kWarpChain = 12;
+constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpMmaO = 2, kWarpOut = 4, kWarpChain = 12;
 constexpr int kThreads = 32 * 20;
 // Registers a thread of the control, out and chain warps (setmaxnreg): 128 x 48 + 256 x 72 + 256 x 144 = 61,440, all of the
 // 640 x 96 = 61,440 the block is launched with (a split above that would wait for ever).
@@ -146,13 +147,13 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
   if (tid == 0) {
     auto init = [&](unsigned long long& b, uint32_t n) { tc::mbar_init(bar(b), n); };
     for (int i = 0; i < 2; ++i) {
-      init(sm.full[i], 1); init(sm.empty[i], kState ? 9 : 17);
+      init(sm.full[i], 1); init(sm.empty[i], kState ? 9 : 18);
       init(sm.sready[i], 4); init(sm.xready[i], 4); init(sm.wready[i], 4);
       init(sm.gu[i], 1); init(sm.gs[i], 1);
     }
     init(sm.raw, 1); init(sm.gx, 1); init(sm.gq, 1); init(sm.vready, 8); init(sm.go, 1); init(sm.ofree, 8); init(sm.ufree, 8);
     init(sm.scopied, 8); init(sm.clcbar, 1);
-    for (int i = 0; i < kRing; ++i) { init(sm.rfull[i], 1); init(sm.rempty[i], kState ? 9 : 17); }
+    for (int i = 0; i < kRing; ++i) { init(sm.rfull[i], 1); init(sm.rempty[i], kState ? 9 : 18); }
   }
   tc::fence_before();
   __syncthreads();
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
       for (; any_chunk(left); ++g, --left) {
         const uint32_t s = g % kStages;
         const uint32_t k = tc::smem_u32(sm.tok[s][0]), T = tc::smem_u32(sm.packet[s]) + kPkT;
-        const uint64_t kk = tc::kmajor(k), qk = tc::kmajor(tc::smem_u32(sm.tok[s][1])), kn = tc::mnmajor(k, kPanel);
+        const uint64_t kk = tc::kmajor(k), kn = tc::mnmajor(k, kPanel);
         if (!wait(sm.full[s], g / kStages)) break;
         if (kTrain && g && !wait(sm.ufree, g - 1)) break;
         // S K^T, the columns of S as they come
@@ -302,15 +303,6 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
           __syncwarp();
         }
         if (!ok) break;
-        // S Q^T
-        if (!kState && g && !wait(sm.ofree, g - 1)) break;
-        if (!kState && tc::elect_one()) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            tc::mma_bf16_ts(tbase + kColQ, tbase + kColS + 64 * (i >> 2) + 8 * (i & 3), qk + (i >> 2) * (kPanel >> 4) + (i & 3) * 2, kN64, i > 0);
-          tc::mma_commit(bar(sm.gq));
-        }
-        __syncwarp();
         // T x: what the first 32 tokens give to all, what the others give to themselves
         const uint64_t th = tc::kmajor(T), tlo = tc::kmajor(T + 8192);
 #pragma unroll
@@ -352,13 +344,30 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
                 tc::mma_bf16_ts(tbase + kColS + 64 * h, tbase + kColA + 8 * i + 32 * part, kn + h * (kPanel >> 4) + 128 * i,
                                 tc::idesc_bf16(128, 64, false, true), 1);
             tc::mma_commit(bar(sm.gs[h]));
-            if (kState && h) tc::mma_commit(bar(sm.empty[s]));
+            if (h) tc::mma_commit(bar(sm.empty[s]));
           }
         __syncwarp();
-        // beta u's part of the output
-        if (!kState && !wait(sm.vready, g)) break;
-        if (!kState && tc::elect_one()) {
-          const uint64_t p = tc::kmajor(T + kPkP);
+      }
+    } else if (!kState && warp == kWarpMmaO) {
+      // ================= o's products: S Q^T behind S K^T, and P beta u
+      constexpr uint32_t kN64 = tc::idesc_bf16(128, 64, false, false);
+      uint32_t g = 0;
+      int left = 0;
+      for (; any_chunk(left); ++g, --left) {
+        const uint32_t s = g % kStages;
+        const uint64_t qk = tc::kmajor(tc::smem_u32(sm.tok[s][1])), p = tc::kmajor(tc::smem_u32(sm.packet[s]) + kPkP);
+        if (!wait(sm.full[s], g / kStages)) break;
+        if (g && !wait(sm.ofree, g - 1)) break;
+        if (!wait(sm.gx, g)) break;
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            tc::mma_bf16_ts(tbase + kColQ, tbase + kColS + 64 * (i >> 2) + 8 * (i & 3), qk + (i >> 2) * (kPanel >> 4) + (i & 3) * 2, kN64, i > 0);
+          tc::mma_commit(bar(sm.gq));
+        }
+        __syncwarp();
+        if (!wait(sm.vready, g)) break;
+        if (tc::elect_one()) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             tc::mma_bf16_ts(tbase + kColO, tbase + kColA + 64 + 8 * i, p + 2 * i, kN64, i > 0);
@@ -633,6 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
         arrive(sm.wready[half]);
         arrive(sm.empty[s]);
         if (!kState) {
+          if (g && !wait(sm.go, g - 1)) break;  // (the last one is read)
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             uint32_t hi[8], lo[8];
