@@ -29,7 +29,8 @@ struct DeltaAux {
   float w[64];     // e^{b_C - b_i}
   float beta[64];  // 0 past the sequence's end
   float whole;     // b_C in base 2
-  float pad[63];
+  float bound;     // log2 of a bound on what the chunk leaves of a state's norm: b_C + sum of max(0, log2 |1 - beta_i k_i . k_i|)
+  float pad[62];
   float a[64];     // decays of the tokens
   float b[64];     // b_i in base 2
 };
@@ -59,9 +60,10 @@ __device__ __forceinline__ DeltaChunk delta_chunk(const DeltaProblem& P, int64_t
 }
 
 // Workspace: packets; of the training pair, the states at the chunks' starts and u from the forward, the states' adjoints at
-// the chunks' ends from the backward; where sequences are cut, what the segments make of zero and of the identity.
+// the chunks' ends from the backward; where sequences are cut, what the segments make of zero and of the identity (and whether
+// that is zero).
 struct DeltaWs {
-  size_t packet, states, u, adjoints, segments, through, total;
+  size_t packet, states, u, adjoints, segments, through, none, total;
 };
 DeltaWs delta_workspace(const DeltaProblem& P, bool training);  // (goes by N, Ttot, Hv, slots and seg)
 

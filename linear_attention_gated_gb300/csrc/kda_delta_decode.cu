@@ -97,8 +97,6 @@ __global__ void __launch_bounds__(kThreads) kda_delta_decode_kernel(const DeltaP
   }
 }
 
-__device__ int32_t g_unused_status;  // (decode reports a bad slot in o)
-
 }  // namespace
 }  // namespace kda
 
@@ -125,7 +123,9 @@ extern "C" kda_status kda_gated_delta_decode(const kda_bf16* q, const kda_bf16* 
     const Span outs[] = {pool_span(pool, Hv), {o, gates * kda::kDim}};
     const Span ins[] = {in[0], in[1], in[2], {log_decay, gates}, {beta, gates}, {state_indices, 4 * (size_t)N}};
     if (aliasing(outs, ins)) return fail(op, KDA_ERR_ALIASING, "an output overlaps an input or another output");
-    if ((st = check_device(op, nullptr, &kda::g_unused_status, &P.status)) != KDA_OK) return st;
+    int32_t none = 0;  // (no status word: the kernel reports a bad slot in o)
+    if ((st = check_device(op, &none, nullptr, &P.status)) != KDA_OK) return st;
+    P.status = nullptr;
     if (N == 0) return KDA_OK;
     P.N = N;
     P.beta = reinterpret_cast<const __nv_bfloat16*>(beta);

@@ -16,7 +16,8 @@
 //
 // Long axis, few units: each sequence is cut into segments. A pass over every segment but the last goes from a state of zero
 // and, without values, from the identity (a chunk takes S to S M + N, whatever S is: so does a segment); a small kernel
-// chains them, and the main pass starts every segment from its state.
+// chains them, and the main pass starts every segment from its state. Where a segment's decays leave nothing of any state, the
+// identity is not followed: with decays of 0.02 to 0.34 a token and head, seven of eight heads over 1728 tokens.
 #include <algorithm>
 
 #include "kda_delta.cuh"
@@ -75,7 +76,8 @@ struct Segments {
   int64_t len;     // tokens of a segment (a multiple of kC), 0: sequences are not cut
   int most;        // most segments of a sequence
   float* state;    // [slots, Hv, 128, 128]: what a segment makes of zero, then the state it starts from
-  float* through;  // [slots, Hv, 128, 128]: what it makes of the identity
+  __nv_bfloat16* through;  // [slots, Hv, 2, 128, 128]: what it makes of the identity, in two parts,
+  int32_t* none;   // [slots, Hv]: 1 where that is zero and was not written
 };
 // Slot of a sequence's first segment: leaves each sequence ceil(len_n / len) slots.
 __device__ __forceinline__ int64_t seg_slot(const Segments& g, int64_t t0, int64_t n) { return t0 / g.len + n; }
@@ -131,6 +133,20 @@ __device__ __forceinline__ Unit unit_of(const PassArgs& a, int u) {
   }
   x.nchunks = x.run ? (int)((x.len + kC - 1) / kC) : 0;
   x.none = false;
+  if (x.identity && x.run) {
+    // Decays that leave less than FP32 holds of the identity (its smallest number is 2^-149): zero, whatever the tokens are.
+    float bound = 0.f;
+    for (int c = threadIdx.x & 31; c < x.nchunks; c += 32)
+      bound += reinterpret_cast<const DeltaAux*>(a.packets + ((x.place + c) * P.Hv + x.h) * (int64_t)a.stride + kPkAux)->bound;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) bound += __shfl_xor_sync(0xffffffffu, bound, k);
+    const bool none = bound < -160.f;
+    if ((threadIdx.x & 31) == 0) a.sg.none[x.sslot * P.Hv + x.h] = none;
+    if (none) {
+      x.run = false;
+      x.nchunks = 0;
+    }
+  }
   return x;
 }
 
@@ -673,8 +689,18 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
         if (c + 1 < x.nchunks) put_state();
       }
       if (!ok) break;
-      if (kState) {
-        float4* dst = reinterpret_cast<float4*>((x.identity ? a.sg.through : a.sg.state) + sat);
+      if (kState && x.identity) {
+        __nv_bfloat16* dst = a.sg.through + 2 * (sat - v * kDim - 64 * half) + v * kDim + 64 * half;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split2(S[4 * j + e], hi[e], lo[e]);
+          *reinterpret_cast<uint4*>(dst + 8 * j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(dst + kDim * kDim + 8 * j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      } else if (kState) {
+        float4* dst = reinterpret_cast<float4*>(a.sg.state + sat);
 #pragma unroll
         for (int j = 0; j < 16; ++j) dst[j] = reinterpret_cast<const float4*>(S)[j];
       } else if (!x.last) {
@@ -699,14 +725,19 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
 }
 
 // Chains the segments of one (sequence, head), x <- x M + N: in, each segment's N and M but the last's; out, the state each
-// segment starts from, in N's place. A CTA takes 16 of the state's 128 rows (independent of each other) and multiplies them with M in
-// four parts of 32 rows, which come through a ring of asynchronous copies. FP32.
-constexpr int kChainRows = 16, kChainThreads = 256, kPart = 32, kParts = kDim / kPart, kChainStages = 3;
-constexpr int kChainSmem = (kChainStages * kPart * kDim + kDim * kChainRows) * 4;
+// segment starts from, in N's place. A CTA takes 32 of the state's 128 rows (independent of each other), a warp 16 columns. x
+// stays in FP32; for the product it and M are in two BF16 parts (mma.sync: the chain is short products one after the other, and x comes
+// out where the next turn's N is loaded). M comes in parts of 32 rows through a ring of asynchronous copies.
+constexpr int kChainRows = 32, kChainThreads = 256, kPart = 32, kParts = kDim / kPart, kChainStages = 6;
+constexpr int kPartBytes = 2 * kPart * kDim * 2;
+constexpr int kChainSmem = kChainStages * kPartBytes + 2 * kChainRows * kDim * 2;
+// Byte of (row, 16-byte piece) in a tile of 256-byte rows.
+__device__ __forceinline__ uint32_t chain_piece(int row, int c) { return row * 256 + ((c ^ (row & 7)) << 4); }
+
 __global__ void __launch_bounds__(kChainThreads) kda_delta_chain_kernel(const __grid_constant__ PassArgs a) {
-  extern __shared__ float chain_smem[];
-  float* M = chain_smem;                                   // [stages][32][128]
-  float* xs = chain_smem + kChainStages * kPart * kDim;    // [128][16]: the rows, transposed
+  extern __shared__ __align__(16) unsigned char chain_smem[];
+  __shared__ uint32_t bad[2];  // bits of the rows that are not finite, of two segments in turn
+  const uint32_t ring = tc::smem_u32(chain_smem), xs = ring + kChainStages * kPartBytes;  // xs: x in two parts, [2][32][128]
   const DeltaProblem& P = a.P;
   const Segments& sg = a.sg;
   const int64_t n = blockIdx.x / P.Hv;
@@ -714,62 +745,136 @@ __global__ void __launch_bounds__(kChainThreads) kda_delta_chain_kernel(const __
   const DecaySpan sp = decay_span(P, n);
   const int64_t slot = a.st.slots ? a.st.slots[n] : n;
   if (slot < 0 || slot >= a.st.num_slots) return;  // the main pass flags it
-  // rows row .. row + 3, columns col and the next
-  const int tid = threadIdx.x, col = 2 * (tid & 63), r0 = 4 * (tid >> 6), row = kChainRows * blockIdx.y + r0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // this thread's values, as products leave them: rows r0 + 8 j, columns c0 + 8 t (and the next)
+  const int r0 = lane >> 2, c0 = 16 * warp + 2 * (lane & 3);
   const int64_t base = seg_slot(sg, sp.t0, n);
   const int64_t m = sp.len > sg.len ? (sp.len + sg.len - 1) / sg.len : 1;
   auto at = [&](int64_t i) { return ((base + i) * P.Hv + h) * kDim * kDim; };
+  auto own = [&](int j, int t) { return (kChainRows * (int)blockIdx.y + r0 + 8 * j) * kDim + c0 + 8 * t; };
+  auto none_of = [&](int64_t i) { return i + 1 < m && sg.none[(base + i) * P.Hv + h] != 0; };
+  bool none = none_of(0), none1 = none_of(1), none2 = none_of(2);  // of segment i and the next two
+  int64_t i = 0;
   auto fetch = [&](int64_t p) {  // part p of all
-    if (p < (m - 1) * kParts) {
-      const float* src = sg.through + at(p / kParts) + (p % kParts) * kPart * kDim;
+    const int64_t k = p / kParts;
+    if (k + 1 < m && !(k == i ? none : k == i + 1 ? none1 : none2)) {
+      const __nv_bfloat16* src = sg.through + 2 * at(k) + (p % kParts) * kPart * kDim;
+      unsigned char* dst = chain_smem + (p % kChainStages) * kPartBytes;
 #pragma unroll
-      for (int k = 0; k < kPart * kDim / 4 / kChainThreads; ++k)
-        tc::cp_async16(M + (p % kChainStages) * kPart * kDim + 4 * (tid + k * kChainThreads), src + 4 * (tid + k * kChainThreads), 16);
+      for (int x = tid; x < kPartBytes / 16; x += kChainThreads) {
+        const int part = x >> 9, row = (x >> 4) & 31, c = x & 15;
+        tc::cp_async16(dst + part * (kPartBytes / 2) + chain_piece(row, c), src + part * kDim * kDim + row * kDim + 8 * c, 16);
+      }
     }
     tc::cp_async_commit();
   };
   for (int p = 0; p < kChainStages - 1; ++p) fetch(p);
-  float2 x[4];
+  if (tid < 2) bad[tid] = 0u;
+  __syncthreads();
+  float2 x[4][2], y1[4][2];
   const int64_t from = (slot * P.Hv + h) * kDim * kDim;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int64_t k = from + (row + r) * kDim + col;
-    if (!a.st.in) x[r] = make_float2(0.f, 0.f);
-    else if (a.st.bf16) x[r] = unpack2(*reinterpret_cast<const uint32_t*>(reinterpret_cast<const __nv_bfloat16*>(a.st.in) + k));
-    else x[r] = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(a.st.in) + k);
-  }
-  for (int64_t i = 0; i < m; ++i) {
-    float* s = sg.state + at(i) + row * kDim + col;
-    float2 y[4];
-    if (i + 1 < m)
+  for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) y[r] = *reinterpret_cast<const float2*>(s + r * kDim);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) *reinterpret_cast<float2*>(s + r * kDim) = x[r];
-    if (i + 1 == m) break;
-    *reinterpret_cast<float4*>(xs + col * kChainRows + r0) = make_float4(x[0].x, x[1].x, x[2].x, x[3].x);
-    *reinterpret_cast<float4*>(xs + (col + 1) * kChainRows + r0) = make_float4(x[0].y, x[1].y, x[2].y, x[3].y);
-#pragma unroll 1
-    for (int p = 0; p < kParts; ++p) {
-      const int64_t at_part = i * kParts + p;
-      tc::cp_async_wait<kChainStages - 2>();
-      __syncthreads();  // the part is there for all (and xs); the one before is read
-      fetch(at_part + kChainStages - 1);
-      const float* Mp = M + (at_part % kChainStages) * kPart * kDim + col;
-      const float* xp = xs + p * kPart * kChainRows + r0;
-#pragma unroll 16
-      for (int k = 0; k < kPart; ++k) {
-        const float4 q = *reinterpret_cast<const float4*>(xp + k * kChainRows);
-        const float2 w = *reinterpret_cast<const float2*>(Mp + k * kDim);
-        y[0] = tc::fma2(make_float2(q.x, q.x), w, y[0]);
-        y[1] = tc::fma2(make_float2(q.y, q.y), w, y[1]);
-        y[2] = tc::fma2(make_float2(q.z, q.z), w, y[2]);
-        y[3] = tc::fma2(make_float2(q.w, q.w), w, y[3]);
-      }
+    for (int t = 0; t < 2; ++t) {
+      const int64_t k = from + own(j, t);
+      if (!a.st.in) x[j][t] = make_float2(0.f, 0.f);
+      else if (a.st.bf16) x[j][t] = unpack2(*reinterpret_cast<const uint32_t*>(reinterpret_cast<const __nv_bfloat16*>(a.st.in) + k));
+      else x[j][t] = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(a.st.in) + k);
     }
+  auto load = [&](int64_t k) {  // N of segment k
+    if (k + 1 < m)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) x[r] = y[r];
-    __syncthreads();  // xs is read
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) y1[j][t] = *reinterpret_cast<const float2*>(sg.state + at(k) + own(j, t));
+  };
+  load(0);
+  for (; i < m; ++i) {
+    float2 y[4][2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        y[j][t] = y1[j][t];
+        *reinterpret_cast<float2*>(sg.state + at(i) + own(j, t)) = x[j][t];
+      }
+    if (i + 1 == m) break;
+    load(i + 1);
+    if (none) {
+      // M is zero: what is not finite gives NaN for its row, as a product would
+      uint32_t found = 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) found |= isfinite(x[j][t].x) && isfinite(x[j][t].y) ? 0u : 1u << (r0 + 8 * j);
+      if (found) atomicOr(&bad[i & 1], found);
+      __syncthreads();
+      const uint32_t rows = bad[i & 1];
+      const float nan = __int_as_float(0x7fc00000);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (rows >> (r0 + 8 * j) & 1u) y[j][0] = y[j][1] = make_float2(nan, nan);
+      for (int p = 0; p < kParts; ++p) fetch(i * kParts + p + kChainStages - 1);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          uint32_t hi, lo;
+          split2(x[j][t], hi, lo);
+          const uint32_t to = xs + chain_piece(r0 + 8 * j, 2 * warp + t) + 4 * (lane & 3);
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(hi) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + kChainRows * 256), "r"(lo) : "memory");
+        }
+      float acc[2][2][4] = {}, cross[2][2][4] = {};  // [16 rows][8 columns]: of the high parts, of a high and a low one
+#pragma unroll 1
+      for (int p = 0; p < kParts; ++p) {
+        const int64_t at_part = i * kParts + p;
+        tc::cp_async_wait<kChainStages - 2>();
+        __syncthreads();  // the part is there for all (and xs); the one before is read
+        fetch(at_part + kChainStages - 1);
+        const uint32_t Mp = ring + (uint32_t)(at_part % kChainStages) * kPartBytes;
+        const int lr = (lane & 7) + 8 * ((lane >> 3) & 1), lc = lane >> 4;  // row and piece this lane gives the address of
+#pragma unroll
+        for (int k = 0; k < kPart / 16; ++k) {
+          uint32_t bh[4], bl[4], ah[2][4], al[2][4];
+          const uint32_t b = Mp + chain_piece(16 * k + lr, 2 * warp + lc);
+          tc::ldmatrix4_trans(b, bh);
+          tc::ldmatrix4_trans(b + kPartBytes / 2, bl);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t ax = xs + chain_piece(16 * q + lr, 2 * (p * (kPart / 16) + k) + lc);
+            tc::ldmatrix4(ax, ah[q]);
+            tc::ldmatrix4(ax + kChainRows * 256, al[q]);
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              tc::mma_sync(acc[q][t], ah[q], bh + 2 * t);
+              tc::mma_sync(cross[q][t], ah[q], bl + 2 * t);
+              tc::mma_sync(cross[q][t], al[q], bh + 2 * t);
+            }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float* c = acc[j >> 1][t] + 2 * (j & 1);
+          const float* d = cross[j >> 1][t] + 2 * (j & 1);
+          y[j][t] = make_float2(y[j][t].x + (c[0] + d[0]), y[j][t].y + (c[1] + d[1]));
+        }
+      __syncthreads();  // xs is read
+    }
+    none = none1;
+    none1 = none2;
+    none2 = none_of(i + 3);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) x[j][t] = y[j][t];
   }
   tc::cp_async_wait_all();
 }
@@ -820,7 +925,8 @@ cudaError_t forward(const DeltaProblem& P, const DecayStates& st, __nv_bfloat16*
       a.first[t + 1] = a.first[t] + (int32_t)have;
     }
     a.sg.state = reinterpret_cast<float*>(ws + w.segments);
-    a.sg.through = reinterpret_cast<float*>(ws + w.through);
+    a.sg.through = reinterpret_cast<__nv_bfloat16*>(ws + w.through);
+    a.sg.none = reinterpret_cast<int32_t*>(ws + w.none);
     if ((e = launch<false, true>(maps, a, s)) != cudaSuccess) return e;
     if ((e = cudaFuncSetAttribute(kda_delta_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kChainSmem)) != cudaSuccess) return e;
     kda_delta_chain_kernel<<<dim3((unsigned)(P.N * P.Hv), kDim / kChainRows), kChainThreads, kChainSmem, s>>>(a);

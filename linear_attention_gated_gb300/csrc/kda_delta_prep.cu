@@ -37,6 +37,7 @@ struct Smem {
   DeltaAux aux;
   float far[2][kC];               // e^{-b_j} beta_j, e^{-b_j}
   unsigned long long full, done;
+  float growth[2];                // of the rows of each of two warps: sum of max(0, log2 |1 - beta_i k_i . k_i|)
   uint32_t tmem;
 };
 constexpr int kSmemBytes = (int)sizeof(Smem) + 1024;
@@ -46,18 +47,16 @@ __device__ __forceinline__ float token_decay(float x) {
   return fabsf(x) < 0.5f ? 1.f + expm1f(x * 0.6931471805599453f) : fast_exp2(x);
 }
 
+// x = y where i == j (in C++ it becomes an indexed read of y's array, through local memory: 439 us instead of 130).
+__device__ __forceinline__ void take_if(float& x, int i, int j, float y) {
+  asm("{\n .reg .pred p;\n setp.eq.s32 p, %1, %2;\n @p mov.f32 %0, %3;\n}\n" : "+f"(x) : "r"(i), "r"(j), "f"(y));
+}
+
 // acc += A B for a 16 x 8 tile over 16 inner values, BF16 operands each in two parts (low x low left out).
 __device__ __forceinline__ void mma_split(float* c, const uint32_t* ah, const uint32_t* al, const uint32_t* bh, const uint32_t* bl) {
-  auto mma = [&](const uint32_t* a, const uint32_t* b) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-  };
-  mma(ah, bl);
-  mma(al, bh);
-  mma(ah, bh);
-}
-__device__ __forceinline__ void ldmatrix4(uint32_t saddr, uint32_t* r) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(saddr) : "memory");
+  tc::mma_sync(c, ah, bl);
+  tc::mma_sync(c, al, bh);
+  tc::mma_sync(c, ah, bh);
 }
 // Byte of (row, 16-byte piece) in a tile of 128-byte rows, swizzled.
 __device__ __forceinline__ uint32_t piece(int row, int c) { return row * 128 + ((c ^ (row & 7)) << 4); }
@@ -153,6 +152,7 @@ __global__ void __launch_bounds__(128, 6) kda_delta_prep_kernel(const __grid_con
   const bool range = sm.aux.whole > -100.f && nt == kC;
   const float bi = sm.aux.eb[i];
   float d = 0.f, a1 = 0.f;
+  float own = 0.f;  // beta_i k_i . k_i
 #pragma unroll 1
   for (int m = 2 * hw + 1; m >= 0; --m) {
     float r[16];
@@ -170,7 +170,10 @@ __global__ void __launch_bounds__(128, 6) kda_delta_prep_kernel(const __grid_con
       }
       if (m >= 2 * hw)  // (the other half lies before all of its rows)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) r[j] = j <= last ? r[j] : 0.f;
+        for (int j = 0; j < 16; ++j) {
+          take_if(own, j, last + 1, r[j]);
+          r[j] = j <= last ? r[j] : 0.f;
+        }
     } else {
 #pragma unroll
       for (int q = 3; q >= 0; --q) {
@@ -183,7 +186,9 @@ __global__ void __launch_bounds__(128, 6) kda_delta_prep_kernel(const __grid_con
           d = 16 * m + j == i ? 1.f : d * a1;
           a1 = av[e];
           // (selected, not multiplied: rows past the end may hold anything)
-          r[j] = j <= last ? r[j] * (bv[e] * d) : 0.f;
+          r[j] *= bv[e] * d;
+          take_if(own, 16 * m + j, i, r[j]);
+          r[j] = j <= last ? r[j] : 0.f;
         }
       }
     }
@@ -212,6 +217,12 @@ __global__ void __launch_bounds__(128, 6) kda_delta_prep_kernel(const __grid_con
   const uint32_t Ts = tc::smem_u32(T);
   const int r8 = lane & 7, q1 = (lane >> 3) & 1, q2 = lane >> 4;  // row and place of the 8 x 8 matrix whose address this lane gives
   if (keys) {
+    // (a little more, for the factors' roundings; NaN stays)
+    float grown = i < nt ? __log2f(fabsf(1.f - own)) : 0.f;
+    grown = grown < 0.f ? 1e-4f : grown + 1e-4f;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) grown += __shfl_xor_sync(0xffffffffu, grown, k);
+    if (lane == 0) sm.growth[w] = grown;
     // the blocks on the diagonal, a column a thread: t_l -= A_lj t_j for l > j once t_j is known
     __syncwarp();
     const int blk = lane >> 4, col = lane & 15;
@@ -246,13 +257,13 @@ __global__ void __launch_bounds__(128, 6) kda_delta_prep_kernel(const __grid_con
     const uint32_t t11 = Ts + piece(32 * w + 16 + 8 * q1 + r8, 4 * w + 2 + q2);
     tc::ldmatrix4_trans(t00, ah);
     tc::ldmatrix4_trans(t00 + 8192, al);
-    ldmatrix4(a10, bh);
-    ldmatrix4(a10 + 8192, bl);
+    tc::ldmatrix4(a10, bh);
+    tc::ldmatrix4(a10 + 8192, bl);
     float y[2][4] = {};
     mma_split(y[0], ah, al, bh, bl);
     mma_split(y[1], ah, al, bh + 2, bl + 2);
-    ldmatrix4(t11, ah);
-    ldmatrix4(t11 + 8192, al);
+    tc::ldmatrix4(t11, ah);
+    tc::ldmatrix4(t11 + 8192, al);
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       split2(make_float2(y[0][2 * n], y[0][2 * n + 1]), bh[0], bl[0]);
@@ -285,8 +296,8 @@ __global__ void __launch_bounds__(128, 6) kda_delta_prep_kernel(const __grid_con
         for (int n = 0; n < 4; n += 2) {
           uint32_t ch[4], cl[4];
           const uint32_t a21 = Ts + piece(8 * n + 8 * q2 + r8, 4 + 2 * k + q1);
-          ldmatrix4(a21, ch);
-          ldmatrix4(a21 + 8192, cl);
+          tc::ldmatrix4(a21, ch);
+          tc::ldmatrix4(a21 + 8192, cl);
           mma_split(y[n], ah, al, ch, cl);
           mma_split(y[n + 1], ah, al, ch + 2, cl + 2);
         }
@@ -311,8 +322,8 @@ __global__ void __launch_bounds__(128, 6) kda_delta_prep_kernel(const __grid_con
         for (int k = 0; k <= m; ++k) {
           uint32_t ah[4], al[4];
           const uint32_t t22 = Ts + piece(32 + 16 * m + 8 * q1 + r8, 4 + 2 * k + q2);
-          ldmatrix4(t22, ah);
-          ldmatrix4(t22 + 8192, al);
+          tc::ldmatrix4(t22, ah);
+          tc::ldmatrix4(t22 + 8192, al);
 #pragma unroll
           for (int n = 0; n < 2; ++n) mma_split(z[n], ah, al, bh[n] + 2 * k, bl[n] + 2 * k);
         }
@@ -329,6 +340,7 @@ __global__ void __launch_bounds__(128, 6) kda_delta_prep_kernel(const __grid_con
       }
     }
   }
+  if (tid == 0) sm.aux.bound = sm.aux.whole + (sm.growth[0] + sm.growth[1]);
   tc::fence_async_smem();
   tc::fence_before();
   __syncthreads();
@@ -370,7 +382,8 @@ DeltaWs delta_workspace(const DeltaProblem& P, bool training) {
   w.segments = w.adjoints + (training ? n * kStateTile : 0);
   const size_t cut = P.seg ? sizeof(float) * (size_t)(P.Ttot / P.seg + P.N) * P.Hv * kDim * kDim : 0;
   w.through = w.segments + cut;
-  w.total = w.through + cut;
+  w.none = w.through + cut;
+  w.total = w.none + ctx_align_up(cut / (kDim * kDim));
   return w;
 }
 

@@ -128,6 +128,16 @@ __device__ __forceinline__ void stmatrix4_trans(uint32_t saddr, uint32_t r0, uin
                : "memory");
 }
 
+// Four 8 x 8 matrices of 16-bit values from shared memory, as an operand of mma_sync lies.
+__device__ __forceinline__ void ldmatrix4(uint32_t saddr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(saddr) : "memory");
+}
+// c += a b, a warp's 16 x 8 tile over 16 inner values: for products too small for a tcgen05 tile.
+__device__ __forceinline__ void mma_sync(float* c, const uint32_t* a, const uint32_t* b) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
 // The reverse: four 8 x 8 matrices of 16-bit values, each transposed on its way to registers.
 __device__ __forceinline__ void ldmatrix4_trans(uint32_t saddr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"

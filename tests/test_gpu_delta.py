@@ -10,7 +10,8 @@ and five its adjoint (G, P, d, T, rho), and solving the triangular system of key
 Single values: every operand's error is relative to the operand, and all operands of a value belong to its own token (its
 row of 128 values): with u or rho ten times the usual length in a token, the roundings of that token's gradients are ten
 times the usual too, also in the values that happen to be small. So a value is held to half a step of its own and six
-of its row's rms (or the tensor's, where that is more); tokens' scalars to the tensor's. A scalar is a sum of products that
+of its row's rms (or the tensor's, where that is more); tokens' scalars to their head's (or the tensor's): a head's numbers come
+from its own states, and those of slow decays are larger than the others'. A scalar is a sum of products that
 may come out far smaller than they are: dg has <G, S>, 128^2 products of two states' values, rms 128 STATE^2, and dbeta
 u . (G k), 128 products of values of 1 and of STATE, rms sqrt(128) STATE. Few scalars are held to the rms that such sums have.
 """
@@ -115,6 +116,8 @@ def check_rows(name, x, ref, rel):
     assert off <= rel, (name, off.item(), rel)
     if ref.dim() == 4:
         size = torch.maximum(size, ref.square().mean(-1, keepdim=True).sqrt())
+    elif name in SCALAR:
+        size = torch.maximum(size, ref.square().mean((0, 1), keepdim=True).sqrt())
     bad = (x - ref).abs() > BF16 * ref.abs() + 6 * BF16 * torch.maximum(size, ref.abs())
     assert not bad.any(), (name, int(bad.sum()))
 
