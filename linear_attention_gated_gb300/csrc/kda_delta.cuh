@@ -31,18 +31,18 @@ struct DeltaAux {
   float whole;     // b_C in base 2
   float bound;     // log2 of a bound on what the chunk leaves of a state's norm: b_C + sum of max(0, log2 |1 - beta_i k_i . k_i|)
   float pad[62];
-  float a[64];     // decays of the tokens
   float b[64];     // b_i in base 2
 };
 constexpr uint32_t kPkPass = kPkAux + 1024;  // what the forward's pass reads: up to `whole`
-static_assert(sizeof(DeltaAux) <= kPkPlo - kPkAux && offsetof(DeltaAux, a) == 1024, "a chunk's numbers");
+static_assert(sizeof(DeltaAux) <= kPkPlo - kPkAux && offsetof(DeltaAux, b) == 1024, "a chunk's numbers");
 
 constexpr uint32_t kStateTile = 32768, kUTile = 16384;  // a state in BF16 [2][128 rows][64], u [2][64 tokens][64], swizzled
 
 // Place of a sequence's first chunk: leaves each sequence ceil(len / 64) places.
 __host__ __device__ __forceinline__ int64_t delta_slot(int64_t t0, int64_t n) { return t0 / kDecayChunk + n; }
 
-// The chunk of a place, as a kernel for all chunks side by side finds it: nt <= 0 where there is none.
+// The chunk of a place, as a kernel for all chunks side by side finds it: nt <= 0 where there is none. A warp looks for it, 32
+// sequences at a time (one by one the loads take 2000 cycles).
 struct DeltaChunk {
   int64_t t0;
   int nt;
@@ -50,9 +50,10 @@ struct DeltaChunk {
 __device__ __forceinline__ DeltaChunk delta_chunk(const DeltaProblem& P, int64_t slot) {
   int64_t lo = 0, hi = P.N;  // the last sequence whose first place is not behind this one
   while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) / 2;
-    if (delta_slot(decay_span(P, mid).t0, mid) <= slot) lo = mid;
-    else hi = mid;
+    const int64_t step = (hi - lo + 31) / 32, mid = lo + (threadIdx.x & 31) * step;
+    const uint32_t b = __ballot_sync(0xffffffffu, mid < hi && delta_slot(decay_span(P, mid).t0, mid) <= slot);
+    lo += b ? (31 - __clz(b)) * step : 0;
+    hi = lo + step < hi ? lo + step : hi;
   }
   const DecaySpan sp = decay_span(P, lo);
   const int64_t c = slot - delta_slot(sp.t0, lo), left = sp.len - c * kDecayChunk;
