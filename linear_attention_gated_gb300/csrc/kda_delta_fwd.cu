@@ -56,18 +56,23 @@ struct Unit {
 
 struct Smem {
   unsigned char tok[kStages][3][kTile];  // K, Q, V
-  unsigned char packet[kStages][kPkInfer];
+  unsigned char packet[kStages][kPkPass];
   unsigned char out[kTile];              // o on its way out
-  unsigned char u[kUTile];               // training: u on its way out,
-  unsigned char S[kStateTile];           // and the state in BF16
+  union {
+    struct {
+      unsigned char u[kUTile];           // training: u on its way out,
+      unsigned char S[kStateTile];       // and the state in BF16
+    };
+    unsigned char state[4 * kDim * kDim];  // serving: the state that the next unit starts from, in boxes of 128 bytes of a row
+  };
   uint4 clc;
   Unit ring[kRing];
-  unsigned long long full[kStages], empty[kStages], raw, sready[2], gx, xready[2], gu[2], gq, wready[2], gs[2], vready, go, ofree, ufree, scopied;
+  unsigned long long full[kStages], empty[kStages], raw, sfull, sempty, fready, ffree, sready[2], gx, xready[2], gu[2], gq, wready[2], gs[2], vready, go, ofree, ufree, scopied;
   unsigned long long clcbar, rfull[kRing], rempty[kRing];
   uint32_t tmem;
 };
-constexpr int kSmemBytes = (int)sizeof(Smem) + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
+constexpr int kSmemBytes = (int)sizeof(Smem);
+static_assert(kSmemBytes <= 227 * 1024 && kPkPass % 1024 == 0, "shared memory of a CTA");
 
 constexpr int kOrder = 512;      // sequences whose order is passed (more run in index order, whole)
 constexpr int kMost = 4 * kSms;  // most segments of a sequence
@@ -96,7 +101,7 @@ struct PassArgs {
   uint16_t order[kOrder];  // longest sequence first
 };
 struct Maps {
-  CUtensorMap q, k, v, o;
+  CUtensorMap q, k, v, o, st;
 };
 
 __device__ __forceinline__ float* regs(uint32_t* x) { return reinterpret_cast<float*>(x); }
@@ -153,9 +158,17 @@ __device__ __forceinline__ Unit unit_of(const PassArgs& a, int u) {
 // kTrain: states and u are saved. kState: the pass over segments (states alone).
 template <bool kTrain, bool kState>
 __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PassArgs a) {
-  extern __shared__ unsigned char raw_smem[];
-  Smem& sm = *reinterpret_cast<Smem*>(raw_smem + ((1024 - (tc::smem_u32(raw_smem) & 1023)) & 1023));
+  extern __shared__ __align__(1024) unsigned char raw_smem[];
+  Smem& sm = *reinterpret_cast<Smem*>(raw_smem);
   const DeltaProblem& P = a.P;
+  if (tc::smem_u32(raw_smem) & 1023) {  // (never: the tiles' swizzle needs the alignment that is asked for, and there is no room for more)
+    if (threadIdx.x == 0) atomicOr(P.status, 1);
+    return;
+  }
+  // Serving: a unit's start state comes by tiled copies, while the unit before it is worked on. (Loaded by the warps that need it,
+  // behind the tiles that are on their way, it took two chunks' time.)
+  const bool staged = !kTrain && !kState && (a.sg.len || a.st.in);
+  const uint32_t state_bytes = a.sg.len || !a.st.bf16 ? 4 * kDim * kDim : 2 * kDim * kDim;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto bar = [](unsigned long long& b) { return tc::smem_u32(&b); };
 
@@ -167,9 +180,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
       init(sm.sready[i], 4); init(sm.xready[i], 4); init(sm.wready[i], 4);
       init(sm.gu[i], 1); init(sm.gs[i], 1);
     }
-    init(sm.raw, 1); init(sm.gx, 1); init(sm.gq, 1); init(sm.vready, 8); init(sm.go, 1); init(sm.ofree, 8); init(sm.ufree, 8);
+    init(sm.raw, 1); init(sm.sfull, 1); init(sm.sempty, 8); init(sm.fready, 8); init(sm.ffree, 8); init(sm.gx, 1); init(sm.gq, 1); init(sm.vready, 8); init(sm.go, 1); init(sm.ofree, 8); init(sm.ufree, 8);
     init(sm.scopied, 8); init(sm.clcbar, 1);
-    for (int i = 0; i < kRing; ++i) { init(sm.rfull[i], 1); init(sm.rempty[i], kState ? 9 : 18); }
+    for (int i = 0; i < kRing; ++i) { init(sm.rfull[i], 1); init(sm.rempty[i], kState ? 17 : 18); }
   }
   tc::fence_before();
   __syncthreads();
@@ -194,12 +207,19 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
     ++ur;
     return !x.none;
   };
-  // A consumer that sees chunks alone: is there one more, `left` those of the unit at hand?
+  // A unit whose end state leaves by way of the warps that store o. (In training there are few units to an SM, and that would
+  // come after the last one.)
+  auto keeps = [&](const Unit& x) { return !kTrain && x.run && (kState || (x.last && a.st.out)); };
+  // A consumer that sees chunks alone: is there one more, `left` those of the unit at hand? kept: end states before this unit's.
+  uint32_t kept = 0;
+  bool keep_this = false;
   auto any_chunk = [&](int& left) {
     Unit x;
     while (left == 0) {
       if (!next_unit(x)) return false;
       left = x.nchunks;
+      kept += keep_this;
+      keep_this = keeps(x);
     }
     return true;
   };
@@ -226,7 +246,22 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
         }
         __syncwarp();
       };
+      uint32_t loaded = 0;  // states
+      auto load_state = [&](const Unit& x) {
+        if (!staged || !x.run || !ok) return;
+        if (loaded) ok = tc::mbar_wait_lanes(bar(sm.sempty), (loaded - 1) & 1);
+        if (!ok) return;
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(bar(sm.sfull), state_bytes);
+          const int each = state_bytes == 4 * kDim * kDim ? 32 : 64;
+          for (int b = 0; b < kDim / each; ++b)
+            tc::tma_load4(tc::smem_u32(sm.state) + b * 16384, &maps.st, b * each, 0, x.h, (int)(a.sg.len ? x.sslot : x.slot), bar(sm.sfull));
+        }
+        __syncwarp();
+        ++loaded;
+      };
       Unit x = unit_of<kState>(a, (int)blockIdx.x), next;
+      load_state(x);
       push(x);
       ask();
       for (;;) {
@@ -249,7 +284,10 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
             __syncwarp();
             if (more) next = unit_of<kState>(a, (int)nx);
             push(next);
-            if (ok && more) ask();
+            if (ok && more) {
+              ask();
+              load_state(next);
+            }
           }
           if (!ok || c == x.nchunks) break;
           const uint32_t s = g % kStages;
@@ -291,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
         if (lane == 0) atomicOr(P.status, 1);
         tc::mbar_wait_lanes(bar(sm.clcbar), asked & 1, 1u << 16);
         if (tails) tc::mbar_wait_lanes(bar(sm.raw), (tails - 1) & 1, 1u << 16);
+        if (loaded) tc::mbar_wait_lanes(bar(sm.sfull), (loaded - 1) & 1, 1u << 16);
         for (uint32_t k = g > kStages ? g - kStages : 0; k < g; ++k) tc::mbar_wait_lanes(bar(sm.full[k % kStages]), (k / kStages) & 1, 1u << 16);
       }
     } else if (warp == kWarpMma) {
@@ -319,7 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
           __syncwarp();
         }
         if (!ok) break;
-        // T x: what the first 32 tokens give to all, what the others give to themselves
+        // T x: what the first 32 tokens give to all, what the others give to themselves (an end state in its place has been read)
+        if (kept && !wait(sm.ffree, kept - 1)) break;
         const uint64_t th = tc::kmajor(T), tlo = tc::kmajor(T + 8192);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -419,10 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
       }
     };
     uint32_t g = 0;
-    for (Unit x; !kState;) {
+    for (Unit x;;) {
       const bool more = next_unit(x);
       if (!agree() || !more) break;
-      for (int c = 0; c < x.nchunks; ++c, ++g) {
+      for (int c = 0; !kState && c < x.nchunks; ++c, ++g) {
         const int nt = (int)(x.len - (int64_t)c * kC < kC ? x.len - (int64_t)c * kC : kC);
         const int64_t t0 = x.t0 + (int64_t)c * kC;
         const uint32_t s = g % kStages;
@@ -519,6 +559,43 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
         }
       }
       if (!ok) break;
+      if (!keeps(x)) continue;
+      // the end state
+      wait(sm.fready, kept);
+      const int64_t to = ((kState ? x.sslot : x.slot) * P.Hv + x.h) * kDim * kDim;
+      const int at = (32 * wq + lane) * kDim + 64 * half;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        float r[16];
+        tc::tmem_ld16(tl + (half ? kColA + 64 : kColU) + 16 * m, r);
+        if (m == 3) {
+          tc::fence_before();
+          arrive(sm.ffree);
+        }
+        if (!ok) break;
+        uint32_t hi[8], lo[8];
+        if (kState && x.identity) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) split2(make_float2(r[2 * e], r[2 * e + 1]), hi[e], lo[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) hi[e] = pack2(make_float2(r[2 * e], r[2 * e + 1]));
+        }
+        if (kState ? !x.identity : !a.st.bf16) {
+          float4* dst = reinterpret_cast<float4*>((kState ? a.sg.state : reinterpret_cast<float*>(a.st.out)) + to + at + 16 * m);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) dst[j] = make_float4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+        } else {
+          __nv_bfloat16* dst = kState ? a.sg.through + 2 * to + at + 16 * m : reinterpret_cast<__nv_bfloat16*>(a.st.out) + to + at + 16 * m;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            reinterpret_cast<uint4*>(dst)[j] = make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
+            if (kState) reinterpret_cast<uint4*>(dst + kDim * kDim)[j] = make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
+          }
+        }
+      }
+      ++kept;
+      if (!agree()) break;
     }
     if (warp == kWarpOut && lane == 0) tc::bulk_wait();
     if (!ok && lane == 0) atomicOr(P.status, 1);
@@ -529,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
     const int v = 32 * wq + lane;  // state row of this thread, its columns 64 half .. + 63
     const uint32_t tl = tbase + ((uint32_t)(32 * wq) << 16);
     const int j0 = 32 * half + 2 * (lane & 3);
-    uint32_t g = 0;
+    uint32_t g = 0, states = 0;
     for (Unit x; next_unit(x);) {
       if (!x.run) {
         if (kState) continue;
@@ -545,26 +622,38 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
 #pragma unroll
         for (int j = 0; j < 32; ++j)
           S[j] = make_float2(x.identity && v == 64 * half + 2 * j ? 1.f : 0.f, x.identity && v == 64 * half + 2 * j + 1 ? 1.f : 0.f);
-      } else if (a.sg.len) {
+      } else if (kTrain && a.sg.len) {
         const float4* src = reinterpret_cast<const float4*>(a.sg.state + sat);
 #pragma unroll
         for (int j = 0; j < 16; ++j) reinterpret_cast<float4*>(S)[j] = src[j];
-      } else if (!a.st.in) {
+      } else if (!a.st.in && !a.sg.len) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) S[j] = make_float2(0.f, 0.f);
-      } else if (!a.st.bf16) {
+      } else if (kTrain) {  // (FP32 there)
         const float4* src = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.st.in) + at);
 #pragma unroll
         for (int j = 0; j < 16; ++j) reinterpret_cast<float4*>(S)[j] = src[j];
       } else {
-        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.st.in) + at);
+        if (!wait(sm.sfull, states)) break;
+        ++states;
+        const unsigned char* row = sm.state + v * 128;
+        if (state_bytes == 4 * kDim * kDim) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 r = src[j];
-          S[4 * j] = unpack2(r.x); S[4 * j + 1] = unpack2(r.y); S[4 * j + 2] = unpack2(r.z); S[4 * j + 3] = unpack2(r.w);
+          for (int j = 0; j < 16; ++j)
+            reinterpret_cast<float4*>(S)[j] = *reinterpret_cast<const float4*>(row + (2 * half + (j >> 3)) * 16384 + (((j & 7) ^ (v & 7)) << 4));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint4 r = *reinterpret_cast<const uint4*>(row + half * 16384 + ((j ^ (v & 7)) << 4));
+            S[4 * j] = unpack2(r.x); S[4 * j + 1] = unpack2(r.y); S[4 * j + 2] = unpack2(r.z); S[4 * j + 3] = unpack2(r.w);
+          }
         }
+        arrive(sm.sempty);
       }
-      auto put_state = [&] {  // as the next chunk's operand
+      StateFactor factor;
+      for (int c = 0; c < x.nchunks; ++c, ++g) {
+        // the state as an operand (here, not where it comes from: there are two such places, and code that runs once a unit
+        // comes to the instruction cache anew each time)
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           uint32_t hi[8], lo[8];
@@ -576,10 +665,6 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
         tc::tmem_wait_st();
         tc::fence_before();
         arrive(sm.sready[half]);
-      };
-      StateFactor factor;
-      if (x.nchunks) put_state();
-      for (int c = 0; c < x.nchunks; ++c, ++g) {
         const uint32_t s = g % kStages;
         const DeltaAux& aux = *reinterpret_cast<const DeltaAux*>(sm.packet[s] + kPkAux);
         if (!wait(sm.full[s], g / kStages)) break;
@@ -658,7 +743,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
         arrive(sm.wready[half]);
         arrive(sm.empty[s]);
         if (!kState) {
-          if (g && !wait(sm.go, g - 1)) break;  // (the last one is read)
+          if (g && !wait(sm.go, g - 1)) break;  // (the last one is read, and so is an end state)
+          if (kept && !wait(sm.ffree, kept - 1)) break;
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             uint32_t hi[8], lo[8];
@@ -686,33 +772,24 @@ __global__ void __launch_bounds__(kThreads, 1) kda_delta_fwd_kernel(const __grid
             S[8 * m + 8 + j] = tc::fma2(lam, S[8 * m + 8 + j], make_float2(z[2 * j], z[2 * j + 1]));
           }
         }
-        if (c + 1 < x.nchunks) put_state();
       }
       if (!ok) break;
-      if (kState && x.identity) {
-        __nv_bfloat16* dst = a.sg.through + 2 * (sat - v * kDim - 64 * half) + v * kDim + 64 * half;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) split2(S[4 * j + e], hi[e], lo[e]);
-          *reinterpret_cast<uint4*>(dst + 8 * j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(dst + kDim * kDim + 8 * j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-      } else if (kState) {
-        float4* dst = reinterpret_cast<float4*>(a.sg.state + sat);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) dst[j] = reinterpret_cast<const float4*>(S)[j];
-      } else if (!x.last) {
-      } else if (a.st.out && !a.st.bf16) {
+      if (kTrain && x.run && x.last) {
         float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.st.out) + at);
 #pragma unroll
         for (int j = 0; j < 16; ++j) dst[j] = reinterpret_cast<const float4*>(S)[j];
-      } else if (a.st.out) {
-        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.st.out) + at);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dst[j] = make_uint4(pack2(S[4 * j]), pack2(S[4 * j + 1]), pack2(S[4 * j + 2]), pack2(S[4 * j + 3]));
       }
+      if (!keeps(x)) continue;
+      // By way of tensor memory, in u's place and beta u's. (Stored from here, behind the tiles that are on their way, it took a
+      // chunk's time.)
+      if (!kState && half == 1 && g && !wait(sm.go, g - 1)) break;
+      if (kept && !wait(sm.ffree, kept - 1)) break;
+#pragma unroll
+      for (int m = 0; m < 8; ++m) tc::tmem_st8(tl + (half ? kColA + 64 : kColU) + 8 * m, reinterpret_cast<const uint32_t*>(S + 4 * m));
+      tc::tmem_wait_st();
+      tc::fence_before();
+      arrive(sm.fready);
+      ++kept;
     }
     if (!ok && lane == 0) atomicOr(P.status, 1);
   }
@@ -916,6 +993,11 @@ cudaError_t forward(const DeltaProblem& P, const DecayStates& st, __nv_bfloat16*
     std::stable_sort(a.order, a.order + P.N, [&](uint16_t i, uint16_t j) { return len(i) > len(j); });
   }
   a.sg.most = 1;
+  if (!kTrain && P.seg) {
+    if ((e = state_map(&maps.st, ws + w.segments, false, P.Hv, P.Ttot / P.seg + P.N)) != cudaSuccess) return e;
+  } else if (!kTrain && st.in) {
+    if ((e = state_map(&maps.st, st.in, st.bf16, P.Hv, st.num_slots)) != cudaSuccess) return e;
+  }
   if (P.seg) {
     a.sg.len = P.seg;
     a.sg.most = (int)((P.longest + P.seg - 1) / P.seg);

@@ -106,6 +106,12 @@ __device__ __forceinline__ void tma_load3(uint32_t dst_smem, const void* map, in
       ::"r"(dst_smem), "l"(map), "r"(mbar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+__device__ __forceinline__ void tma_load4(uint32_t dst_smem, const void* map, int x, int y, int z, int w, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+      ::"r"(dst_smem), "l"(map), "r"(mbar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
 // Tiled copy shared -> global of a 3-D box (all coordinates inside the tensor), and its bookkeeping by the
 // thread that starts it.
 __device__ __forceinline__ void tma_store3(const void* map, uint32_t src_smem, int x, int y, int z) {
