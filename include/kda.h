@@ -550,12 +550,17 @@ kda_status kda_qk_norm_rope_bwd(const void* dq, const void* dk, const void* q, c
  * its triangular system in FP32; what enters a state or is solved from one is taken in two
  * BF16 parts (16 bits), states are FP32: what a call leaves in FP32 states is within 1e-5 of the
  * exact (relative, in the 2-norm) for keys of norm 1. o, dq, dk, dv, dlog_decay and dbeta are
- * rounded to BF16 from operands that were rounded to BF16 once: within 5e-3. A decode step is FP32
- * throughout. Results do not depend on the order of execution. A NaN or infinity of a token stays
- * in its sequence, but may reach all tokens of its chunk (64 tokens from the sequence's first). */
+ * rounded to BF16 from operands that were rounded to BF16 once: within 5e-3. (Where all keys of a
+ * chunk point nearly the same way, sums of up to 64 terms come out small: up to ten times these
+ * errors, and with beta near 2, which turns such a key's value round at every token, up to 2e-3 in
+ * the states.) A decode step is FP32 throughout. Results do not depend on the order of execution. A
+ * NaN or infinity of a token stays in its sequence, but may reach all tokens of its chunk (64
+ * tokens from the sequence's first). */
 
-/* Bytes of device workspace (256-byte aligned, possibly 0): `training` 1 for
- * kda_gated_delta_fwd and _bwd, 0 for kda_gated_delta_prefill. */
+/* Bytes of device workspace (256-byte aligned, 0 without tokens): `training` 1 for
+ * kda_gated_delta_fwd and _bwd, 0 for kda_gated_delta_prefill. 26 KiB (training: 114 KiB) for every
+ * 64 tokens and head, and for long sequences of few heads, which are cut into segments, 128 KiB a
+ * segment and head. */
 kda_status kda_gated_delta_workspace_bytes(int64_t B, int64_t T, int64_t Hqk, int64_t Hv,
                                            const int64_t* cu_seqlens_host, int64_t num_seqs,
                                            int32_t training, size_t* bytes);

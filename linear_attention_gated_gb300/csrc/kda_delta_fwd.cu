@@ -1029,7 +1029,12 @@ int64_t delta_segment_tokens(const int64_t* cu, int64_t N, int64_t T, int64_t Hv
   }
   if (!cu) chunks *= N;
   const int64_t share = (chunks * Hv + kSms - 1) / kSms;  // an SM's even share of the chunks
-  if (longest <= 4 * share + 40) return 0;
+  // Whole, the longest sequence takes its chunks' time; cut, all take their share two to three times (with decays that leave
+  // nothing over a segment, or none), and some 20 chunks' time goes into launches and the chain. One after the other, in us, whole
+  // and cut (with decays; without): 1 head, 1024 tokens 56, 70 (70), 2048 tokens 91, 75 (75); 8 heads, 2048 tokens 94, 77 (77);
+  // 32 heads, 4096 tokens 184, 170 (170), 16384 tokens 671, 476 (533); 64 heads, 16384 tokens 749, 822 (930), 32771 tokens 1478, 1477
+  // (1739).
+  if (longest <= 3 * share + 20) return 0;
   // a quarter of it, so that the last turn is short, 8 chunks at least (and no more segments than are passed)
   const int64_t seg = std::max({(share + 3) / 4, (int64_t)8, (longest + kMost - 1) / kMost});
   return seg * kC;

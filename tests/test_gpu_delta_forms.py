@@ -207,7 +207,7 @@ def test_what_a_workspace_held_does_not_matter(lens):
 
 def test_context_reuse_and_repeatability():
     from linear_attention_gated_gb300 import KdaError, kda_gated_delta_bwd
-    x, y = make((90, 3140), 1, 1, seed=21), make((1600, 1630), 1, 1, seed=22)  # the first is cut into segments
+    x, y = make((90, 3140), 1, 1, seed=21), make((1600, 1630), 1, 1, seed=22)  # both are cut into segments, at other places
     b, ctx = run(y)
     a, _ = run(x)
     c, ctx2 = run(x, ctx=ctx)
