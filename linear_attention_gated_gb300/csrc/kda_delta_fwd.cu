@@ -6,13 +6,17 @@
 //            (cluster launch control: the grid has a CTA for each unit, one (sequence, head), longest first, and a running
 //            CTA takes over the next one that has not started)
 //   warps 1, 2   products (tcgen05.mma kind::f16, BF16 operands, FP32 accumulators in tensor memory): the chain's, and o's (a
-//            warp that waits for room for o does not hold up the chain: 257 -> 249 us)
+//            warp that waits for room for o does not hold up the chain: 257 us from one warp, 249 from two)
 //   warps 4-11   o (and u) on their way out
 //   warps 12-19  the state, 64 of a row's 128 values a thread in registers, and the elements between the chain's products
 // The chain of a chunk: S K^T -> x = v - e^b S k -> T x -> w beta u -> the state's update. Elements go in two halves of the
 // tokens, T being lower triangular: the first half's u does not wait for the second's x. So does the update, in halves of
 // the state's columns, and S K^T starts with the first of them. What is off the chain (S Q^T, beta u for the output) is put where
 // the tensor core and the warps would wait.
+// Bound: that chain, 4450 cycles a chunk: the turns of its three products (issue, tensor core, commit, wake: some 500 each) and the
+// element-wise steps between them (430 to 700). 8 x 1024 tokens of 96 heads, 5.05 units an SM: 246 us, 1.1 GB moved; issue slots
+// used to 40 %. With W = T e^b K made a chunk ahead the chain has two products and takes 301 us: the products a chunk ahead
+// cost more issue time than that saves. Waits that poll instead of being suspended: 277 us.
 //
 // Long axis, few units: each sequence is cut into segments. A pass over every segment but the last goes from a state of zero
 // and, without values, from the identity (a chunk takes S to S M + N, whatever S is: so does a segment); a small kernel

@@ -9,6 +9,8 @@
 // ring of asynchronous copies, each thread's part to its own place: nobody waits for anybody but in the rows' sums. Forward, the
 // sum of the next row and the squares of this one are joined in one exchange.
 // The CTAs' sums of dw and db are joined by a second small kernel in a fixed order.
+// 8192 rows of 12288 BF16 forward 64 us, 6.3 TB/s (103 us with rows loaded when they are needed); 8192 rows of 4096 backward 40 us,
+// 5.1 TB/s (64), and 3.7 for the join.
 #include "../../include/kda.h"
 #include "kda_decay_host.h"
 #include "tc.cuh"

@@ -205,6 +205,34 @@ def test_what_a_workspace_held_does_not_matter(lens):
         kda_gated_delta_prefill(*(d[n] for n in TOKENS), pool, d["cu"], workspace=ws[:nbytes - 256], cu_seqlens_cpu=x["cu"])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_prefill_cut_into_segments(dtype):
+    """From and to slots of a pool, in any order; the short sequences beside the long one are not cut."""
+    from linear_attention_gated_gb300 import kda_gated_delta_prefill
+    x = make((20, 3000, 0, 66), 1, 2, seed=41)
+    idx = torch.tensor([5, 0, 3, 2], dtype=torch.int32)
+    pool = (0.05 * torch.randn(6, 2, D, D, generator=torch.Generator().manual_seed(42))).to(dtype)
+    x["h0"] = pool[idx.long()].float()
+    ref = reference(x, grads=False, device="cuda")
+    got = pool.cuda()
+    o = kda_gated_delta_prefill(*(x[n].cuda() for n in TOKENS), got, x["cu"].cuda(), idx.cuda(), cu_seqlens_cpu=x["cu"],
+                                state_indices_cpu=idx)
+    check_rows("o", o, ref["o"], O_REL)
+    assert rel_l2(got[idx.long().cuda()], ref["hT"]) <= STATE_REL["hT"] + (0 if dtype == torch.float32 else BF16)
+    assert torch.equal(got[[1, 4]].cpu(), pool[[1, 4]]) and torch.equal(got[3].cpu(), pool[3])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_prefill_of_nothing(dtype):
+    """Sequences without tokens leave their states as they are."""
+    from linear_attention_gated_gb300 import kda_gated_delta_prefill
+    pool = torch.randn(5, 2, D, D, generator=torch.Generator().manual_seed(43)).to(dtype)
+    got, cu, idx = pool.cuda(), torch.zeros(4, dtype=torch.int64), torch.tensor([4, 0, 1], dtype=torch.int32)
+    e = torch.empty(1, 0, 2, D, dtype=torch.bfloat16, device="cuda")
+    o = kda_gated_delta_prefill(e, e, e, None, e[..., 0].contiguous(), got, cu.cuda(), idx.cuda(), cu_seqlens_cpu=cu, state_indices_cpu=idx)
+    assert o.shape == (1, 0, 2, D) and torch.equal(got.cpu(), pool)
+
+
 def test_context_reuse_and_repeatability():
     from linear_attention_gated_gb300 import KdaError, kda_gated_delta_bwd
     x, y = make((90, 3140), 1, 1, seed=21), make((1600, 1630), 1, 1, seed=22)  # both are cut into segments, at other places
