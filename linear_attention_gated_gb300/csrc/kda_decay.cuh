@@ -101,10 +101,14 @@ struct StateFactor {
     return f;
   }
 };
-// x as BF16 pairs hi + lo: 16 mantissa bits together
+// x as BF16 pairs hi + lo: 16 mantissa bits together. x - hi by multiply-adds that take BF16 factors as they are, -1 hi + x: two
+// instructions for two values where a subtraction takes three (8 x 1024 tokens of 96 heads of the gated delta rule 234 us, 246).
 __device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
   hi = pack2(x);
-  lo = pack2(tc::sub2(x, unpack2(hi)));
+  float a, b;
+  asm("{\n .reg .b16 p, q, m;\n mov.b32 {p, q}, %2;\n mov.b16 m, 0xBF80;\n fma.rn.f32.bf16 %0, p, m, %3;\n fma.rn.f32.bf16 %1, q, m, %4;\n}\n"
+      : "=f"(a), "=f"(b) : "r"(hi), "f"(x.x), "f"(x.y));
+  lo = pack2(make_float2(a, b));
 }
 
 // Eight values of a state row, as they come from memory.
