@@ -60,11 +60,11 @@ __device__ __forceinline__ DeltaChunk delta_chunk(const DeltaProblem& P, int64_t
   return DeltaChunk{sp.t0 + c * kDecayChunk, c < 0 || left <= 0 ? 0 : left < kDecayChunk ? (int)left : kDecayChunk};
 }
 
-// Workspace: packets; of the training pair, the states at the chunks' starts and u from the forward, the states' adjoints at
-// the chunks' ends from the backward; where sequences are cut, what the segments make of zero and of the identity (and whether
+// Workspace: packets; of the training pair, the places' chunks (first token, tokens), the states at the chunks' starts and u from
+// the forward, the states' adjoints at the chunks' ends from the backward; where sequences are cut, what the segments make of zero and of the identity (and whether
 // that is zero).
 struct DeltaWs {
-  size_t packet, states, u, adjoints, segments, through, none, total;
+  size_t packet, chunks, states, u, adjoints, segments, through, none, total;
 };
 DeltaWs delta_workspace(const DeltaProblem& P, bool training);  // (goes by N, Ttot, Hv, slots and seg)
 

@@ -50,7 +50,7 @@ struct Smem {
   unsigned char A[8192], R[8192];
   DeltaAux aux[2];
   Numbers num[2];
-  unsigned long long fullqk[2], full, g1, g2;
+  unsigned long long fullqk[2], full, g1, gs, g2;
   uint32_t tmem;
 };
 constexpr int kSmemBytes = (int)sizeof(Smem) + 1024;
@@ -81,14 +81,14 @@ __device__ __forceinline__ int over_token(int token, int lane) { return token + 
 // transposed, [128 values x 64 tokens], so that all have M = 128 and the tokens' factors are applied where the sums are read.
 __global__ void __launch_bounds__(kThreads, 1)
 kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, const unsigned char* packets, const unsigned char* states,
-                      const unsigned char* adjoints, const unsigned char* us, const DeltaGrads G) {
+                      const unsigned char* adjoints, const unsigned char* us, const int2* chunks, const DeltaGrads G) {
   extern __shared__ unsigned char raw_smem[];
   Smem& sm = *reinterpret_cast<Smem*>(raw_smem + ((1024 - (tc::smem_u32(raw_smem) & 1023)) & 1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wq = warp & 3, quarter = warp >> 2;
   auto bar = [](unsigned long long& b) { return tc::smem_u32(&b); };
   if (warp == 0) tc::tmem_alloc(tc::smem_u32(&sm.tmem), 512);
   if (tid == 0)
-    for (unsigned long long* b : {&sm.fullqk[0], &sm.fullqk[1], &sm.full, &sm.g1, &sm.g2}) tc::mbar_init(bar(*b), 1);
+    for (unsigned long long* b : {&sm.fullqk[0], &sm.fullqk[1], &sm.full, &sm.g1, &sm.gs, &sm.g2}) tc::mbar_init(bar(*b), 1);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -99,13 +99,13 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
     if (ok) ok = tc::mbar_wait_lanes(bar(b), parity & 1);
     tc::fence_after();
   };
-  const int64_t units = P.slots * P.Hqk;
-  // the first unit from x on that has a chunk
-  DeltaChunk ch{0, 0}, ch1{0, 0};
-  auto find = [&](int64_t x, DeltaChunk& c) {
+  const uint32_t units = (uint32_t)(P.slots * P.Hqk);
+  // the first unit from x on that has a chunk (from prep's list: looking for it took 2000 cycles)
+  int2 ch{0, 0}, ch1{0, 0};
+  auto find = [&](uint32_t x, int2& c) {
     for (; x < units; x += gridDim.x) {
-      c = delta_chunk(P, x / P.Hqk);
-      if (c.nt > 0) break;
+      c = chunks[x / (uint32_t)P.Hqk];
+      if (c.y > 0) break;
     }
     return x;
   };
@@ -136,17 +136,16 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
       }
     }
   };
-  int64_t unit = find(blockIdx.x, ch), unit1 = unit;
-  int hq = unit < units ? (int)(unit % P.Hqk) : 0, hq1 = hq;
-  if (unit < units) load(unit / P.Hqk, hq, ch.t0, 0, 0, 0);
+  uint32_t unit = find(blockIdx.x, ch), unit1 = unit;
+  int slot = (int)(unit / (uint32_t)P.Hqk), slot1 = slot, hq = (int)(unit - (uint32_t)slot * P.Hqk), hq1 = hq;
+  if (unit < units) load(slot, hq, ch.x, 0, 0, 0);
   __syncwarp();
   const int tok0 = 16 * quarter + 2 * (lane & 3);  // this thread's tokens: tok0 + 8 m + e
   uint32_t n = 0;                                  // heads so far
-  for (uint32_t un = 0; unit < units; ++un, unit = unit1, ch = ch1, hq = hq1) {
+  for (uint32_t un = 0; unit < units; ++un, unit = unit1, ch = ch1, slot = slot1, hq = hq1) {
     const uint32_t qk = tc::smem_u32(sm.qk[un & 1]);
-    const int nt = ch.nt;
-    const int64_t slot = unit / P.Hqk;
-    const int64_t t0 = ch.t0;
+    const int nt = ch.y;
+    const int64_t t0 = ch.x;
     float sq[2][8], sk[2][8];  // dq, dk: values 32 wq + 16 q + 8 j + lane / 4 of tokens tok0 + 8 m + e, at 4 m + 2 j + e
 #pragma unroll
     for (int i = 0; i < 16; ++i) sq[i >> 3][i & 7] = sk[i >> 3][i & 7] = 0.f;
@@ -156,10 +155,6 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
       const DeltaAux& aux = sm.aux[par];
       Numbers& num = sm.num[par];
       const bool last = r + 1 == P.r;
-      if (last) {
-        unit1 = find(unit + gridDim.x, ch1);
-        hq1 = (int)(unit1 % P.Hqk);
-      }
       if (r == 0) wait(sm.fullqk[un & 1], un >> 1);
       wait(sm.full, n);
       if (nt < kC) {  // rows past the end hold other tokens
@@ -175,15 +170,21 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
       if (warp == 0) {
         if (ok && tc::elect_one()) {
           const uint64_t u = tc::kmajor(tc::smem_u32(sm.u)), St = tc::mnmajor(tc::smem_u32(sm.S), 16384), Gt = tc::mnmajor(tc::smem_u32(sm.G), 16384);
+          // (the scores first: their elements are worked on while the states' products run)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t off = (i >> 2) * (16384 >> 4) + (i & 3) * 2, off64 = (i >> 2) * (8192 >> 4) + (i & 3) * 2;
             tc::mma_bf16_ss(tbase + kColUU, tc::kmajor(dr) + off, u + off64, kn, i > 0);
             if (r == 0) tc::mma_bf16_ss(tbase + kColKK, tc::kmajor(qk) + off, tc::kmajor(qk + 8192) + off, kn, i > 0);
+          }
+          tc::mma_commit(bar(sm.g1));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t off = (i >> 2) * (16384 >> 4) + (i & 3) * 2, off64 = (i >> 2) * (8192 >> 4) + (i & 3) * 2;
             tc::mma_bf16_ss(tbase + kColQS, St + 128 * i, tc::kmajor(dr) + off, tc::idesc_bf16(128, 128, true, false), i > 0);
             tc::mma_bf16_ss(tbase + kColKG, Gt + 128 * i, u + off64, tn, i > 0);
           }
-          tc::mma_commit(bar(sm.g1));
+          tc::mma_commit(bar(sm.gs));
         }
         __syncwarp();
       }
@@ -198,6 +199,11 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
 #pragma unroll
         for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
         if (lane == 0) num.gs[warp] = x;
+      }
+      if (last) {  // (here, where the warps wait for the products)
+        unit1 = find(unit + gridDim.x, ch1);
+        slot1 = (int)(unit1 / (uint32_t)P.Hqk);
+        hq1 = (int)(unit1 - (uint32_t)slot1 * P.Hqk);
       }
       wait(sm.g1, n);
       // the scores: rows i = 32 (wq % 2) + 16 q + 8 j + lane / 4 of dO and Q (wq < 2) or rho and K, columns tok0 + 8 m + e
@@ -275,9 +281,10 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
         }
         __syncwarp();
       }
+      wait(sm.gs, n);
       if (ok) {  // the next head's tiles: the readers of this one's are done
         if (!last) load(slot, hq, t0, r + 1, par ^ 1, un & 1);
-        else if (unit1 < units) load(unit1 / P.Hqk, hq1, ch1.t0, 0, par ^ 1, (un + 1) & 1);
+        else if (unit1 < units) load(slot1, hq1, ch1.x, 0, par ^ 1, (un + 1) & 1);
       }
       __syncwarp();
       // products with the states, and their dots with q and k
@@ -414,7 +421,7 @@ cudaError_t launch_delta_grads(const DeltaProblem& P, const DeltaGrads& g, void*
   const DeltaWs w = delta_workspace(P, true);
   unsigned char* b = reinterpret_cast<unsigned char*>(ws);
   const int64_t units = P.slots * P.Hqk;
-  kda_delta_grad_kernel<<<(unsigned)(units < kSms ? units : kSms), kThreads, kSmemBytes, s>>>(maps, P, b + w.packet, b + w.states, b + w.adjoints, b + w.u, g);
+  kda_delta_grad_kernel<<<(unsigned)(units < kSms ? units : kSms), kThreads, kSmemBytes, s>>>(maps, P, b + w.packet, b + w.states, b + w.adjoints, b + w.u, reinterpret_cast<const int2*>(b + w.chunks), g);
   return cudaGetLastError();
 }
 

@@ -83,7 +83,7 @@ __device__ __forceinline__ uint32_t piece(int row, int c) { return row * 128 + (
 // kTrain: P's low part too.
 template <bool kTrain>
 __global__ void __launch_bounds__(128, kCtas) kda_delta_prep_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, const int group,
-                                                                    unsigned char* packets) {
+                                                                    unsigned char* packets, int2* chunks) {
   extern __shared__ unsigned char raw_smem[];
   Smem& sm = *reinterpret_cast<Smem*>(raw_smem + ((1024 - (tc::smem_u32(raw_smem) & 1023)) & 1023));
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(128, kCtas) kda_delta_prep_kernel(const __grid
         t0 = (int)ch.t0;
         nt = ch.nt;
         h = (int)(unit - (uint32_t)slot * groups) * group;
+        if (kTrain && h == 0 && lane == 0) chunks[slot] = make_int2(t0, nt);
       }
       left = group - 1;
     }
@@ -475,7 +476,8 @@ cudaError_t launch(const Maps& maps, const DeltaProblem& P, void* ws, cudaStream
   int group = P.r;
   while (group > 1 && (P.r % group || P.slots * (P.Hv / group) < 8 * ctas)) --group;
   const int64_t units = P.slots * (P.Hv / group);
-  kern<<<(unsigned)(units < ctas ? units : ctas), 128, kSmemBytes, s>>>(maps, P, group, reinterpret_cast<unsigned char*>(ws));
+  kern<<<(unsigned)(units < ctas ? units : ctas), 128, kSmemBytes, s>>>(maps, P, group, reinterpret_cast<unsigned char*>(ws),
+                                                                             reinterpret_cast<int2*>(reinterpret_cast<unsigned char*>(ws) + delta_workspace(P, kTrain).chunks));
   return cudaGetLastError();
 }
 
@@ -484,7 +486,8 @@ cudaError_t launch(const Maps& maps, const DeltaProblem& P, void* ws, cudaStream
 DeltaWs delta_workspace(const DeltaProblem& P, bool training) {
   const size_t n = (size_t)P.slots * P.Hv;
   DeltaWs w{};
-  w.states = ctx_align_up(n * (training ? kPkTrain : kPkInfer));
+  w.chunks = ctx_align_up(n * (training ? kPkTrain : kPkInfer));
+  w.states = w.chunks + (training ? ctx_align_up((size_t)P.slots * sizeof(int2)) : 0);
   w.u = w.states + (training ? n * kStateTile : 0);
   w.adjoints = w.u + (training ? n * kUTile : 0);
   w.segments = w.adjoints + (training ? n * kStateTile : 0);
