@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kC = kDecayChunk;
 constexpr int kThreads = 512;
+constexpr int kWarpMma = 12;  // issues the products: all its scores lie above the diagonal, so it has time
 // Tensor memory, columns (64 each)
 constexpr uint32_t kColUU = 0;     // [dO; rho] u^T
 constexpr uint32_t kColKK = 64;    // [Q; K] K^T
@@ -51,6 +52,7 @@ struct Smem {
   DeltaAux aux[2];
   Numbers num[2];
   unsigned long long fullqk[2], full, g1, gs, g2;
+  int2 next[2];                // the next unit's chunk, of two units in turn
   uint32_t tmem;
 };
 constexpr int kSmemBytes = (int)sizeof(Smem) + 1024;
@@ -100,7 +102,8 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
     tc::fence_after();
   };
   const uint32_t units = (uint32_t)(P.slots * P.Hqk);
-  // the first unit from x on that has a chunk (from prep's list: looking for it took 2000 cycles)
+  // the first unit from x on that has a chunk, from prep's list (looking for it took 2000 cycles, and so does a load behind all the
+  // tiles on their way: the usual one is asked for when a unit begins)
   int2 ch{0, 0}, ch1{0, 0};
   auto find = [&](uint32_t x, int2& c) {
     for (; x < units; x += gridDim.x) {
@@ -155,6 +158,10 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
       const DeltaAux& aux = sm.aux[par];
       Numbers& num = sm.num[par];
       const bool last = r + 1 == P.r;
+      if (last && tid == 0) {
+        if (unit + gridDim.x < units) tc::cp_async_small<8>(&sm.next[un & 1], chunks + (unit + gridDim.x) / (uint32_t)P.Hqk, 8);
+        tc::cp_async_commit();
+      }
       if (r == 0) wait(sm.fullqk[un & 1], un >> 1);
       wait(sm.full, n);
       if (nt < kC) {  // rows past the end hold other tokens
@@ -167,7 +174,7 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
         __syncthreads();
       }
       constexpr uint32_t kn = tc::idesc_bf16(128, 64, false, false), tn = tc::idesc_bf16(128, 64, true, false), tt = tc::idesc_bf16(128, 64, true, true);
-      if (warp == 0) {
+      if (warp == kWarpMma) {
         if (ok && tc::elect_one()) {
           const uint64_t u = tc::kmajor(tc::smem_u32(sm.u)), St = tc::mnmajor(tc::smem_u32(sm.S), 16384), Gt = tc::mnmajor(tc::smem_u32(sm.G), 16384);
           // (the scores first: their elements are worked on while the states' products run)
@@ -199,11 +206,6 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
 #pragma unroll
         for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
         if (lane == 0) num.gs[warp] = x;
-      }
-      if (last) {  // (here, where the warps wait for the products)
-        unit1 = find(unit + gridDim.x, ch1);
-        slot1 = (int)(unit1 / (uint32_t)P.Hqk);
-        hq1 = (int)(unit1 - (uint32_t)slot1 * P.Hqk);
       }
       wait(sm.g1, n);
       // the scores: rows i = 32 (wq % 2) + 16 q + 8 j + lane / 4 of dO and Q (wq < 2) or rho and K, columns tok0 + 8 m + e
@@ -262,11 +264,12 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
         const float c = over_rows(col, lane);
         if (lane < 16) num.colp[wq][over_token(16 * quarter, lane)] = c;
       }
+      if (last && tid == 0) tc::cp_async_wait_all();
       tc::fence_async_smem();
       tc::fence_before();
       __syncthreads();
       tc::fence_after();
-      if (warp == 0) {
+      if (warp == kWarpMma) {
         if (ok && tc::elect_one()) {
           const uint64_t Qt = tc::mnmajor(qk, 16384), Kt = tc::mnmajor(qk + 8192, 16384);
           const uint32_t A = tc::smem_u32(sm.A), R = tc::smem_u32(sm.R);
@@ -282,6 +285,15 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
         __syncwarp();
       }
       wait(sm.gs, n);
+      if (last) {
+        unit1 = unit + gridDim.x;
+        if (unit1 < units) {
+          ch1 = sm.next[un & 1];
+          if (ch1.y <= 0) unit1 = find(unit1 + gridDim.x, ch1);
+        }
+        slot1 = (int)(unit1 / (uint32_t)P.Hqk);
+        hq1 = (int)(unit1 - (uint32_t)slot1 * P.Hqk);
+      }
       if (ok) {  // the next head's tiles: the readers of this one's are done
         if (!last) load(slot, hq, t0, r + 1, par ^ 1, un & 1);
         else if (unit1 < units) load(slot1, hq1, ch1.x, 0, par ^ 1, (un + 1) & 1);

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(128, kCtas) kda_delta_prep_kernel(const __grid
     const int64_t at = (int64_t)(of.t0 + 2 * lane) * P.Hv + of.h;
     auto copy = [](float* to, const void* p) {
       const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-      tc::cp_async4(to, reinterpret_cast<const void*>(a & ~(uintptr_t)3), a & 2 ? 4u : 2u);
+      tc::cp_async_small<4>(to, reinterpret_cast<const void*>(a & ~(uintptr_t)3), a & 2 ? 4u : 2u);
     };
 #pragma unroll
     for (int q = 0; q < 2; ++q)

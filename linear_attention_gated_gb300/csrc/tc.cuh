@@ -267,8 +267,9 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
 
 // Asynchronous 16-byte global -> shared copy (bypassing L1); src_bytes < 16
 // zero-fills the rest (0 copies nothing and writes zeros).
-__device__ __forceinline__ void cp_async4(void* smem_dst, const void* gsrc, uint32_t src_bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(smem_dst)), "l"(gsrc), "r"(src_bytes) : "memory");
+template <int kBytes>  // 4 or 8
+__device__ __forceinline__ void cp_async_small(void* smem_dst, const void* gsrc, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(smem_dst)), "l"(gsrc), "n"(kBytes), "r"(src_bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async16(void* smem_dst, const void* gsrc, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(gsrc), "r"(src_bytes)
