@@ -52,7 +52,8 @@ struct Smem {
   DeltaAux aux[2];
   Numbers num[2];
   unsigned long long fullqk[2], full, g1, gs, g2;
-  int2 next[2];                // the next unit's chunk, of two units in turn
+  int2 next[2];                // chunks of units to come, of two in turn,
+  uint32_t asked[2];           // and which they are
   uint32_t tmem;
 };
 constexpr int kSmemBytes = (int)sizeof(Smem) + 1024;
@@ -102,8 +103,8 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
     tc::fence_after();
   };
   const uint32_t units = (uint32_t)(P.slots * P.Hqk);
-  // the first unit from x on that has a chunk, from prep's list (looking for it took 2000 cycles, and so does a load behind all the
-  // tiles on their way: the usual one is asked for when a unit begins)
+  // the first unit from x on that has a chunk, from prep's list (looking for it took 2000 cycles, and a load behind all the tiles
+  // on their way 5000: the usual one is asked for two units before)
   int2 ch{0, 0}, ch1{0, 0};
   auto find = [&](uint32_t x, int2& c) {
     for (; x < units; x += gridDim.x) {
@@ -111,6 +112,12 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
       if (c.y > 0) break;
     }
     return x;
+  };
+  auto ask = [&](uint32_t x, uint32_t to) {
+    if (tid) return;
+    sm.asked[to] = x;
+    if (x < units) tc::cp_async_small<8>(&sm.next[to], chunks + x / (uint32_t)P.Hqk, 8);
+    tc::cp_async_commit();
   };
   // The tiles of one head (and, of a unit's first, of Q and K), by one lane of each of six warps. (One warp took 2000 cycles.)
   auto load = [&](int64_t slot, int hq, int64_t t, int r, uint32_t par, uint32_t ub) {
@@ -145,6 +152,7 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
   __syncwarp();
   const int tok0 = 16 * quarter + 2 * (lane & 3);  // this thread's tokens: tok0 + 8 m + e
   uint32_t n = 0;                                  // heads so far
+  ask(unit + gridDim.x, 0);
   for (uint32_t un = 0; unit < units; ++un, unit = unit1, ch = ch1, slot = slot1, hq = hq1) {
     const uint32_t qk = tc::smem_u32(sm.qk[un & 1]);
     const int nt = ch.y;
@@ -158,10 +166,7 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
       const DeltaAux& aux = sm.aux[par];
       Numbers& num = sm.num[par];
       const bool last = r + 1 == P.r;
-      if (last && tid == 0) {
-        if (unit + gridDim.x < units) tc::cp_async_small<8>(&sm.next[un & 1], chunks + (unit + gridDim.x) / (uint32_t)P.Hqk, 8);
-        tc::cp_async_commit();
-      }
+      if (last) ask(unit + 2 * gridDim.x, ~un & 1);
       if (r == 0) wait(sm.fullqk[un & 1], un >> 1);
       wait(sm.full, n);
       if (nt < kC) {  // rows past the end hold other tokens
@@ -264,7 +269,7 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
         const float c = over_rows(col, lane);
         if (lane < 16) num.colp[wq][over_token(16 * quarter, lane)] = c;
       }
-      if (last && tid == 0) tc::cp_async_wait_all();
+      if (last && tid == 0) tc::cp_async_wait<1>();
       tc::fence_async_smem();
       tc::fence_before();
       __syncthreads();
@@ -288,8 +293,9 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
       if (last) {
         unit1 = unit + gridDim.x;
         if (unit1 < units) {
-          ch1 = sm.next[un & 1];
-          if (ch1.y <= 0) unit1 = find(unit1 + gridDim.x, ch1);
+          const bool here = sm.asked[un & 1] == unit1;
+          if (here) ch1 = sm.next[un & 1];
+          if (!here || ch1.y <= 0) unit1 = find(here ? unit1 + gridDim.x : unit1, ch1);
         }
         slot1 = (int)(unit1 / (uint32_t)P.Hqk);
         hq1 = (int)(unit1 - (uint32_t)slot1 * P.Hqk);
@@ -404,6 +410,7 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
     }
     tc::fence_async_smem();  // (read before the next but one unit's copies)
   }
+  if (tid == 0) tc::cp_async_wait_all();
   if (!ok) {  // flag it, and let the copies land before the memory is given back
     if (lane == 0) atomicOr(P.status, 1);
     for (uint32_t k = 0; k < 2; ++k) {
