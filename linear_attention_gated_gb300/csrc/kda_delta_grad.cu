@@ -119,9 +119,9 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
     if (x < units) tc::cp_async_small<8>(&sm.next[to], chunks + x / (uint32_t)P.Hqk, 8);
     tc::cp_async_commit();
   };
-  // The tiles of one head (and, of a unit's first, of Q and K), by one lane of each of seven warps. (One warp took 2000 cycles.)
+  // The tiles of one head (and, of a unit's first, of Q and K), by one lane of each of six warps. (One warp took 2000 cycles.)
   auto load = [&](int64_t slot, int hq, int64_t t, int r, uint32_t par, uint32_t ub) {
-    if (warp > 6 || !tc::elect_one()) return;
+    if (warp > 5 || !tc::elect_one()) return;
     const int h = hq * P.r + r;
     const int64_t place = slot * P.Hv + h;
     const uint32_t f = bar(sm.full), fq = bar(sm.fullqk[ub]);
@@ -137,20 +137,17 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
     } else if (warp == 4) {
       tc::bulk_g2s(tc::smem_u32(sm.G), adjoints + place * kStateTile, kStateTile, f);
     } else if (r == 0) {
-      const uint32_t to = tc::smem_u32(sm.qk[ub]) + 8192 * (warp - 5);
-      if (warp == 5) tc::mbar_arrive_expect_tx(fq, 32768);
+      const uint32_t qk = tc::smem_u32(sm.qk[ub]);
+      tc::mbar_arrive_expect_tx(fq, 32768);
 #pragma unroll
-      for (int p = 0; p < 2; ++p) tc::tma_load3(to + p * 16384, warp == 5 ? &maps.q : &maps.k, 64 * p, hq, (int)t, fq);
+      for (int p = 0; p < 2; ++p) {
+        tc::tma_load3(qk + p * 16384, &maps.q, 64 * p, hq, (int)t, fq);
+        tc::tma_load3(qk + p * 16384 + 8192, &maps.k, 64 * p, hq, (int)t, fq);
+      }
     }
   };
   uint32_t unit = find(blockIdx.x, ch), unit1 = unit;
-  auto split = [&](uint32_t x, int& slot, int& hq) {
-    slot = (int)(x / (uint32_t)P.Hqk);
-    hq = (int)(x - (uint32_t)slot * P.Hqk);
-  };
-  int slot, hq;
-  split(unit, slot, hq);
-  int slot1 = slot, hq1 = hq;
+  int slot = (int)(unit / (uint32_t)P.Hqk), slot1 = slot, hq = (int)(unit - (uint32_t)slot * P.Hqk), hq1 = hq;
   if (unit < units) load(slot, hq, ch.x, 0, 0, 0);
   __syncwarp();
   const int tok0 = 16 * quarter + 2 * (lane & 3);  // this thread's tokens: tok0 + 8 m + e
@@ -214,10 +211,6 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
 #pragma unroll
         for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
         if (lane == 0) num.gs[warp] = x;
-      }
-      if (last) {  // (here, where the warps wait)
-        unit1 = unit + gridDim.x;
-        split(unit1, slot1, hq1);
       }
       wait(sm.g1, n);
       // the scores: rows i = 32 (wq % 2) + 16 q + 8 j + lane / 4 of dO and Q (wq < 2) or rho and K, columns tok0 + 8 m + e
@@ -297,13 +290,15 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
         __syncwarp();
       }
       wait(sm.gs, n);
-      if (last && unit1 < units) {
-        const bool here = sm.asked[un & 1] == unit1;
-        if (here) ch1 = sm.next[un & 1];
-        if (!here || ch1.y <= 0) {
-          unit1 = find(here ? unit1 + gridDim.x : unit1, ch1);
-          split(unit1, slot1, hq1);
+      if (last) {
+        unit1 = unit + gridDim.x;
+        if (unit1 < units) {
+          const bool here = sm.asked[un & 1] == unit1;
+          if (here) ch1 = sm.next[un & 1];
+          if (!here || ch1.y <= 0) unit1 = find(here ? unit1 + gridDim.x : unit1, ch1);
         }
+        slot1 = (int)(unit1 / (uint32_t)P.Hqk);
+        hq1 = (int)(unit1 - (uint32_t)slot1 * P.Hqk);
       }
       if (ok) {  // the next head's tiles: the readers of this one's are done
         if (!last) load(slot, hq, t0, r + 1, par ^ 1, un & 1);
