@@ -14,9 +14,9 @@
 // the state's columns, and S K^T starts with the first of them. What is off the chain (S Q^T, beta u for the output) is put where
 // the tensor core and the warps would wait.
 // Bound: that chain, 4450 cycles a chunk: the turns of its three products (issue, tensor core, commit, wake: some 500 each) and the
-// element-wise steps between them (430 to 700). 8 x 1024 tokens of 96 heads, 5.05 units an SM: 246 us, 1.1 GB moved; issue slots
-// used to 40 %. With W = T e^b K made a chunk ahead the chain has two products and takes 301 us: the products a chunk ahead
-// cost more issue time than that saves. Waits that poll instead of being suspended: 277 us.
+// element-wise steps between them (430 to 700). 8 x 1024 tokens of 96 heads, 5.05 units an SM: 233 us, 1.1 GB moved; issue slots
+// used to 40 %. When this took 249 us: with W = T e^b K made a chunk ahead the chain has two products and takes 301 us: the products a chunk ahead
+// cost more issue time than that saves; waits that poll instead of being suspended, 277 us.
 //
 // Long axis, few units: each sequence is cut into segments. A pass over every segment but the last goes from a state of zero
 // and, without values, from the identity (a chunk takes S to S M + N, whatever S is: so does a segment); a small kernel
@@ -1035,9 +1035,9 @@ int64_t delta_segment_tokens(const int64_t* cu, int64_t N, int64_t T, int64_t Hv
   const int64_t share = (chunks * Hv + kSms - 1) / kSms;  // an SM's even share of the chunks
   // Whole, the longest sequence takes its chunks' time; cut, all take their share two to three times (with decays that leave
   // nothing over a segment, or none), and some 20 chunks' time goes into launches and the chain. One after the other, in us, whole
-  // and cut (with decays; without): 1 head, 1024 tokens 56, 70 (70), 2048 tokens 91, 75 (75); 8 heads, 2048 tokens 94, 77 (77);
-  // 32 heads, 4096 tokens 184, 170 (170), 16384 tokens 671, 476 (533); 64 heads, 16384 tokens 749, 822 (930), 32771 tokens 1478, 1477
-  // (1739).
+  // and cut (with decays; without): 1 head, 1024 tokens 57, 71 (71), 2048 tokens 91, 75 (75); 8 heads, 2048 tokens 92, 77 (77);
+  // 32 heads, 4096 tokens 179, 168 (169), 16384 tokens 655, 470 (530); 64 heads, 16384 tokens 732, 816 (923), 32771 tokens 1445, 1466
+  // (1730).
   if (longest <= 3 * share + 20) return 0;
   // a quarter of it, so that the last turn is short, 8 chunks at least (and no more segments than are passed)
   const int64_t seg = std::max({(share + 3) / 4, (int64_t)8, (longest + kMost - 1) / kMost});

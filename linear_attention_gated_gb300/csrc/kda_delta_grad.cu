@@ -79,8 +79,8 @@ __device__ __forceinline__ int over_token(int token, int lane) { return token + 
 
 // One CTA an SM goes through the (chunk, query/key head) units b, b + gridDim.x, ..., and in each through the group's value heads. The
 // tiles of the next head are on their way once the first products of this one, their only readers, are done. Bound: a pair's
-// chain of two products' groups and the elements between them, 16 warps (10,000 cycles, of which the 144 KiB of tiles in and out take
-// 60 %): 4 x 2048 tokens of 16 / 32 heads 145 us; a CTA for each unit, with nothing on its way, 236 us. Products are
+// chain of two products' groups and the elements between them, 16 warps (8000 cycles, of which the 144 KiB of tiles in and out take
+// 70 %): 4 x 2048 tokens of 16 / 32 heads 132 us; a CTA for each unit, with nothing on its way, 236 us. Products are
 // transposed, [128 values x 64 tokens], so that all have M = 128 and the tokens' factors are applied where the sums are read.
 __global__ void __launch_bounds__(kThreads, 1)
 kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, const unsigned char* packets, const unsigned char* states,
