@@ -461,3 +461,30 @@ def test_a_pool_past_32_bit_offsets():
     used = torch.zeros(slots, dtype=torch.bool)
     used[idx.long()] = True
     assert not pool[~used.cuda()].any()
+
+
+def test_tokens_past_32_bit_offsets():
+    """A sequence of 100 tokens behind one whose values take 4 GiB: as alone, in training and in prefill."""
+    from linear_attention_gated_gb300 import kda_gated_delta_bwd, kda_gated_delta_fwd, kda_gated_delta_prefill
+    hv = 64
+    before = 2 ** 32 // (hv * D * 2) + 130
+    small = make((100,), 1, hv, seed=44)
+    cu = torch.tensor([0, before, before + 100])
+    big = {n: torch.zeros(1, before + 100, *small[n].shape[2:], dtype=torch.bfloat16, device="cuda") for n in TOKENS + ("do",)}
+    for n in big:
+        big[n][:, before:] = small[n].cuda()
+    d = {n: t.cuda() for n, t in small.items()}
+    h0, dhT = (torch.cat([torch.zeros_like(d[n]), d[n]]) for n in ("h0", "dhT"))
+    o, hT, ctx = kda_gated_delta_fwd(*(big[n] for n in TOKENS), h0, cu.cuda(), cu_seqlens_cpu=cu)
+    got = (o, hT) + kda_gated_delta_bwd(ctx, big["do"], dhT)
+    ctx.status()
+    want, _ = run(small)
+    for n, t in zip(NAMES, got):
+        assert torch.equal(t[1:] if n in ("hT", "dh0") else t[:, before:], want[n]), n
+    assert not got[0][:, :before].any()
+    del got, ctx, o
+    pool = h0.clone()
+    o = kda_gated_delta_prefill(*(big[n] for n in TOKENS), pool, cu.cuda(), cu_seqlens_cpu=cu)
+    alone = d["h0"].clone()
+    assert torch.equal(o[:, before:], kda_gated_delta_prefill(*(d[n] for n in TOKENS), alone, d["cu"], cu_seqlens_cpu=small["cu"]))
+    assert torch.equal(pool[1:], alone)

@@ -158,3 +158,19 @@ def test_captured_and_on_another_stream():
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, c) for a, c in zip(got + gotg, want + wantg))
+
+
+def test_rows_past_32_bit_offsets():
+    """The last 100 rows of a tensor of 4 GiB, as alone."""
+    from linear_attention_gated_gb300 import kda_layer_norm_bwd, kda_layer_norm_fwd
+    width, before = 4096, 2 ** 31 // 4096 + 7
+    x, w, b, dy = make((100, width), torch.bfloat16, seed=10)
+    big, bigd = (torch.zeros(before + 100, width, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    big[before:], bigd[before:] = x, dy
+    y, mean, rstd = kda_layer_norm_fwd(big, w, b)
+    want = kda_layer_norm_fwd(x, w, b)
+    for got, alone in zip((y, mean, rstd), want):
+        assert torch.equal(got[before:], alone)
+    assert torch.equal(y[:before:997], b.bfloat16().expand(y[:before:997].shape))
+    dx = kda_layer_norm_bwd(bigd, big, w, mean, rstd)[0]
+    assert torch.equal(dx[before:], kda_layer_norm_bwd(dy, x, w, *want[1:])[0]) and not dx[:before].any()
