@@ -9,8 +9,8 @@
 // ring of asynchronous copies, each thread's part to its own place: nobody waits for anybody but in the rows' sums. Forward, the
 // sum of the next row and the squares of this one are joined in one exchange.
 // The CTAs' sums of dw and db are joined by a second small kernel in a fixed order.
-// 8192 rows of 12288 BF16 forward 64 us, 6.3 TB/s (103 us with rows loaded when they are needed); 8192 rows of 4096 backward 40 us,
-// 5.1 TB/s (64), and 3.7 for the join.
+// 8192 rows of 12288 BF16 forward 64 us, 6.3 TB/s (103 us with rows loaded when they are needed); 8192 rows of 4096 backward 39 us,
+// 5.2 TB/s (64), and 3.6 for the join.
 #include "../../include/kda.h"
 #include "kda_decay_host.h"
 #include "tc.cuh"
@@ -130,8 +130,8 @@ struct Part {
   }
 };
 
-// Sums of kN numbers over the kG threads of a row. The whole CTA calls it; `turn` picks one of two buffers, so that
-// one barrier a call is enough.
+// Sums of kN numbers over the kG threads of a row. The row's threads call it; `turn` picks one of two buffers, so that one barrier
+// a call is enough: the row's own, so that a CTA's rows do not wait for each other.
 template <int kG, int kN>
 __device__ __forceinline__ void row_sums(float (&x)[kN], float* buf, int turn) {
 #pragma unroll
@@ -145,7 +145,8 @@ __device__ __forceinline__ void row_sums(float (&x)[kN], float* buf, int turn) {
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
       for (int n = 0; n < kN; ++n) at[n * (kThreads / 32) + warp] = x[n];
-    __syncthreads();
+    if constexpr (kG < kThreads) asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + threadIdx.x / kG), "n"(kG) : "memory");
+    else __syncthreads();
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
       float s = 0.f;
