@@ -1,7 +1,7 @@
 """A block of the gated delta rule, trained and served.
 
 y = x + o W_out: a layer norm (kda_layer_norm), one fused projection that gives queries, keys, values, the heads' decays and
-step sizes, queries and keys brought to norm 1 (kda_qk_norm_rope without a rotation), and the gated delta rule with a state per
+step sizes, keys brought to norm 1 and queries to sqrt(128) (kda_qk_norm_rope without a rotation), and the gated delta rule with a state per
 sequence (kda_gated_delta). Training goes over packed sequences with the kernels' own backward passes; serving prefills
 prompts into a state pool and then takes one token a sequence at a time. The projections are plain matrix products of torch.
 
@@ -36,6 +36,7 @@ class DeltaBlock:
         self.weights = {"in": w_in.to(device), "out": w_out.to(device),  # FP32 masters; products run in BF16
                         "norm": torch.ones(width, device=device), "bias": torch.zeros(width, device=device)}
         self.unit = torch.full((D,), UNIT, device=device)
+        self.one = torch.ones(D, device=device)
         self.context = None
 
     def _inputs(self, x):
@@ -47,7 +48,7 @@ class DeltaBlock:
         v = v.unflatten(-1, (self.hv, D))
         g = -F.softplus(z.float() - 2.0).bfloat16()  # log decays <= 0, about 0.88 a token at the start
         beta = torch.sigmoid(b.float()).bfloat16()
-        qn, kn = kda_qk_norm_rope_fwd(q, k, self.unit, self.unit, None, None)
+        qn, kn = kda_qk_norm_rope_fwd(q, k, self.one, self.unit, None, None)
         return normed, (q, k, z, b), (qn, kn, v, g, beta)
 
     def step(self, x, target, cu, cu_cpu, rate=0.0):
@@ -64,7 +65,7 @@ class DeltaBlock:
         d_out = flat[0].T @ dy[0]
         do = (dy @ w["out"].bfloat16().T).unflatten(-1, (self.hv, D))
         dqn, dkn, dv, dg, dbeta, _ = kda_gated_delta_bwd(self.context, do)
-        dq, dk, _, _ = kda_qk_norm_rope_bwd(dqn, dkn, q, k, self.unit, self.unit, None, None)
+        dq, dk, _, _ = kda_qk_norm_rope_bwd(dqn, dkn, q, k, self.one, self.unit, None, None)
         dz = -torch.sigmoid(z.float() - 2.0) * dg.float()
         s = torch.sigmoid(b.float())
         db = s * (1 - s) * dbeta.float()
@@ -130,7 +131,7 @@ def serve(block, prompts, tokens, width, seed=2):
     return stepped, torch.cat([whole[:, e - tokens:e] for e in ends])
 
 
-def main(width=512, hqk=2, hv=4, lens=(700, 1, 260, 63), steps=60, rate=1.0):
+def main(width=512, hqk=2, hv=4, lens=(700, 1, 260, 63), steps=60, rate=30.0):
     block, teacher = (DeltaBlock(width, hqk, hv) for _ in range(2))
     for n, t in DeltaBlock(width, hqk, hv, seed=7).weights.items():  # starts next to what it is to learn
         if n in ("in", "out"):

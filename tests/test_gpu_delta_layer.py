@@ -36,7 +36,7 @@ def plain_step(block, x, target, spans):
     x = x.double().requires_grad_()
     q, k, v, z, b, _ = (layer_norm(x, w["norm"], w["bias"], 1e-5)[0] @ w["in"]).split(block.split, -1)
     q, k = (t.unflatten(-1, (block.hqk, D)) for t in (q, k))
-    q, k = (t / (D * t.square().mean(-1, keepdim=True) + D * 1e-6).sqrt() for t in (q, k))
+    q, k = (t / (t.square().mean(-1, keepdim=True) + 1e-6).sqrt() * f for t, f in ((q, 1.0), (k, D ** -0.5)))
     g, beta = -torch.nn.functional.softplus(z - 2.0), torch.sigmoid(b)
     h0 = torch.zeros(len(spans), block.hv, D, D, dtype=torch.float64, device=x.device)
     o, _ = delta_scan(q[0], k[0], v[0].unflatten(-1, (block.hv, D)), g[0], beta[0], h0, spans, D ** -0.5)
