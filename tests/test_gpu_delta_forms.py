@@ -188,6 +188,25 @@ def test_buffers_of_the_caller():
     same(want, mine)
 
 
+def test_gradients_that_are_not_wanted():
+    """At the C interface the decays' gradient and the start state's may be left out; the others are the same."""
+    from linear_attention_gated_gb300 import kda_gated_delta_fwd
+    from linear_attention_gated_gb300.decay import _call
+    from linear_attention_gated_gb300.kda import load_library
+    x = make((90, 40), 2, 4, seed=45)
+    want, _ = run(x)
+    d = {n: t.cuda() for n, t in x.items()}
+    ctx = kda_gated_delta_fwd(*(d[n] for n in TOKENS), d["h0"], d["cu"], cu_seqlens_cpu=x["cu"])[2]
+    got = {n: torch.full_like(want[n], float("nan")) for n in ("dq", "dk", "dv", "dbeta")}
+    ws = ctx.workspace
+    _call(load_library().kda_gated_delta_bwd, ctx.device, *ctx.call, d["do"].data_ptr(), d["dhT"].data_ptr(), got["dq"].data_ptr(),
+          got["dk"].data_ptr(), got["dv"].data_ptr(), None, got["dbeta"].data_ptr(), None, ws.data_ptr(), ws.numel(),
+          ctx.device_status.data_ptr())
+    torch.cuda.synchronize()
+    ctx.status()
+    same(got, want)
+
+
 @pytest.mark.parametrize("lens", [(90, 40), (3100, 20)], ids=str)
 def test_what_a_workspace_held_does_not_matter(lens):
     """Prefill in a workspace of all ones bits (NaN), and one that is too small."""
