@@ -81,13 +81,6 @@ def kda_gated_delta_fwd(q, k, v, log_decay, beta, initial_state=None, cu_seqlens
     if cu_host is not None:
         known = ctx is not None and ctx.cu is not None and torch.equal(cu_host, ctx.cu)
         cu_host = ctx.cu if known else cu_host.clone()
-    if ctx is None:
-        ctx = DeltaContext(key, gated_delta_workspace_bytes(B, T, Hqk, Hv, cu_host), dev, stream)
-    elif cu_host is not None and not known:
-        nbytes = gated_delta_workspace_bytes(B, T, Hqk, Hv, cu_host)  # other lengths may need more
-        if nbytes > ctx.workspace.numel():
-            ctx.outgrown.append(ctx.workspace)
-            ctx.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     if out is None:
         out = torch.empty((B, T, Hv, D), dtype=_BF16, device=dev)
     else:
@@ -96,13 +89,22 @@ def kda_gated_delta_fwd(q, k, v, log_decay, beta, initial_state=None, cu_seqlens
         final_state_out = torch.empty((N, Hv, D, D), dtype=_F32, device=dev)
     else:
         _want(final_state_out, "final_state_out", _F32, (N, Hv, D, D), dev)
+    if ctx is None:
+        ctx = DeltaContext(key, gated_delta_workspace_bytes(B, T, Hqk, Hv, cu_host), dev, stream)
+    ws = ctx.workspace
+    if context_out is not None and cu_host is not None and not known:
+        nbytes = gated_delta_workspace_bytes(B, T, Hqk, Hv, cu_host)  # other lengths may need more
+        if nbytes > ws.numel():  # (the context keeps its own until the call has gone through: the last forward's backward needs it)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     s = _NAN if scale is None else float(scale)
     shape = (_p(cu_seqlens), _p(cu_host), N, B, T, Hqk, Hv, D, s, strides)
     tokens = (q.data_ptr(), k.data_ptr(), v.data_ptr(), _p(log_decay), beta.data_ptr())
-    ws = ctx.workspace
     _call(lib.kda_gated_delta_fwd, dev, *tokens, _p(initial_state), *shape, out.data_ptr(), final_state_out.data_ptr(),
           ws.data_ptr(), ws.numel(), ctx.device_status.data_ptr())
     _written((out, final_state_out))
+    if ws is not ctx.workspace:
+        ctx.outgrown.append(ctx.workspace)
+        ctx.workspace = ws
     # (the final state is not read again)
     ctx._snapshot((q, k, v, log_decay, beta, initial_state, cu_seqlens, None), tokens + shape, cu_host,
                   (q.shape, v.shape, (N, Hv, D, D), log_decay is not None))

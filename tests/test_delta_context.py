@@ -83,6 +83,38 @@ def test_a_workspace_that_was_too_small_lives_as_long_as_the_context(calls):
     assert first() is None
 
 
+def test_a_refused_forward_leaves_the_one_before_as_it_was(calls):
+    """A forward on a used context that needs a larger workspace and is refused, by the binding or by the library: the backward of the
+    forward before still gets that forward's workspace and offsets."""
+    from linear_attention_gated_gb300 import KdaError, delta, kda_gated_delta_bwd, kda_gated_delta_fwd
+    x = inputs(8192)
+    *_, ctx = kda_gated_delta_fwd(*x, cu_seqlens=offsets(EVEN), cu_seqlens_cpu=offsets(EVEN))
+    more = dict(cu_seqlens=offsets(LONG), cu_seqlens_cpu=offsets(LONG), context_out=ctx)
+
+    def refused(error, **kw):
+        with pytest.raises(error):
+            kda_gated_delta_fwd(*x, **more, **kw)
+        made = len(calls)
+        kda_gated_delta_bwd(ctx, x[2])
+        assert len(calls) == made + 1
+        assert (calls[-1].workspace, calls[-1].workspace_bytes, calls[-1].cu) == (calls[0].workspace, calls[0].workspace_bytes, calls[0].cu)
+
+    refused(ValueError, out=x[0][:, :5])
+    refused(ValueError, final_state_out=torch.zeros(1, 1, D, D))
+    caught = delta._call
+
+    def overlap(f, device, *args):
+        if f.__name__ == "kda_gated_delta_fwd":
+            raise KdaError(3, "an output overlaps an input or another output")
+        caught(f, device, *args)
+
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(delta, "_call", overlap)
+        refused(KdaError)
+    kda_gated_delta_fwd(*x, **more)  # and the larger one is taken when the call goes through
+    assert calls[-1].workspace_bytes >= need(LONG) > calls[0].workspace_bytes
+
+
 def test_reuse_that_is_refused(calls, monkeypatch):
     """Another stream (two steps at once would share one workspace), other shapes, a context of another operator."""
     from linear_attention_gated_gb300 import KdaError, delta, kda_gated_delta_bwd, kda_gated_delta_fwd
