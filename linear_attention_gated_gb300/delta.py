@@ -99,8 +99,14 @@ def kda_gated_delta_fwd(q, k, v, log_decay, beta, initial_state=None, cu_seqlens
     s = _NAN if scale is None else float(scale)
     shape = (_p(cu_seqlens), _p(cu_host), N, B, T, Hqk, Hv, D, s, strides)
     tokens = (q.data_ptr(), k.data_ptr(), v.data_ptr(), _p(log_decay), beta.data_ptr())
-    _call(lib.kda_gated_delta_fwd, dev, *tokens, _p(initial_state), *shape, out.data_ptr(), final_state_out.data_ptr(),
-          ws.data_ptr(), ws.numel(), ctx.device_status.data_ptr())
+    last, ctx.inputs = ctx.inputs, ()
+    try:
+        _call(lib.kda_gated_delta_fwd, dev, *tokens, _p(initial_state), *shape, out.data_ptr(), final_state_out.data_ptr(),
+              ws.data_ptr(), ws.numel(), ctx.device_status.data_ptr())
+    except KdaError as e:
+        if e.status != 5:  # refused before any launch: the last forward stands (after a CUDA error the workspace may hold a part of this one)
+            ctx.inputs = last
+        raise
     _written((out, final_state_out))
     if ws is not ctx.workspace:
         ctx.outgrown.append(ctx.workspace)

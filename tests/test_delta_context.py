@@ -115,6 +115,36 @@ def test_a_refused_forward_leaves_the_one_before_as_it_was(calls):
     assert calls[-1].workspace_bytes >= need(LONG) > calls[0].workspace_bytes
 
 
+def test_a_forward_that_failed_on_its_way_has_no_backward(calls, monkeypatch):
+    """Its first launches may have written to the workspace: neither its own backward nor that of the forward before is right."""
+    from linear_attention_gated_gb300 import KdaError, delta, kda_gated_delta_bwd, kda_gated_delta_fwd
+    x = inputs(64)
+    *_, ctx = kda_gated_delta_fwd(*x)
+    caught = delta._call
+
+    def fails(*args):
+        raise KdaError(5, "a launch failed")
+
+    monkeypatch.setattr(delta, "_call", fails)
+    with pytest.raises(KdaError, match="launch"):
+        kda_gated_delta_fwd(*x, context_out=ctx)
+    monkeypatch.setattr(delta, "_call", caught)
+    with pytest.raises(KdaError, match="no forward"):
+        kda_gated_delta_bwd(ctx, x[2])
+    kda_gated_delta_fwd(*x, context_out=ctx)
+    kda_gated_delta_bwd(ctx, x[2])
+    assert len(calls) == 3
+
+    def unversioned(tensors):
+        raise RuntimeError("an inference tensor outside of inference mode")
+
+    monkeypatch.setattr(delta, "_written", unversioned)
+    with pytest.raises(RuntimeError, match="inference"):
+        kda_gated_delta_fwd(*x, context_out=ctx)
+    with pytest.raises(KdaError, match="no forward"):
+        kda_gated_delta_bwd(ctx, x[2])
+
+
 def test_reuse_that_is_refused(calls, monkeypatch):
     """Another stream (two steps at once would share one workspace), other shapes, a context of another operator."""
     from linear_attention_gated_gb300 import KdaError, delta, kda_gated_delta_bwd, kda_gated_delta_fwd
