@@ -580,7 +580,8 @@ kda_status kda_gated_delta_fwd(const kda_bf16* q, const kda_bf16* k, const kda_b
  * d_o BF16 [B, T, Hv, 128], d_hT FP32 [N, Hv, 128, 128] or NULL (zeros); dq, dk BF16
  * [B, T, Hqk, 128] (sums over the value heads of the group, rounded once), dv BF16
  * [B, T, Hv, 128], dlog_decay BF16 [B, T, Hv] (or NULL: not wanted; NULL without decays), dbeta BF16
- * [B, T, Hv], dh0 FP32 or NULL. All gradients contiguous. */
+ * [B, T, Hv], dh0 FP32 or NULL. All gradients contiguous. The kernels stay inside the tensors
+ * whatever the workspace holds (the gradients mean nothing where it is not the forward's). */
 kda_status kda_gated_delta_bwd(const kda_bf16* q, const kda_bf16* k, const kda_bf16* v,
                                const kda_bf16* log_decay, const kda_bf16* beta,
                                const int64_t* cu_seqlens_dev, const int64_t* cu_seqlens_host,

@@ -106,9 +106,14 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
   // the first unit from x on that has a chunk, from prep's list (looking for it took 2000 cycles, and a load behind all the tiles
   // on their way 5000: the usual one is asked for two units before)
   int2 ch{0, 0}, ch1{0, 0};
+  // (held inside the tensors, whatever the workspace holds: tokens of none where it does not begin in one)
+  auto held = [&](int2 c) {
+    const uint32_t all = (uint32_t)P.Ttot, at = (uint32_t)c.x;
+    return make_int2(c.x, at >= all ? 0 : min(c.y, (int)min(all - at, (uint32_t)kC)));
+  };
   auto find = [&](uint32_t x, int2& c) {
     for (; x < units; x += gridDim.x) {
-      c = chunks[x / (uint32_t)P.Hqk];
+      c = held(chunks[x / (uint32_t)P.Hqk]);
       if (c.y > 0) break;
     }
     return x;
@@ -294,7 +299,7 @@ kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, c
         unit1 = unit + gridDim.x;
         if (unit1 < units) {
           const bool here = sm.asked[un & 1] == unit1;
-          if (here) ch1 = sm.next[un & 1];
+          if (here) ch1 = held(sm.next[un & 1]);
           if (!here || ch1.y <= 0) unit1 = find(here ? unit1 + gridDim.x : unit1, ch1);
         }
         slot1 = (int)(unit1 / (uint32_t)P.Hqk);
