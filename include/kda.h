@@ -405,6 +405,7 @@ kda_status kda_prefill(const kda_bf16* q, const kda_bf16* k, const kda_bf16* v, 
  *   log_decay   g <= 0 (meant; larger values let the state grow): FP32 [Hv], fixed
  *               for each head (decay_per_token 0), or BF16 [B, T, Hv]
  *               (decay_per_token 1). -inf resets the state.
+ *               (This and the other device arrays that need no 16 bytes are aligned to their elements.)
  *   cu_seqlens  packed layout as above (B = 1, device tensor and host mirror);
  *               sequences may be empty here: their state passes through. The
  *               kernels hold device offsets that disagree with the mirror inside

@@ -103,6 +103,7 @@ extern "C" kda_status kda_decay_attn_bwd(const kda_bf16* q, const kda_bf16* k, c
       return fail(KDA_ERR_INVALID_ARGUMENT, "the decays' gradient needs the forward's h_T where there is a d_hT");
     if (((uintptr_t)h_T | (uintptr_t)d_o | (uintptr_t)d_hT | (uintptr_t)dq | (uintptr_t)dk | (uintptr_t)dv | (uintptr_t)h0 | (uintptr_t)dh0) & 15u)
       return fail(KDA_ERR_INVALID_ARGUMENT, "state, adjoint and gradient tensors must be 16-byte aligned");
+    if (kda::host::misaligned(dlog_decay, 2)) return fail(KDA_ERR_INVALID_ARGUMENT, kda::host::kMisaligned);
     if ((st = check_workspace(P, workspace, workspace_bytes, true)) != KDA_OK) return st;
     const size_t states = 4 * (size_t)P.N * Hv * kda::kDim * kda::kDim;
     const size_t tq = 2 * (size_t)P.Ttot * Hqk * kda::kDim, tv = 2 * (size_t)P.Ttot * Hv * kda::kDim;
@@ -144,6 +145,7 @@ extern "C" kda_status kda_decay_attn_prefill(const kda_bf16* q, const kda_bf16* 
     if (!state || (P.Ttot && !o)) return fail(KDA_ERR_INVALID_ARGUMENT, "null tensor pointer");
     if (((uintptr_t)o | (uintptr_t)state) & 15u)
       return fail(KDA_ERR_INVALID_ARGUMENT, "state and output tensors must be 16-byte aligned");
+    if (kda::host::misaligned(state_indices, 4)) return fail(KDA_ERR_INVALID_ARGUMENT, kda::host::kMisaligned);
     if (num_slots < 1 || num_slots > (int64_t(1) << 31) || kda::pool_too_large(num_slots, Hv))
       return fail(KDA_ERR_UNSUPPORTED, "the pool needs 1 to 2^31 slots, and at most 2^40 states");
     if ((state_indices == nullptr) != (state_indices_host == nullptr))

@@ -123,6 +123,8 @@ extern "C" kda_status kda_decay_attn_decode(const kda_bf16* q, const kda_bf16* k
     }
     if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)state | (uintptr_t)o) & 15u)
       return dfail(KDA_ERR_INVALID_ARGUMENT, "decay_attn decode: token and state tensors must be 16-byte aligned");
+    if (((uintptr_t)state_indices & 3u) || ((uintptr_t)log_decay & (decay_per_token ? 1u : 3u)))
+      return dfail(KDA_ERR_INVALID_ARGUMENT, "decay_attn decode: tensors must be aligned to their elements");
     const int64_t D = kda::kDim, heads[3] = {Hqk, Hqk, Hv};
     int64_t x[6] = {Hqk * D, D, Hqk * D, D, Hv * D, D};
     if (strides)

@@ -19,6 +19,10 @@ inline kda_status fail(const char* op, kda_status st, const char* what) {
   return st;
 }
 
+// (device pointers: a kernel that reads through one that is not aligned to its elements faults)
+inline bool misaligned(const void* p, size_t to) { return ((uintptr_t)p & (to - 1)) != 0; }
+constexpr const char* kMisaligned = "tensors must be aligned to their elements";
+
 struct Span {
   const void* p;
   size_t bytes;
@@ -84,6 +88,7 @@ inline kda_status check_tokens(const char* op, const void* q, const void* k, con
   if ((decays && !g && (s.Ttot || !per_token)) || (s.Ttot && (!q || !k || !v))) return fail(op, KDA_ERR_INVALID_ARGUMENT, "null tensor pointer");
   if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v) & 15u)
     return fail(op, KDA_ERR_INVALID_ARGUMENT, "token tensors must be 16-byte aligned");
+  if (misaligned(g, per_token ? 2 : 4) || misaligned(cu_dev, 8)) return fail(op, KDA_ERR_INVALID_ARGUMENT, kMisaligned);
   const int64_t D = kDim;
   int64_t x[6] = {Hqk * D, D, Hqk * D, D, Hv * D, D};
   if (strides)
@@ -133,6 +138,7 @@ inline kda_status check_pool(const char* op, const Pool& p, int64_t N, int64_t H
   if (p.slots < 0 || p.slots > (int64_t(1) << 31) || pool_too_large(p.slots, Hv))
     return fail(op, KDA_ERR_UNSUPPORTED, "more than 2^31 pool slots or 2^40 states");
   if ((uintptr_t)p.state & 15u) return fail(op, KDA_ERR_INVALID_ARGUMENT, "state and output tensors must be 16-byte aligned");
+  if (misaligned(p.idx, 4)) return fail(op, KDA_ERR_INVALID_ARGUMENT, kMisaligned);
   if ((p.idx == nullptr) != (p.idx_host == nullptr))
     return fail(op, KDA_ERR_INVALID_ARGUMENT, "state_indices needs its host mirror (and the reverse)");
   if (p.idx_host) {
@@ -150,6 +156,7 @@ inline Span pool_span(const Pool& p, int64_t Hv) {
 
 // The device is one that the kernels are built for; *status: the caller's word, or the library's `own` one.
 inline kda_status check_device(const char* op, int32_t* device_status, const void* own, int32_t** status) {
+  if (misaligned(device_status, 4)) return fail(op, KDA_ERR_INVALID_ARGUMENT, kMisaligned);
   int dev = -1, major = 0, minor = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);

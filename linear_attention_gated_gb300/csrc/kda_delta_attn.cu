@@ -26,6 +26,7 @@ kda_status check(const void* q, const void* k, const void* v, const void* g, con
   const kda_status st = check_tokens(kOp, q, k, v, g, false, 1, cu_dev, cu_host, num_seqs, B, T, Hqk, Hv, head_dim, scale, strides, P, in);
   if (st != KDA_OK) return st;
   if (P->Ttot && !beta) return fail(KDA_ERR_INVALID_ARGUMENT, "null tensor pointer");
+  if (misaligned(beta, 2)) return fail(KDA_ERR_INVALID_ARGUMENT, kMisaligned);
   for (int i = 0; i < 5; ++i) spans[i] = in[i];
   spans[5] = Span{beta, 2 * (size_t)P->Ttot * Hv};
   P->beta = reinterpret_cast<const __nv_bfloat16*>(beta);
@@ -102,6 +103,7 @@ extern "C" kda_status kda_gated_delta_bwd(const kda_bf16* q, const kda_bf16* k, 
     if (dlog_decay && !log_decay) return fail(KDA_ERR_INVALID_ARGUMENT, "no log_decay: dlog_decay must be NULL");
     if (((uintptr_t)d_o | (uintptr_t)d_hT | (uintptr_t)dq | (uintptr_t)dk | (uintptr_t)dv | (uintptr_t)dh0) & 15u)
       return fail(KDA_ERR_INVALID_ARGUMENT, "state, adjoint and gradient tensors must be 16-byte aligned");
+    if (misaligned(dlog_decay, 2) || misaligned(dbeta, 2)) return fail(KDA_ERR_INVALID_ARGUMENT, kMisaligned);
     if ((st = check_workspace(P, workspace, workspace_bytes, true)) != KDA_OK) return st;
     const size_t states = 4 * (size_t)P.N * Hv * kda::kDim * kda::kDim, gates = 2 * (size_t)P.Ttot * Hv;
     const size_t tq = 2 * (size_t)P.Ttot * Hqk * kda::kDim, tv = gates * kda::kDim;

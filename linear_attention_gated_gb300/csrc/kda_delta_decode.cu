@@ -117,6 +117,7 @@ extern "C" kda_status kda_gated_delta_decode(const kda_bf16* q, const kda_bf16* 
     if (st != KDA_OK) return st;
     if (N > INT32_MAX / 4 / Hv) return fail(op, KDA_ERR_UNSUPPORTED, "too many (sequence, head) units");
     if (N && (!beta || !state || !o)) return fail(op, KDA_ERR_INVALID_ARGUMENT, "null tensor pointer");
+    if (misaligned(beta, 2)) return fail(op, KDA_ERR_INVALID_ARGUMENT, kMisaligned);
     const kda::host::Pool pool{state, state_dtype, state_indices, state_indices_host, num_slots};
     if ((st = check_pool(op, pool, N, Hv)) != KDA_OK) return st;
     if ((uintptr_t)o & 15u) return fail(op, KDA_ERR_INVALID_ARGUMENT, "state and output tensors must be 16-byte aligned");

@@ -504,7 +504,6 @@ kda_status check_rows(int32_t dtype, int64_t rows, int64_t D, int64_t stride, si
   *bytes = rows ? (dtype == KDA_DTYPE_FP32 ? 4 : 2) * (size_t)((rows - 1) * stride + D) : 0;
   return KDA_OK;
 }
-bool misaligned(const void* p, size_t to) { return ((uintptr_t)p & (to - 1)) != 0; }
 
 }  // namespace
 }  // namespace kda
@@ -522,9 +521,9 @@ extern "C" kda_status kda_layer_norm_fwd(const void* x, int32_t dtype, const flo
     if (!(eps >= 0.f) || eps > 3.0e38f) return fail(KDA_ERR_INVALID_ARGUMENT, "eps must be finite and not negative");
     if (rows && (!x || !y || !mean || !rstd)) return fail(KDA_ERR_INVALID_ARGUMENT, "null tensor pointer");
     const size_t size = dtype == KDA_DTYPE_FP32 ? 4 : 2;
-    if (kda::misaligned(x, size) || kda::misaligned(y, size) || kda::misaligned(weight, 4) || kda::misaligned(bias, 4) ||
-        kda::misaligned(mean, 4) || kda::misaligned(rstd, 4))
-      return fail(KDA_ERR_INVALID_ARGUMENT, "tensors must be aligned to their elements");
+    if (kda::host::misaligned(x, size) || kda::host::misaligned(y, size) || kda::host::misaligned(weight, 4) || kda::host::misaligned(bias, 4) ||
+        kda::host::misaligned(mean, 4) || kda::host::misaligned(rstd, 4))
+      return fail(KDA_ERR_INVALID_ARGUMENT, kda::host::kMisaligned);
     const Span outs[] = {{y, yb}, {mean, 4 * (size_t)rows}, {rstd, 4 * (size_t)rows}};
     const Span own[] = {{weight, 4 * (size_t)width}, {bias, 4 * (size_t)width}, {x == y && row_stride == width ? nullptr : x, xb}};
     if (kda::host::aliasing(outs, own) || kda::host::overlap(Span{x, xb}, outs[1]) || kda::host::overlap(Span{x, xb}, outs[2]))
@@ -568,10 +567,10 @@ extern "C" kda_status kda_layer_norm_bwd(const void* dy, const void* x, int32_t 
     if (need && (!workspace || workspace_bytes < need))
       return fail(KDA_ERR_WORKSPACE_TOO_SMALL, "workspace below kda_layer_norm_workspace_bytes()");
     const size_t size = dtype == KDA_DTYPE_FP32 ? 4 : 2;
-    if (kda::misaligned(x, size) || kda::misaligned(dy, size) || kda::misaligned(dx, size) || kda::misaligned(weight, 4) ||
-        kda::misaligned(mean, 4) || kda::misaligned(rstd, 4) || kda::misaligned(dweight, 4) || kda::misaligned(dbias, 4) ||
-        kda::misaligned(workspace, 4))
-      return fail(KDA_ERR_INVALID_ARGUMENT, "tensors must be aligned to their elements");
+    if (kda::host::misaligned(x, size) || kda::host::misaligned(dy, size) || kda::host::misaligned(dx, size) || kda::host::misaligned(weight, 4) ||
+        kda::host::misaligned(mean, 4) || kda::host::misaligned(rstd, 4) || kda::host::misaligned(dweight, 4) || kda::host::misaligned(dbias, 4) ||
+        kda::host::misaligned(workspace, 4))
+      return fail(KDA_ERR_INVALID_ARGUMENT, kda::host::kMisaligned);
     // dx may take the place of dy or x (contiguous ones): a row is read before it is written. Rows wider than registers hold
     // are read again for the sums, so there it may not.
     const bool again = width > (dtype == KDA_DTYPE_FP32 ? 8192 : 12288);
