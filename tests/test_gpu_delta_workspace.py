@@ -42,3 +42,38 @@ def test_a_list_of_chunks_that_is_not_the_forwards(entry, hqk, hv):
     for n in d:
         assert torch.equal(d[n].cpu(), x[n]), n
     same(want, step(False))
+
+
+@pytest.mark.parametrize("lens,hqk,hv,gate", [((90, 0, 40, 1), 2, 4, True), ((3100, 0, 20), 1, 1, True), ((3100, 70), 1, 2, False),
+                                              ((0, 0), 1, 2, True)], ids=str)
+@pytest.mark.parametrize("fill", [0xff, 0x7f, 1])
+def test_what_a_contexts_workspace_held_does_not_matter(lens, hqk, hv, gate, fill):
+    """A step on a used context whose workspace was overwritten before its forward: NaN in all types, the largest numbers, ones.
+    Places of no chunk, segments' maps that are known to be zero and the last segments' stay unwritten."""
+    x = make(lens, hqk, hv, seed=51, gate=gate)
+    if gate and len(lens) == 3:  # resets: the first head's maps are zero
+        x["g"][:, 700::500] = -float("inf")
+    want, ctx = run(x)
+    ctx.workspace.fill_(fill)
+    same(want, run(x, ctx=ctx)[0])
+
+
+def test_contexts_of_growing_and_shrinking_lengths():
+    """Steps whose backward follows a refused forward, and steps of other lengths on one context."""
+    from linear_attention_gated_gb300 import KdaError, kda_gated_delta_bwd, kda_gated_delta_fwd
+    even, long = make([512] * 16, 1, 1, seed=52), make([7680] + [34] * 14 + [36], 1, 1, seed=53)
+    first, ctx = run(even)
+    d = {n: t.cuda() for n, t in even.items()}
+    e = {n: t.cuda() for n, t in long.items()}
+    before = ctx.workspace
+    for error, wrong in ((ValueError, dict(out=e["v"][:, :5])), (KdaError, dict(out=e["v"]))):  # (of another shape, and over an input)
+        kda_gated_delta_fwd(*(d[n] for n in TOKENS), d["h0"], d["cu"], context_out=ctx, cu_seqlens_cpu=even["cu"])
+        with pytest.raises(error):
+            kda_gated_delta_fwd(*(e[n] for n in TOKENS), e["h0"], e["cu"], context_out=ctx, cu_seqlens_cpu=long["cu"], **wrong)
+        assert ctx.workspace is before
+        got = kda_gated_delta_bwd(ctx, d["do"], d["dhT"])
+        same({n: first[n] for n in GRADS}, dict(zip(GRADS, got)))
+    alone, _ = run(long)
+    same(alone, run(long, ctx=ctx)[0])
+    assert ctx.workspace is not before
+    same(first, run(even, ctx=ctx)[0])

@@ -174,3 +174,29 @@ def test_rows_past_32_bit_offsets():
     assert torch.equal(y[:before:997], b.bfloat16().expand(y[:before:997].shape))
     dx = kda_layer_norm_bwd(bigd, big, w, mean, rstd)[0]
     assert torch.equal(dx[before:], kda_layer_norm_bwd(dy, x, w, *want[1:])[0]) and not dx[:before].any()
+
+
+@pytest.mark.parametrize("width,dtype", [(96, torch.bfloat16), (4096, torch.bfloat16), (1001, torch.float32), (12296, torch.bfloat16)], ids=str)
+def test_a_workspace_of_the_caller(width, dtype):
+    """Of the documented size, used for two numbers of rows in turn (fewer and more than there are SMs): what it held does not
+    matter, and what lies behind it stays."""
+    import ctypes
+
+    from linear_attention_gated_gb300 import KdaError, kda_layer_norm_bwd, kda_layer_norm_fwd
+    from linear_attention_gated_gb300.kda import load_library
+
+    def need(rows):
+        n = ctypes.c_size_t(0)
+        assert load_library().kda_layer_norm_workspace_bytes(rows, width, ctypes.byref(n)) == 0
+        return n.value
+
+    room = torch.full((need(700) + 4096,), 255, dtype=torch.uint8, device="cuda")
+    for rows in (700, 5, 151, 153, 700):
+        x, w, b, dy = make((rows, width), dtype, seed=rows)
+        _, mean, rstd = kda_layer_norm_fwd(x, w, b)
+        want = kda_layer_norm_bwd(dy, x, w, mean, rstd)
+        got = kda_layer_norm_bwd(dy, x, w, mean, rstd, workspace=room[:need(rows)])
+        assert all(torch.equal(a, c) for a, c in zip(got, want)), rows
+        assert (room[need(700):] == 255).all()
+        with pytest.raises(KdaError):
+            kda_layer_norm_bwd(dy, x, w, mean, rstd, workspace=room[:need(rows) - 1])
