@@ -267,13 +267,14 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
 
 // Asynchronous 16-byte global -> shared copy (bypassing L1); src_bytes < 16
 // zero-fills the rest (0 copies nothing and writes zeros).
-template <int kBytes>  // 4 or 8
-__device__ __forceinline__ void cp_async_small(void* smem_dst, const void* gsrc, uint32_t src_bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(smem_dst)), "l"(gsrc), "n"(kBytes), "r"(src_bytes) : "memory");
-}
 __device__ __forceinline__ void cp_async16(void* smem_dst, const void* gsrc, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(gsrc), "r"(src_bytes)
                : "memory");
+}
+// The same of 4 or 8 bytes, aligned to that, through L1; what src_bytes leaves is filled with zeros.
+template <int kBytes>
+__device__ __forceinline__ void cp_async_small(void* smem_dst, const void* gsrc, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(smem_dst)), "l"(gsrc), "n"(kBytes), "r"(src_bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
