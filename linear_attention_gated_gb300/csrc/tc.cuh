@@ -424,7 +424,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
   return d;
 }
-__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.f, -1.f), a); }
 
 // 4x4 transpose among the four lanes of an aligned lane quad: on entry lane (quad base + j) holds
 // row j of the block, on exit it holds column j (four shuffles; the whole warp takes part).
