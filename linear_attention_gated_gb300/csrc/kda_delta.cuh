@@ -21,7 +21,9 @@ struct DeltaProblem : DecayProblem {  // (g may be null: no decay)
 };
 
 // What is made for each (chunk, head). T and P are BF16 tiles [64][64] in the 128-byte swizzle, in two parts hi + lo
-// (16 mantissa bits); P's low part is for the backward alone.
+// (16 mantissa bits). P's low part is for the backward alone, where it feeds an adjoint: o, which is rounded to BF16 itself, reads P in
+// one part, since 8 KiB more a chunk leave no room for two stages of tiles (2.3e-3 from 64 bits with decays, 1.7e-3 of it o's own
+// rounding).
 constexpr uint32_t kPkT = 0, kPkTlo = 8192, kPkP = 16384, kPkAux = 24576, kPkPlo = 26624;
 constexpr uint32_t kPkInfer = kPkPlo, kPkTrain = kPkPlo + 8192;
 struct DeltaAux {
@@ -36,6 +38,7 @@ struct DeltaAux {
 constexpr uint32_t kPkPass = kPkAux + 1024;  // what the forward's pass reads: up to `whole`
 static_assert(sizeof(DeltaAux) <= kPkPlo - kPkAux && offsetof(DeltaAux, b) == 1024, "a chunk's numbers");
 
+// The passes carry states and adjoints on in FP32; these are copies for the gradients within chunks, whose operands they are and no more.
 constexpr uint32_t kStateTile = 32768, kUTile = 16384;  // a state in BF16 [2][128 rows][64], u [2][64 tokens][64], swizzled
 
 // Place of a sequence's first chunk: leaves each sequence ceil(len / 64) places.

@@ -13,8 +13,8 @@
 // tokens, T being lower triangular: the first half's u does not wait for the second's x. So does the update, in halves of
 // the state's columns, and S K^T starts with the first of them. What is off the chain (S Q^T, beta u for the output) is put where
 // the tensor core and the warps would wait.
-// Bound: that chain, 4450 cycles a chunk: the turns of its three products (issue, tensor core, commit, wake: some 500 each) and the
-// element-wise steps between them (430 to 700). 8 x 1024 tokens of 96 heads, 5.05 units an SM: 233 us, 1.1 GB moved; issue slots
+// Bound: that chain, 4470 cycles a chunk (2.16 us): the turns of its three products (issue, tensor core, commit, wake: some 500 each) and the
+// element-wise steps between them (430 to 700). 8 x 1024 tokens of 96 heads, 5.05 units an SM: 235 us, 1.1 GB moved; issue slots
 // used to 40 %. When this took 249 us: with W = T e^b K made a chunk ahead the chain has two products and takes 301 us: the products a chunk ahead
 // cost more issue time than that saves; waits that poll instead of being suspended, 277 us.
 //

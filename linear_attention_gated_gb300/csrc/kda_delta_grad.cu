@@ -10,7 +10,9 @@
 //   dg_t = sum_{i >= t} e^{b_i} (s q_i . S^T dO_i - k_i . S^T rho_i) + sum_{j < t} w_j beta_j k_j . G^T u_j + e^{b_C} <G, S>
 //        + sum_{i >= t > j} beta_j (E_ij - F_ij)
 // whose last sum grows from t to t + 1 by the column t below the diagonal less the row t before it. (The shorter
-// q_i . dq_i - v_i . dv_i summed from t on has the same value, but its terms cancel: 1.8e-2 off from operands in BF16, this 2e-3.)
+// q_i . dq_i - v_i . dv_i summed from t on has the same value, but its terms cancel: 1.8e-2 off from operands in BF16, this 2.5e-3.)
+// No sum of sums goes on from here, so operands are in one BF16 part (S, G, u, rho = dv as it is returned, A, R): gradients are 2.4e-3
+// to 3.0e-3 from 64 bits, 1.7e-3 of it their own rounding. Second parts of the tiles would be twice the bytes, and have no room.
 #include "kda_delta.cuh"
 #include "kda_layout.h"
 #include "kda_tma.h"
@@ -80,7 +82,7 @@ __device__ __forceinline__ int over_token(int token, int lane) { return token + 
 // One CTA an SM goes through the (chunk, query/key head) units b, b + gridDim.x, ..., and in each through the group's value heads. The
 // tiles of the next head are on their way once the first products of this one, their only readers, are done. Bound: a pair's
 // chain of two products' groups and the elements between them, 16 warps (8000 cycles, of which the 144 KiB of tiles in and out take
-// 70 %): 4 x 2048 tokens of 16 / 32 heads 132 us; a CTA for each unit, with nothing on its way, 236 us. Products are
+// 70 %): 4 x 2048 tokens of 16 / 32 heads 135 us; a CTA for each unit, with nothing on its way, 236 us. Products are
 // transposed, [128 values x 64 tokens], so that all have M = 128 and the tokens' factors are applied where the sums are read.
 __global__ void __launch_bounds__(kThreads, 1)
 kda_delta_grad_kernel(const __grid_constant__ Maps maps, const DeltaProblem P, const unsigned char* packets, const unsigned char* states,

@@ -12,7 +12,7 @@
 // sequences, 8 / 64 heads: 289 us, of 46,000 pairs; 499 us with a CTA a pair, each with its own scores, where the loads of the
 // decays took 5000 cycles behind all the tiles on their way and the search for the chunk 2000).
 // Made inside the pass that uses them, a chunk ahead of it, T and P cost no traffic, but their chain of some 900 instructions a
-// warp takes longer than a chunk's pass (7000 cycles against 4300), and 91 KiB of code of seven kinds of warps does not stay in the
+// warp takes longer than a chunk's pass (7000 cycles against 4470), and 91 KiB of code of seven kinds of warps does not stay in the
 // instruction cache: 8 x 1024 tokens of 96 heads 378 us so.
 #include "kda_delta.cuh"
 #include "kda_layout.h"
@@ -71,7 +71,7 @@ __device__ __forceinline__ void take_if(float& x, int i, int j, float y) {
   asm("{\n .reg .pred p;\n setp.eq.s32 p, %1, %2;\n @p mov.f32 %0, %3;\n}\n" : "+f"(x) : "r"(i), "r"(j), "f"(y));
 }
 
-// acc += A B for a 16 x 8 tile over 16 inner values, BF16 operands each in two parts (low x low left out).
+// acc += A B for a 16 x 8 tile over 16 inner values, BF16 operands each in two parts (low x low left out: 2^-16 of a product at most).
 __device__ __forceinline__ void mma_split(float* c, const uint32_t* ah, const uint32_t* al, const uint32_t* bh, const uint32_t* bl) {
   tc::mma_sync(c, ah, bl);
   tc::mma_sync(c, al, bh);
@@ -124,6 +124,8 @@ __global__ void __launch_bounds__(128, kCtas) kda_delta_prep_kernel(const __grid
   };
   // ... and, a turn later, warp 2 asks for them, two tokens a lane, before it waits for the scores (behind all the tiles that are on
   // their way this can take 5000 cycles; a load to a register is waited for at the next loop) ...
+  // (A number in the upper half of a word comes with the two bytes before it, the tensor's own or not: in the same word, so
+  // they can be read, and are not looked at.)
   auto ask = [&](const Next& of, Numbers& num) {  // to f: the 4-byte words that they are in
     const int64_t at = (int64_t)(of.t0 + 2 * lane) * P.Hv + of.h;
     auto copy = [](float* to, const void* p) {
