@@ -102,7 +102,8 @@ struct StateFactor {
   }
 };
 // x as BF16 pairs hi + lo: 16 mantissa bits together, for what feeds a state (products of two such operands leave out low x low, as
-// small as what the pairs leave: states come out within 1e-5; a third part would take six products in place of three). x - hi by multiply-adds that take BF16 factors as they are, -1 hi + x: two
+// small as what the pairs leave: states come out within 1e-5; a third part would take six products in place of three).
+// x - hi by multiply-adds that take BF16 factors as they are, -1 hi + x: two
 // instructions for two values where a subtraction takes three (8 x 1024 tokens of 96 heads of the gated delta rule 234 us, 246).
 __device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
   hi = pack2(x);

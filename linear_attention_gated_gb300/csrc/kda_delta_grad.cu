@@ -11,7 +11,7 @@
 //        + sum_{i >= t > j} beta_j (E_ij - F_ij)
 // whose last sum grows from t to t + 1 by the column t below the diagonal less the row t before it. (The shorter
 // q_i . dq_i - v_i . dv_i summed from t on has the same value, but its terms cancel: 1.8e-2 off from operands in BF16, this 2.5e-3.)
-// No sum of sums goes on from here, so operands are in one BF16 part (S, G, u, rho = dv as it is returned, A, R): gradients are 2.4e-3
+// Nothing is carried on from these sums, so operands are in one BF16 part (S, G, u, rho = dv as it is returned, A, R): gradients are 2.4e-3
 // to 3.0e-3 from 64 bits, 1.7e-3 of it their own rounding. Second parts of the tiles would be twice the bytes, and have no room.
 #include "kda_delta.cuh"
 #include "kda_layout.h"
